@@ -151,7 +151,9 @@ typedef struct zero_step_state {
                                     did not land within 4 more bounded waits: the
                                     CTA exited with it possibly still in flight,
                                     so treat the context as unreliable */
-    int32_t reserved[3];
+    float grad_scale;            /* zero_multi_grad_norm: the loss scale the gradients of
+                                    the last decided step carried (0: none decided)  */
+    int32_t reserved[2];
 } zero_step_state;
 
 /* AdamW hyperparameters that may change between steps (lr schedules).  The
@@ -593,6 +595,147 @@ zero_status_t zero_fused_step_noalloc(const zero_layout* L, const zero_adamw_hp*
                                       float* const* m, float* const* v, zero_step_state* st,
                                       void* const* param16_out, int32_t out_kind,
                                       zero_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* AdamW over a list of tensors, with 32-bit or 8-bit states                  */
+/* ------------------------------------------------------------------------ */
+/* The update of zero_adamw_shard_step for tensors that stay where they are:
+ * parameters that are replicated instead of sharded (norms, biases), models
+ * without a flat buffer, groups of tensors with learning rates and weight
+ * decays of their own, and, with 8-bit states, the rank shards themselves.
+ * The pages have no counterpart ([RN] §2.1 counts fp32 m and v, 8 of its 12
+ * bytes a parameter; here they take 2.06).
+ *
+ * A zero_multi is a list of n tensors: element counts (0 allowed), one of up
+ * to ZERO_MAX_GROUPS hyperparameter groups each, and after zero_multi_bind
+ * the device addresses.  Differences from the conventions above:
+ *   - The arrays of a tensor need the natural alignment of their elements
+ *     only (a tensor may begin anywhere in a flat buffer), else
+ *     ZERO_ERR_ALIGN; arrays of tensors with 0 elements may be NULL.  The
+ *     workspace and the state are 256-byte aligned as everywhere.  Tensors
+ *     whose arrays all begin on 32-byte boundaries (8-bit codes: 8) take the
+ *     fast path.
+ *   - Arrays of one call must not overlap, except that arrays that are only
+ *     read may.
+ *   - The object holds the addresses of the last bind; its workspace must
+ *     live as long, and only one stream at a time may run calls on it.
+ *
+ * 8-bit states.  Blocks of 32 consecutive elements of one tensor (the last
+ * one shorter); m holds E4M3 codes, v holds E5M2 codes, and one E8M0 byte s
+ * per block and state scales them: value = code * 2^(s - 127).  With E the
+ * biased binary32 exponent of the largest magnitude of the block (one more if
+ * its mantissa is above 1.75), s = max(1, E - 8) for m and max(1, E - 15) for
+ * v, so that the largest scaled value is at most 1.75 * 2^8 = 448, E4M3's
+ * largest (1.75 * 2^15 = 57344, E5M2's); E is at most 254, and magnitudes
+ * above 1.75 * 2^127 are stored as that.  A v above zero is stored as the
+ * smallest code at least.  A block that holds an inf or a NaN gets s = 255 and
+ * NaN codes.  A tensor of N elements has N code bytes and ceil(N / 32) scale
+ * bytes for each state; all zero bytes are m = v = 0. */
+#define ZERO_MAX_GROUPS 16
+#define ZERO_FP32 2      /* gradients of a zero_multi may also be binary32  */
+#define ZERO_NO_OUT (-1) /* no 16-bit copy of the parameters                */
+
+typedef struct zero_multi zero_multi; /* opaque */
+
+/* Host arrays of n_tensors device pointers each; NULL for what the calls on
+ * this list do not use. */
+typedef struct zero_multi_arrays {
+    const void* const* grads;    /* grad_dtype                                 */
+    float* const* master;        /* fp32 parameters                            */
+    float* const* m;             /* fp32 states                                */
+    float* const* v;
+    uint8_t* const* m8;          /* 8-bit states: codes and block scales       */
+    uint8_t* const* m8_scale;
+    uint8_t* const* v8;
+    uint8_t* const* v8_scale;
+    void* const* param16;        /* 16-bit copies of the parameters            */
+} zero_multi_arrays;
+
+typedef struct zero_multi_info {
+    int32_t n_tensors, n_groups, grad_dtype, param_dtype;
+    int64_t numel;               /* elements of all tensors                    */
+    int64_t n_chunks;            /* work items of the update kernels           */
+    int64_t state8_bytes;        /* codes and scales of both 8-bit states      */
+    int64_t workspace_bytes;     /* device workspace of zero_multi_bind        */
+} zero_multi_info;
+
+/*   numels[n_tensors]  element counts, 0 .. 2^34, n_tensors >= 1.
+ *   group_of_tensor    a group 0 .. n_groups-1 per tensor; NULL: all 0.
+ *   n_groups           1 .. ZERO_MAX_GROUPS.
+ *   grad_dtype         ZERO_BF16, ZERO_FP16 or ZERO_FP32.
+ *   param_dtype        ZERO_BF16 or ZERO_FP16 copies, or ZERO_NO_OUT.
+ * Host only.  On success *out owns a new object; on error it is untouched. */
+zero_status_t zero_multi_init(const int64_t* numels, int32_t n_tensors, const int32_t* group_of_tensor,
+                              int32_t n_groups, int32_t grad_dtype, int32_t param_dtype, zero_multi** out);
+zero_status_t zero_multi_query(const zero_multi* M, zero_multi_info* out);
+void zero_multi_destroy(zero_multi* M);
+
+/* Take the tensors' addresses: checks them, and writes them and the map of
+ * the work into `workspace` (at least info.workspace_bytes) by kernels on
+ * `stream`, which the calls on M have to follow.  The pointer arrays are read
+ * during the call only.  May be called again, with other addresses or another
+ * workspace (gradients that move): it costs a few short launches. */
+zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays* arrays, void* workspace,
+                              zero_stream_t stream);
+
+/* Global gradient norm over the list and the step decision: what
+ * ZERO_NORM_DECIDE does, for gradients x that still carry the loss scale:
+ * norm = sqrt(sum x^2) / loss_scale.  Overflow (the step is skipped): an inf
+ * or NaN gradient, or a sum of squares beyond binary32.  Also keeps the scale
+ * the gradients carry in st->grad_scale, since a dynamic one may grow here.
+ * Deterministic: fixed slices of the list, binary32 sums with their rounding
+ * errors carried along, combined in binary64 in a fixed order.  Needs grads.
+ * One launch. */
+zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_norm, zero_step_state* st,
+                                   zero_stream_t stream);
+
+/* Flags of the updates. */
+enum {
+    ZERO_MULTI_DECIDED = 0,  /* after zero_multi_grad_norm (or zero_grad_norm):
+                                apply st's decision and clip coefficient       */
+    ZERO_MULTI_ADVANCE = 1,  /* no norm: update with the constants of step t+1,
+                                clip 1, and advance t and beta^t (no skip)     */
+    ZERO_MULTI_UNSCALED = 2  /* the gradients carry no loss scale any more
+                                (e.g. reduced by zero_reduce_scatter)          */
+};
+
+/* AdamW with 32-bit states: per element of tensor i, with its group's hp and
+ * g = x * (1 / loss_scale) (one binary32 product; the reciprocal of a power
+ * of two is exact), the arithmetic of zero_adamw_shard_step, bit for bit.
+ * hp: n_groups entries.  Needs grads, master, m, v, and param16 unless
+ * param_dtype is ZERO_NO_OUT.  One launch.
+ * Errors: what the list was not bound with (ZERO_ERR_STATE); hp out of range,
+ * unknown flags, NULL (ZERO_ERR_INVALID). */
+zero_status_t zero_multi_adamw(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags, zero_step_state* st,
+                               zero_stream_t stream);
+
+/* The same with 8-bit states.  m and v are read as values, updated with the
+ * same binary32 operations, used for the parameters unrounded, and stored
+ * with stochastic rounding: a random integer below 2^20 (m) or 2^21 (v) is
+ * added to the bits of the scaled binary32 value, the lowest 20 (21) bits are
+ * cut off, and what is left is rounded to nearest into the code (exactly,
+ * above the smallest normal 2^-6 (2^-14)).  Nearest rounding alone would
+ * leave v where it is: a step with beta2 = 0.999 moves it by at most 0.1% of
+ * itself downwards, a code step is 14 to 25%.
+ * The random integers are a function of (seed, step number t, tensor index,
+ * element index): x = mix(mix(mix(seed ^ mix(t)) + tensor) + 0x9E3779B1 *
+ * (element / 8)), then x = 1664525 x + 1013904223 (the linear congruential
+ * generator of Numerical Recipes) twice for each of the 8 elements, x >> 12
+ * for m and x >> 11 for v; mix(x): x ^= x >> 16, x *= 0x9E3779B1, x ^= x >> 15,
+ * x *= 0xBB67AE85, x ^= x >> 16, all modulo 2^32.  Same inputs, same result.
+ * The square root and the division of the parameter update are approximate
+ * (about 2^-22 relative, of the update only).  Needs grads, master, m8,
+ * m8_scale, v8, v8_scale, and param16 unless ZERO_NO_OUT.  One launch. */
+zero_status_t zero_multi_adamw8(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags, uint32_t seed,
+                                zero_step_state* st, zero_stream_t stream);
+
+/* 32-bit states of every tensor into the 8-bit form, nearest codes (ties to
+ * even), and back (exact).  Decoded states encode to the same values again (a
+ * block may get half the scale and codes of twice the value).  For
+ * checkpoints: a run may be resumed with the other width of states, or
+ * another partition.  Need m, v and the four 8-bit arrays.  One launch. */
+zero_status_t zero_multi_encode8(const zero_multi* M, zero_stream_t stream);
+zero_status_t zero_multi_decode8(const zero_multi* M, zero_stream_t stream);
 
 /* Cap on the CTAs of every later launch by this library (process-wide;
  * 0 = no cap: each kernel's own persistent grid, one full wave of CTAs or,

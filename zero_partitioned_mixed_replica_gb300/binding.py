@@ -34,6 +34,12 @@ ZERO_OUT_FULL_REPLICAS = 0
 ZERO_OUT_SHARDS = 1
 ZERO_NORM_DECIDE = 0
 ZERO_NORM_AFTER_FUSED = 1
+ZERO_FP32 = 2
+ZERO_NO_OUT = -1
+ZERO_MAX_GROUPS = 16
+ZERO_MULTI_DECIDED = 0
+ZERO_MULTI_ADVANCE = 1
+ZERO_MULTI_UNSCALED = 2
 
 EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero_layout_unit",
             "zero_layout_tensor_offset", "zero_layout_destroy", "zero_state_init",
@@ -43,7 +49,9 @@ EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero
             "zero_reduce_scatter_accumulated", "zero_reduce_scatter_micro", "zero_step", "zero_micro_step", "zero_step_from_host",
             "zero_trace_enable", "zero_trace_read", "zero_trace_timeline", "zero_set_max_ctas",
             "zero_last_error", "zero_launch_count", "zero_checked_build", "zero_bounds_violations",
-            "zero_checked_set_slack"]
+            "zero_checked_set_slack", "zero_multi_init", "zero_multi_query", "zero_multi_destroy", "zero_multi_bind",
+            "zero_multi_grad_norm", "zero_multi_adamw", "zero_multi_adamw8", "zero_multi_encode8",
+            "zero_multi_decode8"]
 ZERO_NOALLOC_MAX_ELEMS = 67108864
 
 
@@ -73,7 +81,7 @@ class zero_step_state(ctypes.Structure):
                 [(n, ctypes.c_int32) for n in ("t", "skipped", "good_steps", "growth_interval",
                                                "dynamic_scale", "nonfinite", "overflow", "apply",
                                                "error")] +
-                [("reserved", ctypes.c_int32 * 3)])
+                [("grad_scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 2)])
 
 
 class zero_copy_segment(ctypes.Structure):
@@ -95,6 +103,16 @@ class zero_trace_totals(ctypes.Structure):
 class zero_trace_record(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("device", ctypes.c_int32), ("stream", ctypes.c_uint64),
                 ("start_ms", ctypes.c_double), ("end_ms", ctypes.c_double)]
+
+
+class zero_multi_arrays(ctypes.Structure):
+    _fields_ = [(n, ctypes.POINTER(ctypes.c_void_p)) for n in
+                ("grads", "master", "m", "v", "m8", "m8_scale", "v8", "v8_scale", "param16")]
+
+
+class zero_multi_info(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_tensors", "n_groups", "grad_dtype", "param_dtype")] +
+                [(n, ctypes.c_int64) for n in ("numel", "n_chunks", "state8_bytes", "workspace_bytes")])
 
 
 ZERO_UNIT_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
@@ -200,6 +218,14 @@ def lib():
         "zero_bounds_violations": [ctypes.POINTER(i64), i32],
         "zero_checked_set_slack": [i64],
         "zero_checked_build": [],
+        "zero_multi_init": [ctypes.POINTER(i64), i32, ctypes.POINTER(i32), i32, i32, i32, ctypes.POINTER(P)],
+        "zero_multi_query": [P, ctypes.POINTER(zero_multi_info)],
+        "zero_multi_bind": [P, ctypes.POINTER(zero_multi_arrays), P, P],
+        "zero_multi_grad_norm": [P, dbl, P, P],
+        "zero_multi_adamw": [P, ctypes.POINTER(zero_adamw_hp), i32, P, P],
+        "zero_multi_adamw8": [P, ctypes.POINTER(zero_adamw_hp), i32, ctypes.c_uint32, P, P],
+        "zero_multi_encode8": [P, P],
+        "zero_multi_decode8": [P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -207,6 +233,8 @@ def lib():
         fn.restype = i32
     L.zero_layout_destroy.argtypes = [P]
     L.zero_layout_destroy.restype = None
+    L.zero_multi_destroy.argtypes = [P]
+    L.zero_multi_destroy.restype = None
     L.zero_last_error.argtypes = []
     L.zero_last_error.restype = ctypes.c_char_p
     L.zero_launch_count.argtypes = [i32]
@@ -483,3 +511,94 @@ def zero_checked_set_slack(elems: int) -> None:
     """Test hook of the bounds-checked build: every checked extent is
     ``elems`` short of the real one."""
     _check(lib().zero_checked_set_slack(int(elems)))
+
+
+class Multi:
+    """Owns a ``zero_multi*``; destroyed with the object."""
+
+    def __init__(self, handle: int, n_tensors: int, n_groups: int):
+        self.handle = ctypes.c_void_p(handle)
+        self.n_tensors, self.n_groups = n_tensors, n_groups
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h and _lib is not None:
+            _lib.zero_multi_destroy(h)
+
+    @property
+    def _as_parameter_(self):
+        return self.handle
+
+
+def zero_multi_init(numels: Sequence[int], group_of_tensor: Optional[Sequence[int]] = None, n_groups: int = 1,
+                    grad_dtype: int = ZERO_BF16, param_dtype: int = ZERO_BF16) -> Multi:
+    n = len(numels)
+    if group_of_tensor is not None and len(group_of_tensor) != n:
+        raise ZeroError(ZERO_ERR_INVALID, "expected %d groups (one per tensor), got %d" % (n, len(group_of_tensor)))
+    arr = (ctypes.c_int64 * max(n, 1))(*numels)
+    groups = (ctypes.c_int32 * max(n, 1))(*group_of_tensor) if group_of_tensor is not None else None
+    out = ctypes.c_void_p()
+    _check(lib().zero_multi_init(arr, n, groups, n_groups, grad_dtype, param_dtype, ctypes.byref(out)))
+    return Multi(out.value, n, n_groups)
+
+
+def zero_multi_query(M: Multi) -> zero_multi_info:
+    info = zero_multi_info()
+    _check(lib().zero_multi_query(M, ctypes.byref(info)))
+    return info
+
+
+def zero_multi_destroy(M: Multi) -> None:
+    h, M.handle = M.handle, None
+    if h:
+        lib().zero_multi_destroy(h)
+
+
+def zero_multi_bind(M: Multi, workspace, stream=None, **arrays) -> None:
+    """arrays: any of zero_multi_arrays' fields, one device pointer or tensor
+    per tensor of the list; the others are passed as NULL."""
+    a = zero_multi_arrays()
+    keep = []
+    for name, xs in arrays.items():
+        if name not in dict(zero_multi_arrays._fields_):
+            raise TypeError("zero_multi_bind: no array %r" % name)
+        if xs is None:
+            continue
+        if len(xs) != M.n_tensors:
+            raise ZeroError(ZERO_ERR_INVALID, "%s: expected %d pointers (one per tensor), got %d"
+                            % (name, M.n_tensors, len(xs)))
+        keep.append((ctypes.c_void_p * len(xs))(*[_addr(x) for x in xs]))
+        setattr(a, name, ctypes.cast(keep[-1], ctypes.POINTER(ctypes.c_void_p)))
+    _check(lib().zero_multi_bind(M, ctypes.byref(a), _addr(workspace), _stream(stream)))
+
+
+def _hps(M: Multi, hp):
+    """The groups' hyperparameters: the library reads exactly n_groups entries."""
+    if hp is None:
+        return None
+    if isinstance(hp, zero_adamw_hp):
+        hp = [hp]
+    if len(hp) != M.n_groups:
+        raise ZeroError(ZERO_ERR_INVALID, "expected %d hyperparameter groups, got %d" % (M.n_groups, len(hp)))
+    return hp if isinstance(hp, ctypes.Array) else (zero_adamw_hp * len(hp))(*hp)
+
+
+def zero_multi_grad_norm(M: Multi, max_norm: float, st, stream=None) -> None:
+    _check(lib().zero_multi_grad_norm(M, max_norm, _addr(st), _stream(stream)))
+
+
+def zero_multi_adamw(M: Multi, hp, flags: int, st, stream=None) -> None:
+    """hp: one zero_adamw_hp per group (a list or a ctypes array)."""
+    _check(lib().zero_multi_adamw(M, _hps(M, hp), flags, _addr(st), _stream(stream)))
+
+
+def zero_multi_adamw8(M: Multi, hp, flags: int, seed: int, st, stream=None) -> None:
+    _check(lib().zero_multi_adamw8(M, _hps(M, hp), flags, seed & 0xFFFFFFFF, _addr(st), _stream(stream)))
+
+
+def zero_multi_encode8(M: Multi, stream=None) -> None:
+    _check(lib().zero_multi_encode8(M, _stream(stream)))
+
+
+def zero_multi_decode8(M: Multi, stream=None) -> None:
+    _check(lib().zero_multi_decode8(M, _stream(stream)))

@@ -51,6 +51,17 @@ class AdamW:
     weight_decay: float = 0.01
 
 
+def read_step_state(state: torch.Tensor) -> dict:
+    """The fields of a device step state, after everything queued on the device."""
+    torch.cuda.synchronize(state.device)
+    raw = bytes(state.cpu().numpy().tobytes())
+    st = B.zero_step_state.from_buffer_copy(raw)
+    return {"t": st.t, "skipped": st.skipped, "overflow": st.overflow, "apply": st.apply,
+            "grad_norm": st.grad_norm, "clip_coef": st.clip_coef, "loss_scale": st.loss_scale,
+            "good_steps": st.good_steps, "nonfinite": st.nonfinite, "error": st.error,
+            "beta1_pow": st.beta1_pow, "beta2_pow": st.beta2_pow}
+
+
 class ZeroStep:
     def __init__(self, numels: Sequence[int], n_d: int, stage: int, dtype: int = B.ZERO_BF16,
                  bucket_elems: int = 0, unit_of_tensor: Optional[Sequence[int]] = None,
@@ -477,13 +488,7 @@ class ZeroStep:
 
     # -- readback -------------------------------------------------------------------
     def read_state(self) -> dict:
-        torch.cuda.synchronize(self.device)
-        raw = bytes(self.state.cpu().numpy().tobytes())
-        st = B.zero_step_state.from_buffer_copy(raw)
-        return {"t": st.t, "skipped": st.skipped, "overflow": st.overflow, "apply": st.apply,
-                "grad_norm": st.grad_norm, "clip_coef": st.clip_coef, "loss_scale": st.loss_scale,
-                "good_steps": st.good_steps, "nonfinite": st.nonfinite, "error": st.error,
-                "beta1_pow": st.beta1_pow, "beta2_pow": st.beta2_pow}
+        return read_step_state(self.state)
 
     def flat(self, which: str) -> torch.Tensor:
         """Reassemble master/m/v (fp32) or shard16 (ZeRO-3) into flat order."""
