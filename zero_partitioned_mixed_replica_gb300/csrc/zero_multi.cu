@@ -14,30 +14,33 @@
 
 namespace zk {
 
-constexpr int kChunk = kThreads * kVec;  // elements of one work item
+constexpr int kChunk = 4096;             // elements of one work item
 constexpr int kBlock8 = 32;              // elements under one scale of an 8-bit state
 constexpr int kSlices = 1216;            // fixed split of a list for the norm (8 CTAs on each of 152 SMs)
 constexpr int kRowsPerLaunch = 256;      // table rows passed through one launch's parameters
 
 enum { kVecGrad = 1, kVec32 = 2, kVec8 = 4, kVecOut = 8, kVecMaster = 16 };  // MultiRow::vec
 
-// What the kernels know of one tensor.
+// What the kernels know of one tensor: 12 words of 8 bytes, which a warp reads
+// with 12 lanes.
 struct MultiRow {
     const void* grad;
     float* master;
-    float* m;
-    float* v;
     uint8_t* m8;
-    uint8_t* ms;
     uint8_t* v8;
+    uint8_t* ms;
     uint8_t* vs;
     uint16_t* out;
     int64_t numel;
     uint32_t first_chunk;
+    uint32_t tensor;  // its own index
+    uint32_t vec;     // arrays that begin on a boundary for the widest access
     int32_t group;
-    uint32_t vec;  // arrays that begin on a boundary for the widest access
-    uint32_t pad0;
+    float* m;
+    float* v;
 };
+constexpr int kRowWords = sizeof(MultiRow) / 8;
+static_assert(kRowWords == 12 && kRowWords <= 32, "a warp reads a row");
 
 // The device workspace: counters, rows, chunk map, norm partials.
 struct MultiTable {
@@ -98,16 +101,27 @@ struct GradBf16 {
     using T = uint16_t;
     static __device__ __forceinline__ float one(uint16_t h) { return Bf16::dec1(h); }
     static __device__ __forceinline__ void eight(const uint16_t* p, float (&o)[8]) { unpack8<Bf16>(ld_stream(p), o); }
+    static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
+        unpack8<Bf16>(*reinterpret_cast<const uint4*>(p), o);
+    }
 };
 struct GradFp16 {
     using T = uint16_t;
     static __device__ __forceinline__ float one(uint16_t h) { return Fp16::dec1(h); }
     static __device__ __forceinline__ void eight(const uint16_t* p, float (&o)[8]) { unpack8<Fp16>(ld_stream(p), o); }
+    static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
+        unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o);
+    }
 };
 struct GradFp32 {
     using T = float;
     static __device__ __forceinline__ float one(float x) { return x; }
     static __device__ __forceinline__ void eight(const float* p, float (&o)[8]) { ld8(p, o); }
+    static __device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+        o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+    }
 };
 struct NoOut {
     static constexpr bool kOut = false;
@@ -280,10 +294,16 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // ----------------------------------------------------------------------------
 // The step's constants of every group
 // ----------------------------------------------------------------------------
+struct __align__(16) Const8 {
+    float b1, omb1, b2, omb2;
+    float decay, step_size, eps, isb;  // isb: 1 / sqrt(1 - beta2^t)
+};
 struct MultiShared {
     AdamConsts k[ZERO_MAX_GROUPS];
-    float isb[ZERO_MAX_GROUPS];  // 1 / sqrt(1 - beta2^t)
+    Const8 c8[ZERO_MAX_GROUPS];  // of the 8-bit update
     float unscale;               // 1 / loss scale the gradients carry
+    float factor;                // 8-bit update: the last factor of the gradients, and
+    int32_t two;                 // whether unscale is another one before it
     uint32_t key;                // of the step's random numbers
     int32_t apply;
 };
@@ -297,12 +317,17 @@ __device__ __forceinline__ void multi_constants(const MultiArgs& a, MultiShared&
         const double b2p = advance ? __dmul_rn(st->beta2_pow, st->beta2) : st->beta2_pow;
         s.k[g] = make_consts(st->beta1, st->beta2, b1p, b2p, a.hp.lr[g], a.hp.eps[g], a.hp.wd[g],
                              advance ? 1.0f : st->clip_coef);
-        s.isb[g] = __double2float_rn(__ddiv_rn(1.0, __dsqrt_rn(__dsub_rn(1.0, b2p))));
+        const AdamConsts& k = s.k[g];
+        s.c8[g] = Const8{k.b1, k.omb1, k.b2, k.omb2, k.decay, k.step_size, fmaxf(k.eps, 1.17549435e-38f),
+                         __double2float_rn(__ddiv_rn(1.0, __dsqrt_rn(__dsub_rn(1.0, b2p))))};
     }
     if (g == 0) {
         s.apply = advance ? 1 : st->apply;
         const float scale = !advance && st->grad_scale > 0.0f ? st->grad_scale : st->loss_scale;
         s.unscale = (a.flags & ZERO_MULTI_UNSCALED) ? 1.0f : __fdiv_rn(1.0f, scale);
+        const float clip = advance ? 1.0f : st->clip_coef;
+        s.two = clip != 1.0f && s.unscale != 1.0f;  // a factor of 1 changes nothing
+        s.factor = clip != 1.0f ? clip : s.unscale;
         s.key = mix32(a.seed ^ mix32((uint32_t)(st->t + (advance ? 1 : 0))));
     }
     __syncthreads();
@@ -324,9 +349,10 @@ __device__ __forceinline__ void multi_advance(const MultiArgs& a) {
     st->good_steps += 1;
 }
 
-// This thread's 8 elements of chunk c.
-__device__ __forceinline__ int multi_place(const MultiTable& t, uint32_t c, const MultiRow& r, int64_t& i) {
-    i = (int64_t)(c - r.first_chunk) * kChunk + threadIdx.x * kVec;
+// This thread's 8 elements of part h of chunk c.
+constexpr int kParts = kChunk / (kThreads * kVec);
+__device__ __forceinline__ int multi_place(const MultiTable& t, uint32_t c, const MultiRow& r, int h, int64_t& i) {
+    i = (int64_t)(c - r.first_chunk) * kChunk + (h * kThreads + threadIdx.x) * kVec;
     const int64_t left = r.numel - i;
     int nv = left >= kVec ? kVec : (left > 0 ? (int)left : 0);
     const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
@@ -345,8 +371,9 @@ __global__ void __launch_bounds__(kThreads, 4) multi_adamw_kernel(const __grid_c
         const float unscale = s.unscale;
         for (uint32_t c = blockIdx.x; c < a.t.n_chunks; c += gridDim.x) {
             const MultiRow& r = a.t.rows[a.t.tensor[c]];
+            for (int h = 0; h < kParts; ++h) {
             int64_t i;
-            const int nv = multi_place(a.t, c, r, i);
+            const int nv = multi_place(a.t, c, r, h, i);
             if (nv == 0) continue;
             const uint32_t vec = r.vec;
             const AdamConsts k = s.k[r.group];
@@ -368,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 4) multi_adamw_kernel(const __grid_c
             store_f32(r.m + i, nv, vec & kVec32, m);
             store_f32(r.v + i, nv, vec & kVec32, v);
             if constexpr (O::kOut) store_out<O>(r.out + i, nv, vec & kVecOut, p);
+            }
         }
     }
     multi_advance(a);
@@ -376,67 +404,329 @@ __global__ void __launch_bounds__(kThreads, 4) multi_adamw_kernel(const __grid_c
 // ----------------------------------------------------------------------------
 // AdamW, 8-bit states
 // ----------------------------------------------------------------------------
+// A CTA has kWarps8 warps that compute and one that fetches.  Its tiles are the
+// list's chunks; a ring of kStages8 tiles arrives in shared memory by bulk
+// copies that the fetching warp issues, so that the inputs of the next tiles
+// are on their way while one is computed.  A computing warp takes 512 elements
+// of a tile, 16 consecutive ones per lane (a block of 32 is two lanes).  What
+// is not 512 whole elements at a tensor's end, or not aligned, is read by plain
+// loads instead.
+constexpr int kLane8 = 16;
+constexpr int kItem8 = 32 * kLane8;
+constexpr int kWarps8 = kChunk / kItem8;
+constexpr int kThreads8 = 32 * (kWarps8 + 1);
+static_assert(kChunk / kBlock8 <= 128, "a fetching lane copies 4 scale bytes of a tile");
+
+template <class G>
+struct __align__(128) Stage8 {
+    float p[kChunk];
+    typename G::T g[kChunk];
+    uint8_t m[kChunk];
+    uint8_t v[kChunk];
+    uint8_t ms[kChunk / kBlock8];
+    uint8_t vs[kChunk / kBlock8];
+    MultiRow row;
+    int64_t begin;  // the tile's first element in its tensor
+    int64_t whole;  // elements from there on that were copied
+};
+template <class G>
+struct Smem8 {
+    static constexpr int kStages8 = sizeof(typename G::T) == 4 ? 2 : 3;  // two CTAs on an SM
+    Stage8<G> stage[kStages8];
+    uint64_t full[kStages8], empty[kStages8];
+};
+
+// 4 bytes into shared memory, counted by an mbarrier.
+__device__ __forceinline__ void copy4_async(void* dst_smem, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {  // arrives when the thread's copies so far have landed
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 16 codes <-> values.
+template <class Q>
+__device__ __forceinline__ void decode16(uint4 c, float scale, float (&o)[16]) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float2 f = Q::dec2((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+        o[2 * k] = __fmul_rn(f.x, scale);
+        o[2 * k + 1] = __fmul_rn(f.y, scale);
+    }
+}
+// Largest magnitude, NaN if one is NaN: three-input maxima.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float top16(const float (&x)[16]) {
+    const float a = max3_abs(x[0], x[1], x[2]), b = max3_abs(x[3], x[4], x[5]), c = max3_abs(x[6], x[7], x[8]);
+    const float d = max3_abs(x[9], x[10], x[11]), e = max3_abs(x[12], x[13], x[14]);
+    return max3_abs(max3_abs(a, b, c), max3_abs(d, e, x[15]), 0.0f);
+}
+template <class Q>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    if (top >= 0x7F800000u) return 255u;
+    // one more when the mantissa is above 1.75; in binary32's last binade there
+    // is no more, and what is above 1.75 * 2^127 saturates
+    const int e = (int)min((top + 0x1FFFFFu) >> 23, 254u);
+    return (uint32_t)max(1, e - Q::kTop);
+}
+template <class Q>
+__device__ __forceinline__ uint32_t block_scale16(const float (&x)[16]) {
+    float t = top16(x);
+    t = max3_abs(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1), 0.0f);
+    return scale_byte<Q>(__float_as_uint(t));
+}
+// One stochastically rounded value before its conversion to a code: x on the
+// block's scale, a random integer added below the bits that are kept.
+template <class Q>
+__device__ __forceinline__ float dither(float x, float inv, uint32_t rnd) {
+    const float z = __fmul_rn(x, inv);
+    float y = __uint_as_float((__float_as_uint(z) + (rnd >> (32 - Q::kCut))) & ~((1u << Q::kCut) - 1u));
+    if constexpr (Q::kFloor)
+        if (z > 0.0f) y = fmaxf(y, kSmallestE5m2);
+    return y;
+}
+// Codes of a lane's 16 m and v, whose random integers alternate.
+__device__ __forceinline__ void encode16(const float (&m)[16], const float (&v)[16], uint32_t bm, uint32_t bv, uint32_t key,
+                                         uint32_t group, uint4& cm, uint4& cv) {
+    const float im = __uint_as_float((254u - bm) << 23), iv = __uint_as_float((254u - bv) << 23);
+    uint32_t wm[4], wv[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t x = mix32(key + 0x9E3779B1u * (group + h));
+#pragma unroll
+        for (int k = 2 * h; k < 2 * h + 2; ++k) {
+            uint32_t qm[2], qv[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float ym[2], yv[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int e = 4 * k + 2 * j + i;
+                    x = x * 1664525u + 1013904223u;
+                    ym[i] = dither<E4m3>(m[e], im, x);
+                    x = x * 1664525u + 1013904223u;
+                    yv[i] = dither<E5m2>(v[e], iv, x);
+                }
+                qm[j] = E4m3::enc2(ym[0], ym[1]);
+                qv[j] = E5m2::enc2(yv[0], yv[1]);
+            }
+            wm[k] = qm[0] | (qm[1] << 16);
+            wv[k] = qv[0] | (qv[1] << 16);
+        }
+    }
+    // NaN in both types
+    if (bm == 255u) wm[0] = wm[1] = wm[2] = wm[3] = 0x7F7F7F7Fu;
+    if (bv == 255u) wv[0] = wv[1] = wv[2] = wv[3] = 0x7F7F7F7Fu;
+    cm = make_uint4(wm[0], wm[1], wm[2], wm[3]);
+    cv = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+}
+
+// Plain access to the up to 16 elements of a lane (nv of them).
+__device__ __forceinline__ uint4 load_codes16(const uint8_t* p, int nv) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < nv) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_codes16(uint8_t* p, int nv, uint4 c) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (e < nv) p[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+}
+
+// The parameter update needs neither the rounded square root nor the rounded
+// division: their errors (2^-22 of the update) stay out of the states.  v below
+// 2^-126 counts as zero in the root; the constants keep eps at 2^-126 at least.
 __device__ __forceinline__ float sqrt_approx(float x) {
     float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
 template <class G, class O>
-__global__ void __launch_bounds__(kThreads, 4) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
+__global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    Smem8<G>& sh = *reinterpret_cast<Smem8<G>*>(smem);
     __shared__ MultiShared s;
-    multi_constants(a, s);
-    if (s.apply) {
-        const float unscale = s.unscale;
-        for (uint32_t c = blockIdx.x; c < a.t.n_chunks; c += gridDim.x) {
-            const uint32_t n = a.t.tensor[c];
-            const MultiRow& r = a.t.rows[n];
-            int64_t i;
-            const int nv = multi_place(a.t, c, r, i);
-            if (!__any_sync(0xFFFFFFFFu, nv > 0)) continue;
-            const uint32_t vec = r.vec;
-            const AdamConsts k = s.k[r.group];
-            const float isb = s.isb[r.group];
-            float g[8], p[8], m[8], v[8];
-            load_grad<G>(r.grad, i, nv, vec & kVecGrad, g);
-            load_f32(r.master + i, nv, vec & kVecMaster, p);
-            const int64_t blk = i / kBlock8;
-            float sm = 0.0f, sv = 0.0f;
-            if (nv > 0) {
-                sm = scale_of(r.ms[blk]);
-                sv = scale_of(r.vs[blk]);
+    constexpr int kStages8 = Smem8<G>::kStages8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t first = blockIdx.x, step = gridDim.x;
+    const uint32_t count = first < a.t.n_chunks ? (a.t.n_chunks - first + step - 1) / step : 0u;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kStages8; ++k) {
+            mbar_init(&sh.full[k], 33);  // the fetching warp's lanes' copies, and the bulk copies' bytes
+            mbar_init(&sh.empty[k], kWarps8);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (warp == kWarps8) {
+        // Of the CTA's k-th tile: its tensor's index, and this lane's word of
+        // that tensor's row; both a tile ahead of their use.
+        auto tensor_of = [&](uint32_t k) { return k < count ? a.t.tensor[first + k * step] : 0u; };
+        auto word_of = [&](uint32_t n) {
+            return lane < kRowWords ? __ldg(reinterpret_cast<const unsigned long long*>(a.t.rows + n) + lane) : 0ull;
+        };
+        auto issue = [&](uint32_t k, unsigned long long word) {
+            Stage8<G>& x = sh.stage[k % kStages8];
+            uint64_t* bar = &sh.full[k % kStages8];
+            if (lane < kRowWords) reinterpret_cast<unsigned long long*>(&x.row)[lane] = word;
+            __syncwarp();
+            const MultiRow& r = x.row;
+            const int64_t w0 = (int64_t)(first + k * step - r.first_chunk) * kChunk;
+            constexpr uint32_t kAll = kVecGrad | kVecMaster | kVec8 | kVecOut;
+            int64_t left = r.numel - w0;
+            if (kChecked) left -= (int64_t)a.t.slack;
+            const int n = (r.vec & kAll) != kAll || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
+            if (lane * 4 < n / kBlock8) {
+                copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4);
+                copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4);
             }
-            decode8<E4m3>(load_codes(r.m8 + i, nv, vec & kVec8), sm, m);
-            decode8<E5m2>(load_codes(r.v8 + i, nv, vec & kVec8), sv, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float gc = __fmul_rn(__fmul_rn(g[e], unscale), k.clip);
-                m[e] = __fadd_rn(__fmul_rn(k.b1, m[e]), __fmul_rn(k.omb1, gc));
-                v[e] = __fadd_rn(__fmul_rn(k.b2, v[e]), __fmul_rn(k.omb2, __fmul_rn(gc, gc)));
-                const float den = __fmaf_rn(sqrt_approx(v[e]), isb, k.eps);
-                p[e] = __fsub_rn(__fmul_rn(p[e], k.decay), __fmul_rn(k.step_size, __fdividef(m[e], den)));
-            }
-            store_f32(r.master + i, nv, vec & kVecMaster, p);
-            if constexpr (O::kOut) store_out<O>(r.out + i, nv, vec & kVecOut, p);
-            uint32_t x = mix32(mix32(s.key + n) + 0x9E3779B1u * (uint32_t)(i >> 3));
-            uint32_t rm[8], rv[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x = x * 1664525u + 1013904223u;
-                rm[e] = x >> 12;
-                x = x * 1664525u + 1013904223u;
-                rv[e] = x >> 11;
-            }
-            const uint32_t bm = block_scale<E4m3>(m), bv = block_scale<E5m2>(v);
-            if (nv > 0) {
-                store_codes(r.m8 + i, nv, vec & kVec8, encode8<E4m3, true>(m, bm, rm));
-                store_codes(r.v8 + i, nv, vec & kVec8, encode8<E5m2, true>(v, bv, rv));
-                if ((threadIdx.x & 3) == 0) {
-                    r.ms[blk] = (uint8_t)bm;
-                    r.vs[blk] = (uint8_t)bv;
+            copies_arrive(bar);
+            if (lane == 0) {
+                x.begin = w0;
+                x.whole = n;
+                mbar_arrive_expect_tx(bar, (uint32_t)n * (sizeof(float) + sizeof(typename G::T) + 2));
+                if (n > 0) {
+                    bulk_g2s(x.p, r.master + w0, n * sizeof(float), bar);
+                    bulk_g2s(x.g, static_cast<const typename G::T*>(r.grad) + w0, n * sizeof(typename G::T), bar);
+                    bulk_g2s(x.m, r.m8 + w0, n, bar);
+                    bulk_g2s(x.v, r.v8 + w0, n, bar);
                 }
             }
+        };
+        uint32_t n[kStages8];
+        unsigned long long w[kStages8];
+#pragma unroll
+        for (int k = 0; k < kStages8; ++k) n[k] = tensor_of(k);
+#pragma unroll
+        for (int k = 0; k < kStages8; ++k) w[k] = word_of(n[k]);
+        uint32_t k = 0;  // tiles issued
+#pragma unroll
+        for (int j = 0; j < kStages8; ++j)
+            if (j < count) issue(k++, w[j]);
+        unsigned long long next_word = word_of(tensor_of(kStages8));
+        uint32_t next_tensor = tensor_of(kStages8 + 1);
+        multi_constants(a, s);
+        const uint32_t todo = s.apply ? count : 0u;
+        for (; k < todo; ++k) {
+            // every warp is done with the tile that the stage holds
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.empty[k % kStages8], (k / kStages8 - 1) & 1u))) {
+                if (lane == 0) atomicOr(&a.st->error, ZERO_DEVERR_WAIT_TIMEOUT);
+                break;
+            }
+            issue(k, next_word);
+            next_word = word_of(next_tensor);
+            next_tensor = tensor_of(k + 2);
         }
+        // the last copies land before the CTA gives up its shared memory (they
+        // have, unless the step is skipped or a wait ran out)
+        for (uint32_t j = k > kStages8 ? k - kStages8 : 0u; j < k; ++j) {
+            bool landed = false;
+            for (int tries = 0; tries < kDrainTries && !landed; ++tries)
+                landed = mbar_wait_bounded(&sh.full[j % kStages8], (j / kStages8) & 1u);
+            if (!landed) atomicOr(&a.st->error, ZERO_DEVERR_DRAIN_TIMEOUT);
+        }
+        return;
+    }
+    multi_constants(a, s);
+    const uint32_t todo = s.apply ? count : 0u;
+    const float factor = s.factor, unscale = s.unscale;
+    const bool two = s.two != 0;
+    for (uint32_t k = 0; k < todo; ++k) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.full[k % kStages8], (k / kStages8) & 1u))) {
+            if (lane == 0) atomicOr(&a.st->error, ZERO_DEVERR_WAIT_TIMEOUT);
+            break;
+        }
+        Stage8<G>& x = sh.stage[k % kStages8];
+        const MultiRow& r = x.row;
+        const int at = (warp * 32 + lane) * kLane8;  // place in the tile
+        const bool fast = (warp + 1) * kItem8 <= x.whole;
+        const int64_t i = x.begin + at;
+        int nv = kLane8;
+        if (!fast) {
+            const int64_t left = r.numel - i;
+            nv = left >= kLane8 ? kLane8 : (left > 0 ? (int)left : 0);
+            const uint64_t lim = (uint64_t)r.numel > a.t.slack ? (uint64_t)r.numel - a.t.slack : 0;
+            if (nv > 0 && !in_bounds((uint64_t)i + nv, lim)) nv = 0;
+        }
+        if (__any_sync(0xFFFFFFFFu, nv > 0)) {
+            const int64_t blk = i / kBlock8;
+            const Const8 c = s.c8[r.group];
+            float m[16], v[16];
+            if (fast) {
+                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
+                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
+            } else {
+                float sm = 0.0f, sv = 0.0f;
+                if (nv > 0) {
+                    sm = scale_of(r.ms[blk]);
+                    sv = scale_of(r.vs[blk]);
+                }
+                decode16<E4m3>(load_codes16(r.m8 + i, nv), sm, m);
+                decode16<E5m2>(load_codes16(r.v8 + i, nv), sv, v);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int o = 8 * h;
+                float g[8], p[8];
+                if (fast) {
+                    G::load8(&x.g[at + o], g);
+                    const float4 p0 = *reinterpret_cast<const float4*>(&x.p[at + o]);
+                    const float4 p1 = *reinterpret_cast<const float4*>(&x.p[at + o + 4]);
+                    p[0] = p0.x, p[1] = p0.y, p[2] = p0.z, p[3] = p0.w;
+                    p[4] = p1.x, p[5] = p1.y, p[6] = p1.z, p[7] = p1.w;
+                } else {
+                    load_grad<G>(r.grad, i + o, nv - o, false, g);
+                    load_f32(r.master + i + o, nv - o, false, p);
+                }
+                if (two) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float gc = __fmul_rn(g[e], factor);
+                    m[o + e] = __fadd_rn(__fmul_rn(c.b1, m[o + e]), __fmul_rn(c.omb1, gc));
+                    v[o + e] = __fadd_rn(__fmul_rn(c.b2, v[o + e]), __fmul_rn(c.omb2, __fmul_rn(gc, gc)));
+                    const float den = __fmaf_rn(sqrt_approx(v[o + e]), c.isb, c.eps);
+                    p[e] = __fmaf_rn(-c.step_size, __fmul_rn(m[o + e], rcp_approx(den)), __fmul_rn(p[e], c.decay));
+                }
+                store_f32(r.master + i + o, fast ? 8 : nv - o, fast, p);
+                if constexpr (O::kOut) store_out<O>(r.out + i + o, fast ? 8 : nv - o, fast, p);
+            }
+            const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
+            uint4 cm, cv;
+            encode16(m, v, bm, bv, mix32(s.key + r.tensor), (uint32_t)(i >> 3), cm, cv);
+            if (fast) {
+                __stcs(reinterpret_cast<uint4*>(r.m8 + i), cm);
+                __stcs(reinterpret_cast<uint4*>(r.v8 + i), cv);
+            } else {
+                store_codes16(r.m8 + i, nv, cm);
+                store_codes16(r.v8 + i, nv, cv);
+            }
+            if ((lane & 1) == 0 && nv > 0) {
+                r.ms[blk] = (uint8_t)bm;
+                r.vs[blk] = (uint8_t)bv;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[k % kStages8]);
     }
     multi_advance(a);
 }
@@ -448,8 +738,9 @@ template <bool ENCODE>
 __global__ void __launch_bounds__(kThreads) multi_codec_kernel(const __grid_constant__ MultiTable t) {
     for (uint32_t c = blockIdx.x; c < t.n_chunks; c += gridDim.x) {
         const MultiRow& r = t.rows[t.tensor[c]];
+        for (int h = 0; h < kParts; ++h) {
         int64_t i;
-        const int nv = multi_place(t, c, r, i);
+        const int nv = multi_place(t, c, r, h, i);
         if (!__any_sync(0xFFFFFFFFu, nv > 0)) continue;
         const uint32_t vec = r.vec;
         const int64_t blk = i / kBlock8;
@@ -472,6 +763,7 @@ __global__ void __launch_bounds__(kThreads) multi_codec_kernel(const __grid_cons
             decode8<E5m2>(load_codes(r.v8 + i, nv, vec & kVec8), scale_of(r.vs[blk]), v);
             store_f32(r.m + i, nv, vec & kVec32, m);
             store_f32(r.v + i, nv, vec & kVec32, v);
+        }
         }
     }
 }
@@ -498,7 +790,7 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
             const int64_t end = min(r.numel, begin + (int64_t)take * kChunk);
             const bool vec = r.vec & kVecGrad;
             const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
-            for (int64_t i = begin + threadIdx.x * kVec; i < end; i += kChunk) {
+            for (int64_t i = begin + threadIdx.x * kVec; i < end; i += kThreads * kVec) {
                 const int nv = end - i >= kVec ? kVec : (int)(end - i);
                 if (!in_bounds((uint64_t)i + nv, lim)) continue;
                 float g[8];
@@ -623,12 +915,33 @@ zero_status_t missing(const char* what, const char* arrays) {
     return fail(ZERO_ERR_STATE, std::string(what) + ": the list is not bound with " + arrays);
 }
 
+// Dynamic shared memory beyond 48 KB is a kernel attribute of each device.
+template <class Kernel>
+zero_status_t allow_smem(Kernel kern, size_t bytes, const char* what) {
+    static std::mutex mu;
+    static std::unordered_map<const void*, uint64_t> done;  // a bit per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    std::lock_guard<std::mutex> lock(mu);
+    uint64_t& mask = done[reinterpret_cast<const void*>(kern)];
+    if (!(mask & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+            return after_launch(what);
+        mask |= bit;
+    }
+    return ZERO_OK;
+}
+
 template <class G, class O>
 zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
     const int64_t work = a.t.n_chunks;
     if (eight) {
         auto kern = zk::multi_adamw8_kernel<G, O>;
-        kern<<<persistent_grid(kern, work), zk::kThreads, 0, s>>>(a);
+        constexpr size_t smem = sizeof(zk::Smem8<G>);
+        const zero_status_t rc = allow_smem(kern, smem, "zero_multi_adamw8");
+        if (rc != ZERO_OK) return rc;
+        kern<<<persistent_grid(kern, work, smem, zk::kThreads8), zk::kThreads8, smem, s>>>(a);
         return after_launch("zero_multi_adamw8");
     }
     auto kern = zk::multi_adamw_kernel<G, O>;
@@ -774,6 +1087,7 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         r = zk::MultiRow{};
         r.numel = M->numels[i];
         r.group = M->groups[i];
+        r.tensor = (uint32_t)i;
         r.first_chunk = chunk;
         chunk += (uint32_t)((r.numel + zk::kChunk - 1) / zk::kChunk);
         // address of tensor i in one array; `wide`: every array so far begins on a boundary for the wide access
@@ -786,16 +1100,16 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
             if (p % vector) wide = false;
             return arr[i];
         };
-        bool wg = true, wp = true, w32 = true, w8 = true, wo = true, any = true;
+        bool wg = true, wp = true, w32 = true, w8 = true, wo = true;
         r.grad = take(x->grads, gs, gs * 8, "grads", wg);
         r.master = (float*)take((const void* const*)x->master, 4, 32, "master", wp);
         r.m = (float*)take((const void* const*)x->m, 4, 32, "m", w32);
         r.v = (float*)take((const void* const*)x->v, 4, 32, "v", w32);
-        r.m8 = (uint8_t*)take((const void* const*)x->m8, 1, 8, "m8", w8);
-        r.v8 = (uint8_t*)take((const void* const*)x->v8, 1, 8, "v8", w8);
-        r.ms = (uint8_t*)take((const void* const*)x->m8_scale, 1, 1, "m8_scale", any);
-        r.vs = (uint8_t*)take((const void* const*)x->v8_scale, 1, 1, "v8_scale", any);
-        r.out = (uint16_t*)take((const void* const*)x->param16, 2, 16, "param16", wo);
+        r.m8 = (uint8_t*)take((const void* const*)x->m8, 1, 16, "m8", w8);
+        r.v8 = (uint8_t*)take((const void* const*)x->v8, 1, 16, "v8", w8);
+        r.ms = (uint8_t*)take((const void* const*)x->m8_scale, 1, 4, "m8_scale", w8);
+        r.vs = (uint8_t*)take((const void* const*)x->v8_scale, 1, 4, "v8_scale", w8);
+        r.out = (uint16_t*)take((const void* const*)x->param16, 2, 32, "param16", wo);
         if (rc != ZERO_OK) return rc;
         r.vec = (wg ? zk::kVecGrad : 0) | (wp ? zk::kVecMaster : 0) | (w32 ? zk::kVec32 : 0) | (w8 ? zk::kVec8 : 0) |
                 (wo ? zk::kVecOut : 0);
