@@ -612,9 +612,11 @@ zero_status_t zero_fused_step_noalloc(const zero_layout* L, const zero_adamw_hp*
  *   - The arrays of a tensor need the natural alignment of their elements
  *     only (a tensor may begin anywhere in a flat buffer), else
  *     ZERO_ERR_ALIGN; arrays of tensors with 0 elements may be NULL.  The
- *     workspace and the state are 256-byte aligned as everywhere.  Tensors
- *     whose arrays all begin on 32-byte boundaries (8-bit codes: 8) take the
- *     fast path.
+ *     workspace and the state are 256-byte aligned as everywhere.  With
+ *     32-bit states a tensor is fast wherever it begins, as long as its
+ *     arrays are equally many elements away from a 32-byte boundary (16-bit
+ *     ones: 16), as in flat buffers of one layout; with 8-bit states if they
+ *     begin on such boundaries (codes 16, scales 4 bytes).
  *   - Arrays of one call must not overlap, except that arrays that are only
  *     read may.
  *   - The object holds the addresses of the last bind; its workspace must
@@ -654,7 +656,7 @@ typedef struct zero_multi_arrays {
 typedef struct zero_multi_info {
     int32_t n_tensors, n_groups, grad_dtype, param_dtype;
     int64_t numel;               /* elements of all tensors                    */
-    int64_t n_chunks;            /* work items of the update kernels           */
+    int64_t n_chunks;            /* work items of the kernels, at most         */
     int64_t state8_bytes;        /* codes and scales of both 8-bit states      */
     int64_t workspace_bytes;     /* device workspace of zero_multi_bind        */
 } zero_multi_info;

@@ -19,7 +19,11 @@ constexpr int kBlock8 = 32;              // elements under one scale of an 8-bit
 constexpr int kSlices = 1216;            // fixed split of a list for the norm (8 CTAs on each of 152 SMs)
 constexpr int kRowsPerLaunch = 256;      // table rows passed through one launch's parameters
 
-enum { kVecGrad = 1, kVec32 = 2, kVec8 = 4, kVecOut = 8, kVecMaster = 16 };  // MultiRow::vec
+// MultiRow::vec: which arrays begin on a boundary for the widest access.  The
+// first four after `shift` elements were put in front of the tensor; the others
+// at the tensor's own first element: all that the 8-bit update copies (kWhole8),
+// m and v for the codec, the codes.
+enum { kVecGrad = 1, kVecMaster = 2, kVecStates = 4, kVecOut = 8, kWhole8 = 16, kCodec = 32, kCodes = 64 };
 
 // What the kernels know of one tensor: 12 words of 8 bytes, which a warp reads
 // with 12 lanes.
@@ -34,7 +38,8 @@ struct MultiRow {
     int64_t numel;
     uint32_t first_chunk;
     uint32_t tensor;  // its own index
-    uint32_t vec;     // arrays that begin on a boundary for the widest access
+    uint16_t vec;
+    uint16_t shift;   // elements by which the 32-bit kernels' work items begin before the tensor
     int32_t group;
     float* m;
     float* v;
@@ -66,6 +71,12 @@ struct MultiArgs {
     uint32_t seed;
 };
 
+// The norm and the updates are launched so that they may begin while the
+// kernel before them in the stream ends; what that kernel wrote is read after
+// grid_wait() only.  grid_launch_next() lets the next kernel begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------
 // Binding
 // ----------------------------------------------------------------------------
@@ -94,13 +105,14 @@ __global__ void multi_map_kernel(const MultiRow* rows, uint32_t n_tensors, uint3
 }
 
 // ----------------------------------------------------------------------------
-// Loads and stores of up to 8 consecutive elements: nv of them exist; `vec`:
-// the array begins on a boundary for the wide access.
+// Loads and stores of 8 consecutive elements of which [e0, e1) exist; `vec`:
+// the first is on a boundary for the wide access.
 // ----------------------------------------------------------------------------
 struct GradBf16 {
     using T = uint16_t;
     static __device__ __forceinline__ float one(uint16_t h) { return Bf16::dec1(h); }
     static __device__ __forceinline__ void eight(const uint16_t* p, float (&o)[8]) { unpack8<Bf16>(ld_stream(p), o); }
+    static __device__ __forceinline__ void eight_kept(const uint16_t* p, float (&o)[8]) { unpack8<Bf16>(*reinterpret_cast<const uint4*>(p), o); }
     static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
         unpack8<Bf16>(*reinterpret_cast<const uint4*>(p), o);
     }
@@ -109,6 +121,7 @@ struct GradFp16 {
     using T = uint16_t;
     static __device__ __forceinline__ float one(uint16_t h) { return Fp16::dec1(h); }
     static __device__ __forceinline__ void eight(const uint16_t* p, float (&o)[8]) { unpack8<Fp16>(ld_stream(p), o); }
+    static __device__ __forceinline__ void eight_kept(const uint16_t* p, float (&o)[8]) { unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o); }
     static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
         unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o);
     }
@@ -117,6 +130,11 @@ struct GradFp32 {
     using T = float;
     static __device__ __forceinline__ float one(float x) { return x; }
     static __device__ __forceinline__ void eight(const float* p, float (&o)[8]) { ld8(p, o); }
+    static __device__ __forceinline__ void eight_kept(const float* p, float (&o)[8]) {
+        asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                     : "l"(p));
+    }
     static __device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
         const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
         o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
@@ -135,61 +153,51 @@ struct OutFp16 : Fp16 {
     static constexpr bool kOut = true;
 };
 
+// Which of the 8 elements from i on a tensor has; false: none.
+__device__ __forceinline__ bool span8(const MultiTable& t, const MultiRow& r, int64_t i, int& e0, int& e1) {
+    if (i >= r.numel || i <= -kVec) return false;
+    e0 = i < 0 ? (int)-i : 0;
+    e1 = r.numel - i < kVec ? (int)(r.numel - i) : kVec;
+    const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
+    return in_bounds((uint64_t)(i + e1), lim);
+}
 template <class G>
-__device__ __forceinline__ void load_grad(const void* base, int64_t i, int nv, bool vec, float (&o)[8]) {
+__device__ __forceinline__ void load_grad(const void* base, int64_t i, int e0, int e1, bool vec, float (&o)[8]) {
     const typename G::T* p = static_cast<const typename G::T*>(base) + i;
-    if (vec && nv == 8) {
+    if (vec && e0 <= 0 && e1 >= 8) {
         G::eight(p, o);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = e < nv ? G::one(p[e]) : 0.0f;
+        for (int e = 0; e < 8; ++e) o[e] = e >= e0 && e < e1 ? G::one(p[e]) : 0.0f;
     }
 }
-__device__ __forceinline__ void load_f32(const float* p, int nv, bool vec, float (&o)[8]) {
-    if (vec && nv == 8) {
+__device__ __forceinline__ void load_f32(const float* p, int e0, int e1, bool vec, float (&o)[8]) {
+    if (vec && e0 <= 0 && e1 >= 8) {
         ld8(p, o);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = e < nv ? p[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) o[e] = e >= e0 && e < e1 ? p[e] : 0.0f;
     }
 }
-__device__ __forceinline__ void store_f32(float* p, int nv, bool vec, const float (&o)[8]) {
-    if (vec && nv == 8) {
+__device__ __forceinline__ void store_f32(float* p, int e0, int e1, bool vec, const float (&o)[8]) {
+    if (vec && e0 <= 0 && e1 >= 8) {
         st8(p, o);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < nv) p[e] = o[e];
+            if (e >= e0 && e < e1) p[e] = o[e];
     }
 }
 template <class O>
-__device__ __forceinline__ void store_out(uint16_t* p, int nv, bool vec, const float (&o)[8]) {
+__device__ __forceinline__ void store_out(uint16_t* p, int e0, int e1, bool vec, const float (&o)[8]) {
     if constexpr (O::kOut) {
-        if (vec && nv == 8) {
+        if (vec && e0 <= 0 && e1 >= 8) {
             st_stream(p, pack8<O>(o));
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < nv) p[e] = O::enc1(o[e]);
+                if (e >= e0 && e < e1) p[e] = O::enc1(o[e]);
         }
-    }
-}
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int nv, bool vec) {
-    if (vec && nv == 8) return __ldcs(reinterpret_cast<const uint2*>(p));
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < nv) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
-    return make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void store_codes(uint8_t* p, int nv, bool vec, uint2 c) {
-    if (vec && nv == 8) {
-        __stcs(reinterpret_cast<uint2*>(p), c);
-    } else {
-        const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < nv) p[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
     }
 }
 
@@ -234,54 +242,6 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
     return __uint_as_float(byte ? byte << 23 : 1u << 22);
 }
 
-template <class Q>
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&o)[8]) {
-    const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = Q::dec2((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
-        o[2 * k] = __fmul_rn(f.x, scale);
-        o[2 * k + 1] = __fmul_rn(f.y, scale);
-    }
-}
-
-// Scale byte of the block that this lane's 8 values belong to (its 4 lanes get
-// the same); values behind the tensor's end are zero.  All lanes call it.
-template <class Q>
-__device__ __forceinline__ uint32_t block_scale(const float (&x)[8]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    if (top >= 0x7F800000u) return 255u;
-    // one more when the mantissa is above 1.75; in binary32's last binade there
-    // is no more, and what is above 1.75 * 2^127 saturates
-    const int e = (int)min((top + 0x1FFFFFu) >> 23, 254u);
-    return (uint32_t)max(1, e - Q::kTop);
-}
-
-// Codes of 8 values; rnd: random integers below 2^kCut (stochastic), or null
-// (nearest).
-template <class Q, bool STOCHASTIC>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte, const uint32_t (&rnd)[8]) {
-    if (byte == 255u) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // NaN in both types
-    const float inv = __uint_as_float((254u - byte) << 23);
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float z = __fmul_rn(x[e], inv);
-        y[e] = z;
-        if constexpr (STOCHASTIC) y[e] = __uint_as_float((__float_as_uint(z) + rnd[e]) & ~((1u << Q::kCut) - 1u));
-        if constexpr (Q::kFloor)
-            if (z > 0.0f) y[e] = fmaxf(y[e], kSmallestE5m2);
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = Q::enc2(y[2 * k], y[2 * k + 1]);
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-}
-
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x ^= x >> 16;
     x *= 0x9E3779B1u;
@@ -308,20 +268,35 @@ struct MultiShared {
     int32_t apply;
 };
 
+// Four threads a group: binary64 divisions and square roots are slow here, and
+// a short step waits for them.
 __device__ __forceinline__ void multi_constants(const MultiArgs& a, MultiShared& s) {
     const zero_step_state* st = a.st;
     const bool advance = (a.flags & ZERO_MULTI_ADVANCE) != 0;
-    const int g = threadIdx.x;
+    const int g = threadIdx.x >> 2, role = threadIdx.x & 3;
     if (g < a.hp.n) {
-        const double b1p = advance ? __dmul_rn(st->beta1_pow, st->beta1) : st->beta1_pow;
-        const double b2p = advance ? __dmul_rn(st->beta2_pow, st->beta2) : st->beta2_pow;
-        s.k[g] = make_consts(st->beta1, st->beta2, b1p, b2p, a.hp.lr[g], a.hp.eps[g], a.hp.wd[g],
-                             advance ? 1.0f : st->clip_coef);
-        const AdamConsts& k = s.k[g];
-        s.c8[g] = Const8{k.b1, k.omb1, k.b2, k.omb2, k.decay, k.step_size, fmaxf(k.eps, 1.17549435e-38f),
-                         __double2float_rn(__ddiv_rn(1.0, __dsqrt_rn(__dsub_rn(1.0, b2p))))};
+        AdamConsts& k = s.k[g];
+        Const8& q = s.c8[g];
+        if (role == 0) {
+            const double b1p = advance ? __dmul_rn(st->beta1_pow, st->beta1) : st->beta1_pow;
+            k.step_size = q.step_size = __double2float_rn(__ddiv_rn(a.hp.lr[g], __dsub_rn(1.0, b1p)));
+        } else if (role == 1) {
+            const double b2p = advance ? __dmul_rn(st->beta2_pow, st->beta2) : st->beta2_pow;
+            k.sqrt_bc2 = __double2float_rn(__dsqrt_rn(__dsub_rn(1.0, b2p)));
+            q.isb = __fdiv_rn(1.0f, k.sqrt_bc2);
+        } else if (role == 2) {
+            k.b1 = q.b1 = __double2float_rn(st->beta1);
+            k.b2 = q.b2 = __double2float_rn(st->beta2);
+            k.omb1 = q.omb1 = __double2float_rn(__dsub_rn(1.0, st->beta1));
+            k.omb2 = q.omb2 = __double2float_rn(__dsub_rn(1.0, st->beta2));
+        } else {
+            k.decay = q.decay = __double2float_rn(__dsub_rn(1.0, __dmul_rn(a.hp.lr[g], a.hp.wd[g])));
+            k.eps = __double2float_rn(a.hp.eps[g]);
+            q.eps = fmaxf(k.eps, 1.17549435e-38f);
+            k.clip = advance ? 1.0f : st->clip_coef;
+        }
     }
-    if (g == 0) {
+    if (threadIdx.x == 4 * ZERO_MAX_GROUPS) {
         s.apply = advance ? 1 : st->apply;
         const float scale = !advance && st->grad_scale > 0.0f ? st->grad_scale : st->loss_scale;
         s.unscale = (a.flags & ZERO_MULTI_UNSCALED) ? 1.0f : __fdiv_rn(1.0f, scale);
@@ -349,52 +324,52 @@ __device__ __forceinline__ void multi_advance(const MultiArgs& a) {
     st->good_steps += 1;
 }
 
-// This thread's 8 elements of part h of chunk c.
-constexpr int kParts = kChunk / (kThreads * kVec);
-__device__ __forceinline__ int multi_place(const MultiTable& t, uint32_t c, const MultiRow& r, int h, int64_t& i) {
-    i = (int64_t)(c - r.first_chunk) * kChunk + (h * kThreads + threadIdx.x) * kVec;
-    const int64_t left = r.numel - i;
-    int nv = left >= kVec ? kVec : (left > 0 ? (int)left : 0);
-    const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
-    if (nv > 0 && !in_bounds((uint64_t)i + nv, lim)) nv = 0;
-    return nv;
-}
-
 // ----------------------------------------------------------------------------
 // AdamW, 32-bit states
 // ----------------------------------------------------------------------------
+// A thread updates 8 consecutive elements at a time.  The 8 begin on the
+// boundaries that the arrays' addresses give (MultiRow::shift), so that a
+// tensor anywhere in a flat buffer has whole vectors but for its ends.
+constexpr int kParts = kChunk / (kThreads * kVec);
+
 template <class G, class O>
 __global__ void __launch_bounds__(kThreads, 4) multi_adamw_kernel(const __grid_constant__ MultiArgs a) {
     __shared__ MultiShared s;
+    const uint32_t n = a.t.n_chunks;
+    grid_wait();
     multi_constants(a, s);
     if (s.apply) {
         const float unscale = s.unscale;
-        for (uint32_t c = blockIdx.x; c < a.t.n_chunks; c += gridDim.x) {
+        for (uint32_t d = blockIdx.x; d < n; d += gridDim.x) {
+            // from the list's end to its beginning: the gradients that the norm
+            // has read last are still in the L2 cache
+            const uint32_t c = n - 1 - d;
             const MultiRow& r = a.t.rows[a.t.tensor[c]];
-            for (int h = 0; h < kParts; ++h) {
-            int64_t i;
-            const int nv = multi_place(a.t, c, r, h, i);
-            if (nv == 0) continue;
             const uint32_t vec = r.vec;
             const AdamConsts k = s.k[r.group];
-            float g[8], p[8], m[8], v[8];
-            load_grad<G>(r.grad, i, nv, vec & kVecGrad, g);
-            load_f32(r.master + i, nv, vec & kVecMaster, p);
-            load_f32(r.m + i, nv, vec & kVec32, m);
-            load_f32(r.v + i, nv, vec & kVec32, v);
+#pragma unroll 1
+            for (int h = 0; h < kParts; ++h) {
+                const int64_t i = (int64_t)(c - r.first_chunk) * kChunk - r.shift + (h * kThreads + threadIdx.x) * kVec;
+                float g[8], p[8], m[8], v[8];
+                int e0, e1;
+                if (!span8(a.t, r, i, e0, e1)) continue;
+                load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g);
+                load_f32(r.master + i, e0, e1, vec & kVecMaster, p);
+                load_f32(r.m + i, e0, e1, vec & kVecStates, m);
+                load_f32(r.v + i, e0, e1, vec & kVecStates, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
-            if (all_zero8x3(g, m, v)) {  // e.g. embedding rows that no batch has held
+                for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
+                if (all_zero8x3(g, m, v)) {  // e.g. embedding rows that no batch has held
 #pragma unroll
-                for (int e = 0; e < 8; ++e) adamw1_zero_state(p[e], m[e], v[e], g[e], k);
-            } else {
+                    for (int e = 0; e < 8; ++e) adamw1_zero_state(p[e], m[e], v[e], g[e], k);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) adamw1(p[e], m[e], v[e], g[e], k);
-            }
-            store_f32(r.master + i, nv, vec & kVecMaster, p);
-            store_f32(r.m + i, nv, vec & kVec32, m);
-            store_f32(r.v + i, nv, vec & kVec32, v);
-            if constexpr (O::kOut) store_out<O>(r.out + i, nv, vec & kVecOut, p);
+                    for (int e = 0; e < 8; ++e) adamw1(p[e], m[e], v[e], g[e], k);
+                }
+                store_f32(r.master + i, e0, e1, vec & kVecMaster, p);
+                store_f32(r.m + i, e0, e1, vec & kVecStates, m);
+                store_f32(r.v + i, e0, e1, vec & kVecStates, v);
+                if constexpr (O::kOut) store_out<O>(r.out + i, e0, e1, vec & kVecOut, p);
             }
         }
     }
@@ -529,15 +504,20 @@ __device__ __forceinline__ void encode16(const float (&m)[16], const float (&v)[
     cv = make_uint4(wv[0], wv[1], wv[2], wv[3]);
 }
 
-// Plain access to the up to 16 elements of a lane (nv of them).
-__device__ __forceinline__ uint4 load_codes16(const uint8_t* p, int nv) {
+// A lane's 16 codes, of which nv exist.
+__device__ __forceinline__ uint4 load_codes16(const uint8_t* p, int nv, bool vec) {
+    if (vec && nv == 16) return __ldcs(reinterpret_cast<const uint4*>(p));
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < 16; ++e)
         if (e < nv) w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store_codes16(uint8_t* p, int nv, uint4 c) {
+__device__ __forceinline__ void store_codes16(uint8_t* p, int nv, bool vec, uint4 c) {
+    if (vec && nv == 16) {
+        __stcs(reinterpret_cast<uint4*>(p), c);
+        return;
+    }
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int e = 0; e < 16; ++e)
@@ -575,6 +555,7 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
         fence_mbar_init();
     }
     __syncthreads();
+    grid_wait();
     if (warp == kWarps8) {
         // Of the CTA's k-th tile: its tensor's index, and this lane's word of
         // that tensor's row; both a tile ahead of their use.
@@ -589,10 +570,9 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
             __syncwarp();
             const MultiRow& r = x.row;
             const int64_t w0 = (int64_t)(first + k * step - r.first_chunk) * kChunk;
-            constexpr uint32_t kAll = kVecGrad | kVecMaster | kVec8 | kVecOut;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
-            const int n = (r.vec & kAll) != kAll || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
+            const int n = !(r.vec & kWhole8) || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
             if (lane * 4 < n / kBlock8) {
                 copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4);
                 copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4);
@@ -657,15 +637,16 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kLane8;  // place in the tile
         const bool fast = (warp + 1) * kItem8 <= x.whole;
-        const int64_t i = x.begin + at;
-        int nv = kLane8;
+        const int64_t w0 = x.begin + warp * kItem8, i = x.begin + at;
+        int some = kItem8;  // elements of the item, and of the lane
         if (!fast) {
-            const int64_t left = r.numel - i;
-            nv = left >= kLane8 ? kLane8 : (left > 0 ? (int)left : 0);
+            const int64_t left = r.numel - w0;
+            some = left >= kItem8 ? kItem8 : (left > 0 ? (int)left : 0);
             const uint64_t lim = (uint64_t)r.numel > a.t.slack ? (uint64_t)r.numel - a.t.slack : 0;
-            if (nv > 0 && !in_bounds((uint64_t)i + nv, lim)) nv = 0;
+            if (some > 0 && !in_bounds((uint64_t)(w0 + some), lim)) some = 0;
         }
-        if (__any_sync(0xFFFFFFFFu, nv > 0)) {
+        const int nv = min(max(some - lane * kLane8, 0), kLane8);
+        if (some > 0) {
             const int64_t blk = i / kBlock8;
             const Const8 c = s.c8[r.group];
             float m[16], v[16];
@@ -673,27 +654,37 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                 decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
                 decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
             } else {
+                // neighbouring lanes read neighbouring elements, whatever the
+                // alignment; their places in the stage turn them round
+                const typename G::T* const g = static_cast<const typename G::T*>(r.grad) + w0;
+                const float* const p = r.master + w0;
+#pragma unroll 8
+                for (int e = lane; e < kItem8; e += 32)
+                    if (e < some) {
+                        x.p[warp * kItem8 + e] = p[e];
+                        x.g[warp * kItem8 + e] = g[e];
+                    }
                 float sm = 0.0f, sv = 0.0f;
                 if (nv > 0) {
                     sm = scale_of(r.ms[blk]);
                     sv = scale_of(r.vs[blk]);
                 }
-                decode16<E4m3>(load_codes16(r.m8 + i, nv), sm, m);
-                decode16<E5m2>(load_codes16(r.v8 + i, nv), sv, v);
+                decode16<E4m3>(load_codes16(r.m8 + i, nv, r.vec & kCodes), sm, m);
+                decode16<E5m2>(load_codes16(r.v8 + i, nv, r.vec & kCodes), sv, v);
+                __syncwarp();
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int o = 8 * h;
                 float g[8], p[8];
-                if (fast) {
-                    G::load8(&x.g[at + o], g);
-                    const float4 p0 = *reinterpret_cast<const float4*>(&x.p[at + o]);
-                    const float4 p1 = *reinterpret_cast<const float4*>(&x.p[at + o + 4]);
-                    p[0] = p0.x, p[1] = p0.y, p[2] = p0.z, p[3] = p0.w;
-                    p[4] = p1.x, p[5] = p1.y, p[6] = p1.z, p[7] = p1.w;
-                } else {
-                    load_grad<G>(r.grad, i + o, nv - o, false, g);
-                    load_f32(r.master + i + o, nv - o, false, p);
+                G::load8(&x.g[at + o], g);
+                const float4 p0 = *reinterpret_cast<const float4*>(&x.p[at + o]);
+                const float4 p1 = *reinterpret_cast<const float4*>(&x.p[at + o + 4]);
+                p[0] = p0.x, p[1] = p0.y, p[2] = p0.z, p[3] = p0.w;
+                p[4] = p1.x, p[5] = p1.y, p[6] = p1.z, p[7] = p1.w;
+                if (!fast) {  // what is behind the tensor's end is zero: the block's scale goes by it
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = o + e < nv ? g[e] : 0.0f;
                 }
                 if (two) {
 #pragma unroll
@@ -707,8 +698,13 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                     const float den = __fmaf_rn(sqrt_approx(v[o + e]), c.isb, c.eps);
                     p[e] = __fmaf_rn(-c.step_size, __fmul_rn(m[o + e], rcp_approx(den)), __fmul_rn(p[e], c.decay));
                 }
-                store_f32(r.master + i + o, fast ? 8 : nv - o, fast, p);
-                if constexpr (O::kOut) store_out<O>(r.out + i + o, fast ? 8 : nv - o, fast, p);
+                if (fast) {
+                    st8(r.master + i + o, p);
+                    if constexpr (O::kOut) st_stream(r.out + i + o, pack8<O>(p));
+                } else {
+                    *reinterpret_cast<float4*>(&x.p[at + o]) = make_float4(p[0], p[1], p[2], p[3]);
+                    *reinterpret_cast<float4*>(&x.p[at + o + 4]) = make_float4(p[4], p[5], p[6], p[7]);
+                }
             }
             const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
             uint4 cm, cv;
@@ -717,8 +713,17 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                 __stcs(reinterpret_cast<uint4*>(r.m8 + i), cm);
                 __stcs(reinterpret_cast<uint4*>(r.v8 + i), cv);
             } else {
-                store_codes16(r.m8 + i, nv, cm);
-                store_codes16(r.v8 + i, nv, cv);
+                store_codes16(r.m8 + i, nv, r.vec & kCodes, cm);
+                store_codes16(r.v8 + i, nv, r.vec & kCodes, cv);
+                __syncwarp();
+#pragma unroll 8
+                for (int e = lane; e < kItem8; e += 32)
+                    if (e < some) {
+                        const float p = x.p[warp * kItem8 + e];
+                        r.master[w0 + e] = p;
+                        if constexpr (O::kOut) r.out[w0 + e] = O::enc1(p);
+                    }
+                fence_proxy_async_smem();  // bulk copies into the same places come later
             }
             if ((lane & 1) == 0 && nv > 0) {
                 r.ms[blk] = (uint8_t)bm;
@@ -734,36 +739,65 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
 // ----------------------------------------------------------------------------
 // 32-bit states into the 8-bit form and back
 // ----------------------------------------------------------------------------
+// Nearest codes (ties to even) of 16 values.
+template <class Q>
+__device__ __forceinline__ uint4 nearest16(const float (&x)[16], uint32_t byte) {
+    const float inv = __uint_as_float((254u - byte) << 23);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float z = __fmul_rn(x[2 * k + i], inv);
+            y[i] = Q::kFloor && z > 0.0f ? fmaxf(z, kSmallestE5m2) : z;
+        }
+        const uint32_t q = Q::enc2(y[0], y[1]);
+        if (k & 1) w[k >> 1] |= q << 16;
+        else w[k >> 1] = q;
+    }
+    if (byte == 255u) w[0] = w[1] = w[2] = w[3] = 0x7F7F7F7Fu;  // NaN in both types
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A lane has 16 consecutive elements, a CTA a chunk.
 template <bool ENCODE>
 __global__ void __launch_bounds__(kThreads) multi_codec_kernel(const __grid_constant__ MultiTable t) {
+    static_assert(kThreads * 16 == kChunk, "one pass of a CTA is one chunk");
     for (uint32_t c = blockIdx.x; c < t.n_chunks; c += gridDim.x) {
         const MultiRow& r = t.rows[t.tensor[c]];
-        for (int h = 0; h < kParts; ++h) {
-        int64_t i;
-        const int nv = multi_place(t, c, r, h, i);
+        const int64_t i = (int64_t)(c - r.first_chunk) * kChunk + threadIdx.x * 16;
+        const int64_t left = r.numel - i;
+        int nv = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
+        const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
+        if (nv > 0 && !in_bounds((uint64_t)(i + nv), lim)) nv = 0;
         if (!__any_sync(0xFFFFFFFFu, nv > 0)) continue;
-        const uint32_t vec = r.vec;
+        const bool wide = r.vec & kCodec, codes = r.vec & kCodes;
         const int64_t blk = i / kBlock8;
-        float m[8], v[8];
+        float m[16], v[16];
         if constexpr (ENCODE) {
-            const uint32_t none[8] = {};
-            load_f32(r.m + i, nv, vec & kVec32, m);
-            load_f32(r.v + i, nv, vec & kVec32, v);
-            const uint32_t bm = block_scale<E4m3>(m), bv = block_scale<E5m2>(v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                load_f32(r.m + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<float(*)[8]>(&m[8 * h]));
+                load_f32(r.v + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<float(*)[8]>(&v[8 * h]));
+            }
+            const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
             if (nv > 0) {
-                store_codes(r.m8 + i, nv, vec & kVec8, encode8<E4m3, false>(m, bm, none));
-                store_codes(r.v8 + i, nv, vec & kVec8, encode8<E5m2, false>(v, bv, none));
-                if ((threadIdx.x & 3) == 0) {
+                store_codes16(r.m8 + i, nv, codes, nearest16<E4m3>(m, bm));
+                store_codes16(r.v8 + i, nv, codes, nearest16<E5m2>(v, bv));
+                if ((threadIdx.x & 1) == 0) {
                     r.ms[blk] = (uint8_t)bm;
                     r.vs[blk] = (uint8_t)bv;
                 }
             }
         } else if (nv > 0) {
-            decode8<E4m3>(load_codes(r.m8 + i, nv, vec & kVec8), scale_of(r.ms[blk]), m);
-            decode8<E5m2>(load_codes(r.v8 + i, nv, vec & kVec8), scale_of(r.vs[blk]), v);
-            store_f32(r.m + i, nv, vec & kVec32, m);
-            store_f32(r.v + i, nv, vec & kVec32, v);
-        }
+            decode16<E4m3>(load_codes16(r.m8 + i, nv, codes), scale_of(r.ms[blk]), m);
+            decode16<E5m2>(load_codes16(r.v8 + i, nv, codes), scale_of(r.vs[blk]), v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                store_f32(r.m + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<const float(*)[8]>(&m[8 * h]));
+                store_f32(r.v + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<const float(*)[8]>(&v[8 * h]));
+            }
         }
     }
 }
@@ -771,11 +805,28 @@ __global__ void __launch_bounds__(kThreads) multi_codec_kernel(const __grid_cons
 // ----------------------------------------------------------------------------
 // Global norm and step decision
 // ----------------------------------------------------------------------------
+// Sum of the CTA's (hi, lo) pairs in a fixed order; thread 0 gets it.
+__device__ __forceinline__ float2 sum_pairs(float hi, float lo, float2* sh) {
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) combine_lanes(hi, lo, m);
+    __syncthreads();  // sh: the sum before
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(hi, lo);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const float2 q = threadIdx.x < kThreads / 32 ? sh[threadIdx.x] : make_float2(0.0f, 0.0f);
+        hi = q.x, lo = q.y;
+#pragma unroll
+        for (int m = 1; m < kThreads / 32; m <<= 1) combine_lanes(hi, lo, m);
+    }
+    return make_float2(hi, lo);
+}
+
 template <class G>
 __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_constant__ MultiTable t, double max_norm,
                                                               zero_step_state* st, uint32_t n_slices) {
-    __shared__ double sh[kThreads];
+    __shared__ float2 sh[kThreads / 32];
     __shared__ bool last;
+    grid_wait();
     for (uint32_t sl = blockIdx.x; sl < n_slices; sl += gridDim.x) {
         // the slice's chunks, tensor by tensor
         const uint32_t c1 = (uint32_t)((uint64_t)(sl + 1) * t.n_chunks / n_slices);
@@ -784,17 +835,13 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
         while (c < c1) {
             const uint32_t n = t.tensor[c];
             const MultiRow& r = t.rows[n];
-            const int64_t begin = (int64_t)(c - r.first_chunk) * kChunk;
-            const uint32_t chunks = (uint32_t)((r.numel + kChunk - 1) / kChunk) - (c - r.first_chunk);
+            const int64_t begin = (int64_t)(c - r.first_chunk) * kChunk - r.shift;
+            const uint32_t chunks = (uint32_t)((r.numel + r.shift + kChunk - 1) / kChunk) - (c - r.first_chunk);
             const uint32_t take = min(chunks, c1 - c);
             const int64_t end = min(r.numel, begin + (int64_t)take * kChunk);
             const bool vec = r.vec & kVecGrad;
             const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
-            for (int64_t i = begin + threadIdx.x * kVec; i < end; i += kThreads * kVec) {
-                const int nv = end - i >= kVec ? kVec : (int)(end - i);
-                if (!in_bounds((uint64_t)i + nv, lim)) continue;
-                float g[8];
-                load_grad<G>(r.grad, i, nv, vec, g);
+            auto add = [&](const float (&g)[8]) {
                 float q = __fmul_rn(g[0], g[0]);
 #pragma unroll
                 for (int e = 1; e < 8; ++e) q = __fmaf_rn(g[e], g[e], q);
@@ -802,21 +849,37 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
                 two_sum(hi, q, sum, err);
                 hi = sum;
                 lo = __fadd_rn(lo, err);
-            }
+            };
+            // kUnroll loads in flight per thread
+            constexpr int kUnroll = 4, kStep = kThreads * kVec;
+            int64_t i = begin + threadIdx.x * kVec;
+            auto one = [&]() {
+                int e0, e1;
+                if (span8(t, r, i, e0, e1)) {
+                    float g[8];
+                    load_grad<G>(r.grad, i, e0, e1, vec, g);
+                    add(g);
+                }
+                i += kStep;
+            };
+            if (begin < 0) one();  // the first vector is not whole
+            if (vec)
+                for (; i + (kUnroll - 1) * kStep + kVec <= end; i += kUnroll * kStep) {
+                    if (!in_bounds((uint64_t)i + (kUnroll - 1) * kStep + kVec, lim)) break;
+                    float g[kUnroll][8];
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        G::eight_kept(static_cast<const typename G::T*>(r.grad) + i + u * kStep, g[u]);
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u) add(g[u]);
+                }
+            while (i < end) one();
             c += take;
         }
-        __syncthreads();  // sh: the slice before
-        sh[threadIdx.x] = __dadd_rn((double)hi, (double)lo);
-        __syncthreads();
-        for (int w = kThreads / 2; w > 0; w >>= 1) {
-            if ((int)threadIdx.x < w) sh[threadIdx.x] = __dadd_rn(sh[threadIdx.x], sh[threadIdx.x + w]);
-            __syncthreads();
-        }
-        if (threadIdx.x == 0) {
-            const float h = __double2float_rn(sh[0]);
-            t.partials[sl] = make_float2(h, __double2float_rn(__dsub_rn(sh[0], (double)h)));
-        }
+        const float2 sum = sum_pairs(hi, lo, sh);
+        if (threadIdx.x == 0) t.partials[sl] = sum;
     }
+    grid_launch_next();
     if (threadIdx.x == 0) {
         __threadfence();
         last = atomicInc(&t.counters[0], gridDim.x - 1) == gridDim.x - 1;
@@ -824,22 +887,20 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double sum = 0.0;
+    float hi = 0.0f, lo = 0.0f;
     for (uint32_t sl = threadIdx.x; sl < n_slices; sl += kThreads) {
         const float2 q = __ldcg(&t.partials[sl]);
-        sum = __dadd_rn(sum, __dadd_rn((double)q.x, (double)q.y));
+        float sum, err;
+        two_sum(hi, q.x, sum, err);
+        hi = sum;
+        lo = __fadd_rn(lo, __fadd_rn(err, q.y));
     }
-    __syncthreads();
-    sh[threadIdx.x] = sum;
-    __syncthreads();
-    for (int w = kThreads / 2; w > 0; w >>= 1) {
-        if ((int)threadIdx.x < w) sh[threadIdx.x] = __dadd_rn(sh[threadIdx.x], sh[threadIdx.x + w]);
-        __syncthreads();
-    }
+    const float2 both = sum_pairs(hi, lo, sh);
     if (threadIdx.x != 0) return;
-    const bool bad = !isfinite(sh[0]);  // an inf or NaN gradient, or a square beyond binary32
+    const double total = __dadd_rn((double)both.x, (double)both.y);
+    const bool bad = !isfinite(total);  // an inf or NaN gradient, or a square beyond binary32
     const float scale = st->loss_scale;
-    const double norm = bad ? (double)INFINITY : __ddiv_rn(__dsqrt_rn(sh[0]), (double)scale);
+    const double norm = bad ? (double)INFINITY : __ddiv_rn(__dsqrt_rn(total), (double)scale);
     st->nonfinite = 0;
     st->overflow = bad;
     st->grad_norm = norm;
@@ -855,8 +916,9 @@ struct zero_multi {
     std::vector<int64_t> numels;
     std::vector<int32_t> groups;
     int32_t n_groups = 0, grad_dtype = 0, param_dtype = 0;
-    int64_t n_chunks = 0;
+    int64_t most_chunks = 0;  // wherever the tensors begin
     // the last bind
+    int64_t n_chunks = 0;
     bool bound = false, grads = false, master = false, states32 = false, states8 = false, param16 = false;
     char* workspace = nullptr;
 };
@@ -864,6 +926,10 @@ struct zero_multi {
 namespace {
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+int64_t chunks_of(int64_t numel, int64_t shift) {
+    return numel > 0 ? (numel + shift + zk::kChunk - 1) / zk::kChunk : 0;
+}
 
 // Workspace layout: counters (256 bytes), rows, chunk map, norm partials.
 struct Places {
@@ -873,7 +939,7 @@ Places places(const zero_multi* M) {
     Places p;
     p.rows = 256;
     p.map = p.rows + up256((int64_t)M->numels.size() * (int64_t)sizeof(zk::MultiRow));
-    p.partials = p.map + up256(M->n_chunks * (int64_t)sizeof(uint32_t));
+    p.partials = p.map + up256(M->most_chunks * (int64_t)sizeof(uint32_t));
     p.total = p.partials + up256(zk::kSlices * (int64_t)sizeof(float2));
     return p;
 }
@@ -933,6 +999,27 @@ zero_status_t allow_smem(Kernel kern, size_t bytes, const char* what) {
     return ZERO_OK;
 }
 
+// A launch that may begin while the stream's last kernel ends (grid_wait).
+template <class... P, class... A>
+zero_status_t launch_early(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, const char* what, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    }
+    return after_launch(what);
+}
+
 template <class G, class O>
 zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
     const int64_t work = a.t.n_chunks;
@@ -941,12 +1028,10 @@ zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) 
         constexpr size_t smem = sizeof(zk::Smem8<G>);
         const zero_status_t rc = allow_smem(kern, smem, "zero_multi_adamw8");
         if (rc != ZERO_OK) return rc;
-        kern<<<persistent_grid(kern, work, smem, zk::kThreads8), zk::kThreads8, smem, s>>>(a);
-        return after_launch("zero_multi_adamw8");
+        return launch_early(kern, persistent_grid(kern, work, smem, zk::kThreads8), zk::kThreads8, smem, s, "zero_multi_adamw8", a);
     }
     auto kern = zk::multi_adamw_kernel<G, O>;
-    kern<<<persistent_grid(kern, work), zk::kThreads, 0, s>>>(a);
-    return after_launch("zero_multi_adamw");
+    return launch_early(kern, persistent_grid(kern, work), zk::kThreads, 0, s, "zero_multi_adamw", a);
 }
 
 template <class G>
@@ -1017,7 +1102,7 @@ extern "C" zero_status_t zero_multi_init(const int64_t* numels, int32_t n_tensor
             return fail(ZERO_ERR_INVALID, std::string(what) + ": element counts must be 0..2^34");
         if (group_of_tensor && (group_of_tensor[i] < 0 || group_of_tensor[i] >= n_groups))
             return fail(ZERO_ERR_INVALID, std::string(what) + ": group out of range");
-        chunks += (numels[i] + zk::kChunk - 1) / zk::kChunk;
+        chunks += chunks_of(numels[i], numels[i] > 0 ? zk::kVec - 1 : 0);
         if (chunks > ((int64_t)1 << 30)) return fail(ZERO_ERR_INVALID, std::string(what) + ": too many elements");
     }
     try {
@@ -1033,7 +1118,7 @@ extern "C" zero_status_t zero_multi_init(const int64_t* numels, int32_t n_tensor
         M->n_groups = n_groups;
         M->grad_dtype = grad_dtype;
         M->param_dtype = param_dtype;
-        M->n_chunks = chunks;
+        M->most_chunks = chunks;
         *out = M;
     } catch (const std::bad_alloc&) {
         return fail(ZERO_ERR_NOMEM, std::string(what) + ": out of host memory");
@@ -1049,7 +1134,7 @@ extern "C" zero_status_t zero_multi_query(const zero_multi* M, zero_multi_info* 
     i.n_groups = M->n_groups;
     i.grad_dtype = M->grad_dtype;
     i.param_dtype = M->param_dtype;
-    i.n_chunks = M->n_chunks;
+    i.n_chunks = M->most_chunks;
     for (int64_t n : M->numels) {
         i.numel += n;
         i.state8_bytes += 2 * (n + (n + zk::kBlock8 - 1) / zk::kBlock8);
@@ -1081,41 +1166,50 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
     } catch (const std::bad_alloc&) {
         return fail(ZERO_ERR_NOMEM, std::string(what) + ": out of host memory");
     }
-    uint32_t chunk = 0;
+    int64_t chunk = 0;
     for (int i = 0; i < n; ++i) {
         zk::MultiRow& r = rows[i];
         r = zk::MultiRow{};
         r.numel = M->numels[i];
         r.group = M->groups[i];
         r.tensor = (uint32_t)i;
-        r.first_chunk = chunk;
-        chunk += (uint32_t)((r.numel + zk::kChunk - 1) / zk::kChunk);
-        // address of tensor i in one array; `wide`: every array so far begins on a boundary for the wide access
-        auto take = [&](const void* const* arr, uintptr_t elem, uintptr_t vector, const char* name, bool& wide) -> const void* {
-            if (!arr) return nullptr;
+        r.first_chunk = (uint32_t)chunk;
+        auto take = [&](const void* const* arr, uintptr_t elem, const char* name) -> uintptr_t {
+            if (!arr || r.numel == 0) return 0;
             const uintptr_t p = reinterpret_cast<uintptr_t>(arr[i]);
-            if (r.numel > 0 && !p) rc = fail(ZERO_ERR_INVALID, std::string(what) + " " + name + ": NULL device pointer");
-            else if (r.numel > 0 && p % elem)
-                rc = fail(ZERO_ERR_ALIGN, std::string(what) + " " + name + ": not aligned to its elements");
-            if (p % vector) wide = false;
-            return arr[i];
+            if (!p) rc = fail(ZERO_ERR_INVALID, std::string(what) + " " + name + ": NULL device pointer");
+            else if (p % elem) rc = fail(ZERO_ERR_ALIGN, std::string(what) + " " + name + ": not aligned to its elements");
+            return p;
         };
-        bool wg = true, wp = true, w32 = true, w8 = true, wo = true;
-        r.grad = take(x->grads, gs, gs * 8, "grads", wg);
-        r.master = (float*)take((const void* const*)x->master, 4, 32, "master", wp);
-        r.m = (float*)take((const void* const*)x->m, 4, 32, "m", w32);
-        r.v = (float*)take((const void* const*)x->v, 4, 32, "v", w32);
-        r.m8 = (uint8_t*)take((const void* const*)x->m8, 1, 16, "m8", w8);
-        r.v8 = (uint8_t*)take((const void* const*)x->v8, 1, 16, "v8", w8);
-        r.ms = (uint8_t*)take((const void* const*)x->m8_scale, 1, 4, "m8_scale", w8);
-        r.vs = (uint8_t*)take((const void* const*)x->v8_scale, 1, 4, "v8_scale", w8);
-        r.out = (uint16_t*)take((const void* const*)x->param16, 2, 32, "param16", wo);
+        const uintptr_t g = take(x->grads, gs, "grads"), p = take((const void* const*)x->master, 4, "master");
+        const uintptr_t m = take((const void* const*)x->m, 4, "m"), v = take((const void* const*)x->v, 4, "v");
+        const uintptr_t m8 = take((const void* const*)x->m8, 1, "m8"), v8 = take((const void* const*)x->v8, 1, "v8");
+        const uintptr_t ms = take((const void* const*)x->m8_scale, 1, "m8_scale");
+        const uintptr_t vs = take((const void* const*)x->v8_scale, 1, "v8_scale");
+        const uintptr_t o = take((const void* const*)x->param16, 2, "param16");
         if (rc != ZERO_OK) return rc;
-        r.vec = (wg ? zk::kVecGrad : 0) | (wp ? zk::kVecMaster : 0) | (w32 ? zk::kVec32 : 0) | (w8 ? zk::kVec8 : 0) |
-                (wo ? zk::kVecOut : 0);
+        r.grad = reinterpret_cast<const void*>(g);
+        r.master = reinterpret_cast<float*>(p);
+        r.m = reinterpret_cast<float*>(m);
+        r.v = reinterpret_cast<float*>(v);
+        r.m8 = reinterpret_cast<uint8_t*>(m8);
+        r.v8 = reinterpret_cast<uint8_t*>(v8);
+        r.ms = reinterpret_cast<uint8_t*>(ms);
+        r.vs = reinterpret_cast<uint8_t*>(vs);
+        r.out = reinterpret_cast<uint16_t*>(o);
+        // Tensors of a flat buffer have the same distance to a boundary in all
+        // arrays: the gradients' (else the parameters') sets the shift.
+        r.shift = (uint16_t)(g ? g / gs % zk::kVec : p / 4 % zk::kVec);
+        auto on = [&](uintptr_t at, uintptr_t elem, uintptr_t vector) { return (at - r.shift * elem) % vector == 0; };
+        r.vec = (uint16_t)((on(g, gs, gs * zk::kVec) ? zk::kVecGrad : 0) | (on(p, 4, 32) ? zk::kVecMaster : 0) |
+                           (on(m, 4, 32) && on(v, 4, 32) ? zk::kVecStates : 0) | (on(o, 2, 16) ? zk::kVecOut : 0) |
+                           (g % 16 == 0 && p % 32 == 0 && (m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 && o % 16 == 0 ? zk::kWhole8 : 0) |
+                           ((m | v) % 32 == 0 ? zk::kCodec : 0) | ((m8 | v8) % 16 == 0 ? zk::kCodes : 0));
+        chunk += chunks_of(r.numel, r.shift);
     }
     M->bound = false;
     M->workspace = static_cast<char*>(workspace);
+    M->n_chunks = chunk;
     const zk::MultiTable t = table_of(M);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     zk::MultiRow* dst = const_cast<zk::MultiRow*>(t.rows);
@@ -1153,8 +1247,7 @@ extern "C" zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_no
     const uint32_t slices = std::max<uint32_t>(1, std::min<uint32_t>(t.n_chunks, zk::kSlices));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto kern) {
-        kern<<<persistent_grid(kern, slices), zk::kThreads, 0, s>>>(t, max_norm, st, slices);
-        return after_launch(what);
+        return launch_early(kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st, slices);
     };
     if (M->grad_dtype == ZERO_BF16) return go(zk::multi_norm_kernel<zk::GradBf16>);
     if (M->grad_dtype == ZERO_FP16) return go(zk::multi_norm_kernel<zk::GradFp16>);

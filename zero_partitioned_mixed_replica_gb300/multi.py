@@ -150,7 +150,7 @@ class MultiAdamW:
             raise ValueError("a step without the norm cannot clip or skip")
         self.state_bits, self.max_norm, self.seed = state_bits, float(max_norm), int(seed)
         self.beta1, self.beta2 = groups[0].beta1, groups[0].beta2
-        self.hp = (B.zero_adamw_hp * len(groups))(*[B.zero_adamw_hp(lr=g.lr, eps=g.eps, weight_decay=g.weight_decay)
+        self._hp = (B.zero_adamw_hp * len(groups))(*[B.zero_adamw_hp(lr=g.lr, eps=g.eps, weight_decay=g.weight_decay)
                                                     for g in groups])
         self.master, self.grads, self.out16 = master, grads, out16
         self._states(m, v, m_scale, v_scale)
@@ -158,11 +158,40 @@ class MultiAdamW:
                            _PARAM[out16[0].dtype] if out16 is not None else B.ZERO_NO_OUT, self.device)
         self.info = self._list.info
         self.state = torch.zeros(ctypes.sizeof(B.zero_step_state), dtype=torch.uint8, device=self.device)
+        self._norm, self._update = self._calls()
         self._bind()
         B.zero_state_init(self.state, self.beta1, self.beta2, loss_scale, dynamic_scale, growth_interval, self._s())
 
     def _s(self):
         return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+
+    @property
+    def hp(self):
+        """The groups' hyperparameters (``hp[g].lr``, ``.eps``,
+        ``.weight_decay``), read at every step."""
+        return self._hp
+
+    def _calls(self):
+        """The library functions with everything that does not change between
+        steps already converted: a short step costs the host a few microseconds,
+        most of them spent on arguments otherwise."""
+        lib, M, st = B.lib(), self._list.M.handle, ctypes.c_void_p(self.state.data_ptr())
+        hp = self._hp
+        index, raw = self.device.index, torch._C._cuda_getCurrentRawStream
+
+        def handle():
+            return raw(index) if self.stream is None else self.stream.cuda_stream
+
+        def norm():
+            B._check(lib.zero_multi_grad_norm(M, self.max_norm, st, handle()))
+
+        def update(flags):
+            if self.state_bits == 8:
+                B._check(lib.zero_multi_adamw8(M, hp, flags, self.seed & 0xFFFFFFFF, st, handle()))
+            else:
+                B._check(lib.zero_multi_adamw(M, hp, flags, st, handle()))
+
+        return norm, update
 
     def _states(self, m, v, m_scale, v_scale):
         eight = self.state_bits == 8
@@ -200,22 +229,19 @@ class MultiAdamW:
     # -- the step ------------------------------------------------------------------
     def grad_norm(self) -> None:
         """The global norm and the step decision alone (one launch)."""
-        B.zero_multi_grad_norm(self._list.M, self.max_norm, self.state, self._s())
+        self._norm()
 
     def update(self, flags: int = B.ZERO_MULTI_DECIDED) -> None:
         """The update alone, after a decision (``grad_norm``) or, with
         ``ZERO_MULTI_ADVANCE``, without one (one launch)."""
-        if self.state_bits == 8:
-            B.zero_multi_adamw8(self._list.M, self.hp, flags, self.seed, self.state, self._s())
-        else:
-            B.zero_multi_adamw(self._list.M, self.hp, flags, self.state, self._s())
+        self._update(flags)
 
     def step(self) -> None:
         if self.decide:
-            self.grad_norm()
-            self.update()
+            self._norm()
+            self._update(B.ZERO_MULTI_DECIDED)
         else:
-            self.update(B.ZERO_MULTI_ADVANCE)
+            self._update(B.ZERO_MULTI_ADVANCE)
 
     def capture(self) -> torch.cuda.CUDAGraph:
         """Record one step into a CUDA graph; replaying it runs one step (with
