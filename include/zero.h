@@ -739,6 +739,11 @@ zero_status_t zero_multi_adamw8(const zero_multi* M, const zero_adamw_hp* hp, in
 zero_status_t zero_multi_encode8(const zero_multi* M, zero_stream_t stream);
 zero_status_t zero_multi_decode8(const zero_multi* M, zero_stream_t stream);
 
+/* Device-detected errors of zero_multi_encode8 and zero_multi_decode8 since
+ * the last bind, with the bits of zero_step_state.error, where the updates
+ * report theirs (*bits = 0: none).  Synchronises the device. */
+zero_status_t zero_multi_device_error(const zero_multi* M, int32_t* bits);
+
 /* Cap on the CTAs of every later launch by this library (process-wide;
  * 0 = no cap: each kernel's own persistent grid, one full wave of CTAs or,
  * where that measured faster on GB300, fewer CTAs per SM).  For overlapping

@@ -213,7 +213,8 @@ def _codec_case(x, v):
     c.encode()
     m32.zero_(), v32.zero_()
     c.decode()
-    torch.cuda.synchronize()
+    from zero_partitioned_mixed_replica_gb300 import binding as B
+    assert B.zero_multi_device_error(c._list.M) == 0
     return m8.cpu(), ms.cpu().view(torch.uint8), v8.cpu(), vs.cpu().view(torch.uint8), m32.cpu(), v32.cpu()
 
 

@@ -99,6 +99,7 @@ def test_calls_on_an_unbound_list_are_refused():
     assert _status(B.zero_multi_adamw8, M, hp, 0, 1, FAKE, 0) == B.ZERO_ERR_STATE
     assert _status(B.zero_multi_encode8, M, 0) == B.ZERO_ERR_STATE
     assert _status(B.zero_multi_decode8, M, 0) == B.ZERO_ERR_STATE
+    assert _status(B.zero_multi_device_error, M) == B.ZERO_ERR_STATE
     assert _status(B.zero_multi_adamw, M, [hp, hp], 0, FAKE, 0) == B.ZERO_ERR_INVALID     # one group
     for fn, args in (("zero_multi_grad_norm", (None, 0.0, FAKE, None)), ("zero_multi_encode8", (None, None)),
                      ("zero_multi_adamw", (None, None, 0, FAKE, None)), ("zero_multi_query", (None, None))):

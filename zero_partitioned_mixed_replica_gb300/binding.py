@@ -51,7 +51,7 @@ EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero
             "zero_last_error", "zero_launch_count", "zero_checked_build", "zero_bounds_violations",
             "zero_checked_set_slack", "zero_multi_init", "zero_multi_query", "zero_multi_destroy", "zero_multi_bind",
             "zero_multi_grad_norm", "zero_multi_adamw", "zero_multi_adamw8", "zero_multi_encode8",
-            "zero_multi_decode8"]
+            "zero_multi_decode8", "zero_multi_device_error"]
 ZERO_NOALLOC_MAX_ELEMS = 67108864
 
 
@@ -226,6 +226,7 @@ def lib():
         "zero_multi_adamw8": [P, ctypes.POINTER(zero_adamw_hp), i32, ctypes.c_uint32, P, P],
         "zero_multi_encode8": [P, P],
         "zero_multi_decode8": [P, P],
+        "zero_multi_device_error": [P, ctypes.POINTER(i32)],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -602,3 +603,11 @@ def zero_multi_encode8(M: Multi, stream=None) -> None:
 
 def zero_multi_decode8(M: Multi, stream=None) -> None:
     _check(lib().zero_multi_decode8(M, _stream(stream)))
+
+
+def zero_multi_device_error(M: Multi) -> int:
+    """Errors the codec's kernels reported since the last bind (0: none);
+    synchronises the device."""
+    bits = ctypes.c_int32(0)
+    _check(lib().zero_multi_device_error(M, ctypes.byref(bits)))
+    return int(bits.value)

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "zero_launch.h"
@@ -49,7 +50,7 @@ static_assert(kRowWords == 12 && kRowWords <= 32, "a warp reads a row");
 
 // The device workspace: counters, rows, chunk map, norm partials.
 struct MultiTable {
-    uint32_t* counters;      // [0] norm, [1] update: CTAs that are done
+    uint32_t* counters;      // CTAs that are done: [0] norm, [1] others; [2] tiles dealt; [3] errors of the codec
     const MultiRow* rows;
     const uint32_t* tensor;  // tensor of each chunk
     float2* partials;        // kSlices
@@ -87,7 +88,7 @@ struct RowBatch {
 __global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n, uint32_t* counters) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < n) rows[i] = b.rows[i];
-    if (i < 2 && counters) counters[i] = 0;
+    if (i < 4 && counters) counters[i] = 0;
 }
 
 // Tensor of every chunk: the last row whose first chunk is not behind it
@@ -268,9 +269,10 @@ struct MultiShared {
     int32_t apply;
 };
 
-// Four threads a group: binary64 divisions and square roots are slow here, and
+// All threads of the CTA call it; false: the step is skipped.  Four threads a
+// group: binary64 divisions and square roots are slow here, and
 // a short step waits for them.
-__device__ __forceinline__ void multi_constants(const MultiArgs& a, MultiShared& s) {
+__device__ __forceinline__ bool multi_constants(const MultiArgs& a, MultiShared& s) {
     const zero_step_state* st = a.st;
     const bool advance = (a.flags & ZERO_MULTI_ADVANCE) != 0;
     const int g = threadIdx.x >> 2, role = threadIdx.x & 3;
@@ -306,16 +308,10 @@ __device__ __forceinline__ void multi_constants(const MultiArgs& a, MultiShared&
         s.key = mix32(a.seed ^ mix32((uint32_t)(st->t + (advance ? 1 : 0))));
     }
     __syncthreads();
+    return s.apply != 0;
 }
 
-// ZERO_MULTI_ADVANCE: the CTA that ends last moves the step on; every CTA has
-// read the state by then.
-__device__ __forceinline__ void multi_advance(const MultiArgs& a) {
-    if (!(a.flags & ZERO_MULTI_ADVANCE)) return;
-    if (threadIdx.x != 0) return;
-    __threadfence();
-    if (atomicInc(&a.t.counters[1], gridDim.x - 1) != gridDim.x - 1) return;
-    zero_step_state* st = a.st;
+__device__ __forceinline__ void advance_step(zero_step_state* st) {
     st->clip_coef = 1.0f;
     st->apply = 1;
     st->t += 1;
@@ -325,90 +321,25 @@ __device__ __forceinline__ void multi_advance(const MultiArgs& a) {
 }
 
 // ----------------------------------------------------------------------------
-// AdamW, 32-bit states
+// A ring of tiles in shared memory
+//
+// kWarps warps of a CTA compute and one fetches the inputs of the next tiles
+// by bulk copies; two CTAs on an SM.  With the loads of a few tiles always
+// under way the memory is busy whatever the number of warps, and how near the
+// CTAs are to each other in memory decides its rate: with tiles dealt in turns
+// CTAs drift apart.  GB300, 1.56e9 elements, us per launch (32-bit / 8-bit
+// update): dealt by a counter 6137 / 3562 (7.1 / 7.05 TB/s); with one CTA on
+// an SM and twice the tiles in flight 6752 / 3846, with three CTAs 6159 / 3586,
+// with 4 + 1 warps and half the tile 6155 / 3561.  Dealt in turns, two CTAs:
+// 7483 / 3974, one CTA: 6684 / 3664.  The plain form of the 32-bit update (8
+// elements a thread, 32-byte loads, 1024 threads on an SM) 6605 to 6740.
 // ----------------------------------------------------------------------------
-// A thread updates 8 consecutive elements at a time.  The 8 begin on the
-// boundaries that the arrays' addresses give (MultiRow::shift), so that a
-// tensor anywhere in a flat buffer has whole vectors but for its ends.
-constexpr int kParts = kChunk / (kThreads * kVec);
+constexpr int kWarps = 8;
+constexpr int kRingThreads = 32 * (kWarps + 1);
 
-template <class G, class O>
-__global__ void __launch_bounds__(kThreads, 4) multi_adamw_kernel(const __grid_constant__ MultiArgs a) {
-    __shared__ MultiShared s;
-    const uint32_t n = a.t.n_chunks;
-    grid_wait();
-    multi_constants(a, s);
-    if (s.apply) {
-        const float unscale = s.unscale;
-        for (uint32_t d = blockIdx.x; d < n; d += gridDim.x) {
-            // from the list's end to its beginning: the gradients that the norm
-            // has read last are still in the L2 cache
-            const uint32_t c = n - 1 - d;
-            const MultiRow& r = a.t.rows[a.t.tensor[c]];
-            const uint32_t vec = r.vec;
-            const AdamConsts k = s.k[r.group];
-#pragma unroll 1
-            for (int h = 0; h < kParts; ++h) {
-                const int64_t i = (int64_t)(c - r.first_chunk) * kChunk - r.shift + (h * kThreads + threadIdx.x) * kVec;
-                float g[8], p[8], m[8], v[8];
-                int e0, e1;
-                if (!span8(a.t, r, i, e0, e1)) continue;
-                load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g);
-                load_f32(r.master + i, e0, e1, vec & kVecMaster, p);
-                load_f32(r.m + i, e0, e1, vec & kVecStates, m);
-                load_f32(r.v + i, e0, e1, vec & kVecStates, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
-                if (all_zero8x3(g, m, v)) {  // e.g. embedding rows that no batch has held
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) adamw1_zero_state(p[e], m[e], v[e], g[e], k);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) adamw1(p[e], m[e], v[e], g[e], k);
-                }
-                store_f32(r.master + i, e0, e1, vec & kVecMaster, p);
-                store_f32(r.m + i, e0, e1, vec & kVecStates, m);
-                store_f32(r.v + i, e0, e1, vec & kVecStates, v);
-                if constexpr (O::kOut) store_out<O>(r.out + i, e0, e1, vec & kVecOut, p);
-            }
-        }
-    }
-    multi_advance(a);
-}
-
-// ----------------------------------------------------------------------------
-// AdamW, 8-bit states
-// ----------------------------------------------------------------------------
-// A CTA has kWarps8 warps that compute and one that fetches.  Its tiles are the
-// list's chunks; a ring of kStages8 tiles arrives in shared memory by bulk
-// copies that the fetching warp issues, so that the inputs of the next tiles
-// are on their way while one is computed.  A computing warp takes 512 elements
-// of a tile, 16 consecutive ones per lane (a block of 32 is two lanes).  What
-// is not 512 whole elements at a tensor's end, or not aligned, is read by plain
-// loads instead.
-constexpr int kLane8 = 16;
-constexpr int kItem8 = 32 * kLane8;
-constexpr int kWarps8 = kChunk / kItem8;
-constexpr int kThreads8 = 32 * (kWarps8 + 1);
-static_assert(kChunk / kBlock8 <= 128, "a fetching lane copies 4 scale bytes of a tile");
-
-template <class G>
-struct __align__(128) Stage8 {
-    float p[kChunk];
-    typename G::T g[kChunk];
-    uint8_t m[kChunk];
-    uint8_t v[kChunk];
-    uint8_t ms[kChunk / kBlock8];
-    uint8_t vs[kChunk / kBlock8];
-    MultiRow row;
-    int64_t begin;  // the tile's first element in its tensor
-    int64_t whole;  // elements from there on that were copied
-};
-template <class G>
-struct Smem8 {
-    static constexpr int kStages8 = sizeof(typename G::T) == 4 ? 2 : 3;  // two CTAs on an SM
-    Stage8<G> stage[kStages8];
-    uint64_t full[kStages8], empty[kStages8];
+template <int S>
+struct Ring {
+    uint64_t full[S], empty[S];
 };
 
 // 4 bytes into shared memory, counted by an mbarrier.
@@ -421,6 +352,258 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {  // arrives when 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
 }
+
+template <int S>
+__device__ __forceinline__ void ring_init(Ring<S>& ring) {
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < S; ++k) {
+            mbar_init(&ring.full[k], 33);  // the fetching warp's lanes' copies, and the bulk copies' bytes
+            mbar_init(&ring.empty[k], kWarps);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+}
+
+// The fetching warp.  Its k-th tile goes into stage k % S: the row by way of
+// the lanes, then issue(tile, stage, full) by all lanes, which copies what can
+// be copied and arrives at `full` 33 times.  Chunks have PARTS tiles.  The
+// first S tiles of a CTA are its own; the others are dealt one by one by a
+// counter, so that all CTAs work next to each other in memory however long the
+// list is (dealt in turns they drift apart, and the memory's rate with them).
+// ready(), which all warps call once, says after the first copies whether the
+// tiles are wanted.  The CTA that ends last puts the counter back and calls
+// last(); every CTA is past ready() then.
+template <int S, int PARTS, class Stage, class Issue, class Ready, class Last>
+__device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, Stage* stage, Ring<S>& ring, Issue issue,
+                                           Ready ready, Last last) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t n = t.n_chunks * PARTS, own = S * gridDim.x;
+    auto tensor_of = [&](uint32_t c) { return c < n ? t.tensor[c / PARTS] : 0u; };
+    auto word_of = [&](uint32_t i) {
+        return lane < kRowWords ? __ldg(reinterpret_cast<const unsigned long long*>(t.rows + i) + lane) : 0ull;
+    };
+    auto put = [&](uint32_t k, uint32_t tile, unsigned long long word) {  // tile >= n: the end
+        Stage& x = stage[k % S];
+        if (lane < kRowWords) reinterpret_cast<unsigned long long*>(&x.row)[lane] = word;
+        if (lane == 0) x.end = tile >= n;
+        __syncwarp();
+        if (tile < n) {
+            issue(tile, x, &ring.full[k % S]);
+        } else {
+            mbar_arrive(&ring.full[k % S]);
+            if (lane == 0) mbar_arrive(&ring.full[k % S]);
+        }
+    };
+    auto deal = [&]() { return lane == 0 ? own + atomicAdd(&t.counters[2], 1u) : 0u; };  // lane 0 has it
+    uint32_t tensor[S];
+    unsigned long long word[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) tensor[j] = tensor_of(blockIdx.x + j * gridDim.x);
+#pragma unroll
+    for (int j = 0; j < S; ++j) word[j] = word_of(tensor[j]);
+    uint32_t k = 0;  // tiles put
+    bool end = false;
+#pragma unroll
+    for (int j = 0; j < S; ++j)
+        if (!end) {
+            const uint32_t tile = blockIdx.x + j * gridDim.x;
+            put(k++, tile, word[j]);
+            end = tile >= n;
+        }
+    if (ready() && !end) {
+        // three tiles ahead of the copies: the counter, the tensor, the row
+        uint32_t first = __shfl_sync(0xFFFFFFFFu, deal(), 0), second = __shfl_sync(0xFFFFFFFFu, deal(), 0), third = deal();
+        unsigned long long first_word = word_of(tensor_of(first));
+        uint32_t second_tensor = tensor_of(second);
+        while (!end) {
+            // every warp is done with the tile that the stage holds
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&ring.empty[k % S], (k / S - 1) & 1u))) {
+                if (lane == 0) atomicOr(error, ZERO_DEVERR_WAIT_TIMEOUT);
+                break;
+            }
+            put(k++, first, first_word);
+            end = first >= n;
+            first = second;
+            first_word = word_of(second_tensor);
+            second = __shfl_sync(0xFFFFFFFFu, third, 0);
+            second_tensor = tensor_of(second);
+            third = second < n ? deal() : second;
+        }
+    }
+    // the last copies land before the CTA gives up its shared memory (they
+    // have, unless the step is skipped or a wait ran out)
+    for (uint32_t j = k > S ? k - S : 0u; j < k; ++j) {
+        bool landed = false;
+        for (int tries = 0; tries < kDrainTries && !landed; ++tries)
+            landed = mbar_wait_bounded(&ring.full[j % S], (j / S) & 1u);
+        if (!landed) atomicOr(error, ZERO_DEVERR_DRAIN_TIMEOUT);
+    }
+    if (lane == 0) {
+        __threadfence();
+        if (atomicInc(&t.counters[1], gridDim.x - 1) == gridDim.x - 1) {
+            t.counters[2] = 0;
+            last();
+        }
+    }
+}
+
+// A computing warp: work(stage) for each of the CTA's tiles.
+template <int S, class Stage, class Work>
+__device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<S>& ring, Work work) {
+    const int lane = threadIdx.x & 31;
+    for (uint32_t k = 0;; ++k) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&ring.full[k % S], (k / S) & 1u))) {
+            if (lane == 0) atomicOr(error, ZERO_DEVERR_WAIT_TIMEOUT);
+            return;
+        }
+        if (stage[k % S].end) return;
+        work(stage[k % S]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ring.empty[k % S]);
+    }
+}
+
+// ----------------------------------------------------------------------------
+// AdamW, 32-bit states
+// ----------------------------------------------------------------------------
+// A tile is half a chunk; a computing warp takes 256 elements of it, 8
+// consecutive ones per lane.  The 8 begin on the boundaries that the arrays'
+// addresses give (MultiRow::shift), so that a tensor anywhere in a flat buffer
+// is copied but for its ends, which are read by plain loads.
+constexpr int kTile32 = kWarps * 32 * kVec;
+constexpr int kItem32 = 32 * kVec;
+constexpr int kParts32 = kChunk / kTile32;
+
+template <class G>
+struct __align__(128) Stage32 {
+    float p[kTile32];
+    float m[kTile32];
+    float v[kTile32];
+    typename G::T g[kTile32];
+    MultiRow row;
+    int64_t begin;  // the tile's first element in its tensor (below zero: that many do not exist)
+    int32_t lo, hi; // elements of the tile that were copied
+    bool end;       // no tile: the list's end
+};
+template <class G>
+struct Smem32 {
+    static constexpr int kStages = 3;
+    Stage32<G> stage[kStages];
+    Ring<kStages> ring;
+};
+
+__device__ __forceinline__ void lds8(const float* p, float (&o)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+    o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+
+template <class G, class O>
+__global__ void __launch_bounds__(kRingThreads, 2) multi_adamw_kernel(const __grid_constant__ MultiArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    Smem32<G>& sh = *reinterpret_cast<Smem32<G>*>(smem);
+    __shared__ MultiShared s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    ring_init(sh.ring);
+    grid_wait();
+    if (warp == kWarps) {
+        ring_fetch<Smem32<G>::kStages, kParts32>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage32<G>& x, uint64_t* bar) {
+            const MultiRow& r = x.row;
+            const int64_t w0 = (int64_t)(tile / kParts32 - r.first_chunk) * kChunk - r.shift + (tile % kParts32) * kTile32;
+            constexpr uint32_t kAll = kVecGrad | kVecMaster | kVecStates | kVecOut;
+            int64_t left = r.numel - w0;
+            if (kChecked) left -= (int64_t)a.t.slack;
+            const int lo = w0 < 0 ? kItem32 : 0;
+            int hi = left < kItem32 ? 0 : (int)min(left, (int64_t)kTile32) / kItem32 * kItem32;
+            if ((r.vec & kAll) != kAll || hi < lo) hi = lo;
+            copies_arrive(bar);
+            if (lane == 0) {
+                x.begin = w0;
+                x.lo = lo;
+                x.hi = hi;
+                const uint32_t n = (uint32_t)(hi - lo);
+                mbar_arrive_expect_tx(bar, n * (3 * sizeof(float) + sizeof(typename G::T)));
+                if (n > 0) {
+                    bulk_g2s(x.p + lo, r.master + w0 + lo, n * sizeof(float), bar);
+                    bulk_g2s(x.m + lo, r.m + w0 + lo, n * sizeof(float), bar);
+                    bulk_g2s(x.v + lo, r.v + w0 + lo, n * sizeof(float), bar);
+                    bulk_g2s(x.g + lo, static_cast<const typename G::T*>(r.grad) + w0 + lo, n * sizeof(typename G::T), bar);
+                }
+            }
+        }, [&]() { return multi_constants(a, s); }, [&]() {
+            if (a.flags & ZERO_MULTI_ADVANCE) advance_step(a.st);
+        });
+        return;
+    }
+    if (!multi_constants(a, s)) return;
+    const float unscale = s.unscale;
+    ring_compute<Smem32<G>::kStages>(&a.st->error, sh.stage, sh.ring, [&](Stage32<G>& x) {
+        const MultiRow& r = x.row;
+        const int at = (warp * 32 + lane) * kVec;  // place in the tile
+        const bool fast = warp * kItem32 >= x.lo && (warp + 1) * kItem32 <= x.hi;
+        const int64_t i = x.begin + at;
+        int e0 = 0, e1 = kVec;
+        if (!fast && !span8(a.t, r, i, e0, e1)) return;
+        const uint32_t vec = r.vec;
+        const AdamConsts k = s.k[r.group];
+        float g[8], p[8], m[8], v[8];
+        if (fast) {
+            G::load8(&x.g[at], g);
+            lds8(&x.p[at], p);
+            lds8(&x.m[at], m);
+            lds8(&x.v[at], v);
+        } else {
+            load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g);
+            load_f32(r.master + i, e0, e1, vec & kVecMaster, p);
+            load_f32(r.m + i, e0, e1, vec & kVecStates, m);
+            load_f32(r.v + i, e0, e1, vec & kVecStates, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
+        if (all_zero8x3(g, m, v)) {  // e.g. embedding rows that no batch has held
+#pragma unroll
+            for (int e = 0; e < 8; ++e) adamw1_zero_state(p[e], m[e], v[e], g[e], k);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) adamw1(p[e], m[e], v[e], g[e], k);
+        }
+        store_f32(r.master + i, e0, e1, vec & kVecMaster, p);
+        store_f32(r.m + i, e0, e1, vec & kVecStates, m);
+        store_f32(r.v + i, e0, e1, vec & kVecStates, v);
+        if constexpr (O::kOut) store_out<O>(r.out + i, e0, e1, vec & kVecOut, p);
+    });
+}
+
+// ----------------------------------------------------------------------------
+// AdamW, 8-bit states
+// ----------------------------------------------------------------------------
+// A tile is a chunk; a computing warp takes 512 elements of it, 16 consecutive
+// ones per lane (a block of 32 is two lanes).  What is not 512 whole elements
+// at a tensor's end, or not aligned, is read by plain loads instead.
+constexpr int kLane8 = 16;
+constexpr int kItem8 = 32 * kLane8;
+static_assert(kChunk == kWarps * kItem8 && kChunk / kBlock8 <= 128, "a fetching lane copies 4 scale bytes of a tile");
+
+template <class G>
+struct __align__(128) Stage8 {
+    float p[kChunk];
+    typename G::T g[kChunk];
+    uint8_t m[kChunk];
+    uint8_t v[kChunk];
+    uint8_t ms[kChunk / kBlock8];
+    uint8_t vs[kChunk / kBlock8];
+    MultiRow row;
+    int64_t begin;  // the tile's first element in its tensor
+    int64_t whole;  // elements from there on that were copied
+    bool end;       // no tile: the list's end
+};
+template <class G>
+struct Smem8 {
+    static constexpr int kStages = 2;
+    Stage8<G> stage[kStages];
+    Ring<kStages> ring;
+};
 
 // 16 codes <-> values.
 template <class Q>
@@ -539,37 +722,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 template <class G, class O>
-__global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
+__global__ void __launch_bounds__(kRingThreads, 2) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     Smem8<G>& sh = *reinterpret_cast<Smem8<G>*>(smem);
     __shared__ MultiShared s;
-    constexpr int kStages8 = Smem8<G>::kStages8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t first = blockIdx.x, step = gridDim.x;
-    const uint32_t count = first < a.t.n_chunks ? (a.t.n_chunks - first + step - 1) / step : 0u;
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < kStages8; ++k) {
-            mbar_init(&sh.full[k], 33);  // the fetching warp's lanes' copies, and the bulk copies' bytes
-            mbar_init(&sh.empty[k], kWarps8);
-        }
-        fence_mbar_init();
-    }
-    __syncthreads();
+    ring_init(sh.ring);
     grid_wait();
-    if (warp == kWarps8) {
-        // Of the CTA's k-th tile: its tensor's index, and this lane's word of
-        // that tensor's row; both a tile ahead of their use.
-        auto tensor_of = [&](uint32_t k) { return k < count ? a.t.tensor[first + k * step] : 0u; };
-        auto word_of = [&](uint32_t n) {
-            return lane < kRowWords ? __ldg(reinterpret_cast<const unsigned long long*>(a.t.rows + n) + lane) : 0ull;
-        };
-        auto issue = [&](uint32_t k, unsigned long long word) {
-            Stage8<G>& x = sh.stage[k % kStages8];
-            uint64_t* bar = &sh.full[k % kStages8];
-            if (lane < kRowWords) reinterpret_cast<unsigned long long*>(&x.row)[lane] = word;
-            __syncwarp();
+    if (warp == kWarps) {
+        ring_fetch<Smem8<G>::kStages, 1>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage8<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
-            const int64_t w0 = (int64_t)(first + k * step - r.first_chunk) * kChunk;
+            const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
             const int n = !(r.vec & kWhole8) || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
@@ -589,51 +752,15 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                     bulk_g2s(x.v, r.v8 + w0, n, bar);
                 }
             }
-        };
-        uint32_t n[kStages8];
-        unsigned long long w[kStages8];
-#pragma unroll
-        for (int k = 0; k < kStages8; ++k) n[k] = tensor_of(k);
-#pragma unroll
-        for (int k = 0; k < kStages8; ++k) w[k] = word_of(n[k]);
-        uint32_t k = 0;  // tiles issued
-#pragma unroll
-        for (int j = 0; j < kStages8; ++j)
-            if (j < count) issue(k++, w[j]);
-        unsigned long long next_word = word_of(tensor_of(kStages8));
-        uint32_t next_tensor = tensor_of(kStages8 + 1);
-        multi_constants(a, s);
-        const uint32_t todo = s.apply ? count : 0u;
-        for (; k < todo; ++k) {
-            // every warp is done with the tile that the stage holds
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.empty[k % kStages8], (k / kStages8 - 1) & 1u))) {
-                if (lane == 0) atomicOr(&a.st->error, ZERO_DEVERR_WAIT_TIMEOUT);
-                break;
-            }
-            issue(k, next_word);
-            next_word = word_of(next_tensor);
-            next_tensor = tensor_of(k + 2);
-        }
-        // the last copies land before the CTA gives up its shared memory (they
-        // have, unless the step is skipped or a wait ran out)
-        for (uint32_t j = k > kStages8 ? k - kStages8 : 0u; j < k; ++j) {
-            bool landed = false;
-            for (int tries = 0; tries < kDrainTries && !landed; ++tries)
-                landed = mbar_wait_bounded(&sh.full[j % kStages8], (j / kStages8) & 1u);
-            if (!landed) atomicOr(&a.st->error, ZERO_DEVERR_DRAIN_TIMEOUT);
-        }
+        }, [&]() { return multi_constants(a, s); }, [&]() {
+            if (a.flags & ZERO_MULTI_ADVANCE) advance_step(a.st);
+        });
         return;
     }
-    multi_constants(a, s);
-    const uint32_t todo = s.apply ? count : 0u;
+    if (!multi_constants(a, s)) return;
     const float factor = s.factor, unscale = s.unscale;
     const bool two = s.two != 0;
-    for (uint32_t k = 0; k < todo; ++k) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.full[k % kStages8], (k / kStages8) & 1u))) {
-            if (lane == 0) atomicOr(&a.st->error, ZERO_DEVERR_WAIT_TIMEOUT);
-            break;
-        }
-        Stage8<G>& x = sh.stage[k % kStages8];
+    ring_compute<Smem8<G>::kStages>(&a.st->error, sh.stage, sh.ring, [&](Stage8<G>& x) {
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kLane8;  // place in the tile
         const bool fast = (warp + 1) * kItem8 <= x.whole;
@@ -658,12 +785,19 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                 // alignment; their places in the stage turn them round
                 const typename G::T* const g = static_cast<const typename G::T*>(r.grad) + w0;
                 const float* const p = r.master + w0;
-#pragma unroll 8
-                for (int e = lane; e < kItem8; e += 32)
-                    if (e < some) {
-                        x.p[warp * kItem8 + e] = p[e];
-                        x.g[warp * kItem8 + e] = g[e];
-                    }
+                float tp[kLane8];
+                typename G::T tg[kLane8];
+#pragma unroll
+                for (int j = 0; j < kLane8; ++j) {
+                    const int e = 32 * j + lane;
+                    tp[j] = e < some ? p[e] : 0.0f;
+                    tg[j] = e < some ? g[e] : typename G::T(0);
+                }
+#pragma unroll
+                for (int j = 0; j < kLane8; ++j) {
+                    x.p[warp * kItem8 + 32 * j + lane] = tp[j];
+                    x.g[warp * kItem8 + 32 * j + lane] = tg[j];
+                }
                 float sm = 0.0f, sv = 0.0f;
                 if (nv > 0) {
                     sm = scale_of(r.ms[blk]);
@@ -678,14 +812,7 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                 const int o = 8 * h;
                 float g[8], p[8];
                 G::load8(&x.g[at + o], g);
-                const float4 p0 = *reinterpret_cast<const float4*>(&x.p[at + o]);
-                const float4 p1 = *reinterpret_cast<const float4*>(&x.p[at + o + 4]);
-                p[0] = p0.x, p[1] = p0.y, p[2] = p0.z, p[3] = p0.w;
-                p[4] = p1.x, p[5] = p1.y, p[6] = p1.z, p[7] = p1.w;
-                if (!fast) {  // what is behind the tensor's end is zero: the block's scale goes by it
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = o + e < nv ? g[e] : 0.0f;
-                }
+                lds8(&x.p[at + o], p);
                 if (two) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
@@ -716,13 +843,17 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                 store_codes16(r.m8 + i, nv, r.vec & kCodes, cm);
                 store_codes16(r.v8 + i, nv, r.vec & kCodes, cv);
                 __syncwarp();
-#pragma unroll 8
-                for (int e = lane; e < kItem8; e += 32)
+                float tp[kLane8];
+#pragma unroll
+                for (int j = 0; j < kLane8; ++j) tp[j] = x.p[warp * kItem8 + 32 * j + lane];
+#pragma unroll
+                for (int j = 0; j < kLane8; ++j) {
+                    const int e = 32 * j + lane;
                     if (e < some) {
-                        const float p = x.p[warp * kItem8 + e];
-                        r.master[w0 + e] = p;
-                        if constexpr (O::kOut) r.out[w0 + e] = O::enc1(p);
+                        r.master[w0 + e] = tp[j];
+                        if constexpr (O::kOut) r.out[w0 + e] = O::enc1(tp[j]);
                     }
+                }
                 fence_proxy_async_smem();  // bulk copies into the same places come later
             }
             if ((lane & 1) == 0 && nv > 0) {
@@ -730,10 +861,7 @@ __global__ void __launch_bounds__(kThreads8, 2) multi_adamw8_kernel(const __grid
                 r.vs[blk] = (uint8_t)bv;
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[k % kStages8]);
-    }
-    multi_advance(a);
+    });
 }
 
 // ----------------------------------------------------------------------------
@@ -760,46 +888,124 @@ __device__ __forceinline__ uint4 nearest16(const float (&x)[16], uint32_t byte) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A lane has 16 consecutive elements, a CTA a chunk.
+// A tile is a chunk, 16 consecutive elements a lane, as in the 8-bit update.
+struct __align__(128) StageEncode {
+    float m[kChunk];
+    float v[kChunk];
+    MultiRow row;
+    int64_t begin, whole;
+    bool end;
+};
+struct __align__(128) StageDecode {
+    uint8_t m[kChunk];
+    uint8_t v[kChunk];
+    uint8_t ms[kChunk / kBlock8];
+    uint8_t vs[kChunk / kBlock8];
+    MultiRow row;
+    int64_t begin, whole;
+    bool end;
+};
+template <class Stage>
+struct SmemCodec {
+    static constexpr int kStages = 3;
+    Stage stage[kStages];
+    Ring<kStages> ring;
+};
+
 template <bool ENCODE>
-__global__ void __launch_bounds__(kThreads) multi_codec_kernel(const __grid_constant__ MultiTable t) {
-    static_assert(kThreads * 16 == kChunk, "one pass of a CTA is one chunk");
-    for (uint32_t c = blockIdx.x; c < t.n_chunks; c += gridDim.x) {
-        const MultiRow& r = t.rows[t.tensor[c]];
-        const int64_t i = (int64_t)(c - r.first_chunk) * kChunk + threadIdx.x * 16;
-        const int64_t left = r.numel - i;
-        int nv = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
-        const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
-        if (nv > 0 && !in_bounds((uint64_t)(i + nv), lim)) nv = 0;
-        if (!__any_sync(0xFFFFFFFFu, nv > 0)) continue;
+__global__ void __launch_bounds__(kRingThreads, 2) multi_codec_kernel(const __grid_constant__ MultiTable t) {
+    using Stage = std::conditional_t<ENCODE, StageEncode, StageDecode>;
+    using Smem = SmemCodec<Stage>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Smem& sh = *reinterpret_cast<Smem*>(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t* const error = reinterpret_cast<int32_t*>(&t.counters[3]);
+    ring_init(sh.ring);
+    grid_wait();
+    if (warp == kWarps) {
+        ring_fetch<Smem::kStages, 1>(t, error, sh.stage, sh.ring, [&](uint32_t tile, Stage& x, uint64_t* bar) {
+            const MultiRow& r = x.row;
+            const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk;
+            int64_t left = r.numel - w0;
+            if (kChecked) left -= (int64_t)t.slack;
+            const bool wide = (r.vec & kCodec) && (r.vec & kCodes);
+            const int n = !wide || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
+            if constexpr (!ENCODE)
+                if (lane * 4 < n / kBlock8) {
+                    copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4);
+                    copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4);
+                }
+            copies_arrive(bar);
+            if (lane == 0) {
+                x.begin = w0;
+                x.whole = n;
+                mbar_arrive_expect_tx(bar, (uint32_t)n * (ENCODE ? 8 : 2));
+                if (n > 0) {
+                    if constexpr (ENCODE) {
+                        bulk_g2s(x.m, r.m + w0, n * sizeof(float), bar);
+                        bulk_g2s(x.v, r.v + w0, n * sizeof(float), bar);
+                    } else {
+                        bulk_g2s(x.m, r.m8 + w0, n, bar);
+                        bulk_g2s(x.v, r.v8 + w0, n, bar);
+                    }
+                }
+            }
+        }, []() { return true; }, []() {});
+        return;
+    }
+    ring_compute<Smem::kStages>(error, sh.stage, sh.ring, [&](Stage& x) {
+        const MultiRow& r = x.row;
+        const int at = (warp * 32 + lane) * kLane8;
+        const bool fast = (warp + 1) * kItem8 <= x.whole;
+        const int64_t i = x.begin + at;
+        int nv = kLane8;
+        if (!fast) {
+            const int64_t left = r.numel - i;
+            nv = left >= kLane8 ? kLane8 : (left > 0 ? (int)left : 0);
+            const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
+            if (nv > 0 && !in_bounds((uint64_t)(i + nv), lim)) nv = 0;
+            if (!__any_sync(0xFFFFFFFFu, nv > 0)) return;
+        }
         const bool wide = r.vec & kCodec, codes = r.vec & kCodes;
         const int64_t blk = i / kBlock8;
         float m[16], v[16];
         if constexpr (ENCODE) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                load_f32(r.m + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<float(*)[8]>(&m[8 * h]));
-                load_f32(r.v + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<float(*)[8]>(&v[8 * h]));
+                float(&mh)[8] = *reinterpret_cast<float(*)[8]>(&m[8 * h]);
+                float(&vh)[8] = *reinterpret_cast<float(*)[8]>(&v[8 * h]);
+                if (fast) {
+                    lds8(&x.m[at + 8 * h], mh);
+                    lds8(&x.v[at + 8 * h], vh);
+                } else {
+                    load_f32(r.m + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, mh);
+                    load_f32(r.v + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, vh);
+                }
             }
             const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
             if (nv > 0) {
                 store_codes16(r.m8 + i, nv, codes, nearest16<E4m3>(m, bm));
                 store_codes16(r.v8 + i, nv, codes, nearest16<E5m2>(v, bv));
-                if ((threadIdx.x & 1) == 0) {
+                if ((lane & 1) == 0) {
                     r.ms[blk] = (uint8_t)bm;
                     r.vs[blk] = (uint8_t)bv;
                 }
             }
         } else if (nv > 0) {
-            decode16<E4m3>(load_codes16(r.m8 + i, nv, codes), scale_of(r.ms[blk]), m);
-            decode16<E5m2>(load_codes16(r.v8 + i, nv, codes), scale_of(r.vs[blk]), v);
+            if (fast) {
+                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
+                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
+            } else {
+                decode16<E4m3>(load_codes16(r.m8 + i, nv, codes), scale_of(r.ms[blk]), m);
+                decode16<E5m2>(load_codes16(r.v8 + i, nv, codes), scale_of(r.vs[blk]), v);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 store_f32(r.m + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<const float(*)[8]>(&m[8 * h]));
                 store_f32(r.v + i + 8 * h, 0, nv - 8 * h, wide && nv == 16, *reinterpret_cast<const float(*)[8]>(&v[8 * h]));
             }
         }
-    }
+    });
 }
 
 // ----------------------------------------------------------------------------
@@ -1022,16 +1228,13 @@ zero_status_t launch_early(void (*kern)(P...), int grid, int threads, size_t sme
 
 template <class G, class O>
 zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
-    const int64_t work = a.t.n_chunks;
-    if (eight) {
-        auto kern = zk::multi_adamw8_kernel<G, O>;
-        constexpr size_t smem = sizeof(zk::Smem8<G>);
-        const zero_status_t rc = allow_smem(kern, smem, "zero_multi_adamw8");
-        if (rc != ZERO_OK) return rc;
-        return launch_early(kern, persistent_grid(kern, work, smem, zk::kThreads8), zk::kThreads8, smem, s, "zero_multi_adamw8", a);
-    }
-    auto kern = zk::multi_adamw_kernel<G, O>;
-    return launch_early(kern, persistent_grid(kern, work), zk::kThreads, 0, s, "zero_multi_adamw", a);
+    const char* what = eight ? "zero_multi_adamw8" : "zero_multi_adamw";
+    const size_t smem = eight ? sizeof(zk::Smem8<G>) : sizeof(zk::Smem32<G>);
+    const int64_t tiles = eight ? a.t.n_chunks : (int64_t)a.t.n_chunks * zk::kParts32;
+    void (*kern)(zk::MultiArgs) = eight ? zk::multi_adamw8_kernel<G, O> : zk::multi_adamw_kernel<G, O>;
+    const zero_status_t rc = allow_smem(kern, smem, what);
+    if (rc != ZERO_OK) return rc;
+    return launch_early(kern, persistent_grid(kern, tiles, smem, zk::kRingThreads), zk::kRingThreads, smem, s, what, a);
 }
 
 template <class G>
@@ -1071,15 +1274,11 @@ zero_status_t codec(const zero_multi* M, zero_stream_t stream, bool encode, cons
     if (!M->states8) return missing(what, "8-bit states");
     if (M->n_chunks == 0) return ZERO_OK;
     const zk::MultiTable t = table_of(M);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (encode) {
-        auto kern = zk::multi_codec_kernel<true>;
-        kern<<<persistent_grid(kern, t.n_chunks), zk::kThreads, 0, s>>>(t);
-    } else {
-        auto kern = zk::multi_codec_kernel<false>;
-        kern<<<persistent_grid(kern, t.n_chunks), zk::kThreads, 0, s>>>(t);
-    }
-    return after_launch(what);
+    void (*kern)(zk::MultiTable) = encode ? zk::multi_codec_kernel<true> : zk::multi_codec_kernel<false>;
+    const size_t smem = encode ? sizeof(zk::SmemCodec<zk::StageEncode>) : sizeof(zk::SmemCodec<zk::StageDecode>);
+    if ((rc = allow_smem(kern, smem, what)) != ZERO_OK) return rc;
+    return launch_early(kern, persistent_grid(kern, t.n_chunks, smem, zk::kRingThreads), zk::kRingThreads, smem,
+                        reinterpret_cast<cudaStream_t>(stream), what, t);
 }
 
 }  // namespace
@@ -1204,7 +1403,7 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         r.vec = (uint16_t)((on(g, gs, gs * zk::kVec) ? zk::kVecGrad : 0) | (on(p, 4, 32) ? zk::kVecMaster : 0) |
                            (on(m, 4, 32) && on(v, 4, 32) ? zk::kVecStates : 0) | (on(o, 2, 16) ? zk::kVecOut : 0) |
                            (g % 16 == 0 && p % 32 == 0 && (m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 && o % 16 == 0 ? zk::kWhole8 : 0) |
-                           ((m | v) % 32 == 0 ? zk::kCodec : 0) | ((m8 | v8) % 16 == 0 ? zk::kCodes : 0));
+                           ((m | v) % 32 == 0 ? zk::kCodec : 0) | ((m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 ? zk::kCodes : 0));
         chunk += chunks_of(r.numel, r.shift);
     }
     M->bound = false;
@@ -1274,4 +1473,19 @@ extern "C" zero_status_t zero_multi_encode8(const zero_multi* M, zero_stream_t s
 extern "C" zero_status_t zero_multi_decode8(const zero_multi* M, zero_stream_t stream) {
     clear_error();
     return codec(M, stream, false, "zero_multi_decode8");
+}
+
+extern "C" zero_status_t zero_multi_device_error(const zero_multi* M, int32_t* bits) {
+    clear_error();
+    const char* what = "zero_multi_device_error";
+    if (!bits) return fail(ZERO_ERR_INVALID, std::string(what) + ": NULL output");
+    zero_status_t rc;
+    if ((rc = check_bound(M, what)) != ZERO_OK) return rc;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(bits, &table_of(M).counters[3], sizeof *bits, cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    }
+    return ZERO_OK;
 }
