@@ -1288,21 +1288,24 @@ extern "C" zero_status_t zero_multi_init(const int64_t* numels, int32_t n_tensor
     clear_error();
     const char* what = "zero_multi_init";
     if (!numels || !out) return fail(ZERO_ERR_INVALID, std::string(what) + ": NULL argument");
-    if (n_tensors < 1) return fail(ZERO_ERR_INVALID, std::string(what) + ": need at least one tensor");
+    if (n_tensors < 1 || n_tensors > (1 << 29))
+        return fail(ZERO_ERR_INVALID, std::string(what) + ": n_tensors must be 1..2^29");
     if (n_groups < 1 || n_groups > ZERO_MAX_GROUPS)
         return fail(ZERO_ERR_INVALID, std::string(what) + ": n_groups must be 1..16");
     if (grad_dtype != ZERO_BF16 && grad_dtype != ZERO_FP16 && grad_dtype != ZERO_FP32)
         return fail(ZERO_ERR_INVALID, std::string(what) + ": unknown gradient dtype");
     if (param_dtype != ZERO_BF16 && param_dtype != ZERO_FP16 && param_dtype != ZERO_NO_OUT)
         return fail(ZERO_ERR_INVALID, std::string(what) + ": unknown parameter dtype");
-    int64_t chunks = 0;
+    int64_t chunks = 0, total = 0;
     for (int32_t i = 0; i < n_tensors; ++i) {
         if (numels[i] < 0 || numels[i] > ((int64_t)1 << 34))
             return fail(ZERO_ERR_INVALID, std::string(what) + ": element counts must be 0..2^34");
         if (group_of_tensor && (group_of_tensor[i] < 0 || group_of_tensor[i] >= n_groups))
             return fail(ZERO_ERR_INVALID, std::string(what) + ": group out of range");
         chunks += chunks_of(numels[i], numels[i] > 0 ? zk::kVec - 1 : 0);
-        if (chunks > ((int64_t)1 << 30)) return fail(ZERO_ERR_INVALID, std::string(what) + ": too many elements");
+        total += numels[i];
+        if (total > ((int64_t)1 << 41) || chunks > ((int64_t)1 << 30))  // tiles are counted in 32 bits
+            return fail(ZERO_ERR_INVALID, std::string(what) + ": too many elements");
     }
     try {
         zero_multi* M = new zero_multi;
