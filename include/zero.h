@@ -151,9 +151,7 @@ typedef struct zero_step_state {
                                     did not land within 4 more bounded waits: the
                                     CTA exited with it possibly still in flight,
                                     so treat the context as unreliable */
-    float grad_scale;            /* zero_multi_grad_norm: the loss scale the gradients of
-                                    the last decided step carried (0: none decided)  */
-    int32_t reserved[2];
+    int32_t reserved[3];
 } zero_step_state;
 
 /* AdamW hyperparameters that may change between steps (lr schedules).  The
@@ -683,8 +681,9 @@ zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays* arrays, vo
 /* Global gradient norm over the list and the step decision: what
  * ZERO_NORM_DECIDE does, for gradients x that still carry the loss scale:
  * norm = sqrt(sum x^2) / loss_scale.  Overflow (the step is skipped): an inf
- * or NaN gradient, or a sum of squares beyond binary32.  Also keeps the scale
- * the gradients carry in st->grad_scale, since a dynamic one may grow here.
+ * or NaN gradient, or a sum of squares beyond binary32.  The list's workspace
+ * keeps the scale that these gradients carry, since a dynamic one may change
+ * here.
  * Deterministic: fixed slices of the list, binary32 sums with their rounding
  * errors carried along, combined in binary64 in a fixed order.  Needs grads.
  * One launch. */
@@ -693,8 +692,11 @@ zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_norm, zero_st
 
 /* Flags of the updates. */
 enum {
-    ZERO_MULTI_DECIDED = 0,  /* after zero_multi_grad_norm (or zero_grad_norm):
-                                apply st's decision and clip coefficient       */
+    ZERO_MULTI_DECIDED = 0,  /* apply st's decision and clip coefficient.  The
+                                gradients carry the loss scale they had at the
+                                last zero_multi_grad_norm on this list; after
+                                another decision (zero_grad_norm), combine with
+                                ZERO_MULTI_UNSCALED                            */
     ZERO_MULTI_ADVANCE = 1,  /* no norm: update with the constants of step t+1,
                                 clip 1, and advance t and beta^t (no skip)     */
     ZERO_MULTI_UNSCALED = 2  /* the gradients carry no loss scale any more

@@ -156,7 +156,7 @@ def test_list_equals_the_flat_step_bit_for_bit():
                 norm = eng.read_state()["grad_norm"]
                 opt.grad_norm()
                 assert abs(opt.read_state()["grad_norm"] / norm - 1) < 1e-6
-                opt.state.copy_(eng.state)            # grad_scale 0: the scale itself, which did not change
+                opt.state.copy_(eng.state)            # the scale of opt.grad_norm()'s gradients is kept
                 opt.update()
             else:
                 opt.step()
@@ -364,6 +364,15 @@ def test_seeds_and_steps_round_differently_and_equal_seeds_alike():
         runs[name] = [x.cpu().view(torch.uint8) for x in s.opt.m + s.opt.v]
     assert all(torch.equal(a, b) for a, b in zip(runs["a"], runs["b"]))
     assert not any(torch.equal(a, b) for a, b in zip(runs["a"], runs["c"]))
+
+
+def test_binding_between_the_norm_and_the_update_keeps_the_scale():
+    s = Setup(SIZES, "fp16", "fp16", 32, scale=128.0, dynamic_scale=True, growth_interval=1)
+    s.opt.grad_norm()                                # the scale grows to 256
+    moved = s.dg.clone()
+    s.opt.rebind_grads(_views(moved, s.offs, s.sizes))
+    s.opt.update()
+    _check32(s, 1, 1.0)
 
 
 def test_rebound_gradients_are_used():

@@ -11,4 +11,4 @@ declared in ``include/zero.h``); :mod:`.binding` is a ctypes layer with the same
 entry-point names.  The library is loaded on first use, not at import.
 """
 
-__all__ = ["binding", "workloads", "synth"]
+__all__ = ["binding", "workloads", "synth", "engine", "multi"]

@@ -81,7 +81,7 @@ class zero_step_state(ctypes.Structure):
                 [(n, ctypes.c_int32) for n in ("t", "skipped", "good_steps", "growth_interval",
                                                "dynamic_scale", "nonfinite", "overflow", "apply",
                                                "error")] +
-                [("grad_scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 2)])
+                [("reserved", ctypes.c_int32 * 3)])
 
 
 class zero_copy_segment(ctypes.Structure):

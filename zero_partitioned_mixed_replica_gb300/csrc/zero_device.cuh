@@ -348,33 +348,6 @@ __device__ __forceinline__ void adamw1_zero_state(float& p, float& m, float& v, 
 }
 
 // ----------------------------------------------------------------------------
-// The step decision (one thread): skip on overflow, else the clip coefficient,
-// the step counter and beta^t; the loss-scale schedule.
-// ----------------------------------------------------------------------------
-__device__ __forceinline__ void decide_step(zero_step_state* st, bool bad, double norm, double max_norm) {
-    if (bad) {
-        st->apply = 0;
-        st->clip_coef = 1.0f;
-        st->skipped += 1;
-        st->good_steps = 0;
-        if (st->dynamic_scale) st->loss_scale = fmaxf(1.0f, __fmul_rn(st->loss_scale, 0.5f));
-        return;
-    }
-    float clip = 1.0f;
-    if (max_norm > 0.0) clip = __double2float_rn(fmin(1.0, __ddiv_rn(max_norm, __dadd_rn(norm, 1e-6))));
-    st->clip_coef = clip;
-    st->apply = 1;
-    st->t += 1;
-    st->beta1_pow = __dmul_rn(st->beta1_pow, st->beta1);
-    st->beta2_pow = __dmul_rn(st->beta2_pow, st->beta2);
-    st->good_steps += 1;
-    if (st->dynamic_scale && st->good_steps >= st->growth_interval) {
-        st->loss_scale = __fmul_rn(st->loss_scale, 2.0f);
-        st->good_steps = 0;
-    }
-}
-
-// ----------------------------------------------------------------------------
 // Bulk asynchronous copies (TMA, 1-D form) and mbarriers, inline PTX.
 // Every wait on an mbarrier is bounded in time: once kWaitLimitNs of the
 // global timer have passed (or, as a backstop, kWaitMaxPolls polls) the wait

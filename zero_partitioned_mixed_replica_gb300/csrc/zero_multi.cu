@@ -54,6 +54,7 @@ struct MultiTable {
     const MultiRow* rows;
     const uint32_t* tensor;  // tensor of each chunk
     float2* partials;        // kSlices
+    float* grad_scale;       // the loss scale that the gradients of the last norm carried
     uint32_t n_chunks;
     uint32_t n_tensors;
     uint64_t slack;          // bounds-checked builds: test hook
@@ -85,10 +86,12 @@ struct RowBatch {
     MultiRow rows[kRowsPerLaunch];
 };
 
-__global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n, uint32_t* counters) {
+__global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n, uint32_t* counters,
+                                  float* grad_scale) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < n) rows[i] = b.rows[i];
     if (i < 4 && counters) counters[i] = 0;
+    if (i == 0 && grad_scale) *grad_scale = 0.0f;
 }
 
 // Tensor of every chunk: the last row whose first chunk is not behind it
@@ -204,7 +207,7 @@ __device__ __forceinline__ void store_out(uint16_t* p, int e0, int e1, bool vec,
 
 // ----------------------------------------------------------------------------
 // 8-bit states: E4M3 (m) and E5M2 (v) codes under one power of two per 32
-// elements, which 4 neighbouring lanes hold, 8 elements each.
+// elements, which two neighbouring lanes hold, 16 elements each.
 // ----------------------------------------------------------------------------
 struct E4m3 {
     static constexpr int kTop = 8;      // largest exponent
@@ -270,8 +273,8 @@ struct MultiShared {
 };
 
 // All threads of the CTA call it; false: the step is skipped.  Four threads a
-// group: binary64 divisions and square roots are slow here, and
-// a short step waits for them.
+// group: binary64 divisions and square roots are slow here, and a short step
+// waits for them.
 __device__ __forceinline__ bool multi_constants(const MultiArgs& a, MultiShared& s) {
     const zero_step_state* st = a.st;
     const bool advance = (a.flags & ZERO_MULTI_ADVANCE) != 0;
@@ -300,7 +303,8 @@ __device__ __forceinline__ bool multi_constants(const MultiArgs& a, MultiShared&
     }
     if (threadIdx.x == 4 * ZERO_MAX_GROUPS) {
         s.apply = advance ? 1 : st->apply;
-        const float scale = !advance && st->grad_scale > 0.0f ? st->grad_scale : st->loss_scale;
+        const float kept = *a.t.grad_scale;  // zero before the list's first norm
+        const float scale = !advance && kept > 0.0f ? kept : st->loss_scale;
         s.unscale = (a.flags & ZERO_MULTI_UNSCALED) ? 1.0f : __fdiv_rn(1.0f, scale);
         const float clip = advance ? 1.0f : st->clip_coef;
         s.two = clip != 1.0f && s.unscale != 1.0f;  // a factor of 1 changes nothing
@@ -381,7 +385,7 @@ __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, 
     const uint32_t n = t.n_chunks * PARTS, own = S * gridDim.x;
     auto tensor_of = [&](uint32_t c) { return c < n ? t.tensor[c / PARTS] : 0u; };
     auto word_of = [&](uint32_t i) {
-        return lane < kRowWords ? __ldg(reinterpret_cast<const unsigned long long*>(t.rows + i) + lane) : 0ull;
+        return lane < kRowWords ? reinterpret_cast<const unsigned long long*>(t.rows + i)[lane] : 0ull;
     };
     auto put = [&](uint32_t k, uint32_t tile, unsigned long long word) {  // tile >= n: the end
         Stage& x = stage[k % S];
@@ -1011,6 +1015,32 @@ __global__ void __launch_bounds__(kRingThreads, 2) multi_codec_kernel(const __gr
 // ----------------------------------------------------------------------------
 // Global norm and step decision
 // ----------------------------------------------------------------------------
+// The step decision (one thread), as zero_grad_norm makes it: skip on overflow,
+// else the clip coefficient, the step counter and beta^t; the loss-scale
+// schedule.
+__device__ __forceinline__ void decide_step(zero_step_state* st, bool bad, double norm, double max_norm) {
+    if (bad) {
+        st->apply = 0;
+        st->clip_coef = 1.0f;
+        st->skipped += 1;
+        st->good_steps = 0;
+        if (st->dynamic_scale) st->loss_scale = fmaxf(1.0f, __fmul_rn(st->loss_scale, 0.5f));
+        return;
+    }
+    float clip = 1.0f;
+    if (max_norm > 0.0) clip = __double2float_rn(fmin(1.0, __ddiv_rn(max_norm, __dadd_rn(norm, 1e-6))));
+    st->clip_coef = clip;
+    st->apply = 1;
+    st->t += 1;
+    st->beta1_pow = __dmul_rn(st->beta1_pow, st->beta1);
+    st->beta2_pow = __dmul_rn(st->beta2_pow, st->beta2);
+    st->good_steps += 1;
+    if (st->dynamic_scale && st->good_steps >= st->growth_interval) {
+        st->loss_scale = __fmul_rn(st->loss_scale, 2.0f);
+        st->good_steps = 0;
+    }
+}
+
 // Sum of the CTA's (hi, lo) pairs in a fixed order; thread 0 gets it.
 __device__ __forceinline__ float2 sum_pairs(float hi, float lo, float2* sh) {
 #pragma unroll
@@ -1110,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
     st->nonfinite = 0;
     st->overflow = bad;
     st->grad_norm = norm;
-    st->grad_scale = scale;
+    *t.grad_scale = scale;
     decide_step(st, bad, norm, max_norm);
 }
 
@@ -1137,7 +1167,7 @@ int64_t chunks_of(int64_t numel, int64_t shift) {
     return numel > 0 ? (numel + shift + zk::kChunk - 1) / zk::kChunk : 0;
 }
 
-// Workspace layout: counters (256 bytes), rows, chunk map, norm partials.
+// Workspace layout: counters and the gradients' scale (256 bytes), rows, chunk map, norm partials.
 struct Places {
     int64_t rows, map, partials, total;
 };
@@ -1154,6 +1184,7 @@ zk::MultiTable table_of(const zero_multi* M) {
     const Places p = places(M);
     zk::MultiTable t{};
     t.counters = reinterpret_cast<uint32_t*>(M->workspace);
+    t.grad_scale = reinterpret_cast<float*>(M->workspace) + 8;
     t.rows = reinterpret_cast<const zk::MultiRow*>(M->workspace + p.rows);
     t.tensor = reinterpret_cast<const uint32_t*>(M->workspace + p.map);
     t.partials = reinterpret_cast<float2*>(M->workspace + p.partials);
@@ -1409,6 +1440,7 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
                            ((m | v) % 32 == 0 ? zk::kCodec : 0) | ((m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 ? zk::kCodes : 0));
         chunk += chunks_of(r.numel, r.shift);
     }
+    const bool fresh = M->workspace != static_cast<char*>(workspace);  // else a decided step may be under way
     M->bound = false;
     M->workspace = static_cast<char*>(workspace);
     M->n_chunks = chunk;
@@ -1419,7 +1451,8 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         zk::RowBatch b{};
         const int k = std::min(zk::kRowsPerLaunch, n - i);
         std::copy(rows.begin() + i, rows.begin() + i + k, b.rows);
-        zk::multi_rows_kernel<<<1, zk::kRowsPerLaunch, 0, s>>>(b, dst + i, k, i == 0 ? t.counters : nullptr);
+        zk::multi_rows_kernel<<<1, zk::kRowsPerLaunch, 0, s>>>(b, dst + i, k, i == 0 ? t.counters : nullptr,
+                                                                i == 0 && fresh ? t.grad_scale : nullptr);
         if ((rc = after_launch(what)) != ZERO_OK) return rc;
     }
     if (t.n_chunks > 0) {

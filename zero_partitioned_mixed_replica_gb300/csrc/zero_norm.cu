@@ -36,8 +36,7 @@ __global__ void state_init_kernel(zero_step_state* st, double beta1, double beta
     st->overflow = 0;
     st->apply = 0;
     st->error = 0;
-    st->grad_scale = 0.0f;
-    st->reserved[0] = st->reserved[1] = 0;
+    st->reserved[0] = st->reserved[1] = st->reserved[2] = 0;
 }
 
 // Pass 1: block b sums a fixed contiguous range of the partials (fixed
@@ -110,7 +109,26 @@ __global__ void __launch_bounds__(zero_detail::kNormBlocks) norm_final_kernel(
         st->good_steps += 1;
         return;
     }
-    decide_step(st, bad, norm, max_norm);
+    if (bad) {
+        st->apply = 0;
+        st->clip_coef = 1.0f;
+        st->skipped += 1;
+        st->good_steps = 0;
+        if (st->dynamic_scale) st->loss_scale = fmaxf(1.0f, __fmul_rn(st->loss_scale, 0.5f));
+        return;
+    }
+    float clip = 1.0f;
+    if (max_norm > 0.0) clip = __double2float_rn(fmin(1.0, __ddiv_rn(max_norm, __dadd_rn(norm, 1e-6))));
+    st->clip_coef = clip;
+    st->apply = 1;
+    st->t += 1;
+    st->beta1_pow = __dmul_rn(st->beta1_pow, st->beta1);
+    st->beta2_pow = __dmul_rn(st->beta2_pow, st->beta2);
+    st->good_steps += 1;
+    if (st->dynamic_scale && st->good_steps >= st->growth_interval) {
+        st->loss_scale = __fmul_rn(st->loss_scale, 2.0f);
+        st->good_steps = 0;
+    }
 }
 
 }  // namespace zk

@@ -69,9 +69,23 @@ class ZeroStep:
                  dynamic_scale: bool = False, growth_interval: int = 2000,
                  fused: Optional[bool] = None, per_bucket: bool = True, fuse_allgather: bool = True,
                  n_micro: int = 1, device: str = "cuda", stream: Optional[torch.cuda.Stream] = None,
-                 pad_multiple: int = 0, live_units: int = 1):
+                 pad_multiple: int = 0, live_units: int = 1, state_bits: int = 32, seed: int = 0):
+        """``state_bits=8`` keeps m and v in 8 bits (E4M3 and E5M2 codes with a
+        scale per 32 elements, ``zero.h``): 2.06 instead of 8 bytes a
+        parameter.  Such an engine runs the split step with the list update on
+        the rank shards, and unfused all-gathers; ``seed`` seeds the
+        stochastic rounding of its states."""
         if stage not in (1, 2, 3):
             raise ValueError("ZeroStep runs ZeRO stages 1, 2 and 3")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.state_bits, self.seed = state_bits, int(seed)
+        if state_bits == 8:
+            if fused:
+                raise ValueError("8-bit states are updated by the split step")
+            if live_units != 1:
+                raise ValueError("live_units is the executor's; 8-bit states run without it")
+            fused, fuse_allgather = False, False
         self.pad_multiple = pad_multiple    # 0: N_d * 128; else a multiple of it
         self.L = B.zero_layout_init(list(numels), list(unit_of_tensor) if unit_of_tensor is not None else None,
                                     n_d, stage, pad_multiple, bucket_elems, dtype)
@@ -106,8 +120,15 @@ class ZeroStep:
         # rank-major 2-D allocations; row r is rank r's buffer (rows stay 256-byte aligned)
         self.grads = torch.zeros(n_d, P, dtype=dt16, device=dev)
         self.master = torch.zeros(n_d, S, dtype=torch.float32, device=dev)
-        self.m = torch.zeros(n_d, S, dtype=torch.float32, device=dev)
-        self.v = torch.zeros(n_d, S, dtype=torch.float32, device=dev)
+        if state_bits == 8:
+            from . import multi
+            self.m, self.v = (torch.zeros(n_d, S, dtype=torch.uint8, device=dev).view(dt) for dt in (multi.M8, multi.V8))
+            # S is a multiple of 128: no block straddles ranks
+            self.m_scale, self.v_scale = (torch.zeros(n_d, S // multi.BLOCK, dtype=torch.uint8, device=dev).view(multi.SCALE8)
+                                          for _ in range(2))
+        else:
+            self.m = torch.zeros(n_d, S, dtype=torch.float32, device=dev)
+            self.v = torch.zeros(n_d, S, dtype=torch.float32, device=dev)
         self.gshard = None if self.fused else torch.zeros(n_d, S, dtype=torch.float32, device=dev)
         # ZeRO-1 accumulates each rank's full gradient in fp32 ("第 5 课" §2: + 4 Psi per rank);
         # ZeRO-2/3 accumulate in the fp32 shard itself (+ 4 Psi / N_d, already held)
@@ -129,6 +150,11 @@ class ZeroStep:
         self.workspace = torch.zeros(self.info.workspace_bytes, dtype=torch.uint8, device=dev)
         self.state = torch.zeros(96, dtype=torch.uint8, device=dev)
         self._rows()
+        if state_bits == 8:
+            # the rank shards as a list of N_d tensors
+            self._list = multi.BoundList([S] * n_d, None, 1, B.ZERO_FP32, dtype, dev)
+            self._list.bind(self._s(), grads=self.gshard_rows, master=self.master_rows, m8=self.m_rows, v8=self.v_rows,
+                            m8_scale=self.m_scale_rows, v8_scale=self.v_scale_rows, param16=self.shard16_rows)
         self.hp = B.zero_adamw_hp(lr=adamw.lr, eps=adamw.eps, weight_decay=adamw.weight_decay)
         self.transient_hook = None  # called as hook(kind, unit, transient_rows) after each ZeRO-3 gather
         self.reset_state()
@@ -150,6 +176,8 @@ class ZeroStep:
         rows = lambda t: [t[r] for r in range(self.n_d)] if t is not None else None
         self.grad_rows = rows(self.grads)
         self.master_rows, self.m_rows, self.v_rows = rows(self.master), rows(self.m), rows(self.v)
+        if self.state_bits == 8:
+            self.m_scale_rows, self.v_scale_rows = rows(self.m_scale), rows(self.v_scale)
         self.gshard_rows = rows(self.gshard)
         self.param_rows = rows(self.params)
         self.shard16_rows = rows(self.shard16)
@@ -182,8 +210,8 @@ class ZeroStep:
             for r in range(self.n_d):
                 lo = u.offset + r * u.shard
                 self.master[r, u.shard_base:u.shard_base + u.shard].copy_(fm[lo:lo + u.shard])
-        self.m.zero_()
-        self.v.zero_()
+        for t in (self.m, self.v) + ((self.m_scale, self.v_scale) if self.state_bits == 8 else ()):
+            t.view(torch.uint8).zero_()
         s = self._s()
         s.wait_stream(torch.cuda.current_stream(self.device))   # the copies above ran on the current stream
         if self.shard16 is not None:
@@ -227,8 +255,67 @@ class ZeroStep:
         issues the step's calls in the pages' order (see ``zero.h``).  A
         ``transient_hook(kind, unit, rows)`` set on the engine is called after
         each ZeRO-3 unit gather is issued, where a layer's compute would be
-        enqueued."""
+        enqueued.  With 8-bit states the calls are issued from here, in the
+        same order."""
+        if self.state_bits == 8:
+            self._reduce8(0)
+            self._update8()
+            return
         B.zero_step(self.L, self.step_args(), self._s())
+
+    # -- 8-bit states: the split step's calls, with the list update on the shards --------
+    def _reduce8(self, micro: int) -> None:
+        """Reduce micro-batch ``micro`` as zero_micro_step does."""
+        L, s, M = self.L, self._s(), self.n_micro
+        if self.stage == 1 and M > 1:
+            B.zero_accumulate_grads(L, micro, self.grad_rows, self.acc_rows, s)
+            if micro == M - 1:
+                for b in reversed(range(self.n_buckets)):
+                    B.zero_reduce_scatter_accumulated(L, b, self.acc_rows, self.gshard_rows, M, self.state, self.workspace, s)
+            return
+
+        def reduce(i):
+            if M > 1:
+                B.zero_reduce_scatter_micro(L, i, micro, M, self.grad_rows, self.gshard_rows, self.state, self.workspace, s)
+            else:
+                B.zero_reduce_scatter(L, i, self.grad_rows, self.gshard_rows, self.state, self.workspace, s)
+
+        def gather(kind, u):
+            B.zero_stage3_gather_layer(L, u, self.shard16_rows, self.transient_rows, s)
+            if self.transient_hook is not None:
+                self.transient_hook(kind, u, self.transient_rows)
+
+        if self.stage == 3:
+            for u in range(len(self.units)):
+                gather("fwd", u)
+            for u in reversed(range(len(self.units))):
+                gather("bwd", u)
+                reduce(u)
+        else:
+            for b in reversed(range(self.n_buckets)):
+                reduce(b)
+
+    def _update8(self) -> None:
+        s = self._s()
+        B.zero_grad_norm(self.L, self.max_norm, B.ZERO_NORM_DECIDE, self.state, self.workspace, s)
+        B.zero_multi_adamw8(self._list.M, [self.hp], B.ZERO_MULTI_DECIDED | B.ZERO_MULTI_UNSCALED, self.seed, self.state, s)
+        if self.stage != 3:
+            B.zero_allgather_params(self.L, self.shard16_rows, self.param_rows, s)
+
+    def _codec8(self, m: torch.Tensor, v: torch.Tensor):
+        """The 8-bit states and fp32 ones of the same shape, [N_d, S] each."""
+        from . import multi
+        return multi.StateCodec8(list(m), list(v), self.m_rows, self.m_scale_rows, self.v_rows, self.v_scale_rows, self.stream)
+
+    def states32(self):
+        """(m, v) as fp32 [N_d, S] tensors: the states themselves, or, with
+        8-bit states, new tensors of their values."""
+        if self.state_bits == 32:
+            return self.m, self.v
+        m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
+        self._codec8(m, v).decode()
+        torch.cuda.current_stream(self.device).wait_stream(self._s())
+        return m, v
 
     # -- ZeRO-3 prefetch: gathers on a second stream overlap the layers' compute -------
     def step_overlapped(self, compute, max_live_units: int = 2, comm_ctas: int = 0) -> None:
@@ -301,6 +388,11 @@ class ZeroStep:
             return
         if not 0 <= micro < M:
             raise ValueError("micro out of range")
+        if self.state_bits == 8:
+            self._reduce8(micro)
+            if micro == M - 1:
+                self._update8()
+            return
         B.zero_micro_step(self.L, self.step_args(), micro, M, self.acc_rows, self._s())
 
     # -- CUDA graph of one step -------------------------------------------------------
@@ -352,6 +444,8 @@ class ZeroStep:
         The device replicas (``grads``) must then not be touched in between;
         ``upload_grads`` since the last host-input step turns the overlap off
         for the next one."""
+        if self.state_bits == 8:
+            raise ValueError("step_from_host is the executor's: with 8-bit states, upload_grads and step")
         self._check_host(host, True)
         if state_out is not None and (state_out.device.type != "cpu" or state_out.numel() * state_out.element_size()
                                       < self.state.numel()):
@@ -390,8 +484,11 @@ class ZeroStep:
     def save_checkpoint(self, path: str) -> dict:
         """Write one file per simulated rank (its fp32 master/m/v shard and
         16-bit parameter shard), in parallel, plus meta.json with the layout
-        and the 96-byte step state.  Returns the bytes written."""
+        and the 96-byte step state.  Returns the bytes written.  8-bit states
+        are written as the fp32 values they stand for, so a checkpoint loads
+        into engines of either width and any partition."""
         os.makedirs(path, exist_ok=True)
+        m, v = self.states32()
         torch.cuda.synchronize(self.device)
         p16 = self._shard16_rows_view()
 
@@ -403,7 +500,7 @@ class ZeroStep:
             view = stage.numpy()
             stream = torch.cuda.Stream(self.device)
             with open(os.path.join(path, "rank%03d.bin" % r), "wb") as f, torch.cuda.stream(stream):
-                for t in (self.master[r], self.m[r], self.v[r], p16[r].contiguous()):
+                for t in (self.master[r], m[r], v[r], p16[r].contiguous()):
                     flat = t.view(torch.uint8)
                     for off in range(0, flat.numel(), chunk):
                         n = min(chunk, flat.numel() - off)
@@ -466,14 +563,18 @@ class ZeroStep:
                     host[k][do:do + n] = views[sr][k][so:so + n]
             return r, host
 
+        m, v = (self.m, self.v) if self.state_bits == 32 else (torch.zeros_like(self.master), torch.zeros_like(self.master))
         with ThreadPoolExecutor(max_workers=min(16, self.n_d)) as ex:
             for r, host in ex.map(assemble, range(self.n_d)):
                 self.master[r].copy_(torch.from_numpy(host[0]))
-                self.m[r].copy_(torch.from_numpy(host[1]))
-                self.v[r].copy_(torch.from_numpy(host[2]))
+                m[r].copy_(torch.from_numpy(host[1]))
+                v[r].copy_(torch.from_numpy(host[2]))
                 p16_rows[r].view(torch.int16).copy_(torch.from_numpy(host[3].view(np.int16)))
         self.state.copy_(torch.frombuffer(bytearray(st), dtype=torch.uint8))
         self._s().wait_stream(torch.cuda.current_stream(self.device))   # the uploads ran on the current stream
+        if self.state_bits == 8:
+            self._codec8(m, v).encode()      # nearest 8-bit values
+            torch.cuda.synchronize(self.device)
         if self.stage != 3:
             if self.shard16 is None:
                 shards = torch.stack([t.clone() for t in p16_rows])
@@ -491,9 +592,12 @@ class ZeroStep:
         return read_step_state(self.state)
 
     def flat(self, which: str) -> torch.Tensor:
-        """Reassemble master/m/v (fp32) or shard16 (ZeRO-3) into flat order."""
-        src = {"master": self.master, "m": self.m, "v": self.v, "shard16": self.shard16,
-               "gshard": self.gshard}[which]
+        """Reassemble master/m/v (fp32; 8-bit states as their values) or
+        shard16 (ZeRO-3) into flat order."""
+        if which in ("m", "v"):
+            src = self.states32()[which == "v"]
+        else:
+            src = {"master": self.master, "shard16": self.shard16, "gshard": self.gshard}[which]
         # the copies below run on the current stream: after the engine's own stream
         torch.cuda.current_stream(self.device).wait_stream(self._s())
         out = torch.zeros(self.info.psi_pad, dtype=src.dtype, device=src.device)

@@ -60,7 +60,7 @@ def _slices(numels: Sequence[int], dtype, device) -> List[torch.Tensor]:
     return [flat[a:a + n] for a, n in zip(starts, numels)]
 
 
-class _List:
+class BoundList:
     """A bound ``zero_multi`` and its workspace."""
 
     def __init__(self, numels, group_of_tensor, n_groups, grad_dtype, param_dtype, device):
@@ -93,7 +93,7 @@ class StateCodec8:
             _check_list(name, xs, ns, (dt,), device)
         self.stream, self.device = stream, device
         self._keep = (m, v, m8, m8_scale, v8, v8_scale)
-        self._list = _List(numels, None, 1, B.ZERO_BF16, B.ZERO_NO_OUT, device)
+        self._list = BoundList(numels, None, 1, B.ZERO_BF16, B.ZERO_NO_OUT, device)
         self._list.bind(self._s(), m=m, v=v, m8=m8, m8_scale=m8_scale, v8=v8, v8_scale=v8_scale)
 
     def _s(self):
@@ -154,7 +154,7 @@ class MultiAdamW:
                                                     for g in groups])
         self.master, self.grads, self.out16 = master, grads, out16
         self._states(m, v, m_scale, v_scale)
-        self._list = _List(self.numels, group_of_tensor, len(groups), _GRAD[grads[0].dtype],
+        self._list = BoundList(self.numels, group_of_tensor, len(groups), _GRAD[grads[0].dtype],
                            _PARAM[out16[0].dtype] if out16 is not None else B.ZERO_NO_OUT, self.device)
         self.info = self._list.info
         self.state = torch.zeros(ctypes.sizeof(B.zero_step_state), dtype=torch.uint8, device=self.device)
