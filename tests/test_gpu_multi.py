@@ -202,6 +202,43 @@ def test_adamw8_against_references(grad, out, gap):
     s.untouched()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_every_distance_to_a_boundary(bits):
+    """Arrays that begin anywhere, each at a distance of its own, give what aligned ones do, bit for bit."""
+    from zero_partitioned_mixed_replica_gb300 import multi
+    from zero_partitioned_mixed_replica_gb300.engine import AdamW
+    n = 5000
+    gen = torch.Generator("cuda").manual_seed(8)
+    r = lambda: torch.randn(n, generator=gen, device="cuda")  # noqa: E731
+    g, p, m, v = r() * 1e-3, r() * 0.02, r() * 3e-4, (r() ** 2 + 0.01) * 1e-6
+    want = {}
+    for case in range(24):
+        for dt in (torch.bfloat16, torch.float32):
+            # distances in elements: equal ones, one array off, all different
+            d = [0] * 5 if case == 0 else [case % 8] * 5 if case < 8 else \
+                [(case - 8) % 8 if k == (case - 8) // 4 else 0 for k in range(5)] if case < 20 else [(case * (k + 2)) % 9 for k in range(5)]
+
+            def at(x, off):
+                buf = torch.full((n + 32,), 3.0, dtype=x.dtype, device="cuda")
+                buf[off:off + n] = x
+                return buf, buf[off:off + n]
+
+            bufs = [at(x, off) for x, off in zip((g.to(dt), p, m, v, p.bfloat16()), d)]
+            views = [b[1] for b in bufs]
+            if bits == 32:
+                opt = multi.MultiAdamW([views[1]], [views[0]], [views[4]], m=[views[2]], v=[views[3]], decide=False, groups=[AdamW()])
+            else:
+                opt = multi.MultiAdamW([views[1]], [views[0]], [views[4]], state_bits=8, decide=False, groups=[AdamW()], seed=5)
+                opt.load_states([m], [v])
+            opt.step()
+            got = [views[1], views[4], opt.m[0], opt.v[0]] + (opt.m_scale + opt.v_scale if bits == 8 else [])
+            got = [x.contiguous().view(torch.uint8).clone() for x in got]
+            for a, b in zip(got, want.setdefault(dt, got)):
+                assert torch.equal(a, b), (case, dt, d)
+            for (buf, _), off in zip(bufs[1:2] + bufs[4:], (d[1], d[4])):
+                assert bool((buf[:off] == 3).all()) and bool((buf[off + n:] == 3).all())
+
+
 def _codec_case(x, v):
     from zero_partitioned_mixed_replica_gb300 import multi
     n = x.numel()

@@ -15,7 +15,7 @@
 
 namespace zk {
 
-constexpr int kChunk = 4096;             // elements of one work item
+constexpr int kChunk = 2048;             // elements of one work item, a tile of the updates
 constexpr int kBlock8 = 32;              // elements under one scale of an 8-bit state
 constexpr int kSlices = 1216;            // fixed split of a list for the norm (8 CTAs on each of 152 SMs)
 constexpr int kRowsPerLaunch = 256;      // table rows passed through one launch's parameters
@@ -108,6 +108,42 @@ __global__ void multi_map_kernel(const MultiRow* rows, uint32_t n_tensors, uint3
     }
 }
 
+// 8 values that begin `over` places behind a 16-byte boundary of shared memory.
+__device__ __forceinline__ void lds8_over(const float* p, int over, float (&o)[8]) {
+    float q[12];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const float4 f = reinterpret_cast<const float4*>(p)[j];
+        q[4 * j] = f.x, q[4 * j + 1] = f.y, q[4 * j + 2] = f.z, q[4 * j + 3] = f.w;
+    }
+    if (over & 1)
+#pragma unroll
+        for (int j = 0; j < 11; ++j) q[j] = q[j + 1];
+    if (over & 2)
+#pragma unroll
+        for (int j = 0; j < 9; ++j) q[j] = q[j + 2];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = q[e];
+}
+__device__ __forceinline__ uint4 lds8_over(const uint16_t* p, int over) {
+    uint32_t q[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint4 f = reinterpret_cast<const uint4*>(p)[j];
+        q[4 * j] = f.x, q[4 * j + 1] = f.y, q[4 * j + 2] = f.z, q[4 * j + 3] = f.w;
+    }
+    if (over & 2)
+#pragma unroll
+        for (int j = 0; j < 7; ++j) q[j] = q[j + 1];
+    if (over & 4)
+#pragma unroll
+        for (int j = 0; j < 6; ++j) q[j] = q[j + 2];
+    if (over & 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = __funnelshift_r(q[j], q[j + 1], 16);
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
 // ----------------------------------------------------------------------------
 // Loads and stores of 8 consecutive elements of which [e0, e1) exist; `vec`:
 // the first is on a boundary for the wide access.
@@ -120,6 +156,9 @@ struct GradBf16 {
     static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
         unpack8<Bf16>(*reinterpret_cast<const uint4*>(p), o);
     }
+    static __device__ __forceinline__ void load8_over(const uint16_t* p, int over, float (&o)[8]) {
+        unpack8<Bf16>(lds8_over(p, over), o);
+    }
 };
 struct GradFp16 {
     using T = uint16_t;
@@ -128,6 +167,9 @@ struct GradFp16 {
     static __device__ __forceinline__ void eight_kept(const uint16_t* p, float (&o)[8]) { unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o); }
     static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
         unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o);
+    }
+    static __device__ __forceinline__ void load8_over(const uint16_t* p, int over, float (&o)[8]) {
+        unpack8<Fp16>(lds8_over(p, over), o);
     }
 };
 struct GradFp32 {
@@ -144,6 +186,7 @@ struct GradFp32 {
         o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
         o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
     }
+    static __device__ __forceinline__ void load8_over(const float* p, int over, float (&o)[8]) { lds8_over(p, over, o); }
 };
 struct NoOut {
     static constexpr bool kOut = false;
@@ -327,20 +370,16 @@ __device__ __forceinline__ void advance_step(zero_step_state* st) {
 // ----------------------------------------------------------------------------
 // A ring of tiles in shared memory
 //
-// kWarps warps of a CTA compute and one fetches the inputs of the next tiles
-// by bulk copies; two CTAs on an SM.  With the loads of a few tiles always
-// under way the memory is busy whatever the number of warps, and how near the
-// CTAs are to each other in memory decides its rate: with tiles dealt in turns
-// CTAs drift apart.  GB300, 1.56e9 elements, us per launch (32-bit / 8-bit
-// update): dealt by a counter 6137 / 3562 (7.1 / 7.05 TB/s); with one CTA on
-// an SM and twice the tiles in flight 6752 / 3846, with three CTAs 6159 / 3586,
-// with 4 + 1 warps and half the tile 6155 / 3561.  Dealt in turns, two CTAs:
-// 7483 / 3974, one CTA: 6684 / 3664.  The plain form of the 32-bit update (8
-// elements a thread, 32-byte loads, 1024 threads on an SM) 6605 to 6740.
+// W warps of a CTA compute and one fetches the inputs of the next tiles by bulk
+// copies.  With the loads of a few tiles always under way the memory is busy
+// whatever the number of warps, and how near the CTAs are to each other in
+// memory decides its rate: with tiles dealt in turns CTAs drift apart.  GB300,
+// 1.56e9 elements, us per launch (32-bit / 8-bit update), 16 computing warps on
+// an SM: dealt by a counter 6137 / 3561 (7.1 / 7.05 TB/s), 8 warps 6752 / 3846,
+// 24 warps 6159 / 3586; dealt in turns 7483 / 3974, 8 warps 6684 / 3664.  The
+// plain form of the 32-bit update (8 elements a thread, 32-byte loads, 1024
+// threads on an SM) 6605 to 6740.
 // ----------------------------------------------------------------------------
-constexpr int kWarps = 8;
-constexpr int kRingThreads = 32 * (kWarps + 1);
-
 template <int S>
 struct Ring {
     uint64_t full[S], empty[S];
@@ -357,12 +396,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int S>
+template <int W, int S>
 __device__ __forceinline__ void ring_init(Ring<S>& ring) {
     if (threadIdx.x == 0) {
         for (int k = 0; k < S; ++k) {
             mbar_init(&ring.full[k], 33);  // the fetching warp's lanes' copies, and the bulk copies' bytes
-            mbar_init(&ring.empty[k], kWarps);
+            mbar_init(&ring.empty[k], W);
         }
         fence_mbar_init();
     }
@@ -371,19 +410,18 @@ __device__ __forceinline__ void ring_init(Ring<S>& ring) {
 
 // The fetching warp.  Its k-th tile goes into stage k % S: the row by way of
 // the lanes, then issue(tile, stage, full) by all lanes, which copies what can
-// be copied and arrives at `full` 33 times.  Chunks have PARTS tiles.  The
-// first S tiles of a CTA are its own; the others are dealt one by one by a
+// be copied and arrives at `full` 33 times.  The first S tiles of a CTA are its own; the others are dealt one by one by a
 // counter, so that all CTAs work next to each other in memory however long the
 // list is (dealt in turns they drift apart, and the memory's rate with them).
 // ready(), which all warps call once, says after the first copies whether the
 // tiles are wanted.  The CTA that ends last puts the counter back and calls
 // last(); every CTA is past ready() then.
-template <int S, int PARTS, class Stage, class Issue, class Ready, class Last>
+template <int S, class Stage, class Issue, class Ready, class Last>
 __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, Stage* stage, Ring<S>& ring, Issue issue,
                                            Ready ready, Last last) {
     const int lane = threadIdx.x & 31;
-    const uint32_t n = t.n_chunks * PARTS, own = S * gridDim.x;
-    auto tensor_of = [&](uint32_t c) { return c < n ? t.tensor[c / PARTS] : 0u; };
+    const uint32_t n = t.n_chunks, own = S * gridDim.x;
+    auto tensor_of = [&](uint32_t c) { return c < n ? t.tensor[c] : 0u; };
     auto word_of = [&](uint32_t i) {
         return lane < kRowWords ? reinterpret_cast<const unsigned long long*>(t.rows + i)[lane] : 0ull;
     };
@@ -471,20 +509,20 @@ __device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<
 // ----------------------------------------------------------------------------
 // AdamW, 32-bit states
 // ----------------------------------------------------------------------------
-// A tile is half a chunk; a computing warp takes 256 elements of it, 8
-// consecutive ones per lane.  The 8 begin on the boundaries that the arrays'
-// addresses give (MultiRow::shift), so that a tensor anywhere in a flat buffer
-// is copied but for its ends, which are read by plain loads.
-constexpr int kTile32 = kWarps * 32 * kVec;
+// A computing warp takes 256 elements of a tile, 8 consecutive ones per lane.
+// The 8 begin on the boundaries that the arrays' addresses give
+// (MultiRow::shift), so that a tensor anywhere in a flat buffer is copied but
+// for its ends, which are read by plain loads.
 constexpr int kItem32 = 32 * kVec;
-constexpr int kParts32 = kChunk / kTile32;
+constexpr int kWarps32 = kChunk / kItem32;
+constexpr int kThreads32 = 32 * (kWarps32 + 1);
 
 template <class G>
 struct __align__(128) Stage32 {
-    float p[kTile32];
-    float m[kTile32];
-    float v[kTile32];
-    typename G::T g[kTile32];
+    float p[kChunk];
+    float m[kChunk];
+    float v[kChunk];
+    typename G::T g[kChunk];
     MultiRow row;
     int64_t begin;  // the tile's first element in its tensor (below zero: that many do not exist)
     int32_t lo, hi; // elements of the tile that were copied
@@ -504,22 +542,22 @@ __device__ __forceinline__ void lds8(const float* p, float (&o)[8]) {
 }
 
 template <class G, class O>
-__global__ void __launch_bounds__(kRingThreads, 2) multi_adamw_kernel(const __grid_constant__ MultiArgs a) {
+__global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid_constant__ MultiArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     Smem32<G>& sh = *reinterpret_cast<Smem32<G>*>(smem);
     __shared__ MultiShared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    ring_init(sh.ring);
+    ring_init<kWarps32>(sh.ring);
     grid_wait();
-    if (warp == kWarps) {
-        ring_fetch<Smem32<G>::kStages, kParts32>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage32<G>& x, uint64_t* bar) {
+    if (warp == kWarps32) {
+        ring_fetch<Smem32<G>::kStages>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage32<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
-            const int64_t w0 = (int64_t)(tile / kParts32 - r.first_chunk) * kChunk - r.shift + (tile % kParts32) * kTile32;
+            const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk - r.shift;
             constexpr uint32_t kAll = kVecGrad | kVecMaster | kVecStates | kVecOut;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
             const int lo = w0 < 0 ? kItem32 : 0;
-            int hi = left < kItem32 ? 0 : (int)min(left, (int64_t)kTile32) / kItem32 * kItem32;
+            int hi = left < kItem32 ? 0 : (int)min(left, (int64_t)kChunk) / kItem32 * kItem32;
             if ((r.vec & kAll) != kAll || hi < lo) hi = lo;
             copies_arrive(bar);
             if (lane == 0) {
@@ -582,30 +620,40 @@ __global__ void __launch_bounds__(kRingThreads, 2) multi_adamw_kernel(const __gr
 // ----------------------------------------------------------------------------
 // AdamW, 8-bit states
 // ----------------------------------------------------------------------------
-// A tile is a chunk; a computing warp takes 512 elements of it, 16 consecutive
-// ones per lane (a block of 32 is two lanes).  What is not 512 whole elements
-// at a tensor's end, or not aligned, is read by plain loads instead.
+// A computing warp takes 512 elements of a tile, 16 consecutive ones per lane (a
+// block of 32 is two lanes).  The blocks begin where the tensor does, so
+// parameters and gradients that are not on a 16-byte boundary cannot be moved
+// onto one by a shift of the work, as in the 32-bit update: they are copied
+// from the boundary before, taken over by as many elements, and the results
+// turned round in shared memory so that neighbouring lanes store neighbouring
+// elements (GB300, 230e6 elements at odd offsets: see below).  What is not 512
+// whole elements at a tensor's ends is read by plain loads.
 constexpr int kLane8 = 16;
 constexpr int kItem8 = 32 * kLane8;
-static_assert(kChunk == kWarps * kItem8 && kChunk / kBlock8 <= 128, "a fetching lane copies 4 scale bytes of a tile");
+constexpr int kWarps8 = kChunk / kItem8;
+constexpr int kThreads8 = 32 * (kWarps8 + 1);
+static_assert(kChunk / kBlock8 <= 128, "a fetching lane copies 4 scale bytes of a tile");
 
 template <class G>
 struct __align__(128) Stage8 {
-    float p[kChunk];
-    typename G::T g[kChunk];
+    static constexpr int kPad = 16 / sizeof(typename G::T);
+    float p[kChunk + 4];           // element e at e + over_p
+    typename G::T g[kChunk + kPad];
     uint8_t m[kChunk];
     uint8_t v[kChunk];
     uint8_t ms[kChunk / kBlock8];
     uint8_t vs[kChunk / kBlock8];
     MultiRow row;
     int64_t begin;  // the tile's first element in its tensor
-    int64_t whole;  // elements from there on that were copied
+    int32_t lo, hi; // elements of the tile that were copied
+    int32_t over_p, over_g;
     bool end;       // no tile: the list's end
 };
 template <class G>
 struct Smem8 {
     static constexpr int kStages = 2;
     Stage8<G> stage[kStages];
+    float turn[kWarps8][kItem8];
     Ring<kStages> ring;
 };
 
@@ -726,34 +774,51 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 template <class G, class O>
-__global__ void __launch_bounds__(kRingThreads, 2) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
+__global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     Smem8<G>& sh = *reinterpret_cast<Smem8<G>*>(smem);
     __shared__ MultiShared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    ring_init(sh.ring);
+    ring_init<kWarps8>(sh.ring);
     grid_wait();
-    if (warp == kWarps) {
-        ring_fetch<Smem8<G>::kStages, 1>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage8<G>& x, uint64_t* bar) {
+    if (warp == kWarps8) {
+        ring_fetch<Smem8<G>::kStages>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage8<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
             const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
-            const int n = !(r.vec & kWhole8) || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
+            const typename G::T* const g = static_cast<const typename G::T*>(r.grad) + w0;
+            const float* const p = r.master + w0;
+            constexpr int kPad = Stage8<G>::kPad;
+            const int over_p = (int)(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(float));
+            const int over_g = (int)(reinterpret_cast<uintptr_t>(g) % 16 / sizeof(typename G::T));
+            // the copies begin on the boundary before and end on the one
+            // behind, inside the tensor
+            const int lo = w0 == 0 && (over_p | over_g) ? kItem8 : 0;
+            const int more_p = over_p ? 4 - over_p : 0, more_g = over_g ? kPad - over_g : 0;
+            left = min(left - max(more_p, more_g), (int64_t)kChunk);
+            int hi = left < kItem8 || !(r.vec & kCodes) ? 0 : (int)left / kItem8 * kItem8;
+            if (hi < lo) hi = lo;
+            const int n = hi - lo;
             if (lane * 4 < n / kBlock8) {
-                copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4);
-                copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4);
+                const int q = lo / kBlock8 + lane * 4;
+                copy4_async(&x.ms[q], r.ms + w0 / kBlock8 + q);
+                copy4_async(&x.vs[q], r.vs + w0 / kBlock8 + q);
             }
             copies_arrive(bar);
             if (lane == 0) {
                 x.begin = w0;
-                x.whole = n;
-                mbar_arrive_expect_tx(bar, (uint32_t)n * (sizeof(float) + sizeof(typename G::T) + 2));
+                x.lo = lo;
+                x.hi = hi;
+                x.over_p = over_p;
+                x.over_g = over_g;
+                const uint32_t bytes_p = (n + over_p + more_p) * sizeof(float), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
+                mbar_arrive_expect_tx(bar, n > 0 ? bytes_p + bytes_g + 2 * n : 0);
                 if (n > 0) {
-                    bulk_g2s(x.p, r.master + w0, n * sizeof(float), bar);
-                    bulk_g2s(x.g, static_cast<const typename G::T*>(r.grad) + w0, n * sizeof(typename G::T), bar);
-                    bulk_g2s(x.m, r.m8 + w0, n, bar);
-                    bulk_g2s(x.v, r.v8 + w0, n, bar);
+                    bulk_g2s(x.p + lo, p + lo - over_p, bytes_p, bar);
+                    bulk_g2s(x.g + lo, g + lo - over_g, bytes_g, bar);
+                    bulk_g2s(x.m + lo, r.m8 + w0 + lo, n, bar);
+                    bulk_g2s(x.v + lo, r.v8 + w0 + lo, n, bar);
                 }
             }
         }, [&]() { return multi_constants(a, s); }, [&]() {
@@ -767,10 +832,10 @@ __global__ void __launch_bounds__(kRingThreads, 2) multi_adamw8_kernel(const __g
     ring_compute<Smem8<G>::kStages>(&a.st->error, sh.stage, sh.ring, [&](Stage8<G>& x) {
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kLane8;  // place in the tile
-        const bool fast = (warp + 1) * kItem8 <= x.whole;
+        const bool copied = warp * kItem8 >= x.lo && (warp + 1) * kItem8 <= x.hi;
         const int64_t w0 = x.begin + warp * kItem8, i = x.begin + at;
         int some = kItem8;  // elements of the item, and of the lane
-        if (!fast) {
+        if (!copied) {
             const int64_t left = r.numel - w0;
             some = left >= kItem8 ? kItem8 : (left > 0 ? (int)left : 0);
             const uint64_t lim = (uint64_t)r.numel > a.t.slack ? (uint64_t)r.numel - a.t.slack : 0;
@@ -780,28 +845,12 @@ __global__ void __launch_bounds__(kRingThreads, 2) multi_adamw8_kernel(const __g
         if (some > 0) {
             const int64_t blk = i / kBlock8;
             const Const8 c = s.c8[r.group];
+            const bool over = (x.over_p | x.over_g) != 0, wide = copied && (r.vec & kWhole8), turned = copied && !wide;
             float m[16], v[16];
-            if (fast) {
+            if (copied) {
                 decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
                 decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
             } else {
-                // neighbouring lanes read neighbouring elements, whatever the
-                // alignment; their places in the stage turn them round
-                const typename G::T* const g = static_cast<const typename G::T*>(r.grad) + w0;
-                const float* const p = r.master + w0;
-                float tp[kLane8];
-                typename G::T tg[kLane8];
-#pragma unroll
-                for (int j = 0; j < kLane8; ++j) {
-                    const int e = 32 * j + lane;
-                    tp[j] = e < some ? p[e] : 0.0f;
-                    tg[j] = e < some ? g[e] : typename G::T(0);
-                }
-#pragma unroll
-                for (int j = 0; j < kLane8; ++j) {
-                    x.p[warp * kItem8 + 32 * j + lane] = tp[j];
-                    x.g[warp * kItem8 + 32 * j + lane] = tg[j];
-                }
                 float sm = 0.0f, sv = 0.0f;
                 if (nv > 0) {
                     sm = scale_of(r.ms[blk]);
@@ -809,14 +858,21 @@ __global__ void __launch_bounds__(kRingThreads, 2) multi_adamw8_kernel(const __g
                 }
                 decode16<E4m3>(load_codes16(r.m8 + i, nv, r.vec & kCodes), sm, m);
                 decode16<E5m2>(load_codes16(r.v8 + i, nv, r.vec & kCodes), sv, v);
-                __syncwarp();
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int o = 8 * h;
                 float g[8], p[8];
-                G::load8(&x.g[at + o], g);
-                lds8(&x.p[at + o], p);
+                if (!copied) {
+                    load_grad<G>(r.grad, i + o, 0, nv - o, false, g);
+                    load_f32(r.master + i + o, 0, nv - o, false, p);
+                } else if (over) {
+                    G::load8_over(&x.g[at + o], x.over_g, g);
+                    lds8_over(&x.p[at + o], x.over_p, p);
+                } else {
+                    G::load8(&x.g[at + o], g);
+                    lds8(&x.p[at + o], p);
+                }
                 if (two) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
@@ -829,37 +885,36 @@ __global__ void __launch_bounds__(kRingThreads, 2) multi_adamw8_kernel(const __g
                     const float den = __fmaf_rn(sqrt_approx(v[o + e]), c.isb, c.eps);
                     p[e] = __fmaf_rn(-c.step_size, __fmul_rn(m[o + e], rcp_approx(den)), __fmul_rn(p[e], c.decay));
                 }
-                if (fast) {
+                if (wide) {
                     st8(r.master + i + o, p);
                     if constexpr (O::kOut) st_stream(r.out + i + o, pack8<O>(p));
+                } else if (turned) {
+                    float4* const t = reinterpret_cast<float4*>(&sh.turn[warp][lane * kLane8 + o]);
+                    t[0] = make_float4(p[0], p[1], p[2], p[3]);
+                    t[1] = make_float4(p[4], p[5], p[6], p[7]);
                 } else {
-                    *reinterpret_cast<float4*>(&x.p[at + o]) = make_float4(p[0], p[1], p[2], p[3]);
-                    *reinterpret_cast<float4*>(&x.p[at + o + 4]) = make_float4(p[4], p[5], p[6], p[7]);
+                    store_f32(r.master + i + o, 0, nv - o, false, p);
+                    if constexpr (O::kOut) store_out<O>(r.out + i + o, 0, nv - o, false, p);
                 }
+            }
+            if (turned) {
+                __syncwarp();
+                float q[kLane8];
+#pragma unroll
+                for (int j = 0; j < kLane8; ++j) q[j] = sh.turn[warp][32 * j + lane];
+#pragma unroll
+                for (int j = 0; j < kLane8; ++j) {
+                    const int64_t e = w0 + 32 * j + lane;
+                    r.master[e] = q[j];
+                    if constexpr (O::kOut) r.out[e] = O::enc1(q[j]);
+                }
+                __syncwarp();
             }
             const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
             uint4 cm, cv;
             encode16(m, v, bm, bv, mix32(s.key + r.tensor), (uint32_t)(i >> 3), cm, cv);
-            if (fast) {
-                __stcs(reinterpret_cast<uint4*>(r.m8 + i), cm);
-                __stcs(reinterpret_cast<uint4*>(r.v8 + i), cv);
-            } else {
-                store_codes16(r.m8 + i, nv, r.vec & kCodes, cm);
-                store_codes16(r.v8 + i, nv, r.vec & kCodes, cv);
-                __syncwarp();
-                float tp[kLane8];
-#pragma unroll
-                for (int j = 0; j < kLane8; ++j) tp[j] = x.p[warp * kItem8 + 32 * j + lane];
-#pragma unroll
-                for (int j = 0; j < kLane8; ++j) {
-                    const int e = 32 * j + lane;
-                    if (e < some) {
-                        r.master[w0 + e] = tp[j];
-                        if constexpr (O::kOut) r.out[w0 + e] = O::enc1(tp[j]);
-                    }
-                }
-                fence_proxy_async_smem();  // bulk copies into the same places come later
-            }
+            store_codes16(r.m8 + i, nv, r.vec & kCodes, cm);
+            store_codes16(r.v8 + i, nv, r.vec & kCodes, cv);
             if ((lane & 1) == 0 && nv > 0) {
                 r.ms[blk] = (uint8_t)bm;
                 r.vs[blk] = (uint8_t)bv;
@@ -892,7 +947,7 @@ __device__ __forceinline__ uint4 nearest16(const float (&x)[16], uint32_t byte) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A tile is a chunk, 16 consecutive elements a lane, as in the 8-bit update.
+// Tiles and lanes as in the 8-bit update.
 struct __align__(128) StageEncode {
     float m[kChunk];
     float v[kChunk];
@@ -917,17 +972,17 @@ struct SmemCodec {
 };
 
 template <bool ENCODE>
-__global__ void __launch_bounds__(kRingThreads, 2) multi_codec_kernel(const __grid_constant__ MultiTable t) {
+__global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_constant__ MultiTable t) {
     using Stage = std::conditional_t<ENCODE, StageEncode, StageDecode>;
     using Smem = SmemCodec<Stage>;
     extern __shared__ __align__(128) unsigned char smem[];
     Smem& sh = *reinterpret_cast<Smem*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t* const error = reinterpret_cast<int32_t*>(&t.counters[3]);
-    ring_init(sh.ring);
+    ring_init<kWarps8>(sh.ring);
     grid_wait();
-    if (warp == kWarps) {
-        ring_fetch<Smem::kStages, 1>(t, error, sh.stage, sh.ring, [&](uint32_t tile, Stage& x, uint64_t* bar) {
+    if (warp == kWarps8) {
+        ring_fetch<Smem::kStages>(t, error, sh.stage, sh.ring, [&](uint32_t tile, Stage& x, uint64_t* bar) {
             const MultiRow& r = x.row;
             const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk;
             int64_t left = r.numel - w0;
@@ -1261,11 +1316,11 @@ template <class G, class O>
 zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
     const char* what = eight ? "zero_multi_adamw8" : "zero_multi_adamw";
     const size_t smem = eight ? sizeof(zk::Smem8<G>) : sizeof(zk::Smem32<G>);
-    const int64_t tiles = eight ? a.t.n_chunks : (int64_t)a.t.n_chunks * zk::kParts32;
+    const int threads = eight ? zk::kThreads8 : zk::kThreads32;
     void (*kern)(zk::MultiArgs) = eight ? zk::multi_adamw8_kernel<G, O> : zk::multi_adamw_kernel<G, O>;
     const zero_status_t rc = allow_smem(kern, smem, what);
     if (rc != ZERO_OK) return rc;
-    return launch_early(kern, persistent_grid(kern, tiles, smem, zk::kRingThreads), zk::kRingThreads, smem, s, what, a);
+    return launch_early(kern, persistent_grid(kern, a.t.n_chunks, smem, threads), threads, smem, s, what, a);
 }
 
 template <class G>
@@ -1308,7 +1363,7 @@ zero_status_t codec(const zero_multi* M, zero_stream_t stream, bool encode, cons
     void (*kern)(zk::MultiTable) = encode ? zk::multi_codec_kernel<true> : zk::multi_codec_kernel<false>;
     const size_t smem = encode ? sizeof(zk::SmemCodec<zk::StageEncode>) : sizeof(zk::SmemCodec<zk::StageDecode>);
     if ((rc = allow_smem(kern, smem, what)) != ZERO_OK) return rc;
-    return launch_early(kern, persistent_grid(kern, t.n_chunks, smem, zk::kRingThreads), zk::kRingThreads, smem,
+    return launch_early(kern, persistent_grid(kern, t.n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
                         reinterpret_cast<cudaStream_t>(stream), what, t);
 }
 
