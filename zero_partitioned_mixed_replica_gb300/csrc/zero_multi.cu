@@ -50,7 +50,8 @@ static_assert(kRowWords == 12 && kRowWords <= 32, "a warp reads a row");
 
 // The device workspace: counters, rows, chunk map, norm partials.
 struct MultiTable {
-    uint32_t* counters;      // CTAs that are done: [0] norm, [1] others; [2] tiles dealt; [3] errors of the codec
+    uint32_t* counters;      // CTAs that are done: [0] norm, [1] others; [2] tiles dealt; [3] errors of the codec;
+                             // [4] CTAs that have read the state
     const MultiRow* rows;
     const uint32_t* tensor;  // tensor of each chunk
     float2* partials;        // kSlices
@@ -73,11 +74,11 @@ struct MultiArgs {
     uint32_t seed;
 };
 
-// The norm and the updates are launched so that they may begin while the
-// kernel before them in the stream ends; what that kernel wrote is read after
-// grid_wait() only.  grid_launch_next() lets the next kernel begin.
+// The kernels are launched so that they may begin while the kernel before them
+// in the stream ends; what that kernel wrote is read after grid_wait() only.
+// The rows and the chunk map are read before it: the first launch after a bind
+// begins after the bind's end.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------
 // Binding
@@ -90,7 +91,7 @@ __global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* 
                                   float* grad_scale) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < n) rows[i] = b.rows[i];
-    if (i < 4 && counters) counters[i] = 0;
+    if (i < 5 && counters) counters[i] = 0;
     if (i == 0 && grad_scale) *grad_scale = 0.0f;
 }
 
@@ -152,7 +153,13 @@ struct GradBf16 {
     using T = uint16_t;
     static __device__ __forceinline__ float one(uint16_t h) { return Bf16::dec1(h); }
     static __device__ __forceinline__ void eight(const uint16_t* p, float (&o)[8]) { unpack8<Bf16>(ld_stream(p), o); }
-    static __device__ __forceinline__ void eight_kept(const uint16_t* p, float (&o)[8]) { unpack8<Bf16>(*reinterpret_cast<const uint4*>(p), o); }
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw raw(const uint16_t* p) {
+        Raw r;
+        asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+        return r;
+    }
+    static __device__ __forceinline__ void values(const Raw& r, float (&o)[8]) { unpack8<Bf16>(r, o); }
     static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
         unpack8<Bf16>(*reinterpret_cast<const uint4*>(p), o);
     }
@@ -164,7 +171,13 @@ struct GradFp16 {
     using T = uint16_t;
     static __device__ __forceinline__ float one(uint16_t h) { return Fp16::dec1(h); }
     static __device__ __forceinline__ void eight(const uint16_t* p, float (&o)[8]) { unpack8<Fp16>(ld_stream(p), o); }
-    static __device__ __forceinline__ void eight_kept(const uint16_t* p, float (&o)[8]) { unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o); }
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw raw(const uint16_t* p) {
+        Raw r;
+        asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+        return r;
+    }
+    static __device__ __forceinline__ void values(const Raw& r, float (&o)[8]) { unpack8<Fp16>(r, o); }
     static __device__ __forceinline__ void load8(const uint16_t* p, float (&o)[8]) {
         unpack8<Fp16>(*reinterpret_cast<const uint4*>(p), o);
     }
@@ -176,10 +189,19 @@ struct GradFp32 {
     using T = float;
     static __device__ __forceinline__ float one(float x) { return x; }
     static __device__ __forceinline__ void eight(const float* p, float (&o)[8]) { ld8(p, o); }
-    static __device__ __forceinline__ void eight_kept(const float* p, float (&o)[8]) {
+    struct Raw {
+        float x[8];
+    };
+    static __device__ __forceinline__ Raw raw(const float* p) {
+        Raw r;
         asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                     : "=f"(r.x[0]), "=f"(r.x[1]), "=f"(r.x[2]), "=f"(r.x[3]), "=f"(r.x[4]), "=f"(r.x[5]), "=f"(r.x[6]), "=f"(r.x[7])
                      : "l"(p));
+        return r;
+    }
+    static __device__ __forceinline__ void values(const Raw& r, float (&o)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = r.x[e];
     }
     static __device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
         const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -315,6 +337,21 @@ struct MultiShared {
     int32_t apply;
 };
 
+// ZERO_MULTI_ADVANCE: moves the step on once every CTA has read the state
+// (one thread of each calls it, after that).
+__device__ __forceinline__ void advance_step(const MultiArgs& a) {
+    if (!(a.flags & ZERO_MULTI_ADVANCE)) return;
+    __threadfence();
+    if (atomicInc(&a.t.counters[4], gridDim.x - 1) != gridDim.x - 1) return;
+    zero_step_state* st = a.st;
+    st->clip_coef = 1.0f;
+    st->apply = 1;
+    st->t += 1;
+    st->beta1_pow = __dmul_rn(st->beta1_pow, st->beta1);
+    st->beta2_pow = __dmul_rn(st->beta2_pow, st->beta2);
+    st->good_steps += 1;
+}
+
 // All threads of the CTA call it; false: the step is skipped.  Four threads a
 // group: binary64 divisions and square roots are slow here, and a short step
 // waits for them.
@@ -356,15 +393,6 @@ __device__ __forceinline__ bool multi_constants(const MultiArgs& a, MultiShared&
     }
     __syncthreads();
     return s.apply != 0;
-}
-
-__device__ __forceinline__ void advance_step(zero_step_state* st) {
-    st->clip_coef = 1.0f;
-    st->apply = 1;
-    st->t += 1;
-    st->beta1_pow = __dmul_rn(st->beta1_pow, st->beta1);
-    st->beta2_pow = __dmul_rn(st->beta2_pow, st->beta2);
-    st->good_steps += 1;
 }
 
 // ----------------------------------------------------------------------------
@@ -412,13 +440,12 @@ __device__ __forceinline__ void ring_init(Ring<S>& ring) {
 // the lanes, then issue(tile, stage, full) by all lanes, which copies what can
 // be copied and arrives at `full` 33 times.  The first S tiles of a CTA are its own; the others are dealt one by one by a
 // counter, so that all CTAs work next to each other in memory however long the
-// list is (dealt in turns they drift apart, and the memory's rate with them).
-// ready(), which all warps call once, says after the first copies whether the
-// tiles are wanted.  The CTA that ends last puts the counter back and calls
-// last(); every CTA is past ready() then.
-template <int S, class Stage, class Issue, class Ready, class Last>
+// list is (dealt in turns they drift apart, and the memory's rate with them);
+// the CTA that ends last puts the counter back.  ready(), which all warps call
+// once, says after the first copies whether the tiles are wanted.
+template <int S, class Stage, class Issue, class Ready>
 __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, Stage* stage, Ring<S>& ring, Issue issue,
-                                           Ready ready, Last last) {
+                                           Ready ready) {
     const int lane = threadIdx.x & 31;
     const uint32_t n = t.n_chunks, own = S * gridDim.x;
     auto tensor_of = [&](uint32_t c) { return c < n ? t.tensor[c] : 0u; };
@@ -444,6 +471,7 @@ __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, 
     for (int j = 0; j < S; ++j) tensor[j] = tensor_of(blockIdx.x + j * gridDim.x);
 #pragma unroll
     for (int j = 0; j < S; ++j) word[j] = word_of(tensor[j]);
+    grid_wait();
     uint32_t k = 0;  // tiles put
     bool end = false;
 #pragma unroll
@@ -453,9 +481,14 @@ __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, 
             put(k++, tile, word[j]);
             end = tile >= n;
         }
+    const bool dealt = n > own;  // a short list is all the CTAs' own: no counter
     if (ready() && !end) {
         // three tiles ahead of the copies: the counter, the tensor, the row
-        uint32_t first = __shfl_sync(0xFFFFFFFFu, deal(), 0), second = __shfl_sync(0xFFFFFFFFu, deal(), 0), third = deal();
+        uint32_t first = n, second = n, third = n;
+        if (dealt) {
+            first = deal(), second = deal(), third = deal();
+            first = __shfl_sync(0xFFFFFFFFu, first, 0), second = __shfl_sync(0xFFFFFFFFu, second, 0);
+        }
         unsigned long long first_word = word_of(tensor_of(first));
         uint32_t second_tensor = tensor_of(second);
         while (!end) {
@@ -470,7 +503,7 @@ __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, 
             first_word = word_of(second_tensor);
             second = __shfl_sync(0xFFFFFFFFu, third, 0);
             second_tensor = tensor_of(second);
-            third = second < n ? deal() : second;
+            third = second < n ? deal() : n;
         }
     }
     // the last copies land before the CTA gives up its shared memory (they
@@ -481,12 +514,9 @@ __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, 
             landed = mbar_wait_bounded(&ring.full[j % S], (j / S) & 1u);
         if (!landed) atomicOr(error, ZERO_DEVERR_DRAIN_TIMEOUT);
     }
-    if (lane == 0) {
+    if (lane == 0 && dealt) {
         __threadfence();
-        if (atomicInc(&t.counters[1], gridDim.x - 1) == gridDim.x - 1) {
-            t.counters[2] = 0;
-            last();
-        }
+        if (atomicInc(&t.counters[1], gridDim.x - 1) == gridDim.x - 1) t.counters[2] = 0;
     }
 }
 
@@ -548,7 +578,6 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
     __shared__ MultiShared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ring_init<kWarps32>(sh.ring);
-    grid_wait();
     if (warp == kWarps32) {
         ring_fetch<Smem32<G>::kStages>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage32<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
@@ -573,11 +602,14 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
                     bulk_g2s(x.g + lo, static_cast<const typename G::T*>(r.grad) + w0 + lo, n * sizeof(typename G::T), bar);
                 }
             }
-        }, [&]() { return multi_constants(a, s); }, [&]() {
-            if (a.flags & ZERO_MULTI_ADVANCE) advance_step(a.st);
+        }, [&]() {
+            const bool apply = multi_constants(a, s);
+            if (lane == 0) advance_step(a);
+            return apply;
         });
         return;
     }
+    grid_wait();
     if (!multi_constants(a, s)) return;
     const float unscale = s.unscale;
     ring_compute<Smem32<G>::kStages>(&a.st->error, sh.stage, sh.ring, [&](Stage32<G>& x) {
@@ -780,7 +812,6 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
     __shared__ MultiShared s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ring_init<kWarps8>(sh.ring);
-    grid_wait();
     if (warp == kWarps8) {
         ring_fetch<Smem8<G>::kStages>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage8<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
@@ -821,11 +852,14 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
                     bulk_g2s(x.v + lo, r.v8 + w0 + lo, n, bar);
                 }
             }
-        }, [&]() { return multi_constants(a, s); }, [&]() {
-            if (a.flags & ZERO_MULTI_ADVANCE) advance_step(a.st);
+        }, [&]() {
+            const bool apply = multi_constants(a, s);
+            if (lane == 0) advance_step(a);
+            return apply;
         });
         return;
     }
+    grid_wait();
     if (!multi_constants(a, s)) return;
     const float factor = s.factor, unscale = s.unscale;
     const bool two = s.two != 0;
@@ -980,7 +1014,6 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t* const error = reinterpret_cast<int32_t*>(&t.counters[3]);
     ring_init<kWarps8>(sh.ring);
-    grid_wait();
     if (warp == kWarps8) {
         ring_fetch<Smem::kStages>(t, error, sh.stage, sh.ring, [&](uint32_t tile, Stage& x, uint64_t* bar) {
             const MultiRow& r = x.row;
@@ -1009,9 +1042,10 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
                     }
                 }
             }
-        }, []() { return true; }, []() {});
+        }, []() { return true; });
         return;
     }
+    grid_wait();
     ring_compute<Smem::kStages>(error, sh.stage, sh.ring, [&](Stage& x) {
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kLane8;
@@ -1070,22 +1104,21 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
 // ----------------------------------------------------------------------------
 // Global norm and step decision
 // ----------------------------------------------------------------------------
-// The step decision (one thread), as zero_grad_norm makes it: skip on overflow,
-// else the clip coefficient, the step counter and beta^t; the loss-scale
-// schedule.
-__device__ __forceinline__ void decide_step(zero_step_state* st, bool bad, double norm, double max_norm) {
+// The step decision, as zero_grad_norm makes it: skip on overflow, else the clip
+// coefficient, the step counter and beta^t; the loss-scale schedule.  Two
+// threads: the clip coefficient, and what does not depend on the norm's value.
+__device__ __forceinline__ float clip_of(bool bad, double norm, double max_norm) {
+    if (bad || !(max_norm > 0.0)) return 1.0f;
+    return __double2float_rn(fmin(1.0, __ddiv_rn(max_norm, __dadd_rn(norm, 1e-6))));
+}
+__device__ __forceinline__ void decide_step(zero_step_state* st, bool bad) {
+    st->apply = bad ? 0 : 1;
     if (bad) {
-        st->apply = 0;
-        st->clip_coef = 1.0f;
         st->skipped += 1;
         st->good_steps = 0;
         if (st->dynamic_scale) st->loss_scale = fmaxf(1.0f, __fmul_rn(st->loss_scale, 0.5f));
         return;
     }
-    float clip = 1.0f;
-    if (max_norm > 0.0) clip = __double2float_rn(fmin(1.0, __ddiv_rn(max_norm, __dadd_rn(norm, 1e-6))));
-    st->clip_coef = clip;
-    st->apply = 1;
     st->t += 1;
     st->beta1_pow = __dmul_rn(st->beta1_pow, st->beta1);
     st->beta2_pow = __dmul_rn(st->beta2_pow, st->beta2);
@@ -1113,7 +1146,7 @@ __device__ __forceinline__ float2 sum_pairs(float hi, float lo, float2* sh) {
 }
 
 template <class G>
-__global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_constant__ MultiTable t, double max_norm,
+__global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_constant__ MultiTable t, double max_norm,
                                                               zero_step_state* st, uint32_t n_slices) {
     __shared__ float2 sh[kThreads / 32];
     __shared__ bool last;
@@ -1141,8 +1174,9 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
                 hi = sum;
                 lo = __fadd_rn(lo, err);
             };
-            // kUnroll loads in flight per thread
-            constexpr int kUnroll = 4, kStep = kThreads * kVec;
+            // kUnroll loads in flight per thread; they may stay in the cache for
+            // the update
+            constexpr int kUnroll = 64 / sizeof(typename G::Raw), kStep = kThreads * kVec;
             int64_t i = begin + threadIdx.x * kVec;
             auto one = [&]() {
                 int e0, e1;
@@ -1157,12 +1191,15 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
             if (vec)
                 for (; i + (kUnroll - 1) * kStep + kVec <= end; i += kUnroll * kStep) {
                     if (!in_bounds((uint64_t)i + (kUnroll - 1) * kStep + kVec, lim)) break;
-                    float g[kUnroll][8];
+                    typename G::Raw q[kUnroll];
 #pragma unroll
-                    for (int u = 0; u < kUnroll; ++u)
-                        G::eight_kept(static_cast<const typename G::T*>(r.grad) + i + u * kStep, g[u]);
+                    for (int u = 0; u < kUnroll; ++u) q[u] = G::raw(static_cast<const typename G::T*>(r.grad) + i + u * kStep);
 #pragma unroll
-                    for (int u = 0; u < kUnroll; ++u) add(g[u]);
+                    for (int u = 0; u < kUnroll; ++u) {
+                        float g[8];
+                        G::values(q[u], g);
+                        add(g);
+                    }
                 }
             while (i < end) one();
             c += take;
@@ -1170,7 +1207,6 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
         const float2 sum = sum_pairs(hi, lo, sh);
         if (threadIdx.x == 0) t.partials[sl] = sum;
     }
-    grid_launch_next();
     if (threadIdx.x == 0) {
         __threadfence();
         last = atomicInc(&t.counters[0], gridDim.x - 1) == gridDim.x - 1;
@@ -1186,17 +1222,23 @@ __global__ void __launch_bounds__(kThreads) multi_norm_kernel(const __grid_const
         hi = sum;
         lo = __fadd_rn(lo, __fadd_rn(err, q.y));
     }
+    const float scale = st->loss_scale;  // before the decision changes it
     const float2 both = sum_pairs(hi, lo, sh);
-    if (threadIdx.x != 0) return;
-    const double total = __dadd_rn((double)both.x, (double)both.y);
+    if (threadIdx.x == 0) sh[0] = both;
+    __syncthreads();
+    if (threadIdx.x != 0 && threadIdx.x != 32) return;
+    const double total = __dadd_rn((double)sh[0].x, (double)sh[0].y);
     const bool bad = !isfinite(total);  // an inf or NaN gradient, or a square beyond binary32
-    const float scale = st->loss_scale;
+    if (threadIdx.x == 32) {
+        st->nonfinite = 0;
+        st->overflow = bad;
+        *t.grad_scale = scale;
+        decide_step(st, bad);
+        return;
+    }
     const double norm = bad ? (double)INFINITY : __ddiv_rn(__dsqrt_rn(total), (double)scale);
-    st->nonfinite = 0;
-    st->overflow = bad;
     st->grad_norm = norm;
-    *t.grad_scale = scale;
-    decide_step(st, bad, norm, max_norm);
+    st->clip_coef = clip_of(bad, norm, max_norm);
 }
 
 }  // namespace zk
@@ -1212,6 +1254,7 @@ struct zero_multi {
     int64_t n_chunks = 0;
     bool bound = false, grads = false, master = false, states32 = false, states8 = false, param16 = false;
     char* workspace = nullptr;
+    mutable std::atomic<bool> fresh{false};  // bound, and no kernel launched on it yet
 };
 
 namespace {
@@ -1239,7 +1282,7 @@ zk::MultiTable table_of(const zero_multi* M) {
     const Places p = places(M);
     zk::MultiTable t{};
     t.counters = reinterpret_cast<uint32_t*>(M->workspace);
-    t.grad_scale = reinterpret_cast<float*>(M->workspace) + 8;
+    t.grad_scale = reinterpret_cast<float*>(M->workspace + 128);
     t.rows = reinterpret_cast<const zk::MultiRow*>(M->workspace + p.rows);
     t.tensor = reinterpret_cast<const uint32_t*>(M->workspace + p.map);
     t.partials = reinterpret_cast<float2*>(M->workspace + p.partials);
@@ -1291,9 +1334,10 @@ zero_status_t allow_smem(Kernel kern, size_t bytes, const char* what) {
     return ZERO_OK;
 }
 
-// A launch that may begin while the stream's last kernel ends (grid_wait).
+// A launch that may begin while the stream's last kernel ends (grid_wait), but
+// for the first after a bind, whose tables it reads before it waits.
 template <class... P, class... A>
-zero_status_t launch_early(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, const char* what, A... args) {
+zero_status_t launch_early(const zero_multi* M, void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, const char* what, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
@@ -1303,7 +1347,7 @@ zero_status_t launch_early(void (*kern)(P...), int grid, int threads, size_t sme
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = M->fresh.exchange(false) ? 0 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1312,22 +1356,29 @@ zero_status_t launch_early(void (*kern)(P...), int grid, int threads, size_t sme
     return after_launch(what);
 }
 
+// CTAs of a kernel on a ring of tiles: 16 computing warps on an SM.
+template <class Kernel>
+int ring_grid(Kernel kern, int64_t tiles, size_t smem, int threads) {
+    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
+    return persistent_grid(kern, std::min<int64_t>(tiles, sms * (16 / (threads / 32 - 1))), smem, threads);
+}
+
 template <class G, class O>
-zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
+zero_status_t launch_update(const zero_multi* M, bool eight, const zk::MultiArgs& a, cudaStream_t s) {
     const char* what = eight ? "zero_multi_adamw8" : "zero_multi_adamw";
     const size_t smem = eight ? sizeof(zk::Smem8<G>) : sizeof(zk::Smem32<G>);
     const int threads = eight ? zk::kThreads8 : zk::kThreads32;
     void (*kern)(zk::MultiArgs) = eight ? zk::multi_adamw8_kernel<G, O> : zk::multi_adamw_kernel<G, O>;
     const zero_status_t rc = allow_smem(kern, smem, what);
     if (rc != ZERO_OK) return rc;
-    return launch_early(kern, persistent_grid(kern, a.t.n_chunks, smem, threads), threads, smem, s, what, a);
+    return launch_early(M, kern, ring_grid(kern, a.t.n_chunks, smem, threads), threads, smem, s, what, a);
 }
 
 template <class G>
-zero_status_t launch_update_out(bool eight, int32_t param_dtype, const zk::MultiArgs& a, cudaStream_t s) {
-    if (param_dtype == ZERO_BF16) return launch_update<G, zk::OutBf16>(eight, a, s);
-    if (param_dtype == ZERO_FP16) return launch_update<G, zk::OutFp16>(eight, a, s);
-    return launch_update<G, zk::NoOut>(eight, a, s);
+zero_status_t launch_update_out(const zero_multi* M, bool eight, const zk::MultiArgs& a, cudaStream_t s) {
+    if (M->param_dtype == ZERO_BF16) return launch_update<G, zk::OutBf16>(M, eight, a, s);
+    if (M->param_dtype == ZERO_FP16) return launch_update<G, zk::OutFp16>(M, eight, a, s);
+    return launch_update<G, zk::NoOut>(M, eight, a, s);
 }
 
 zero_status_t update(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags, uint32_t seed, zero_step_state* st,
@@ -1348,9 +1399,9 @@ zero_status_t update(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags
     a.flags = flags;
     a.seed = seed;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (M->grad_dtype == ZERO_BF16) return launch_update_out<zk::GradBf16>(eight, M->param_dtype, a, s);
-    if (M->grad_dtype == ZERO_FP16) return launch_update_out<zk::GradFp16>(eight, M->param_dtype, a, s);
-    return launch_update_out<zk::GradFp32>(eight, M->param_dtype, a, s);
+    if (M->grad_dtype == ZERO_BF16) return launch_update_out<zk::GradBf16>(M, eight, a, s);
+    if (M->grad_dtype == ZERO_FP16) return launch_update_out<zk::GradFp16>(M, eight, a, s);
+    return launch_update_out<zk::GradFp32>(M, eight, a, s);
 }
 
 zero_status_t codec(const zero_multi* M, zero_stream_t stream, bool encode, const char* what) {
@@ -1363,7 +1414,7 @@ zero_status_t codec(const zero_multi* M, zero_stream_t stream, bool encode, cons
     void (*kern)(zk::MultiTable) = encode ? zk::multi_codec_kernel<true> : zk::multi_codec_kernel<false>;
     const size_t smem = encode ? sizeof(zk::SmemCodec<zk::StageEncode>) : sizeof(zk::SmemCodec<zk::StageDecode>);
     if ((rc = allow_smem(kern, smem, what)) != ZERO_OK) return rc;
-    return launch_early(kern, persistent_grid(kern, t.n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
+    return launch_early(M, kern, ring_grid(kern, t.n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
                         reinterpret_cast<cudaStream_t>(stream), what, t);
 }
 
@@ -1521,6 +1572,7 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
     M->states8 = x->m8 != nullptr;
     M->param16 = x->param16 != nullptr;
     M->bound = true;
+    M->fresh = true;
     return ZERO_OK;
 }
 
@@ -1537,7 +1589,7 @@ extern "C" zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_no
     const uint32_t slices = std::max<uint32_t>(1, std::min<uint32_t>(t.n_chunks, zk::kSlices));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto kern) {
-        return launch_early(kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st, slices);
+        return launch_early(M, kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st, slices);
     };
     if (M->grad_dtype == ZERO_BF16) return go(zk::multi_norm_kernel<zk::GradBf16>);
     if (M->grad_dtype == ZERO_FP16) return go(zk::multi_norm_kernel<zk::GradFp16>);
