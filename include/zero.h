@@ -685,8 +685,9 @@ zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays* arrays, vo
  * keeps the scale that these gradients carry, since a dynamic one may change
  * here.
  * Deterministic: fixed slices of the list, binary32 sums with their rounding
- * errors carried along, combined in binary64 in a fixed order.  Needs grads.
- * One launch. */
+ * errors carried along, combined in a fixed order (the last bits may differ
+ * between lists whose tensors begin at other distances from a vector
+ * boundary).  Needs grads.  One launch. */
 zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_norm, zero_step_state* st,
                                    zero_stream_t stream);
 

@@ -76,8 +76,7 @@ struct MultiArgs {
 
 // The kernels are launched so that they may begin while the kernel before them
 // in the stream ends; what that kernel wrote is read after grid_wait() only.
-// The rows and the chunk map are read before it: the first launch after a bind
-// begins after the bind's end.
+// The rows and the chunk map are read before it (multi_reset_kernel).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------
@@ -87,12 +86,16 @@ struct RowBatch {
     MultiRow rows[kRowsPerLaunch];
 };
 
-__global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n, uint32_t* counters,
-                                  float* grad_scale) {
+__global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < n) rows[i] = b.rows[i];
-    if (i < 5 && counters) counters[i] = 0;
-    if (i == 0 && grad_scale) *grad_scale = 0.0f;
+}
+
+// The last kernel of a bind: whatever begins while it ends finds the rows and
+// the map whole, since it began after their kernels' end.
+__global__ void multi_reset_kernel(uint32_t* counters, float* grad_scale) {
+    if (threadIdx.x < 5) counters[threadIdx.x] = 0;
+    if (threadIdx.x == 0 && grad_scale) *grad_scale = 0.0f;
 }
 
 // Tensor of every chunk: the last row whose first chunk is not behind it
@@ -538,6 +541,16 @@ __device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<
 
 // ----------------------------------------------------------------------------
 // AdamW, 32-bit states
+//
+//   g = x / scale * clip,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// with one binary32 rounding per operation (adamw1), so that a tensor gets the
+// same bits here as in the flat buffer.  Bound by memory: 14 bytes read and 14
+// written per element with 16-bit gradients and copies.  GB300, 1.56e9
+// elements in 580 tensors: 6.16 ms, 7.1 TB/s (the copy that the roofline is
+// measured with: 6.77).  80K elements in 50 tensors: 4.6 us from a graph, the
+// latency of launch, row, copies, constants and stores one after the other.
 // ----------------------------------------------------------------------------
 // A computing warp takes 256 elements of a tile, 8 consecutive ones per lane.
 // The 8 begin on the boundaries that the arrays' addresses give
@@ -651,6 +664,16 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
 
 // ----------------------------------------------------------------------------
 // AdamW, 8-bit states
+//
+// The same update between decoding and encoding.  16.125 bytes per element, a
+// little over half of the 32-bit form's, leave half of its time for more work,
+// so the work had to shrink: powers of two as scales make scaling exact and
+// need no division, the conversions run in hardware two at a time, stochastic
+// rounding is one integer addition to a value's bits, its random integers one
+// multiplication each, maxima take three inputs, and root and division are
+// approximate.  16 elements a lane halve what is paid per lane and per warp
+// (8 a lane, plain loads: 68 instructions an element and 4694 us at 1.56e9
+// elements; as it is: 3.56 ms, 7.05 TB/s, bound by memory).
 // ----------------------------------------------------------------------------
 // A computing warp takes 512 elements of a tile, 16 consecutive ones per lane (a
 // block of 32 is two lanes).  The blocks begin where the tensor does, so
@@ -658,8 +681,9 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
 // onto one by a shift of the work, as in the 32-bit update: they are copied
 // from the boundary before, taken over by as many elements, and the results
 // turned round in shared memory so that neighbouring lanes store neighbouring
-// elements (GB300, 230e6 elements at odd offsets: see below).  What is not 512
-// whole elements at a tensor's ends is read by plain loads.
+// elements (GB300, 91e6 elements in 150 tensors at odd offsets: 459 us, aligned
+// 408; read by plain loads 588).  What is not 512 whole elements at a tensor's
+// ends is read by plain loads.
 constexpr int kLane8 = 16;
 constexpr int kItem8 = 32 * kLane8;
 constexpr int kWarps8 = kChunk / kItem8;
@@ -958,7 +982,9 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
 }
 
 // ----------------------------------------------------------------------------
-// 32-bit states into the 8-bit form and back
+// 32-bit states into the 8-bit form and back: 10.06 bytes per element, bound by
+// memory.  GB300, 355e6 elements: encode 496 us (7.2 TB/s), decode 511 us (7.0
+// TB/s; 621 with all CTAs that fit on an SM, 690 with two).
 // ----------------------------------------------------------------------------
 // Nearest codes (ties to even) of 16 values.
 template <class Q>
@@ -1103,6 +1129,14 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
 
 // ----------------------------------------------------------------------------
 // Global norm and step decision
+//
+// sum x^2 over the list.  A thread adds the squares of 8 elements with fused
+// multiply-adds and carries the rounding errors of adding those sums up
+// (two_sum); pairs (sum, error) are combined by shuffles and, among the CTAs,
+// by the one that ends last.  The split into kSlices ranges is fixed, so the
+// result does not depend on the grid.  Bound by memory: GB300, 1.56e9 16-bit
+// gradients 433 us (7.2 TB/s read); 30.7e6 of them 16.3 us, of which 9 are the
+// bytes and the rest launch, first loads and the last CTA's sum.
 // ----------------------------------------------------------------------------
 // The step decision, as zero_grad_norm makes it: skip on overflow, else the clip
 // coefficient, the step counter and beta^t; the loss-scale schedule.  Two
@@ -1254,7 +1288,6 @@ struct zero_multi {
     int64_t n_chunks = 0;
     bool bound = false, grads = false, master = false, states32 = false, states8 = false, param16 = false;
     char* workspace = nullptr;
-    mutable std::atomic<bool> fresh{false};  // bound, and no kernel launched on it yet
 };
 
 namespace {
@@ -1334,10 +1367,9 @@ zero_status_t allow_smem(Kernel kern, size_t bytes, const char* what) {
     return ZERO_OK;
 }
 
-// A launch that may begin while the stream's last kernel ends (grid_wait), but
-// for the first after a bind, whose tables it reads before it waits.
+// A launch that may begin while the stream's last kernel ends (grid_wait).
 template <class... P, class... A>
-zero_status_t launch_early(const zero_multi* M, void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, const char* what, A... args) {
+zero_status_t launch_early(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, const char* what, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
@@ -1347,7 +1379,7 @@ zero_status_t launch_early(const zero_multi* M, void (*kern)(P...), int grid, in
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = M->fresh.exchange(false) ? 0 : 1;
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1371,7 +1403,7 @@ zero_status_t launch_update(const zero_multi* M, bool eight, const zk::MultiArgs
     void (*kern)(zk::MultiArgs) = eight ? zk::multi_adamw8_kernel<G, O> : zk::multi_adamw_kernel<G, O>;
     const zero_status_t rc = allow_smem(kern, smem, what);
     if (rc != ZERO_OK) return rc;
-    return launch_early(M, kern, ring_grid(kern, a.t.n_chunks, smem, threads), threads, smem, s, what, a);
+    return launch_early(kern, ring_grid(kern, a.t.n_chunks, smem, threads), threads, smem, s, what, a);
 }
 
 template <class G>
@@ -1414,7 +1446,7 @@ zero_status_t codec(const zero_multi* M, zero_stream_t stream, bool encode, cons
     void (*kern)(zk::MultiTable) = encode ? zk::multi_codec_kernel<true> : zk::multi_codec_kernel<false>;
     const size_t smem = encode ? sizeof(zk::SmemCodec<zk::StageEncode>) : sizeof(zk::SmemCodec<zk::StageDecode>);
     if ((rc = allow_smem(kern, smem, what)) != ZERO_OK) return rc;
-    return launch_early(M, kern, ring_grid(kern, t.n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
+    return launch_early(kern, ring_grid(kern, t.n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
                         reinterpret_cast<cudaStream_t>(stream), what, t);
 }
 
@@ -1557,8 +1589,7 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         zk::RowBatch b{};
         const int k = std::min(zk::kRowsPerLaunch, n - i);
         std::copy(rows.begin() + i, rows.begin() + i + k, b.rows);
-        zk::multi_rows_kernel<<<1, zk::kRowsPerLaunch, 0, s>>>(b, dst + i, k, i == 0 ? t.counters : nullptr,
-                                                                i == 0 && fresh ? t.grad_scale : nullptr);
+        zk::multi_rows_kernel<<<1, zk::kRowsPerLaunch, 0, s>>>(b, dst + i, k);
         if ((rc = after_launch(what)) != ZERO_OK) return rc;
     }
     if (t.n_chunks > 0) {
@@ -1566,13 +1597,14 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         zk::multi_map_kernel<<<ctas, 256, 0, s>>>(t.rows, t.n_tensors, const_cast<uint32_t*>(t.tensor), t.n_chunks);
         if ((rc = after_launch(what)) != ZERO_OK) return rc;
     }
+    zk::multi_reset_kernel<<<1, 32, 0, s>>>(t.counters, fresh ? t.grad_scale : nullptr);
+    if ((rc = after_launch(what)) != ZERO_OK) return rc;
     M->grads = x->grads != nullptr;
     M->master = x->master != nullptr;
     M->states32 = x->m != nullptr;
     M->states8 = x->m8 != nullptr;
     M->param16 = x->param16 != nullptr;
     M->bound = true;
-    M->fresh = true;
     return ZERO_OK;
 }
 
@@ -1589,7 +1621,7 @@ extern "C" zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_no
     const uint32_t slices = std::max<uint32_t>(1, std::min<uint32_t>(t.n_chunks, zk::kSlices));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto kern) {
-        return launch_early(M, kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st, slices);
+        return launch_early(kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st, slices);
     };
     if (M->grad_dtype == ZERO_BF16) return go(zk::multi_norm_kernel<zk::GradBf16>);
     if (M->grad_dtype == ZERO_FP16) return go(zk::multi_norm_kernel<zk::GradFp16>);
