@@ -149,8 +149,8 @@ __device__ __forceinline__ uint4 lds8_over(const uint16_t* p, int over) {
 }
 
 // ----------------------------------------------------------------------------
-// Loads and stores of 8 consecutive elements of which [e0, e1) exist; `vec`:
-// the first is on a boundary for the wide access.
+// Loads and stores of 8 consecutive elements of which [e0, e1) exist (`none` is
+// read for the others); `vec`: the first is on a boundary for the wide access.
 // ----------------------------------------------------------------------------
 struct GradBf16 {
     using T = uint16_t;
@@ -234,21 +234,22 @@ __device__ __forceinline__ bool span8(const MultiTable& t, const MultiRow& r, in
     return in_bounds((uint64_t)(i + e1), lim);
 }
 template <class G>
-__device__ __forceinline__ void load_grad(const void* base, int64_t i, int e0, int e1, bool vec, float (&o)[8]) {
+__device__ __forceinline__ void load_grad(const void* base, int64_t i, int e0, int e1, bool vec, float (&o)[8],
+                                          float none = 0.0f) {
     const typename G::T* p = static_cast<const typename G::T*>(base) + i;
     if (vec && e0 <= 0 && e1 >= 8) {
         G::eight(p, o);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = e >= e0 && e < e1 ? G::one(p[e]) : 0.0f;
+        for (int e = 0; e < 8; ++e) o[e] = e >= e0 && e < e1 ? G::one(p[e]) : none;
     }
 }
-__device__ __forceinline__ void load_f32(const float* p, int e0, int e1, bool vec, float (&o)[8]) {
+__device__ __forceinline__ void load_f32(const float* p, int e0, int e1, bool vec, float (&o)[8], float none = 0.0f) {
     if (vec && e0 <= 0 && e1 >= 8) {
         ld8(p, o);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = e >= e0 && e < e1 ? p[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) o[e] = e >= e0 && e < e1 ? p[e] : none;
     }
 }
 __device__ __forceinline__ void store_f32(float* p, int e0, int e1, bool vec, const float (&o)[8]) {
@@ -555,7 +556,7 @@ __device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<
 // A computing warp takes 256 elements of a tile, 8 consecutive ones per lane.
 // The 8 begin on the boundaries that the arrays' addresses give
 // (MultiRow::shift), so that a tensor anywhere in a flat buffer is copied but
-// for its ends, which are read by plain loads.
+// for its first and last few elements, which are read by plain loads.
 constexpr int kItem32 = 32 * kVec;
 constexpr int kWarps32 = kChunk / kItem32;
 constexpr int kThreads32 = 32 * (kWarps32 + 1);
@@ -598,8 +599,8 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
             constexpr uint32_t kAll = kVecGrad | kVecMaster | kVecStates | kVecOut;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
-            const int lo = w0 < 0 ? kItem32 : 0;
-            int hi = left < kItem32 ? 0 : (int)min(left, (int64_t)kChunk) / kItem32 * kItem32;
+            const int lo = w0 < 0 ? kVec : 0;
+            int hi = left < kVec ? 0 : (int)min(left, (int64_t)kChunk) / kVec * kVec;
             if ((r.vec & kAll) != kAll || hi < lo) hi = lo;
             copies_arrive(bar);
             if (lane == 0) {
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
     ring_compute<Smem32<G>::kStages>(&a.st->error, sh.stage, sh.ring, [&](Stage32<G>& x) {
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kVec;  // place in the tile
-        const bool fast = warp * kItem32 >= x.lo && (warp + 1) * kItem32 <= x.hi;
+        const bool fast = at >= x.lo && at + kVec <= x.hi;
         const int64_t i = x.begin + at;
         int e0 = 0, e1 = kVec;
         if (!fast && !span8(a.t, r, i, e0, e1)) return;
@@ -641,10 +642,12 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
             lds8(&x.m[at], m);
             lds8(&x.v[at], v);
         } else {
-            load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g);
-            load_f32(r.master + i, e0, e1, vec & kVecMaster, p);
-            load_f32(r.m + i, e0, e1, vec & kVecStates, m);
-            load_f32(r.v + i, e0, e1, vec & kVecStates, v);
+            // ones where there is nothing: zeros would take the slow ways of
+            // the division and the root
+            load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g, 1.0f);
+            load_f32(r.master + i, e0, e1, vec & kVecMaster, p, 1.0f);
+            load_f32(r.m + i, e0, e1, vec & kVecStates, m, 1.0f);
+            load_f32(r.v + i, e0, e1, vec & kVecStates, v, 1.0f);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
