@@ -685,8 +685,8 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
 // from the boundary before, taken over by as many elements, and the results
 // turned round in shared memory so that neighbouring lanes store neighbouring
 // elements (GB300, 91e6 elements in 150 tensors at odd offsets: 459 us, aligned
-// 408; read by plain loads 588).  What is not 512 whole elements at a tensor's
-// ends is read by plain loads.
+// 408; read by plain loads 588).  A tensor's last few elements, and its first 16
+// if they are not on a boundary, are read by plain loads.
 constexpr int kLane8 = 16;
 constexpr int kItem8 = 32 * kLane8;
 constexpr int kWarps8 = kChunk / kItem8;
@@ -852,18 +852,27 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             const int over_g = (int)(reinterpret_cast<uintptr_t>(g) % 16 / sizeof(typename G::T));
             // the copies begin on the boundary before and end on the one
             // behind, inside the tensor
-            const int lo = w0 == 0 && (over_p | over_g) ? kItem8 : 0;
+            const int lo = w0 == 0 && (over_p | over_g) ? kLane8 : 0;
             const int more_p = over_p ? 4 - over_p : 0, more_g = over_g ? kPad - over_g : 0;
+            const int blocks = (int)min((left + kBlock8 - 1) / kBlock8, (int64_t)(kChunk / kBlock8));
             left = min(left - max(more_p, more_g), (int64_t)kChunk);
-            int hi = left < kItem8 || !(r.vec & kCodes) ? 0 : (int)left / kItem8 * kItem8;
+            int hi = left < kLane8 || !(r.vec & kCodes) ? 0 : (int)left / kLane8 * kLane8;
             if (hi < lo) hi = lo;
             const int n = hi - lo;
-            if (lane * 4 < n / kBlock8) {
-                const int q = lo / kBlock8 + lane * 4;
-                copy4_async(&x.ms[q], r.ms + w0 / kBlock8 + q);
-                copy4_async(&x.vs[q], r.vs + w0 / kBlock8 + q);
+            // scale bytes 4 at a time; a tensor's last one to three by themselves
+            const uint8_t* const ms = r.ms + w0 / kBlock8;
+            const uint8_t* const vs = r.vs + w0 / kBlock8;
+            const int whole = blocks / 4 * 4;
+            if (n > 0 && lane * 4 < whole) {
+                copy4_async(&x.ms[lane * 4], ms + lane * 4);
+                copy4_async(&x.vs[lane * 4], vs + lane * 4);
+            }
+            if (n > 0 && whole + lane < blocks) {
+                x.ms[whole + lane] = ms[whole + lane];
+                x.vs[whole + lane] = vs[whole + lane];
             }
             copies_arrive(bar);
+            __syncwarp();
             if (lane == 0) {
                 x.begin = w0;
                 x.lo = lo;
@@ -893,10 +902,10 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
     ring_compute<Smem8<G>::kStages>(&a.st->error, sh.stage, sh.ring, [&](Stage8<G>& x) {
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kLane8;  // place in the tile
-        const bool copied = warp * kItem8 >= x.lo && (warp + 1) * kItem8 <= x.hi;
+        const bool copied = at >= x.lo && at + kLane8 <= x.hi;
         const int64_t w0 = x.begin + warp * kItem8, i = x.begin + at;
         int some = kItem8;  // elements of the item, and of the lane
-        if (!copied) {
+        if ((warp + 1) * kItem8 > x.hi) {
             const int64_t left = r.numel - w0;
             some = left >= kItem8 ? kItem8 : (left > 0 ? (int)left : 0);
             const uint64_t lim = (uint64_t)r.numel > a.t.slack ? (uint64_t)r.numel - a.t.slack : 0;
@@ -906,17 +915,19 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
         if (some > 0) {
             const int64_t blk = i / kBlock8;
             const Const8 c = s.c8[r.group];
-            const bool over = (x.over_p | x.over_g) != 0, wide = copied && (r.vec & kWhole8), turned = copied && !wide;
-            float m[16], v[16];
+            const bool over = (x.over_p | x.over_g) != 0, turned = !(r.vec & kWhole8);
+            float m[16], v[16], sm = 0.0f, sv = 0.0f;
             if (copied) {
-                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
-                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
+                sm = scale_of(x.ms[at / kBlock8]);
+                sv = scale_of(x.vs[at / kBlock8]);
+            } else if (nv > 0) {
+                sm = scale_of(r.ms[blk]);
+                sv = scale_of(r.vs[blk]);
+            }
+            if (copied) {
+                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), sm, m);
+                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), sv, v);
             } else {
-                float sm = 0.0f, sv = 0.0f;
-                if (nv > 0) {
-                    sm = scale_of(r.ms[blk]);
-                    sv = scale_of(r.vs[blk]);
-                }
                 decode16<E4m3>(load_codes16(r.m8 + i, nv, r.vec & kCodes), sm, m);
                 decode16<E5m2>(load_codes16(r.v8 + i, nv, r.vec & kCodes), sv, v);
             }
@@ -946,13 +957,13 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
                     const float den = __fmaf_rn(sqrt_approx(v[o + e]), c.isb, c.eps);
                     p[e] = __fmaf_rn(-c.step_size, __fmul_rn(m[o + e], rcp_approx(den)), __fmul_rn(p[e], c.decay));
                 }
-                if (wide) {
-                    st8(r.master + i + o, p);
-                    if constexpr (O::kOut) st_stream(r.out + i + o, pack8<O>(p));
-                } else if (turned) {
+                if (turned) {
                     float4* const t = reinterpret_cast<float4*>(&sh.turn[warp][lane * kLane8 + o]);
                     t[0] = make_float4(p[0], p[1], p[2], p[3]);
                     t[1] = make_float4(p[4], p[5], p[6], p[7]);
+                } else if (copied) {
+                    st8(r.master + i + o, p);
+                    if constexpr (O::kOut) st_stream(r.out + i + o, pack8<O>(p));
                 } else {
                     store_f32(r.master + i + o, 0, nv - o, false, p);
                     if constexpr (O::kOut) store_out<O>(r.out + i + o, 0, nv - o, false, p);
@@ -966,8 +977,10 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
 #pragma unroll
                 for (int j = 0; j < kLane8; ++j) {
                     const int64_t e = w0 + 32 * j + lane;
-                    r.master[e] = q[j];
-                    if constexpr (O::kOut) r.out[e] = O::enc1(q[j]);
+                    if (32 * j + lane < some) {
+                        r.master[e] = q[j];
+                        if constexpr (O::kOut) r.out[e] = O::enc1(q[j]);
+                    }
                 }
                 __syncwarp();
             }
@@ -1050,9 +1063,9 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)t.slack;
             const bool wide = (r.vec & kCodec) && (r.vec & kCodes);
-            const int n = !wide || left < kItem8 ? 0 : (int)min(left, (int64_t)kChunk) / kItem8 * kItem8;
+            const int n = !wide || left < kLane8 ? 0 : (int)min(left, (int64_t)kChunk) / kLane8 * kLane8;
             if constexpr (!ENCODE)
-                if (lane * 4 < n / kBlock8) {
+                if (lane * 4 < n / kBlock8 / 4 * 4) {
                     copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4);
                     copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4);
                 }
@@ -1078,10 +1091,10 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
     ring_compute<Smem::kStages>(error, sh.stage, sh.ring, [&](Stage& x) {
         const MultiRow& r = x.row;
         const int at = (warp * 32 + lane) * kLane8;
-        const bool fast = (warp + 1) * kItem8 <= x.whole;
+        const bool fast = at + kLane8 <= x.whole;
         const int64_t i = x.begin + at;
         int nv = kLane8;
-        if (!fast) {
+        if ((warp + 1) * kItem8 > x.whole) {
             const int64_t left = r.numel - i;
             nv = left >= kLane8 ? kLane8 : (left > 0 ? (int)left : 0);
             const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
@@ -1115,8 +1128,9 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
             }
         } else if (nv > 0) {
             if (fast) {
-                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
-                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
+                const bool here = at / kBlock8 < x.whole / kBlock8 / 4 * 4;
+                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(here ? x.ms[at / kBlock8] : r.ms[blk]), m);
+                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(here ? x.vs[at / kBlock8] : r.vs[blk]), v);
             } else {
                 decode16<E4m3>(load_codes16(r.m8 + i, nv, codes), scale_of(r.ms[blk]), m);
                 decode16<E5m2>(load_codes16(r.v8 + i, nv, codes), scale_of(r.vs[blk]), v);
