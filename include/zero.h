@@ -729,7 +729,8 @@ zero_status_t zero_multi_adamw(const zero_multi* M, const zero_adamw_hp* hp, int
  * for m and x >> 11 for v; mix(x): x ^= x >> 16, x *= 0x9E3779B1, x ^= x >> 15,
  * x *= 0xBB67AE85, x ^= x >> 16, all modulo 2^32.  Same inputs, same result.
  * The square root and the division of the parameter update are approximate
- * (about 2^-22 relative, of the update only).  Needs grads, master, m8,
+ * (about 2^-22 relative, of the update only; a v below 2^-126 counts as zero
+ * in the root, and eps as at least 2^-126).  Needs grads, master, m8,
  * m8_scale, v8, v8_scale, and param16 unless ZERO_NO_OUT.  One launch. */
 zero_status_t zero_multi_adamw8(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags, uint32_t seed,
                                 zero_step_state* st, zero_stream_t stream);

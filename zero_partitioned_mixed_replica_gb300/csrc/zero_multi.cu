@@ -1413,7 +1413,7 @@ int ring_grid(Kernel kern, int64_t tiles, size_t smem, int threads) {
 }
 
 template <class G, class O>
-zero_status_t launch_update(const zero_multi* M, bool eight, const zk::MultiArgs& a, cudaStream_t s) {
+zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
     const char* what = eight ? "zero_multi_adamw8" : "zero_multi_adamw";
     const size_t smem = eight ? sizeof(zk::Smem8<G>) : sizeof(zk::Smem32<G>);
     const int threads = eight ? zk::kThreads8 : zk::kThreads32;
@@ -1425,9 +1425,9 @@ zero_status_t launch_update(const zero_multi* M, bool eight, const zk::MultiArgs
 
 template <class G>
 zero_status_t launch_update_out(const zero_multi* M, bool eight, const zk::MultiArgs& a, cudaStream_t s) {
-    if (M->param_dtype == ZERO_BF16) return launch_update<G, zk::OutBf16>(M, eight, a, s);
-    if (M->param_dtype == ZERO_FP16) return launch_update<G, zk::OutFp16>(M, eight, a, s);
-    return launch_update<G, zk::NoOut>(M, eight, a, s);
+    if (M->param_dtype == ZERO_BF16) return launch_update<G, zk::OutBf16>(eight, a, s);
+    if (M->param_dtype == ZERO_FP16) return launch_update<G, zk::OutFp16>(eight, a, s);
+    return launch_update<G, zk::NoOut>(eight, a, s);
 }
 
 zero_status_t update(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags, uint32_t seed, zero_step_state* st,
@@ -1588,7 +1588,9 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         // Tensors of a flat buffer have the same distance to a boundary in all
         // arrays: the gradients' (else the parameters') sets the shift.
         r.shift = (uint16_t)(g ? g / gs % zk::kVec : p / 4 % zk::kVec);
-        auto on = [&](uintptr_t at, uintptr_t elem, uintptr_t vector) { return (at - r.shift * elem) % vector == 0; };
+        auto on = [&](uintptr_t at, uintptr_t elem, uintptr_t vector) {
+            return at == 0 || (at - r.shift * elem) % vector == 0;  // an array that is not there is in no one's way
+        };
         r.vec = (uint16_t)((on(g, gs, gs * zk::kVec) ? zk::kVecGrad : 0) | (on(p, 4, 32) ? zk::kVecMaster : 0) |
                            (on(m, 4, 32) && on(v, 4, 32) ? zk::kVecStates : 0) | (on(o, 2, 16) ? zk::kVecOut : 0) |
                            (g % 16 == 0 && p % 32 == 0 && (m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 && o % 16 == 0 ? zk::kWhole8 : 0) |
