@@ -202,6 +202,59 @@ def test_adamw8_against_references(grad, out, gap):
     s.untouched()
 
 
+def _check8(s, t, clip, m0, v0):
+    """States bit for bit against the documented form, parameters against binary64 (see test_adamw8_against_references)."""
+    f = lambda x: torch.tensor(x, dtype=torch.float32)  # noqa: E731
+    dp = s.dp.cpu()
+    for i, (o, n) in enumerate(zip(s.offs, s.sizes)):
+        lr, eps, wd = HP[s.groups[i]]
+        sl = slice(o, o + n)
+        g = s.g[sl].float() * f(1.0 / s.scale) * f(clip)
+        m = f(0.9) * m0[i] + f(1 - 0.9) * g
+        v = f(0.999) * v0[i] + f(1 - 0.999) * (g * g)
+        rm, rv = R.random_ints(n, s.opt.seed, t, i)
+        for x, kind, r, code, byte in ((m, R.E4M3, rm, s.opt.m[i], s.opt.m_scale[i]), (v, R.E5M2, rv, s.opt.v[i], s.opt.v_scale[i])):
+            c, b = R.encode_ref(x, kind, r)
+            assert torch.equal(byte.cpu().view(torch.uint8), b), i
+            assert torch.equal(code.cpu().view(torch.uint8), c.view(torch.uint8)), i
+        p, _, _, upd, mmag, _ = R.adamw64(s.p[sl], m0[i], v0[i], s.g[sl], lr=lr, eps=eps, wd=wd, beta1=BETAS[0], beta2=BETAS[1],
+                                          t=t, scale=s.scale, clip=clip)
+        bound = 6 * U * mmag + 16 * U * upd + 4 * U * s.p[sl].double().abs() + 1e-44
+        assert bool(((dp[sl].double() - p).abs() <= bound).all()), i
+        if s.out:
+            assert torch.equal(s.dout.cpu()[sl], dp[sl].to(DT[s.out])), i
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_lists(seed):
+    rng = np.random.default_rng(1000 + seed)
+    sizes = [int(x) for x in np.exp(rng.uniform(0, np.log(60_000), rng.integers(1, 25)))]
+    sizes = [0 if rng.random() < 0.1 else n for n in sizes]
+    grad = ["bf16", "fp16", "fp32"][rng.integers(3)]
+    out = [None, "bf16", "fp16"][rng.integers(3)]
+    gap = ["aligned", "odd"][rng.integers(2)]
+    bits = [32, 8][rng.integers(2)]
+    scale = float(2.0 ** rng.integers(0, 11)) if grad == "fp16" else 1.0
+    max_norm = float(10.0 ** rng.uniform(-3, 1))
+    s = Setup(sizes, grad, out, bits, gap, scale, seed=seed, max_norm=max_norm, decide=True)
+    s.opt.seed = int(rng.integers(1 << 32))
+    s.opt.resume_at(int(rng.integers(0, 50)))
+    t = s.opt.read_state()["t"] + 1
+    if bits == 8:
+        m0 = [R.decode_ref(x.cpu(), y.cpu().view(torch.uint8)) for x, y in zip(s.opt.m, s.opt.m_scale)]
+        v0 = [R.decode_ref(x.cpu(), y.cpu().view(torch.uint8)) for x, y in zip(s.opt.v, s.opt.v_scale)]
+    s.opt.step()
+    st = s.opt.read_state()
+    norm = math.sqrt(sum(float((s.g[o:o + n].double() / scale).square().sum()) for o, n in zip(s.offs, sizes)))
+    assert abs(st["grad_norm"] - norm) <= 5 * U * norm
+    assert (st["t"], st["error"], st["apply"]) == (t, 0, 1)
+    if bits == 32:
+        _check32(s, t, st["clip_coef"])
+    else:
+        _check8(s, t, st["clip_coef"], m0, v0)
+    s.untouched()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_every_distance_to_a_boundary(bits):
     """Arrays that begin anywhere, each at a distance of its own, give what aligned ones do, bit for bit."""

@@ -32,15 +32,18 @@ M8, V8, SCALE8 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu
 def _check_list(name: str, xs: Sequence[torch.Tensor], numels: Sequence[int], dtypes, device) -> None:
     if len(xs) != len(numels):
         raise ValueError("%s: expected %d tensors, got %d" % (name, len(numels), len(xs)))
-    for i, (x, n) in enumerate(zip(xs, numels)):
+    index, dtype = device.index, xs[0].dtype
+    if device.type == "cuda" and dtype in dtypes and all(x.numel() == n and x.dtype is dtype and x.get_device() == index and
+                                                         x.is_contiguous() for x, n in zip(xs, numels)):
+        return
+    for i, (x, n) in enumerate(zip(xs, numels)):     # what it is
         if x.numel() != n:
             raise ValueError("%s[%d]: expected %d elements, got %d" % (name, i, n, x.numel()))
-        if x.dtype not in dtypes or x.dtype != xs[0].dtype:
+        if x.dtype not in dtypes or x.dtype != dtype:
             raise ValueError("%s[%d]: dtype %s (need %s, one for the list)" % (name, i, x.dtype, "/".join(map(str, dtypes))))
         if not x.is_contiguous():
             raise ValueError("%s[%d] is not contiguous" % (name, i))
-        if x.device != device or x.device.type != "cuda":
-            raise ValueError("%s[%d] is on %s, the list on %s" % (name, i, x.device, device))
+    raise ValueError("%s: the list's tensors are on CUDA device %s" % (name, index))
 
 
 def scale_count(numel: int) -> int:
