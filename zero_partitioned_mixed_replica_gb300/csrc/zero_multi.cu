@@ -215,8 +215,6 @@ struct GradFp32 {
 };
 struct NoOut {
     static constexpr bool kOut = false;
-    static __device__ __forceinline__ uint16_t enc1(float) { return 0; }
-    static __device__ __forceinline__ uint32_t pack(float, float) { return 0; }
 };
 struct OutBf16 : Bf16 {
     static constexpr bool kOut = true;
@@ -1266,12 +1264,21 @@ __global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_co
     if (!last) return;
     __threadfence();
     float hi = 0.0f, lo = 0.0f;
-    for (uint32_t sl = threadIdx.x; sl < n_slices; sl += kThreads) {
-        const float2 q = __ldcg(&t.partials[sl]);
+    // all loads at once (one after the other: 0.3 us more on a list of 1216
+    // slices)
+    constexpr int kMost = (kSlices + kThreads - 1) / kThreads;
+    float2 q[kMost];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        const uint32_t sl = threadIdx.x + j * kThreads;
+        q[j] = sl < n_slices ? __ldcg(&t.partials[sl]) : make_float2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
         float sum, err;
-        two_sum(hi, q.x, sum, err);
+        two_sum(hi, q[j].x, sum, err);
         hi = sum;
-        lo = __fadd_rn(lo, __fadd_rn(err, q.y));
+        lo = __fadd_rn(lo, __fadd_rn(err, q[j].y));
     }
     const float scale = st->loss_scale;  // before the decision changes it
     const float2 both = sum_pairs(hi, lo, sh);
