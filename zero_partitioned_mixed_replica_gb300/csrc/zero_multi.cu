@@ -22,8 +22,8 @@ constexpr int kRowsPerLaunch = 256;      // table rows passed through one launch
 
 // MultiRow::vec: which arrays begin on a boundary for the widest access.  The
 // first four after `shift` elements were put in front of the tensor; the others
-// at the tensor's own first element: all that the 8-bit update copies (kWhole8),
-// m and v for the codec, the codes.
+// at the tensor's own first element: gradients, parameters and 16-bit copies of
+// the 8-bit update and its states (kWhole8), m and v for the codec, the codes.
 enum { kVecGrad = 1, kVecMaster = 2, kVecStates = 4, kVecOut = 8, kWhole8 = 16, kCodec = 32, kCodes = 64 };
 
 // What the kernels know of one tensor: 12 words of 8 bytes, which a warp reads
