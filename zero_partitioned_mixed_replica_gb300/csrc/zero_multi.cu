@@ -354,14 +354,15 @@ __device__ __forceinline__ void advance_step(const MultiArgs& a) {
     st->good_steps += 1;
 }
 
-// All threads of the CTA call it; false: the step is skipped.  Four threads a
-// group: binary64 divisions and square roots are slow here, and a short step
-// waits for them.
+// All threads of the CTA (at least four warps) call it; false: the step is
+// skipped.  Binary64 divisions and square roots are slow here, and a short step
+// waits for them: each of four warps has its part of every group.
 __device__ __forceinline__ bool multi_constants(const MultiArgs& a, MultiShared& s) {
     const zero_step_state* st = a.st;
     const bool advance = (a.flags & ZERO_MULTI_ADVANCE) != 0;
-    const int g = threadIdx.x >> 2, role = threadIdx.x & 3;
-    if (g < a.hp.n) {
+    static_assert(ZERO_MAX_GROUPS < 32, "a lane for each group, and one for the rest");
+    const int g = threadIdx.x & 31, role = threadIdx.x >> 5;
+    if (g < a.hp.n && role < 4) {
         AdamConsts& k = s.k[g];
         Const8& q = s.c8[g];
         if (role == 0) {
@@ -376,14 +377,14 @@ __device__ __forceinline__ bool multi_constants(const MultiArgs& a, MultiShared&
             k.b2 = q.b2 = __double2float_rn(st->beta2);
             k.omb1 = q.omb1 = __double2float_rn(__dsub_rn(1.0, st->beta1));
             k.omb2 = q.omb2 = __double2float_rn(__dsub_rn(1.0, st->beta2));
-        } else {
+        } else {  // role 3
             k.decay = q.decay = __double2float_rn(__dsub_rn(1.0, __dmul_rn(a.hp.lr[g], a.hp.wd[g])));
             k.eps = __double2float_rn(a.hp.eps[g]);
             q.eps = fmaxf(k.eps, 1.17549435e-38f);
             k.clip = advance ? 1.0f : st->clip_coef;
         }
     }
-    if (threadIdx.x == 4 * ZERO_MAX_GROUPS) {
+    if (threadIdx.x == 2 * 32 + ZERO_MAX_GROUPS) {
         s.apply = advance ? 1 : st->apply;
         const float kept = *a.t.grad_scale;  // zero before the list's first norm
         const float scale = !advance && kept > 0.0f ? kept : st->loss_scale;
@@ -857,6 +858,20 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             int hi = left < kLane8 || !(r.vec & kCodes) ? 0 : (int)left / kLane8 * kLane8;
             if (hi < lo) hi = lo;
             const int n = hi - lo;
+            const uint32_t bytes_p = (n + over_p + more_p) * sizeof(float), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
+            if (lane == 0) {
+                x.begin = w0;
+                x.lo = lo;
+                x.hi = hi;
+                x.over_p = over_p;
+                x.over_g = over_g;
+                if (n > 0) {  // the bytes are announced below; `full` waits for that
+                    bulk_g2s(x.p + lo, p + lo - over_p, bytes_p, bar);
+                    bulk_g2s(x.g + lo, g + lo - over_g, bytes_g, bar);
+                    bulk_g2s(x.m + lo, r.m8 + w0 + lo, n, bar);
+                    bulk_g2s(x.v + lo, r.v8 + w0 + lo, n, bar);
+                }
+            }
             // scale bytes 4 at a time; a tensor's last one to three by themselves
             const uint8_t* const ms = r.ms + w0 / kBlock8;
             const uint8_t* const vs = r.vs + w0 / kBlock8;
@@ -871,21 +886,7 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             }
             copies_arrive(bar);
             __syncwarp();
-            if (lane == 0) {
-                x.begin = w0;
-                x.lo = lo;
-                x.hi = hi;
-                x.over_p = over_p;
-                x.over_g = over_g;
-                const uint32_t bytes_p = (n + over_p + more_p) * sizeof(float), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
-                mbar_arrive_expect_tx(bar, n > 0 ? bytes_p + bytes_g + 2 * n : 0);
-                if (n > 0) {
-                    bulk_g2s(x.p + lo, p + lo - over_p, bytes_p, bar);
-                    bulk_g2s(x.g + lo, g + lo - over_g, bytes_g, bar);
-                    bulk_g2s(x.m + lo, r.m8 + w0 + lo, n, bar);
-                    bulk_g2s(x.v + lo, r.v8 + w0 + lo, n, bar);
-                }
-            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, n > 0 ? bytes_p + bytes_g + 2 * n : 0);
         }, [&]() {
             const bool apply = multi_constants(a, s);
             if (lane == 0) advance_step(a);
@@ -1157,8 +1158,9 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
 // coefficient, the step counter and beta^t; the loss-scale schedule.  Two
 // threads: the clip coefficient, and what does not depend on the norm's value.
 __device__ __forceinline__ float clip_of(bool bad, double norm, double max_norm) {
-    if (bad || !(max_norm > 0.0)) return 1.0f;
-    return __double2float_rn(fmin(1.0, __ddiv_rn(max_norm, __dadd_rn(norm, 1e-6))));
+    const double most = __dadd_rn(norm, 1e-6);
+    if (bad || !(max_norm > 0.0) || max_norm >= most) return 1.0f;  // a quotient of 1 or more is not needed
+    return __double2float_rn(__ddiv_rn(max_norm, most));
 }
 __device__ __forceinline__ void decide_step(zero_step_state* st, bool bad) {
     st->apply = bad ? 0 : 1;
@@ -1294,7 +1296,8 @@ __global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_co
         decide_step(st, bad);
         return;
     }
-    const double norm = bad ? (double)INFINITY : __ddiv_rn(__dsqrt_rn(total), (double)scale);
+    double norm = bad ? (double)INFINITY : __dsqrt_rn(total);
+    if (!bad && scale != 1.0f) norm = __ddiv_rn(norm, (double)scale);
     st->grad_norm = norm;
     st->clip_coef = clip_of(bad, norm, max_norm);
 }
