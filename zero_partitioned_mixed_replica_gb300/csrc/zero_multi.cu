@@ -416,9 +416,9 @@ struct Ring {
     uint64_t full[S], empty[S];
 };
 
-// 4 bytes into shared memory, counted by an mbarrier.
-__device__ __forceinline__ void copy4_async(void* dst_smem, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
+// Up to 4 bytes into shared memory (zeros behind them), counted by an mbarrier.
+__device__ __forceinline__ void copy4_async(void* dst_smem, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst_smem)), "l"(src), "r"(min(bytes, 4)) : "memory");
 }
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {  // arrives when the thread's copies so far have landed
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -549,8 +549,8 @@ __device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<
 // same bits here as in the flat buffer.  Bound by memory: 14 bytes read and 14
 // written per element with 16-bit gradients and copies.  GB300, 1.56e9
 // elements in 580 tensors: 6.16 ms, 7.1 TB/s (the copy that the roofline is
-// measured with: 6.77).  80K elements in 50 tensors: 4.6 us from a graph, the
-// latency of launch, row, copies, constants and stores one after the other.
+// measured with: 6.77).  80K elements in 50 tensors: 3.4 us from a graph, the
+// latency of launch, copies, constants, update and stores one after the other.
 // ----------------------------------------------------------------------------
 // A computing warp takes 256 elements of a tile, 8 consecutive ones per lane.
 // The 8 begin on the boundaries that the arrays' addresses give
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
 // onto one by a shift of the work, as in the 32-bit update: they are copied
 // from the boundary before, taken over by as many elements, and the results
 // turned round in shared memory so that neighbouring lanes store neighbouring
-// elements (GB300, 91e6 elements in 150 tensors at odd offsets: 459 us, aligned
+// elements (GB300, 91e6 elements in 150 tensors at odd offsets: 467 us, aligned
 // 408; read by plain loads 588).  A tensor's last few elements, and its first 16
 // if they are not on a boundary, are read by plain loads.
 constexpr int kLane8 = 16;
@@ -858,35 +858,26 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             int hi = left < kLane8 || !(r.vec & kCodes) ? 0 : (int)left / kLane8 * kLane8;
             if (hi < lo) hi = lo;
             const int n = hi - lo;
-            const uint32_t bytes_p = (n + over_p + more_p) * sizeof(float), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
+            if (n > 0 && lane * 4 < blocks) {
+                copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4, blocks - lane * 4);
+                copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4, blocks - lane * 4);
+            }
+            copies_arrive(bar);
             if (lane == 0) {
                 x.begin = w0;
                 x.lo = lo;
                 x.hi = hi;
                 x.over_p = over_p;
                 x.over_g = over_g;
-                if (n > 0) {  // the bytes are announced below; `full` waits for that
+                const uint32_t bytes_p = (n + over_p + more_p) * sizeof(float), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
+                mbar_arrive_expect_tx(bar, n > 0 ? bytes_p + bytes_g + 2 * n : 0);
+                if (n > 0) {
                     bulk_g2s(x.p + lo, p + lo - over_p, bytes_p, bar);
                     bulk_g2s(x.g + lo, g + lo - over_g, bytes_g, bar);
                     bulk_g2s(x.m + lo, r.m8 + w0 + lo, n, bar);
                     bulk_g2s(x.v + lo, r.v8 + w0 + lo, n, bar);
                 }
             }
-            // scale bytes 4 at a time; a tensor's last one to three by themselves
-            const uint8_t* const ms = r.ms + w0 / kBlock8;
-            const uint8_t* const vs = r.vs + w0 / kBlock8;
-            const int whole = blocks / 4 * 4;
-            if (n > 0 && lane * 4 < whole) {
-                copy4_async(&x.ms[lane * 4], ms + lane * 4);
-                copy4_async(&x.vs[lane * 4], vs + lane * 4);
-            }
-            if (n > 0 && whole + lane < blocks) {
-                x.ms[whole + lane] = ms[whole + lane];
-                x.vs[whole + lane] = vs[whole + lane];
-            }
-            copies_arrive(bar);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar, n > 0 ? bytes_p + bytes_g + 2 * n : 0);
         }, [&]() {
             const bool apply = multi_constants(a, s);
             if (lane == 0) advance_step(a);
@@ -915,34 +906,36 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             const int64_t blk = i / kBlock8;
             const Const8 c = s.c8[r.group];
             const bool over = (x.over_p | x.over_g) != 0, turned = !(r.vec & kWhole8);
-            float m[16], v[16], sm = 0.0f, sv = 0.0f;
+            // a lane has 16 copied elements, fewer at a tensor's ends, or none
+            float m[16], v[16];
             if (copied) {
-                sm = scale_of(x.ms[at / kBlock8]);
-                sv = scale_of(x.vs[at / kBlock8]);
+                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
+                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
             } else if (nv > 0) {
-                sm = scale_of(r.ms[blk]);
-                sv = scale_of(r.vs[blk]);
-            }
-            if (copied) {
-                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), sm, m);
-                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), sv, v);
+                decode16<E4m3>(load_codes16(r.m8 + i, nv, r.vec & kCodes), scale_of(r.ms[blk]), m);
+                decode16<E5m2>(load_codes16(r.v8 + i, nv, r.vec & kCodes), scale_of(r.vs[blk]), v);
             } else {
-                decode16<E4m3>(load_codes16(r.m8 + i, nv, r.vec & kCodes), sm, m);
-                decode16<E5m2>(load_codes16(r.v8 + i, nv, r.vec & kCodes), sv, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) m[e] = v[e] = 0.0f;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int o = 8 * h;
                 float g[8], p[8];
-                if (!copied) {
+                if (copied) {
+                    if (over) {
+                        G::load8_over(&x.g[at + o], x.over_g, g);
+                        lds8_over(&x.p[at + o], x.over_p, p);
+                    } else {
+                        G::load8(&x.g[at + o], g);
+                        lds8(&x.p[at + o], p);
+                    }
+                } else if (nv > 0) {
                     load_grad<G>(r.grad, i + o, 0, nv - o, false, g);
                     load_f32(r.master + i + o, 0, nv - o, false, p);
-                } else if (over) {
-                    G::load8_over(&x.g[at + o], x.over_g, g);
-                    lds8_over(&x.p[at + o], x.over_p, p);
                 } else {
-                    G::load8(&x.g[at + o], g);
-                    lds8(&x.p[at + o], p);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] = p[e] = 0.0f;
                 }
                 if (two) {
 #pragma unroll
@@ -963,7 +956,7 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
                 } else if (copied) {
                     st8(r.master + i + o, p);
                     if constexpr (O::kOut) st_stream(r.out + i + o, pack8<O>(p));
-                } else {
+                } else if (nv > 0) {
                     store_f32(r.master + i + o, 0, nv - o, false, p);
                     if constexpr (O::kOut) store_out<O>(r.out + i + o, 0, nv - o, false, p);
                 }
@@ -986,11 +979,13 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
             uint4 cm, cv;
             encode16(m, v, bm, bv, mix32(s.key + r.tensor), (uint32_t)(i >> 3), cm, cv);
-            store_codes16(r.m8 + i, nv, r.vec & kCodes, cm);
-            store_codes16(r.v8 + i, nv, r.vec & kCodes, cv);
-            if ((lane & 1) == 0 && nv > 0) {
-                r.ms[blk] = (uint8_t)bm;
-                r.vs[blk] = (uint8_t)bv;
+            if (nv > 0) {
+                store_codes16(r.m8 + i, nv, r.vec & kCodes, cm);
+                store_codes16(r.v8 + i, nv, r.vec & kCodes, cv);
+                if ((lane & 1) == 0) {
+                    r.ms[blk] = (uint8_t)bm;
+                    r.vs[blk] = (uint8_t)bv;
+                }
             }
         }
     });
@@ -1063,11 +1058,13 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
             if (kChecked) left -= (int64_t)t.slack;
             const bool wide = (r.vec & kCodec) && (r.vec & kCodes);
             const int n = !wide || left < kLane8 ? 0 : (int)min(left, (int64_t)kChunk) / kLane8 * kLane8;
-            if constexpr (!ENCODE)
-                if (lane * 4 < n / kBlock8 / 4 * 4) {
-                    copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4);
-                    copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4);
+            if constexpr (!ENCODE) {
+                const int blocks = (n + kBlock8 - 1) / kBlock8;
+                if (lane * 4 < blocks) {
+                    copy4_async(&x.ms[lane * 4], r.ms + w0 / kBlock8 + lane * 4, blocks - lane * 4);
+                    copy4_async(&x.vs[lane * 4], r.vs + w0 / kBlock8 + lane * 4, blocks - lane * 4);
                 }
+            }
             copies_arrive(bar);
             if (lane == 0) {
                 x.begin = w0;
@@ -1127,9 +1124,8 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
             }
         } else if (nv > 0) {
             if (fast) {
-                const bool here = at / kBlock8 < x.whole / kBlock8 / 4 * 4;
-                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(here ? x.ms[at / kBlock8] : r.ms[blk]), m);
-                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(here ? x.vs[at / kBlock8] : r.vs[blk]), v);
+                decode16<E4m3>(*reinterpret_cast<const uint4*>(&x.m[at]), scale_of(x.ms[at / kBlock8]), m);
+                decode16<E5m2>(*reinterpret_cast<const uint4*>(&x.v[at]), scale_of(x.vs[at / kBlock8]), v);
             } else {
                 decode16<E4m3>(load_codes16(r.m8 + i, nv, codes), scale_of(r.ms[blk]), m);
                 decode16<E5m2>(load_codes16(r.v8 + i, nv, codes), scale_of(r.vs[blk]), v);
@@ -1151,7 +1147,7 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
 // (two_sum); pairs (sum, error) are combined by shuffles and, among the CTAs,
 // by the one that ends last.  The split into kSlices ranges is fixed, so the
 // result does not depend on the grid.  Bound by memory: GB300, 1.56e9 16-bit
-// gradients 433 us (7.2 TB/s read); 30.7e6 of them 16.3 us, of which 9 are the
+// gradients 433 us (7.2 TB/s read); 30.7e6 of them 15.5 us, of which 9 are the
 // bytes and the rest launch, first loads and the last CTA's sum.
 // ----------------------------------------------------------------------------
 // The step decision, as zero_grad_norm makes it: skip on overflow, else the clip
