@@ -21,9 +21,10 @@ constexpr int kSlices = 1216;            // fixed split of a list for the norm (
 constexpr int kRowsPerLaunch = 256;      // table rows passed through one launch's parameters
 
 // MultiRow::vec: which arrays begin on a boundary for the widest access.  The
-// first four after `shift` elements were put in front of the tensor; the others
-// at the tensor's own first element: gradients, parameters and 16-bit copies of
-// the 8-bit update and its states (kWhole8), m and v for the codec, the codes.
+// first four after `shift` elements were put in front of the tensor (the
+// gradients' distance for the norm is `gshift`, and always right); the others at
+// the tensor's own first element: gradients, parameters and 16-bit copies of the
+// 8-bit update and its states (kWhole8), m and v for the codec, the codes.
 enum { kVecGrad = 1, kVecMaster = 2, kVecStates = 4, kVecOut = 8, kWhole8 = 16, kCodec = 32, kCodes = 64 };
 
 // What the kernels know of one tensor: 12 words of 8 bytes, which a warp reads
@@ -39,8 +40,10 @@ struct MultiRow {
     int64_t numel;
     uint32_t first_chunk;
     uint32_t tensor;  // its own index
-    uint16_t vec;
-    uint16_t shift;   // elements by which the 32-bit kernels' work items begin before the tensor
+    uint8_t vec;
+    uint8_t shift;    // elements by which the tiles of the 32-bit update begin before the tensor,
+    uint8_t gshift;   // and those of the norm
+    uint8_t pad0;
     int32_t group;
     float* m;
     float* v;
@@ -565,10 +568,12 @@ struct __align__(128) Stage32 {
     float p[kChunk];
     float m[kChunk];
     float v[kChunk];
-    typename G::T g[kChunk];
+    static constexpr int kPad = 16 / sizeof(typename G::T);
+    typename G::T g[kChunk + kPad];  // element e at e + over_g
     MultiRow row;
     int64_t begin;  // the tile's first element in its tensor (below zero: that many do not exist)
     int32_t lo, hi; // elements of the tile that were copied
+    int32_t over_g;
     bool end;       // no tile: the list's end
 };
 template <class G>
@@ -595,24 +600,33 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
         ring_fetch<Smem32<G>::kStages>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage32<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
             const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk - r.shift;
-            constexpr uint32_t kAll = kVecGrad | kVecMaster | kVecStates | kVecOut;
+            constexpr uint32_t kAll = kVecMaster | kVecStates | kVecOut;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
-            const int lo = w0 < 0 ? kVec : 0;
-            int hi = left < kVec ? 0 : (int)min(left, (int64_t)kChunk) / kVec * kVec;
+            // gradients at another distance from a boundary are copied from the
+            // boundary before to the one behind, inside the tensor
+            constexpr int kPad = Stage32<G>::kPad;
+            const typename G::T* const g = static_cast<const typename G::T*>(r.grad) + w0;
+            const int over_g = (int)(reinterpret_cast<uintptr_t>(g) % 16 / sizeof(typename G::T));
+            const int more_g = over_g ? kPad - over_g : 0;
+            int lo = w0 < 0 ? kVec : 0;
+            if (w0 + lo < over_g) lo += kVec;
+            left = min(left - more_g, (int64_t)kChunk);
+            int hi = left < kVec ? 0 : (int)left / kVec * kVec;
             if ((r.vec & kAll) != kAll || hi < lo) hi = lo;
             copies_arrive(bar);
             if (lane == 0) {
                 x.begin = w0;
                 x.lo = lo;
                 x.hi = hi;
-                const uint32_t n = (uint32_t)(hi - lo);
-                mbar_arrive_expect_tx(bar, n * (3 * sizeof(float) + sizeof(typename G::T)));
+                x.over_g = over_g;
+                const uint32_t n = (uint32_t)(hi - lo), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
+                mbar_arrive_expect_tx(bar, n > 0 ? n * 3 * sizeof(float) + bytes_g : 0);
                 if (n > 0) {
                     bulk_g2s(x.p + lo, r.master + w0 + lo, n * sizeof(float), bar);
                     bulk_g2s(x.m + lo, r.m + w0 + lo, n * sizeof(float), bar);
                     bulk_g2s(x.v + lo, r.v + w0 + lo, n * sizeof(float), bar);
-                    bulk_g2s(x.g + lo, static_cast<const typename G::T*>(r.grad) + w0 + lo, n * sizeof(typename G::T), bar);
+                    bulk_g2s(x.g + lo, g + lo - over_g, bytes_g, bar);
                 }
             }
         }, [&]() {
@@ -636,7 +650,8 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
         const AdamConsts k = s.k[r.group];
         float g[8], p[8], m[8], v[8];
         if (fast) {
-            G::load8(&x.g[at], g);
+            if (x.over_g) G::load8_over(&x.g[at], x.over_g, g);
+            else G::load8(&x.g[at], g);
             lds8(&x.p[at], p);
             lds8(&x.m[at], m);
             lds8(&x.v[at], v);
@@ -1206,11 +1221,11 @@ __global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_co
         while (c < c1) {
             const uint32_t n = t.tensor[c];
             const MultiRow& r = t.rows[n];
-            const int64_t begin = (int64_t)(c - r.first_chunk) * kChunk - r.shift;
-            const uint32_t chunks = (uint32_t)((r.numel + r.shift + kChunk - 1) / kChunk) - (c - r.first_chunk);
+            const int64_t begin = (int64_t)(c - r.first_chunk) * kChunk - r.gshift;
+            const uint32_t chunks = (uint32_t)((r.numel + max(r.shift, r.gshift) + kChunk - 1) / kChunk) - (c - r.first_chunk);
             const uint32_t take = min(chunks, c1 - c);
             const int64_t end = min(r.numel, begin + (int64_t)take * kChunk);
-            const bool vec = r.vec & kVecGrad;
+            constexpr bool vec = true;  // gshift puts the gradients on a boundary
             const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
             auto add = [&](const float (&g)[8]) {
                 float q = __fmul_rn(g[0], g[0]);
@@ -1592,16 +1607,28 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         r.vs = reinterpret_cast<uint8_t*>(vs);
         r.out = reinterpret_cast<uint16_t*>(o);
         // Tensors of a flat buffer have the same distance to a boundary in all
-        // arrays: the gradients' (else the parameters') sets the shift.
-        r.shift = (uint16_t)(g ? g / gs % zk::kVec : p / 4 % zk::kVec);
+        // arrays.  Where they do not, the distance with the most bytes behind it
+        // sets the shift (the gradients' own matters to the norm only).
+        const uintptr_t at[4] = {p / 4 % zk::kVec, m / 4 % zk::kVec, v / 4 % zk::kVec, o / 2 % zk::kVec};
+        const int weight[4] = {p ? 8 : 0, m ? 8 : 0, v ? 8 : 0, o ? 2 : 0};
+        int most = -1;
+        for (uintptr_t d = 0; d < (uintptr_t)zk::kVec; ++d) {
+            int sum = 0;
+            for (int k = 0; k < 4; ++k) sum += at[k] == d ? weight[k] : 0;
+            if (sum > most) {
+                most = sum;
+                r.shift = (uint8_t)d;
+            }
+        }
+        r.gshift = (uint8_t)(g / gs % zk::kVec);
         auto on = [&](uintptr_t at, uintptr_t elem, uintptr_t vector) {
             return at == 0 || (at - r.shift * elem) % vector == 0;  // an array that is not there is in no one's way
         };
-        r.vec = (uint16_t)((on(g, gs, gs * zk::kVec) ? zk::kVecGrad : 0) | (on(p, 4, 32) ? zk::kVecMaster : 0) |
+        r.vec = (uint8_t)((on(g, gs, gs * zk::kVec) ? zk::kVecGrad : 0) | (on(p, 4, 32) ? zk::kVecMaster : 0) |
                            (on(m, 4, 32) && on(v, 4, 32) ? zk::kVecStates : 0) | (on(o, 2, 16) ? zk::kVecOut : 0) |
                            (g % 16 == 0 && p % 32 == 0 && (m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 && o % 16 == 0 ? zk::kWhole8 : 0) |
                            ((m | v) % 32 == 0 ? zk::kCodec : 0) | ((m8 | v8) % 16 == 0 && (ms | vs) % 4 == 0 ? zk::kCodes : 0));
-        chunk += chunks_of(r.numel, r.shift);
+        chunk += chunks_of(r.numel, std::max(r.shift, r.gshift));
     }
     const bool fresh = M->workspace != static_cast<char*>(workspace);  // else a decided step may be under way
     M->bound = false;
