@@ -611,11 +611,9 @@ zero_status_t zero_fused_step_noalloc(const zero_layout* L, const zero_adamw_hp*
  *     only (a tensor may begin anywhere in a flat buffer), else
  *     ZERO_ERR_ALIGN; arrays of tensors with 0 elements may be NULL.  The
  *     workspace and the state are 256-byte aligned as everywhere.  With
- *     32-bit states a tensor is fast wherever it begins, as long as its
- *     arrays but the gradients are equally many elements away from a 32-byte
- *     boundary (16-bit ones: 16), as in flat buffers of one layout; with 8-bit
- *     states if the codes begin on 16-byte and the scales on 4-byte
- *     boundaries.
+ *     32-bit states a tensor is fast wherever its arrays begin, if m and v
+ *     are equally far from a 32-byte boundary; with 8-bit states if the codes
+ *     begin on 16-byte and the scales on 4-byte boundaries.
  *   - Arrays of one call must not overlap, except that arrays that are only
  *     read may.
  *   - The object holds the addresses of the last bind; its workspace must

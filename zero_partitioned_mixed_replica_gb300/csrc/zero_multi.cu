@@ -556,16 +556,20 @@ __device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<
 // latency of launch, copies, constants, update and stores one after the other.
 // ----------------------------------------------------------------------------
 // A computing warp takes 256 elements of a tile, 8 consecutive ones per lane.
-// The 8 begin on the boundaries that the arrays' addresses give
+// The 8 begin on the boundaries that the states' addresses give
 // (MultiRow::shift), so that a tensor anywhere in a flat buffer is copied but
 // for its first and last few elements, which are read by plain loads.
+// Parameters and gradients at other distances are copied from the boundary
+// before and taken over by as many elements (GB300, 90e6 elements, one of the
+// arrays apart from a gapless buffer: 363 us as aligned; by plain loads 482 to
+// 716).
 constexpr int kItem32 = 32 * kVec;
 constexpr int kWarps32 = kChunk / kItem32;
 constexpr int kThreads32 = 32 * (kWarps32 + 1);
 
 template <class G>
 struct __align__(128) Stage32 {
-    float p[kChunk];
+    float p[kChunk + 4];  // element e at e + over_p
     float m[kChunk];
     float v[kChunk];
     static constexpr int kPad = 16 / sizeof(typename G::T);
@@ -573,13 +577,14 @@ struct __align__(128) Stage32 {
     MultiRow row;
     int64_t begin;  // the tile's first element in its tensor (below zero: that many do not exist)
     int32_t lo, hi; // elements of the tile that were copied
-    int32_t over_g;
+    int32_t over_p, over_g;
     bool end;       // no tile: the list's end
 };
 template <class G>
 struct Smem32 {
     static constexpr int kStages = 3;
     Stage32<G> stage[kStages];
+    float turn[kWarps32][kItem32];
     Ring<kStages> ring;
 };
 
@@ -600,30 +605,34 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
         ring_fetch<Smem32<G>::kStages>(a.t, &a.st->error, sh.stage, sh.ring, [&](uint32_t tile, Stage32<G>& x, uint64_t* bar) {
             const MultiRow& r = x.row;
             const int64_t w0 = (int64_t)(tile - r.first_chunk) * kChunk - r.shift;
-            constexpr uint32_t kAll = kVecMaster | kVecStates | kVecOut;
             int64_t left = r.numel - w0;
             if (kChecked) left -= (int64_t)a.t.slack;
-            // gradients at another distance from a boundary are copied from the
-            // boundary before to the one behind, inside the tensor
+            // parameters and gradients at another distance from a boundary than
+            // the states are copied from the boundary before to the one behind,
+            // inside the tensor
             constexpr int kPad = Stage32<G>::kPad;
             const typename G::T* const g = static_cast<const typename G::T*>(r.grad) + w0;
+            const float* const p = r.master + w0;
+            const int over_p = (int)(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(float));
             const int over_g = (int)(reinterpret_cast<uintptr_t>(g) % 16 / sizeof(typename G::T));
-            const int more_g = over_g ? kPad - over_g : 0;
+            const int more_p = over_p ? 4 - over_p : 0, more_g = over_g ? kPad - over_g : 0;
             int lo = w0 < 0 ? kVec : 0;
-            if (w0 + lo < over_g) lo += kVec;
-            left = min(left - more_g, (int64_t)kChunk);
+            if (w0 + lo < max(over_p, over_g)) lo += kVec;
+            left = min(left - max(more_p, more_g), (int64_t)kChunk);
             int hi = left < kVec ? 0 : (int)left / kVec * kVec;
-            if ((r.vec & kAll) != kAll || hi < lo) hi = lo;
+            if (!(r.vec & kVecStates) || hi < lo) hi = lo;
             copies_arrive(bar);
             if (lane == 0) {
                 x.begin = w0;
                 x.lo = lo;
                 x.hi = hi;
+                x.over_p = over_p;
                 x.over_g = over_g;
-                const uint32_t n = (uint32_t)(hi - lo), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
-                mbar_arrive_expect_tx(bar, n > 0 ? n * 3 * sizeof(float) + bytes_g : 0);
+                const uint32_t n = (uint32_t)(hi - lo);
+                const uint32_t bytes_p = (n + over_p + more_p) * sizeof(float), bytes_g = (n + over_g + more_g) * sizeof(typename G::T);
+                mbar_arrive_expect_tx(bar, n > 0 ? bytes_p + n * 2 * sizeof(float) + bytes_g : 0);
                 if (n > 0) {
-                    bulk_g2s(x.p + lo, r.master + w0 + lo, n * sizeof(float), bar);
+                    bulk_g2s(x.p + lo, p + lo - over_p, bytes_p, bar);
                     bulk_g2s(x.m + lo, r.m + w0 + lo, n * sizeof(float), bar);
                     bulk_g2s(x.v + lo, r.v + w0 + lo, n * sizeof(float), bar);
                     bulk_g2s(x.g + lo, g + lo - over_g, bytes_g, bar);
@@ -645,37 +654,62 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
         const bool fast = at >= x.lo && at + kVec <= x.hi;
         const int64_t i = x.begin + at;
         int e0 = 0, e1 = kVec;
-        if (!fast && !span8(a.t, r, i, e0, e1)) return;
         const uint32_t vec = r.vec;
-        const AdamConsts k = s.k[r.group];
-        float g[8], p[8], m[8], v[8];
-        if (fast) {
-            if (x.over_g) G::load8_over(&x.g[at], x.over_g, g);
-            else G::load8(&x.g[at], g);
-            lds8(&x.p[at], p);
-            lds8(&x.m[at], m);
-            lds8(&x.v[at], v);
-        } else {
-            // ones where there is nothing: zeros would take the slow ways of
-            // the division and the root
-            load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g, 1.0f);
-            load_f32(r.master + i, e0, e1, vec & kVecMaster, p, 1.0f);
-            load_f32(r.m + i, e0, e1, vec & kVecStates, m, 1.0f);
-            load_f32(r.v + i, e0, e1, vec & kVecStates, v, 1.0f);
+        // parameters or their copies that are not on the states' boundaries:
+        // neighbouring lanes store neighbouring elements
+        const bool turned = (vec & (kVecMaster | kVecOut)) != (kVecMaster | kVecOut);
+        if (fast || span8(a.t, r, i, e0, e1)) {
+            const AdamConsts k = s.k[r.group];
+            float g[8], p[8], m[8], v[8];
+            if (fast) {
+                if (x.over_g) G::load8_over(&x.g[at], x.over_g, g);
+                else G::load8(&x.g[at], g);
+                if (x.over_p) lds8_over(&x.p[at], x.over_p, p);
+                else lds8(&x.p[at], p);
+                lds8(&x.m[at], m);
+                lds8(&x.v[at], v);
+            } else {
+                // ones where there is nothing: zeros would take the slow ways of
+                // the division and the root
+                load_grad<G>(r.grad, i, e0, e1, vec & kVecGrad, g, 1.0f);
+                load_f32(r.master + i, e0, e1, vec & kVecMaster, p, 1.0f);
+                load_f32(r.m + i, e0, e1, vec & kVecStates, m, 1.0f);
+                load_f32(r.v + i, e0, e1, vec & kVecStates, v, 1.0f);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
+            if (all_zero8x3(g, m, v)) {  // e.g. embedding rows that no batch has held
+#pragma unroll
+                for (int e = 0; e < 8; ++e) adamw1_zero_state(p[e], m[e], v[e], g[e], k);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) adamw1(p[e], m[e], v[e], g[e], k);
+            }
+            store_f32(r.m + i, e0, e1, vec & kVecStates, m);
+            store_f32(r.v + i, e0, e1, vec & kVecStates, v);
+            if (fast && turned) {
+                float4* const t = reinterpret_cast<float4*>(&sh.turn[warp][lane * kVec]);
+                t[0] = make_float4(p[0], p[1], p[2], p[3]);
+                t[1] = make_float4(p[4], p[5], p[6], p[7]);
+            } else {
+                store_f32(r.master + i, e0, e1, vec & kVecMaster, p);
+                if constexpr (O::kOut) store_out<O>(r.out + i, e0, e1, vec & kVecOut, p);
+            }
         }
+        if (turned) {
+            __syncwarp();
+            float q[kVec];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], unscale);
-        if (all_zero8x3(g, m, v)) {  // e.g. embedding rows that no batch has held
+            for (int j = 0; j < kVec; ++j) q[j] = sh.turn[warp][32 * j + lane];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) adamw1_zero_state(p[e], m[e], v[e], g[e], k);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) adamw1(p[e], m[e], v[e], g[e], k);
+            for (int j = 0; j < kVec; ++j) {
+                const int e = warp * kItem32 + 32 * j + lane;
+                if (e >= x.lo && e < x.hi) {
+                    r.master[x.begin + e] = q[j];
+                    if constexpr (O::kOut) r.out[x.begin + e] = O::enc1(q[j]);
+                }
+            }
         }
-        store_f32(r.master + i, e0, e1, vec & kVecMaster, p);
-        store_f32(r.m + i, e0, e1, vec & kVecStates, m);
-        store_f32(r.v + i, e0, e1, vec & kVecStates, v);
-        if constexpr (O::kOut) store_out<O>(r.out + i, e0, e1, vec & kVecOut, p);
     });
 }
 
@@ -1607,19 +1641,8 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
         r.vs = reinterpret_cast<uint8_t*>(vs);
         r.out = reinterpret_cast<uint16_t*>(o);
         // Tensors of a flat buffer have the same distance to a boundary in all
-        // arrays.  Where they do not, the distance with the most bytes behind it
-        // sets the shift (the gradients' own matters to the norm only).
-        const uintptr_t at[4] = {p / 4 % zk::kVec, m / 4 % zk::kVec, v / 4 % zk::kVec, o / 2 % zk::kVec};
-        const int weight[4] = {p ? 8 : 0, m ? 8 : 0, v ? 8 : 0, o ? 2 : 0};
-        int most = -1;
-        for (uintptr_t d = 0; d < (uintptr_t)zk::kVec; ++d) {
-            int sum = 0;
-            for (int k = 0; k < 4; ++k) sum += at[k] == d ? weight[k] : 0;
-            if (sum > most) {
-                most = sum;
-                r.shift = (uint8_t)d;
-            }
-        }
+        // arrays.  Where they do not, the states' sets the shift.
+        r.shift = (uint8_t)(m / 4 % zk::kVec);
         r.gshift = (uint8_t)(g / gs % zk::kVec);
         auto on = [&](uintptr_t at, uintptr_t elem, uintptr_t vector) {
             return at == 0 || (at - r.shift * elem) % vector == 0;  // an array that is not there is in no one's way
