@@ -732,9 +732,10 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
 // onto one by a shift of the work, as in the 32-bit update: they are copied
 // from the boundary before, taken over by as many elements, and the results
 // turned round in shared memory so that neighbouring lanes store neighbouring
-// elements (GB300, 91e6 elements in 150 tensors at odd offsets: 467 us, aligned
-// 408; read by plain loads 588).  A tensor's last few elements, and its first 16
-// if they are not on a boundary, are read by plain loads.
+// pairs (GB300, 91e6 elements in 150 tensors at odd offsets: 424 us, aligned 408;
+// stored one by one 467, read by plain loads as well 588).  A tensor's last few
+// elements, and its first 16 if they are not on a boundary, are read by plain
+// loads.
 constexpr int kLane8 = 16;
 constexpr int kItem8 = 32 * kLane8;
 constexpr int kWarps8 = kChunk / kItem8;
@@ -880,6 +881,46 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return r;
 }
 
+// Up to 512 parameters of a tensor from w0 on out of shared memory, and their
+// 16-bit copies: neighbouring lanes store neighbouring pairs, which begin one
+// element later where the addresses are odd.
+template <class O>
+__device__ __forceinline__ void store_turned(const MultiRow& r, const float* turn, int64_t w0, int some) {
+    const int lane = threadIdx.x & 31;
+    float* const p = r.master + w0;
+    uint16_t* const o = r.out + w0;
+    const int odd = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(float) & 1);
+    const bool pairs = !O::kOut || (int)(reinterpret_cast<uintptr_t>(o) / sizeof(uint16_t) & 1) == odd;
+    auto one = [&](int e) {
+        p[e] = turn[e];
+        if constexpr (O::kOut) o[e] = O::enc1(turn[e]);
+    };
+    if (pairs) {
+        float q[kLane8];
+#pragma unroll
+        for (int j = 0; j < kLane8 / 2; ++j) {
+            const int e = 64 * j + 2 * lane + odd;
+            q[2 * j] = turn[e];
+            q[2 * j + 1] = turn[min(e + 1, kItem8 - 1)];
+        }
+#pragma unroll
+        for (int j = 0; j < kLane8 / 2; ++j) {
+            const int e = 64 * j + 2 * lane + odd;
+            if (e + 1 < some) {
+                __stcs(reinterpret_cast<float2*>(p + e), make_float2(q[2 * j], q[2 * j + 1]));
+                if constexpr (O::kOut) __stcs(reinterpret_cast<uint32_t*>(o + e), O::pack(q[2 * j], q[2 * j + 1]));
+            }
+        }
+        // what the pairs leave: the first element where they begin at the second, and the last
+        if (lane == 0 && odd && some > 0) one(0);
+        if (lane == 1 && some > odd && ((some - odd) & 1)) one(some - 1);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kLane8; ++j)
+            if (32 * j + lane < some) one(32 * j + lane);
+    }
+}
+
 template <class G, class O>
 __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid_constant__ MultiArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -1012,17 +1053,7 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
             }
             if (turned) {
                 __syncwarp();
-                float q[kLane8];
-#pragma unroll
-                for (int j = 0; j < kLane8; ++j) q[j] = sh.turn[warp][32 * j + lane];
-#pragma unroll
-                for (int j = 0; j < kLane8; ++j) {
-                    const int64_t e = w0 + 32 * j + lane;
-                    if (32 * j + lane < some) {
-                        r.master[e] = q[j];
-                        if constexpr (O::kOut) r.out[e] = O::enc1(q[j]);
-                    }
-                }
+                store_turned<O>(r, sh.turn[warp], w0, some);
                 __syncwarp();
             }
             const uint32_t bm = block_scale16<E4m3>(m), bv = block_scale16<E5m2>(v);
