@@ -77,6 +77,13 @@ class BoundList:
         B.zero_multi_bind(self.M, self.workspace, stream, **arrays)
 
 
+def _stream_handle(owner):
+    """A function that gives the handle of ``owner.stream``, torch's current
+    stream if that is None."""
+    index, raw = owner.device.index, torch._C._cuda_getCurrentRawStream
+    return lambda: raw(index) if owner.stream is None else owner.stream.cuda_stream
+
+
 class StateCodec8:
     """The 32-bit states ``m``, ``v`` (lists of fp32 tensors) and the 8-bit
     ones ``m8`` (float8_e4m3fn), ``v8`` (float8_e5m2), ``m8_scale`` and
@@ -98,15 +105,16 @@ class StateCodec8:
         self._keep = (m, v, m8, m8_scale, v8, v8_scale)
         self._list = BoundList(numels, None, 1, B.ZERO_BF16, B.ZERO_NO_OUT, device)
         self._list.bind(self._s(), m=m, v=v, m8=m8, m8_scale=m8_scale, v8=v8, v8_scale=v8_scale)
+        self._lib, self._M, self._handle = B.lib(), self._list.M.handle, _stream_handle(self)
 
     def _s(self):
         return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
 
     def encode(self) -> None:
-        B.zero_multi_encode8(self._list.M, self._s())
+        B._check(self._lib.zero_multi_encode8(self._M, self._handle()))
 
     def decode(self) -> None:
-        B.zero_multi_decode8(self._list.M, self._s())
+        B._check(self._lib.zero_multi_decode8(self._M, self._handle()))
 
 
 class MultiAdamW:
@@ -179,11 +187,7 @@ class MultiAdamW:
         steps already converted: a short step costs the host a few microseconds,
         most of them spent on arguments otherwise."""
         lib, M, st = B.lib(), self._list.M.handle, ctypes.c_void_p(self.state.data_ptr())
-        hp = self._hp
-        index, raw = self.device.index, torch._C._cuda_getCurrentRawStream
-
-        def handle():
-            return raw(index) if self.stream is None else self.stream.cuda_stream
+        hp, handle = self._hp, _stream_handle(self)
 
         def norm():
             B._check(lib.zero_multi_grad_norm(M, self.max_norm, st, handle()))
