@@ -109,6 +109,26 @@ def test_accumulated_micro_batches_equal_one_batch_of_their_sum(stage):
     assert a.read_state()["t"] == b.read_state()["t"] == 1
 
 
+@pytest.mark.parametrize("stage", [1, 2, 3])
+def test_a_whole_step_of_an_accumulating_engine_is_one_batch(stage):
+    c = Case([3000, 500, 41], 2, stage, FMT_BF16, units=[0, 1, 1] if stage == 3 else None, grad_std=1e-2)
+    L = c.layout()
+    a, b = _engine(c, n_micro=2), _engine(c)
+    for e in (a, b):
+        e.load_master(torch.from_numpy(c.master0(L)))
+    for step in (1, 2, 3):
+        for e in (a, b):
+            _feed(e, c, L, step)
+        if step < 3:
+            a.step()
+        else:
+            a.capture().replay()
+        b.step()
+        for x, y in ((a.gshard, b.gshard), (a.master, b.master), (a.m, b.m), (a.v, b.v), (a.m_scale, b.m_scale)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), step
+        assert a.read_state() == b.read_state()
+
+
 def test_captured_step_and_transients():
     c = CASES["zero3_bf16"]
     L = c.layout()

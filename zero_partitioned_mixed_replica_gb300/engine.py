@@ -258,15 +258,15 @@ class ZeroStep:
         enqueued.  With 8-bit states the calls are issued from here, in the
         same order."""
         if self.state_bits == 8:
-            self._reduce8(0)
+            self._reduce8(0, 1)          # one batch, whatever n_micro, as zero_step's
             self._update8()
             return
         B.zero_step(self.L, self.step_args(), self._s())
 
     # -- 8-bit states: the split step's calls, with the list update on the shards --------
-    def _reduce8(self, micro: int) -> None:
-        """Reduce micro-batch ``micro`` as zero_micro_step does."""
-        L, s, M = self.L, self._s(), self.n_micro
+    def _reduce8(self, micro: int, M: int) -> None:
+        """Reduce micro-batch ``micro`` of ``M`` as zero_micro_step does."""
+        L, s = self.L, self._s()
         if self.stage == 1 and M > 1:
             B.zero_accumulate_grads(L, micro, self.grad_rows, self.acc_rows, s)
             if micro == M - 1:
@@ -389,7 +389,7 @@ class ZeroStep:
         if not 0 <= micro < M:
             raise ValueError("micro out of range")
         if self.state_bits == 8:
-            self._reduce8(micro)
+            self._reduce8(micro, M)
             if micro == M - 1:
                 self._update8()
             return
