@@ -355,6 +355,24 @@ def test_loaded_states_come_back_and_the_width_can_change():
     assert all(torch.equal(a, b) for a, b in zip(m + v, m2 + v2))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_loaded_states_outlast_a_step_under_way_on_another_stream(bits):
+    stream = torch.cuda.Stream()
+    s = Setup(SIZES + [500_000], "bf16", "bf16", bits, decide=False, stream=stream)
+    m = [x.contiguous().cuda() * 2 for x in _views(s.m, s.offs, s.sizes)]
+    v = [x.contiguous().cuda() * 2 for x in _views(s.v, s.offs, s.sizes)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+    s.opt.step()
+    s.opt.load_states(m, v)
+    torch.cuda.synchronize()
+    got_m, got_v = s.opt.states32()
+    for got, want, kind in ((got_m, m, R.E4M3), (got_v, v, R.E5M2)):
+        for a, b in zip(got, want):
+            assert torch.equal(a.cpu(), b.cpu() if bits == 32 else R.decode_ref(*R.encode_ref(b.cpu(), kind)))
+
+
 # -- the step's decision ----------------------------------------------------------------------------------------
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 3e38])

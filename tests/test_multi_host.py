@@ -1,0 +1,50 @@
+"""The host side of MultiAdamW, StateCodec8 and the 8-bit engine without a GPU: the order of work between streams, what
+is kept alive and for how long, and what is refused.  Streams, tensors and the library are stand-ins that write a log."""
+import torch
+
+from zero_partitioned_mixed_replica_gb300 import multi
+
+
+class Stream:
+    def __init__(self, name, log):
+        self.name, self.log = name, log
+
+    def wait_stream(self, other):
+        if other is not self:
+            self.log.append("%s waits for %s" % (self.name, other.name))
+
+
+class Tensor:
+    """Whatever touches its elements does so on the current stream."""
+
+    def __init__(self, log):
+        self.log = log
+
+    def copy_(self, other):
+        self.log.append("write")
+
+    def clone(self):
+        self.log.append("read")
+        return self
+
+
+def _wide(monkeypatch, own_stream):
+    """A MultiAdamW with 32-bit states on a stream of its own or on the current one, and the log."""
+    log = []
+    cur = Stream("current", log)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: cur)
+    monkeypatch.setattr(multi, "_check_list", lambda *a: None)
+    opt = multi.MultiAdamW.__new__(multi.MultiAdamW)
+    opt.device, opt.state_bits, opt.numels = torch.device("cuda", 0), 32, [5, 6]
+    opt.stream = Stream("own", log) if own_stream else None
+    opt.m, opt.v = [Tensor(log), Tensor(log)], [Tensor(log), Tensor(log)]
+    return opt, log
+
+
+def test_loading_waits_for_the_step_under_way_and_the_next_step_for_the_loading(monkeypatch):
+    opt, log = _wide(monkeypatch, own_stream=True)
+    opt.load_states([0, 0], [0, 0])
+    assert log == ["current waits for own"] + 4 * ["write"] + ["own waits for current"]
+    opt, log = _wide(monkeypatch, own_stream=False)
+    opt.load_states([0, 0], [0, 0])
+    assert log == 4 * ["write"]

@@ -286,11 +286,14 @@ class MultiAdamW:
     def load_states(self, m: Sequence[torch.Tensor], v: Sequence[torch.Tensor]) -> None:
         """Take the states from fp32 tensors (nearest 8-bit values)."""
         if self.state_bits == 32:
-            for name, src, dst in (("m", m, self.m), ("v", v, self.v)):
+            for name, src in (("m", m), ("v", v)):
                 _check_list(name, src, self.numels, (torch.float32,), self.device)
+            cur = torch.cuda.current_stream(self.device)
+            cur.wait_stream(self._s())       # a step under way on a stream of its own
+            for src, dst in ((m, self.m), (v, self.v)):
                 for a, b in zip(src, dst):
                     b.copy_(a)
-            self._s().wait_stream(torch.cuda.current_stream(self.device))
+            self._s().wait_stream(cur)
         else:
             self._codec(m, v).encode()
             # the codec's workspace, and the caller's m and v, may be freed after this on the current stream
