@@ -373,6 +373,22 @@ def test_loaded_states_outlast_a_step_under_way_on_another_stream(bits):
             assert torch.equal(a.cpu(), b.cpu() if bits == 32 else R.decode_ref(*R.encode_ref(b.cpu(), kind)))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_that_are_read_are_those_of_one_step(bits):
+    # the copies are held up on the current stream while the next step, on another one, is already issued
+    stream = torch.cuda.Stream()
+    s, other = (Setup(SIZES + [500_000], "bf16", "bf16", bits, decide=False, stream=x) for x in (stream, None))
+    other.opt.step()
+    want = other.opt.states32()
+    torch.cuda.synchronize()
+    s.opt.step()
+    torch.cuda._sleep(20_000_000)
+    got = s.opt.states32()
+    s.opt.step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got[0] + got[1], want[0] + want[1]))
+
+
 # -- the step's decision ----------------------------------------------------------------------------------------
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 3e38])

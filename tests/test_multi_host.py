@@ -48,3 +48,12 @@ def test_loading_waits_for_the_step_under_way_and_the_next_step_for_the_loading(
     opt, log = _wide(monkeypatch, own_stream=False)
     opt.load_states([0, 0], [0, 0])
     assert log == 4 * ["write"]
+
+
+def test_the_next_step_waits_for_states_that_are_read(monkeypatch):
+    opt, log = _wide(monkeypatch, own_stream=True)
+    opt.states32()
+    assert log == ["current waits for own"] + 4 * ["read"] + ["own waits for current"]
+    opt, log = _wide(monkeypatch, own_stream=False)
+    opt.states32()
+    assert log == 4 * ["read"]

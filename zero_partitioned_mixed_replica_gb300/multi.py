@@ -277,7 +277,9 @@ class MultiAdamW:
         cur = torch.cuda.current_stream(self.device)
         if self.state_bits == 32:
             cur.wait_stream(self._s())
-            return [x.clone() for x in self.m], [x.clone() for x in self.v]
+            copies = [x.clone() for x in self.m], [x.clone() for x in self.v]
+            self._s().wait_stream(cur)       # the next step, on a stream of its own
+            return copies
         m, v = (_slices(self.numels, torch.float32, self.device) for _ in range(2))
         self._codec(m, v).decode()
         cur.wait_stream(self._s())
