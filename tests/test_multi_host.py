@@ -1,8 +1,9 @@
 """The host side of MultiAdamW, StateCodec8 and the 8-bit engine without a GPU: the order of work between streams, what
 is kept alive and for how long, and what is refused.  Streams, tensors and the library are stand-ins that write a log."""
+import pytest
 import torch
 
-from zero_partitioned_mixed_replica_gb300 import multi
+from zero_partitioned_mixed_replica_gb300 import engine, multi
 
 
 class Stream:
@@ -57,3 +58,14 @@ def test_the_next_step_waits_for_states_that_are_read(monkeypatch):
     opt, log = _wide(monkeypatch, own_stream=False)
     opt.states32()
     assert log == 4 * ["read"]
+
+
+def test_the_executor_never_gets_8_bit_states(monkeypatch):
+    # it would read and write four bytes an element of them
+    eng = engine.ZeroStep.__new__(engine.ZeroStep)
+    eng.state_bits, eng._args, eng.hp, eng.transient_hook = 8, "arguments", None, None
+    eng._args_hp = eng._args_hook = None
+    with pytest.raises(ValueError, match="8-bit"):
+        eng.step_args()
+    eng.state_bits = 32
+    assert eng.step_args() == "arguments"

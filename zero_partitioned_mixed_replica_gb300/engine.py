@@ -224,7 +224,9 @@ class ZeroStep:
         """This engine's buffers and settings as the library's zero_step_args
         (built once, as the buffers never move; built again if ``hp`` is
         replaced by another object), with ``transient_hook`` installed as the
-        executor's unit hook."""
+        executor's unit hook.  The executor's calls take 32-bit states."""
+        if self.state_bits == 8:
+            raise ValueError("the step executor updates 32-bit states: an engine with 8-bit states steps by step() and micro_step()")
         if getattr(self, "_args", None) is None or self._args_hp is not self.hp:
             self._args_hp = self.hp
             self._args_hook = None
