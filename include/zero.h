@@ -673,7 +673,11 @@ void zero_multi_destroy(zero_multi* M);
  * the work into `workspace` (at least info.workspace_bytes) by kernels on
  * `stream`, which the calls on M have to follow.  The pointer arrays are read
  * during the call only.  May be called again, with other addresses or another
- * workspace (gradients that move): it costs a few short launches. */
+ * workspace (gradients that move): it costs a few short launches.
+ * Launches recorded into a graph read addresses and the map of the work from
+ * the workspace they were recorded with: after another bind into it, replays
+ * run on the tensors of that bind, which has to give every array that the
+ * recorded calls use.  hp, flags, seed and max_norm stay those of the recording. */
 zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays* arrays, void* workspace,
                               zero_stream_t stream);
 

@@ -499,6 +499,42 @@ def test_binding_between_the_norm_and_the_update_keeps_the_scale():
     _check32(s, 1, 1.0)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", [[2048, 2048, 5000], [2048] * 3000, [1, 4096, 0, 2047]], ids=["few", "many", "mixed"])
+def test_a_replay_follows_gradients_that_moved(bits, sizes):
+    """Recorded with gradients at one distance from a boundary and replayed with them at others, which give a list other
+    numbers of tiles: what the same calls give without a recording, bit for bit."""
+    from zero_partitioned_mixed_replica_gb300 import multi
+    gen = torch.Generator("cuda").manual_seed(9)
+    starts = np.concatenate([[0], np.cumsum(sizes)]).tolist()
+    r = lambda: torch.randn(starts[-1], generator=gen, device="cuda")  # noqa: E731
+    g, p = (r() * 1e-3).bfloat16(), r() * 0.02
+    room = [-(-(n + 8) // 8) * 8 for n in sizes]
+
+    def grads(off):                              # every tensor `off` elements behind a boundary
+        buf, views, at = torch.zeros(sum(room), dtype=g.dtype, device="cuda"), [], off
+        for n, k, o in zip(sizes, room, starts):
+            views.append(buf[at:at + n])
+            views[-1].copy_(g[o:o + n])
+            at += k
+        return views
+
+    def run(first, moves, graph):
+        q = [p[o:o + n].clone() for o, n in zip(starts, sizes)]
+        opt = multi.MultiAdamW(q, grads(first), [x.bfloat16() for x in q], state_bits=bits, max_norm=0.05)
+        step = opt.capture().replay if graph else opt.step
+        for off in moves:
+            opt.rebind_grads(grads(off))
+            step()
+        st = opt.read_state()
+        assert (st["t"], st["error"]) == (len(moves), 0)
+        return q + opt.out16 + [x.view(torch.uint8) for x in opt.m + opt.v] + [opt.state]
+
+    for first, moves in ((0, (1, 0, 5)), (1, (0, 0, 7)), (3, (4, 3, 0))):
+        for a, b in zip(run(first, moves, True), run(first, moves, False)):
+            assert torch.equal(a, b), (first, moves)
+
+
 def test_rebound_gradients_are_used():
     s = Setup(SIZES, "bf16", "bf16", 32, decide=False)
     s.g = s.g * 2

@@ -51,7 +51,9 @@ struct MultiRow {
 constexpr int kRowWords = sizeof(MultiRow) / 8;
 static_assert(kRowWords == 12 && kRowWords <= 32, "a warp reads a row");
 
-// The device workspace: counters, rows, chunk map, norm partials.
+// The device workspace: counters, rows, chunk map, norm partials.  How many chunks
+// a list has goes by where its tensors begin, so a bind writes the count there
+// too: launches recorded into a graph find what the last bind gave.
 struct MultiTable {
     uint32_t* counters;      // CTAs that are done: [0] norm, [1] others; [2] tiles dealt; [3] errors of the codec;
                              // [4] CTAs that have read the state
@@ -59,7 +61,8 @@ struct MultiTable {
     const uint32_t* tensor;  // tensor of each chunk
     float2* partials;        // kSlices
     float* grad_scale;       // the loss scale that the gradients of the last norm carried
-    uint32_t n_chunks;
+    const uint32_t* n_chunks;
+    uint32_t most_chunks;    // wherever the tensors begin: places of the map
     uint32_t n_tensors;
     uint64_t slack;          // bounds-checked builds: test hook
 };
@@ -89,13 +92,14 @@ struct RowBatch {
     MultiRow rows[kRowsPerLaunch];
 };
 
-__global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n) {
+__global__ void multi_rows_kernel(const __grid_constant__ RowBatch b, MultiRow* rows, int n, uint32_t* count, uint32_t n_chunks) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < n) rows[i] = b.rows[i];
+    if (i == 0) *count = n_chunks;
 }
 
-// The last kernel of a bind: whatever begins while it ends finds the rows and
-// the map whole, since it began after their kernels' end.
+// The last kernel of a bind: whatever begins while it ends finds the rows, the
+// count and the map whole, since it began after their kernels' end.
 __global__ void multi_reset_kernel(uint32_t* counters, float* grad_scale) {
     if (threadIdx.x < 5) counters[threadIdx.x] = 0;
     if (threadIdx.x == 0 && grad_scale) *grad_scale = 0.0f;
@@ -453,7 +457,15 @@ template <int S, class Stage, class Issue, class Ready>
 __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, Stage* stage, Ring<S>& ring, Issue issue,
                                            Ready ready) {
     const int lane = threadIdx.x & 31;
-    const uint32_t n = t.n_chunks, own = S * gridDim.x;
+    const uint32_t own = S * gridDim.x;
+    // the count and the first tiles' tensors arrive together
+    const uint32_t n = *t.n_chunks;
+    uint32_t tensor[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const uint32_t c = blockIdx.x + j * gridDim.x;
+        tensor[j] = c < t.most_chunks ? t.tensor[c] : 0u;  // what an earlier bind has left, behind the count
+    }
     auto tensor_of = [&](uint32_t c) { return c < n ? t.tensor[c] : 0u; };
     auto word_of = [&](uint32_t i) {
         return lane < kRowWords ? reinterpret_cast<const unsigned long long*>(t.rows + i)[lane] : 0ull;
@@ -471,12 +483,9 @@ __device__ __forceinline__ void ring_fetch(const MultiTable& t, int32_t* error, 
         }
     };
     auto deal = [&]() { return lane == 0 ? own + atomicAdd(&t.counters[2], 1u) : 0u; };  // lane 0 has it
-    uint32_t tensor[S];
     unsigned long long word[S];
 #pragma unroll
-    for (int j = 0; j < S; ++j) tensor[j] = tensor_of(blockIdx.x + j * gridDim.x);
-#pragma unroll
-    for (int j = 0; j < S; ++j) word[j] = word_of(tensor[j]);
+    for (int j = 0; j < S; ++j) word[j] = word_of(blockIdx.x + j * gridDim.x < n ? tensor[j] : 0u);
     grid_wait();
     uint32_t k = 0;  // tiles put
     bool end = false;
@@ -1274,14 +1283,15 @@ __device__ __forceinline__ float2 sum_pairs(float hi, float lo, float2* sh) {
 
 template <class G>
 __global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_constant__ MultiTable t, double max_norm,
-                                                              zero_step_state* st, uint32_t n_slices) {
+                                                              zero_step_state* st) {
     __shared__ float2 sh[kThreads / 32];
     __shared__ bool last;
+    const uint32_t n_chunks = *t.n_chunks, n_slices = max(1u, min(n_chunks, (uint32_t)kSlices));
     grid_wait();
     for (uint32_t sl = blockIdx.x; sl < n_slices; sl += gridDim.x) {
         // the slice's chunks, tensor by tensor
-        const uint32_t c1 = (uint32_t)((uint64_t)(sl + 1) * t.n_chunks / n_slices);
-        uint32_t c = (uint32_t)((uint64_t)sl * t.n_chunks / n_slices);
+        const uint32_t c1 = (uint32_t)((uint64_t)(sl + 1) * n_chunks / n_slices);
+        uint32_t c = (uint32_t)((uint64_t)sl * n_chunks / n_slices);
         float hi = 0.0f, lo = 0.0f;
         while (c < c1) {
             const uint32_t n = t.tensor[c];
@@ -1388,7 +1398,7 @@ struct zero_multi {
     int32_t n_groups = 0, grad_dtype = 0, param_dtype = 0;
     int64_t most_chunks = 0;  // wherever the tensors begin
     // the last bind
-    int64_t n_chunks = 0;
+    int64_t n_chunks = 0;  // for the grid; the kernels go by the count in the workspace
     bool bound = false, grads = false, master = false, states32 = false, states8 = false, param16 = false;
     char* workspace = nullptr;
 };
@@ -1401,7 +1411,7 @@ int64_t chunks_of(int64_t numel, int64_t shift) {
     return numel > 0 ? (numel + shift + zk::kChunk - 1) / zk::kChunk : 0;
 }
 
-// Workspace layout: counters and the gradients' scale (256 bytes), rows, chunk map, norm partials.
+// Workspace layout: counters, the gradients' scale and the count of chunks (256 bytes), rows, chunk map, norm partials.
 struct Places {
     int64_t rows, map, partials, total;
 };
@@ -1422,7 +1432,8 @@ zk::MultiTable table_of(const zero_multi* M) {
     t.rows = reinterpret_cast<const zk::MultiRow*>(M->workspace + p.rows);
     t.tensor = reinterpret_cast<const uint32_t*>(M->workspace + p.map);
     t.partials = reinterpret_cast<float2*>(M->workspace + p.partials);
-    t.n_chunks = (uint32_t)M->n_chunks;
+    t.n_chunks = reinterpret_cast<const uint32_t*>(M->workspace + 192);
+    t.most_chunks = (uint32_t)M->most_chunks;
     t.n_tensors = (uint32_t)M->numels.size();
     t.slack = (uint64_t)check_slack();
     return t;
@@ -1499,21 +1510,21 @@ int ring_grid(Kernel kern, int64_t tiles, size_t smem, int threads) {
 }
 
 template <class G, class O>
-zero_status_t launch_update(bool eight, const zk::MultiArgs& a, cudaStream_t s) {
+zero_status_t launch_update(const zero_multi* M, bool eight, const zk::MultiArgs& a, cudaStream_t s) {
     const char* what = eight ? "zero_multi_adamw8" : "zero_multi_adamw";
     const size_t smem = eight ? sizeof(zk::Smem8<G>) : sizeof(zk::Smem32<G>);
     const int threads = eight ? zk::kThreads8 : zk::kThreads32;
     void (*kern)(zk::MultiArgs) = eight ? zk::multi_adamw8_kernel<G, O> : zk::multi_adamw_kernel<G, O>;
     const zero_status_t rc = allow_smem(kern, smem, what);
     if (rc != ZERO_OK) return rc;
-    return launch_early(kern, ring_grid(kern, a.t.n_chunks, smem, threads), threads, smem, s, what, a);
+    return launch_early(kern, ring_grid(kern, M->n_chunks, smem, threads), threads, smem, s, what, a);
 }
 
 template <class G>
 zero_status_t launch_update_out(const zero_multi* M, bool eight, const zk::MultiArgs& a, cudaStream_t s) {
-    if (M->param_dtype == ZERO_BF16) return launch_update<G, zk::OutBf16>(eight, a, s);
-    if (M->param_dtype == ZERO_FP16) return launch_update<G, zk::OutFp16>(eight, a, s);
-    return launch_update<G, zk::NoOut>(eight, a, s);
+    if (M->param_dtype == ZERO_BF16) return launch_update<G, zk::OutBf16>(M, eight, a, s);
+    if (M->param_dtype == ZERO_FP16) return launch_update<G, zk::OutFp16>(M, eight, a, s);
+    return launch_update<G, zk::NoOut>(M, eight, a, s);
 }
 
 zero_status_t update(const zero_multi* M, const zero_adamw_hp* hp, int32_t flags, uint32_t seed, zero_step_state* st,
@@ -1549,7 +1560,7 @@ zero_status_t codec(const zero_multi* M, zero_stream_t stream, bool encode, cons
     void (*kern)(zk::MultiTable) = encode ? zk::multi_codec_kernel<true> : zk::multi_codec_kernel<false>;
     const size_t smem = encode ? sizeof(zk::SmemCodec<zk::StageEncode>) : sizeof(zk::SmemCodec<zk::StageDecode>);
     if ((rc = allow_smem(kern, smem, what)) != ZERO_OK) return rc;
-    return launch_early(kern, ring_grid(kern, t.n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
+    return launch_early(kern, ring_grid(kern, M->n_chunks, smem, zk::kThreads8), zk::kThreads8, smem,
                         reinterpret_cast<cudaStream_t>(stream), what, t);
 }
 
@@ -1691,16 +1702,17 @@ extern "C" zero_status_t zero_multi_bind(zero_multi* M, const zero_multi_arrays*
     const zk::MultiTable t = table_of(M);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     zk::MultiRow* dst = const_cast<zk::MultiRow*>(t.rows);
+    uint32_t* count = const_cast<uint32_t*>(t.n_chunks);
     for (int i = 0; i < n; i += zk::kRowsPerLaunch) {
         zk::RowBatch b{};
         const int k = std::min(zk::kRowsPerLaunch, n - i);
         std::copy(rows.begin() + i, rows.begin() + i + k, b.rows);
-        zk::multi_rows_kernel<<<1, zk::kRowsPerLaunch, 0, s>>>(b, dst + i, k);
+        zk::multi_rows_kernel<<<1, zk::kRowsPerLaunch, 0, s>>>(b, dst + i, k, count, (uint32_t)chunk);
         if ((rc = after_launch(what)) != ZERO_OK) return rc;
     }
-    if (t.n_chunks > 0) {
-        const uint32_t ctas = std::min<uint32_t>((t.n_chunks + 255) / 256, 1024);
-        zk::multi_map_kernel<<<ctas, 256, 0, s>>>(t.rows, t.n_tensors, const_cast<uint32_t*>(t.tensor), t.n_chunks);
+    if (chunk > 0) {
+        const uint32_t ctas = (uint32_t)std::min<int64_t>((chunk + 255) / 256, 1024);
+        zk::multi_map_kernel<<<ctas, 256, 0, s>>>(t.rows, t.n_tensors, const_cast<uint32_t*>(t.tensor), (uint32_t)chunk);
         if ((rc = after_launch(what)) != ZERO_OK) return rc;
     }
     zk::multi_reset_kernel<<<1, 32, 0, s>>>(t.counters, fresh ? t.grad_scale : nullptr);
@@ -1724,10 +1736,10 @@ extern "C" zero_status_t zero_multi_grad_norm(const zero_multi* M, double max_no
     if (!M->grads) return missing(what, "grads");
     if ((rc = check_dev_ptr(st, "zero_multi_grad_norm state")) != ZERO_OK) return rc;
     const zk::MultiTable t = table_of(M);
-    const uint32_t slices = std::max<uint32_t>(1, std::min<uint32_t>(t.n_chunks, zk::kSlices));
+    const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(M->n_chunks, zk::kSlices));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto go = [&](auto kern) {
-        return launch_early(kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st, slices);
+        return launch_early(kern, persistent_grid(kern, slices), zk::kThreads, 0, s, what, t, max_norm, st);
     };
     if (M->grad_dtype == ZERO_BF16) return go(zk::multi_norm_kernel<zk::GradBf16>);
     if (M->grad_dtype == ZERO_FP16) return go(zk::multi_norm_kernel<zk::GradFp16>);

@@ -251,8 +251,10 @@ class MultiAdamW:
             self._update(B.ZERO_MULTI_ADVANCE)
 
     def capture(self) -> torch.cuda.CUDAGraph:
-        """Record one step into a CUDA graph; replaying it runs one step (with
-        the hyperparameters of the recording)."""
+        """Record one step into a CUDA graph; replaying it runs one step, with
+        the hyperparameters of the recording and the gradients of the last
+        :meth:`rebind_grads`.  Replays and the object's other calls are
+        ordered like any work: on one stream, or by waits."""
         g = torch.cuda.CUDAGraph()
         side = torch.cuda.Stream(self.device)
         side.wait_stream(torch.cuda.current_stream(self.device))
