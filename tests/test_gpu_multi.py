@@ -545,6 +545,36 @@ def test_rebound_gradients_are_used():
     _check32(s, 1, 1.0)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_objects_may_go_while_their_work_on_another_stream_is_under_way(bits):
+    import gc
+    from zero_partitioned_mixed_replica_gb300 import multi
+    results = []
+    for stream in (None, torch.cuda.Stream()):
+        s = Setup(SIZES + [500_000], "bf16", "bf16", bits, decide=False, stream=stream)
+        sizes = [x.numel() for x in s.opt.m] + [s.opt._list.workspace.numel()]
+        m = [torch.zeros(n, device="cuda") for n in s.sizes]
+        v = [torch.zeros(n, device="cuda") for n in s.sizes]
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+        moved = _views(s.dg.clone(), s.offs, s.sizes)
+        s.opt.rebind_grads(moved)
+        s.opt.step()
+        if bits == 8:
+            multi.StateCodec8(m, v, s.opt.m, s.opt.m_scale, s.opt.v, s.opt.v_scale, stream).decode()
+        else:
+            s.opt.rebind_grads(_views(s.dg, s.offs, s.sizes))
+        del moved, s.opt
+        gc.collect()
+        junk = [torch.full((n * k,), 255, dtype=torch.uint8, device="cuda") for n in sizes for k in (1, 2, 4)]
+        torch.cuda.synchronize()
+        results.append([s.dp, s.dout] + (m + v if bits == 8 else [s.dm, s.dv]))
+        del junk
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_refusals():
     from zero_partitioned_mixed_replica_gb300 import binding as B
     from zero_partitioned_mixed_replica_gb300 import multi

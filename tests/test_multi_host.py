@@ -28,6 +28,14 @@ class Tensor:
         self.log.append("read")
         return self
 
+    device, dtype = torch.device("cuda", 0), torch.float32
+
+    def numel(self):
+        return 5
+
+    def record_stream(self, stream):
+        self.streams = getattr(self, "streams", []) + [stream]
+
 
 def _wide(monkeypatch, own_stream):
     """A MultiAdamW with 32-bit states on a stream of its own or on the current one, and the log."""
@@ -69,3 +77,35 @@ def test_the_executor_never_gets_8_bit_states(monkeypatch):
         eng.step_args()
     eng.state_bits = 32
     assert eng.step_args() == "arguments"
+
+
+class List:
+    """A bound list that only keeps what it was bound with."""
+
+    def __init__(self, *a):
+        self.M = type("Handle", (), {"handle": 1})
+        self.workspace = Tensor([])
+
+    def bind(self, stream, **arrays):
+        self.arrays = arrays
+
+
+def _codec(monkeypatch, stream):
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream("current", []))
+    monkeypatch.setattr(multi, "_check_list", lambda *a: None)
+    monkeypatch.setattr(multi, "BoundList", List)
+    monkeypatch.setattr(multi.B, "lib", lambda: None)
+    return multi.StateCodec8(*[[Tensor([]), Tensor([])] for _ in range(6)], stream)
+
+
+def test_memory_in_use_on_another_stream_is_not_given_away_with_the_last_reference(monkeypatch):
+    own = Stream("own", [])
+    for stream in (own, None):
+        codec = _codec(monkeypatch, stream)
+        used = [codec._list.workspace] + [x for xs in codec._list.arrays.values() for x in xs]
+        assert len(used) == 13
+        assert all(getattr(x, "streams", []) == ([own] if stream else []) for x in used)
+        opt, _ = _wide(monkeypatch, own_stream=False)
+        opt.stream, opt.master, opt.out16, opt._list, opt.grads = stream, None, None, List(), [Tensor([])]
+        opt.rebind_grads([Tensor([]), Tensor([])])
+        assert all(getattr(x, "streams", []) == ([own] if stream else []) for x in opt._list.arrays["grads"])

@@ -153,6 +153,7 @@ class ZeroStep:
         if state_bits == 8:
             # the rank shards as a list of N_d tensors
             self._list = multi.BoundList([S] * n_d, None, 1, B.ZERO_FP32, dtype, dev)
+            multi.used_on(stream, [self._list.workspace])
             self._list.bind(self._s(), grads=self.gshard_rows, master=self.master_rows, m8=self.m_rows, v8=self.v_rows,
                             m8_scale=self.m_scale_rows, v8_scale=self.v_scale_rows, param16=self.shard16_rows)
         self.hp = B.zero_adamw_hp(lr=adamw.lr, eps=adamw.eps, weight_decay=adamw.weight_decay)

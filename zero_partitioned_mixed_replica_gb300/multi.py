@@ -63,6 +63,16 @@ def _slices(numels: Sequence[int], dtype, device) -> List[torch.Tensor]:
     return [flat[a:a + n] for a, n in zip(starts, numels)]
 
 
+def used_on(stream: Optional[torch.cuda.Stream], *lists) -> None:
+    """Tell torch's allocator that kernels on an object's own stream use these
+    tensors: memory whose last reference goes while they run is given out again
+    only after them."""
+    if stream is not None:
+        for xs in lists:
+            for x in xs or ():
+                x.record_stream(stream)
+
+
 class BoundList:
     """A bound ``zero_multi`` and its workspace."""
 
@@ -104,6 +114,7 @@ class StateCodec8:
         self.stream, self.device = stream, device
         self._keep = (m, v, m8, m8_scale, v8, v8_scale)
         self._list = BoundList(numels, None, 1, B.ZERO_BF16, B.ZERO_NO_OUT, device)
+        used_on(stream, [self._list.workspace], *self._keep)
         self._list.bind(self._s(), m=m, v=v, m8=m8, m8_scale=m8_scale, v8=v8, v8_scale=v8_scale)
         self._lib, self._M, self._handle = B.lib(), self._list.M.handle, _stream_handle(self)
 
@@ -170,6 +181,7 @@ class MultiAdamW:
         self.info = self._list.info
         self.state = torch.zeros(ctypes.sizeof(B.zero_step_state), dtype=torch.uint8, device=self.device)
         self._norm, self._update = self._calls()
+        used_on(stream, [self._list.workspace, self.state], grads, master, out16, self.m, self.v, self.m_scale, self.v_scale)
         self._bind()
         B.zero_state_init(self.state, self.beta1, self.beta2, loss_scale, dynamic_scale, growth_interval, self._s())
 
@@ -230,6 +242,7 @@ class MultiAdamW:
     def rebind_grads(self, grads: Sequence[torch.Tensor]) -> None:
         """Take the gradients from other tensors from the next call on."""
         _check_list("grads", grads, self.numels, (self.grads[0].dtype,), self.device)
+        used_on(self.stream, grads)
         self.grads = grads
         self._bind()
 
