@@ -575,6 +575,27 @@ def test_objects_may_go_while_their_work_on_another_stream_is_under_way(bits):
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_memory_comes_back_with_the_last_reference(bits):
+    import gc
+    s = Setup([100_000, 77], "bf16", "bf16", bits, max_norm=1.0)
+    s.opt.step()
+    torch.cuda.synchronize()
+    gc.collect()
+    gc.disable()
+    try:
+        before = torch.cuda.memory_allocated()
+        kept = s.opt.states32()
+        s.opt.load_states(*kept)
+        del kept
+        assert torch.cuda.memory_allocated() == before
+        held = s.opt._list.workspace.numel() + (sum(x.numel() for x in s.opt.m + s.opt.v) if bits == 8 else 0)
+        del s.opt
+        assert torch.cuda.memory_allocated() <= before - held
+    finally:
+        gc.enable()
+
+
 def test_refusals():
     from zero_partitioned_mixed_replica_gb300 import binding as B
     from zero_partitioned_mixed_replica_gb300 import multi

@@ -1,5 +1,8 @@
 """The host side of MultiAdamW, StateCodec8 and the 8-bit engine without a GPU: the order of work between streams, what
 is kept alive and for how long, and what is refused.  Streams, tensors and the library are stand-ins that write a log."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -32,6 +35,9 @@ class Tensor:
 
     def numel(self):
         return 5
+
+    def data_ptr(self):
+        return 256
 
     def record_stream(self, stream):
         self.streams = getattr(self, "streams", []) + [stream]
@@ -84,7 +90,7 @@ class List:
 
     def __init__(self, *a):
         self.M = type("Handle", (), {"handle": 1})
-        self.workspace = Tensor([])
+        self.workspace, self.info = Tensor([]), None
 
     def bind(self, stream, **arrays):
         self.arrays = arrays
@@ -109,3 +115,27 @@ def test_memory_in_use_on_another_stream_is_not_given_away_with_the_last_referen
         opt.stream, opt.master, opt.out16, opt._list, opt.grads = stream, None, None, List(), [Tensor([])]
         opt.rebind_grads([Tensor([]), Tensor([])])
         assert all(getattr(x, "streams", []) == ([own] if stream else []) for x in opt._list.arrays["grads"])
+
+
+def _adamw(monkeypatch, **kw):
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream("current", []))
+    monkeypatch.setattr(multi, "_check_list", lambda *a: None)
+    monkeypatch.setattr(multi, "BoundList", List)
+    monkeypatch.setattr(multi, "_slices", lambda numels, dtype, device: [Tensor([]) for _ in numels])
+    monkeypatch.setattr(multi.B, "lib", lambda: None)
+    monkeypatch.setattr(multi.B, "zero_state_init", lambda *a: None)
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: Tensor([]))
+    return multi.MultiAdamW([Tensor([])], [Tensor([])], **kw)
+
+
+def test_objects_go_with_their_last_reference(monkeypatch):
+    # and their states' memory with them, not at some later collection of cycles
+    gc.disable()
+    try:
+        for make in (lambda: _codec(monkeypatch, None), lambda: _adamw(monkeypatch), lambda: _adamw(monkeypatch, state_bits=8)):
+            obj = make()
+            gone = weakref.ref(obj)
+            del obj
+            assert gone() is None
+    finally:
+        gc.enable()

@@ -87,11 +87,9 @@ class BoundList:
         B.zero_multi_bind(self.M, self.workspace, stream, **arrays)
 
 
-def _stream_handle(owner):
-    """A function that gives the handle of ``owner.stream``, torch's current
-    stream if that is None."""
-    index, raw = owner.device.index, torch._C._cuda_getCurrentRawStream
-    return lambda: raw(index) if owner.stream is None else owner.stream.cuda_stream
+def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """The handle of a stream, of the device's current one if it is None."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 class StateCodec8:
@@ -116,16 +114,16 @@ class StateCodec8:
         self._list = BoundList(numels, None, 1, B.ZERO_BF16, B.ZERO_NO_OUT, device)
         used_on(stream, [self._list.workspace], *self._keep)
         self._list.bind(self._s(), m=m, v=v, m8=m8, m8_scale=m8_scale, v8=v8, v8_scale=v8_scale)
-        self._lib, self._M, self._handle = B.lib(), self._list.M.handle, _stream_handle(self)
+        self._lib, self._M, self._index = B.lib(), self._list.M.handle, device.index
 
     def _s(self):
         return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
 
     def encode(self) -> None:
-        B._check(self._lib.zero_multi_encode8(self._M, self._handle()))
+        B._check(self._lib.zero_multi_encode8(self._M, _stream_handle(self.stream, self._index)))
 
     def decode(self) -> None:
-        B._check(self._lib.zero_multi_decode8(self._M, self._handle()))
+        B._check(self._lib.zero_multi_decode8(self._M, _stream_handle(self.stream, self._index)))
 
 
 class MultiAdamW:
@@ -180,7 +178,10 @@ class MultiAdamW:
                            _PARAM[out16[0].dtype] if out16 is not None else B.ZERO_NO_OUT, self.device)
         self.info = self._list.info
         self.state = torch.zeros(ctypes.sizeof(B.zero_step_state), dtype=torch.uint8, device=self.device)
-        self._norm, self._update = self._calls()
+        # the calls' arguments that do not change between steps, converted once: a short step costs the
+        # host a few microseconds, most of them spent on arguments otherwise
+        self._lib, self._M, self._index = B.lib(), self._list.M.handle, self.device.index
+        self._st = ctypes.c_void_p(self.state.data_ptr())
         used_on(stream, [self._list.workspace, self.state], grads, master, out16, self.m, self.v, self.m_scale, self.v_scale)
         self._bind()
         B.zero_state_init(self.state, self.beta1, self.beta2, loss_scale, dynamic_scale, growth_interval, self._s())
@@ -194,23 +195,15 @@ class MultiAdamW:
         ``.weight_decay``), read at every step."""
         return self._hp
 
-    def _calls(self):
-        """The library functions with everything that does not change between
-        steps already converted: a short step costs the host a few microseconds,
-        most of them spent on arguments otherwise."""
-        lib, M, st = B.lib(), self._list.M.handle, ctypes.c_void_p(self.state.data_ptr())
-        hp, handle = self._hp, _stream_handle(self)
+    def _norm(self):
+        B._check(self._lib.zero_multi_grad_norm(self._M, self.max_norm, self._st, _stream_handle(self.stream, self._index)))
 
-        def norm():
-            B._check(lib.zero_multi_grad_norm(M, self.max_norm, st, handle()))
-
-        def update(flags):
-            if self.state_bits == 8:
-                B._check(lib.zero_multi_adamw8(M, hp, flags, self.seed & 0xFFFFFFFF, st, handle()))
-            else:
-                B._check(lib.zero_multi_adamw(M, hp, flags, st, handle()))
-
-        return norm, update
+    def _update(self, flags):
+        at = _stream_handle(self.stream, self._index)
+        if self.state_bits == 8:
+            B._check(self._lib.zero_multi_adamw8(self._M, self._hp, flags, self.seed & 0xFFFFFFFF, self._st, at))
+        else:
+            B._check(self._lib.zero_multi_adamw(self._M, self._hp, flags, self._st, at))
 
     def _states(self, m, v, m_scale, v_scale):
         eight = self.state_bits == 8
