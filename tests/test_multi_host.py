@@ -85,6 +85,19 @@ def test_the_executor_never_gets_8_bit_states(monkeypatch):
     assert eng.step_args() == "arguments"
 
 
+class Library:
+    """Calls succeed and note the device that is current."""
+
+    def __init__(self, log, current):
+        self.log, self.current = log, current
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.log.append((name, self.current[-1]))
+            return 0
+        return call
+
+
 class List:
     """A bound list that only keeps what it was bound with."""
 
@@ -96,11 +109,16 @@ class List:
         self.arrays = arrays
 
 
-def _codec(monkeypatch, stream):
+def _stand_in(monkeypatch, library=None):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream("current", []))
+    monkeypatch.setattr(multi, "_current_device", lambda: Tensor.device.index)
     monkeypatch.setattr(multi, "_check_list", lambda *a: None)
     monkeypatch.setattr(multi, "BoundList", List)
-    monkeypatch.setattr(multi.B, "lib", lambda: None)
+    monkeypatch.setattr(multi.B, "lib", lambda: library or Library([], [0]))
+
+
+def _codec(monkeypatch, stream, library=None):
+    _stand_in(monkeypatch, library)
     return multi.StateCodec8(*[[Tensor([]), Tensor([])] for _ in range(6)], stream)
 
 
@@ -112,17 +130,14 @@ def test_memory_in_use_on_another_stream_is_not_given_away_with_the_last_referen
         assert len(used) == 13
         assert all(getattr(x, "streams", []) == ([own] if stream else []) for x in used)
         opt, _ = _wide(monkeypatch, own_stream=False)
-        opt.stream, opt.master, opt.out16, opt._list, opt.grads = stream, None, None, List(), [Tensor([])]
+        opt.stream, opt.master, opt.out16, opt._list, opt.grads, opt._index = stream, None, None, List(), [Tensor([])], 0
         opt.rebind_grads([Tensor([]), Tensor([])])
         assert all(getattr(x, "streams", []) == ([own] if stream else []) for x in opt._list.arrays["grads"])
 
 
-def _adamw(monkeypatch, **kw):
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream("current", []))
-    monkeypatch.setattr(multi, "_check_list", lambda *a: None)
-    monkeypatch.setattr(multi, "BoundList", List)
+def _adamw(monkeypatch, library=None, **kw):
+    _stand_in(monkeypatch, library)
     monkeypatch.setattr(multi, "_slices", lambda numels, dtype, device: [Tensor([]) for _ in numels])
-    monkeypatch.setattr(multi.B, "lib", lambda: None)
     monkeypatch.setattr(multi.B, "zero_state_init", lambda *a: None)
     monkeypatch.setattr(torch, "zeros", lambda *a, **k: Tensor([]))
     return multi.MultiAdamW([Tensor([])], [Tensor([])], **kw)
@@ -139,3 +154,38 @@ def test_objects_go_with_their_last_reference(monkeypatch):
             assert gone() is None
     finally:
         gc.enable()
+
+
+def test_calls_go_to_the_device_of_the_tensors(monkeypatch):
+    """With another device current, a launch would go there with this one's addresses."""
+    current, log = [0], []
+
+    class On:
+        def __init__(self, device):
+            self.index = torch.device(device).index if not isinstance(device, int) else device
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    library = Library(log, current)
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(Tensor, "device", torch.device("cuda", 1))
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    opts = [_adamw(monkeypatch, library, decide=True), _adamw(monkeypatch, library, state_bits=8)]
+    codec = _codec(monkeypatch, None, library)
+    monkeypatch.setattr(multi, "_current_device", lambda: current[-1])
+    monkeypatch.setattr(multi, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(List, "bind", lambda self, stream, **arrays: log.append(("bind", current[-1])))
+    monkeypatch.setattr(multi.B, "zero_state_init", lambda *a: log.append(("init", current[-1])))
+    for opt in opts:
+        opt.step()
+    codec.encode()
+    codec.decode()
+    opts[0].rebind_grads([Tensor([])])
+    assert [n for n, _ in log] == ["zero_multi_grad_norm", "zero_multi_adamw", "zero_multi_adamw8", "zero_multi_encode8",
+                                   "zero_multi_decode8", "bind"]
+    assert {d for _, d in log} == {1} and current == [0]

@@ -16,6 +16,7 @@ by default), as everywhere in this package.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from typing import List, Optional, Sequence
 
 import torch
@@ -87,9 +88,12 @@ class BoundList:
         B.zero_multi_bind(self.M, self.workspace, stream, **arrays)
 
 
-def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
-    """The handle of a stream, of the device's current one if it is None."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _device(index: int):
+    """The library launches on the current device: with this one current."""
+    return nullcontext() if _current_device() == index else torch.cuda.device(index)
 
 
 class StateCodec8:
@@ -113,17 +117,30 @@ class StateCodec8:
         self._keep = (m, v, m8, m8_scale, v8, v8_scale)
         self._list = BoundList(numels, None, 1, B.ZERO_BF16, B.ZERO_NO_OUT, device)
         used_on(stream, [self._list.workspace], *self._keep)
-        self._list.bind(self._s(), m=m, v=v, m8=m8, m8_scale=m8_scale, v8=v8, v8_scale=v8_scale)
-        self._lib, self._M, self._index = B.lib(), self._list.M.handle, device.index
+        with _device(device.index):
+            self._list.bind(self._s(), m=m, v=v, m8=m8, m8_scale=m8_scale, v8=v8, v8_scale=v8_scale)
+        lib = B.lib()
+        self._encode, self._decode, self._M = lib.zero_multi_encode8, lib.zero_multi_decode8, self._list.M.handle
+        self._index, self._several = device.index, torch.cuda.device_count() > 1
 
     def _s(self):
         return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
 
     def encode(self) -> None:
-        B._check(self._lib.zero_multi_encode8(self._M, _stream_handle(self.stream, self._index)))
+        if self._several and _current_device() != self._index:
+            with _device(self._index):
+                return self.encode()
+        status = self._encode(self._M, _raw_stream(self._index) if self.stream is None else self.stream.cuda_stream)
+        if status:
+            B._check(status)
 
     def decode(self) -> None:
-        B._check(self._lib.zero_multi_decode8(self._M, _stream_handle(self.stream, self._index)))
+        if self._several and _current_device() != self._index:
+            with _device(self._index):
+                return self.decode()
+        status = self._decode(self._M, _raw_stream(self._index) if self.stream is None else self.stream.cuda_stream)
+        if status:
+            B._check(status)
 
 
 class MultiAdamW:
@@ -180,11 +197,15 @@ class MultiAdamW:
         self.state = torch.zeros(ctypes.sizeof(B.zero_step_state), dtype=torch.uint8, device=self.device)
         # the calls' arguments that do not change between steps, converted once: a short step costs the
         # host a few microseconds, most of them spent on arguments otherwise
-        self._lib, self._M, self._index = B.lib(), self._list.M.handle, self.device.index
+        lib, eight = B.lib(), state_bits == 8
+        self._grad_norm, self._adamw = lib.zero_multi_grad_norm, lib.zero_multi_adamw8 if eight else lib.zero_multi_adamw
+        self._M = self._list.M.handle
+        self._index, self._several = self.device.index, torch.cuda.device_count() > 1
         self._st = ctypes.c_void_p(self.state.data_ptr())
         used_on(stream, [self._list.workspace, self.state], grads, master, out16, self.m, self.v, self.m_scale, self.v_scale)
         self._bind()
-        B.zero_state_init(self.state, self.beta1, self.beta2, loss_scale, dynamic_scale, growth_interval, self._s())
+        with _device(self._index):
+            B.zero_state_init(self.state, self.beta1, self.beta2, loss_scale, dynamic_scale, growth_interval, self._s())
 
     def _s(self):
         return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
@@ -196,14 +217,24 @@ class MultiAdamW:
         return self._hp
 
     def _norm(self):
-        B._check(self._lib.zero_multi_grad_norm(self._M, self.max_norm, self._st, _stream_handle(self.stream, self._index)))
+        if self._several and _current_device() != self._index:
+            with _device(self._index):
+                return self._norm()
+        status = self._grad_norm(self._M, self.max_norm, self._st, self._handle())
+        if status:
+            B._check(status)
 
     def _update(self, flags):
-        at = _stream_handle(self.stream, self._index)
-        if self.state_bits == 8:
-            B._check(self._lib.zero_multi_adamw8(self._M, self._hp, flags, self.seed & 0xFFFFFFFF, self._st, at))
-        else:
-            B._check(self._lib.zero_multi_adamw(self._M, self._hp, flags, self._st, at))
+        if self._several and _current_device() != self._index:
+            with _device(self._index):
+                return self._update(flags)
+        seed = (self.seed & 0xFFFFFFFF,) if self.state_bits == 8 else ()
+        status = self._adamw(self._M, self._hp, flags, *seed, self._st, self._handle())
+        if status:
+            B._check(status)
+
+    def _handle(self) -> int:
+        return _raw_stream(self._index) if self.stream is None else self.stream.cuda_stream
 
     def _states(self, m, v, m_scale, v_scale):
         eight = self.state_bits == 8
@@ -230,7 +261,8 @@ class MultiAdamW:
             states = dict(m8=self.m, v8=self.v, m8_scale=self.m_scale, v8_scale=self.v_scale)
         else:
             states = dict(m=self.m, v=self.v)
-        self._list.bind(self._s(), grads=self.grads, master=self.master, param16=self.out16, **states)
+        with _device(self._index):
+            self._list.bind(self._s(), grads=self.grads, master=self.master, param16=self.out16, **states)
 
     def rebind_grads(self, grads: Sequence[torch.Tensor]) -> None:
         """Take the gradients from other tensors from the next call on."""
