@@ -596,6 +596,20 @@ def test_memory_comes_back_with_the_last_reference(bits):
         gc.enable()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_update_alone_on_an_object_without_decisions_is_a_step(bits):
+    a, b = (Setup(SIZES, "bf16", "bf16", bits, decide=False) for _ in range(2))
+    a.opt.step(), a.opt.update()
+    b.opt.step(), b.opt.step()
+    assert a.opt.read_state()["t"] == 2
+    assert all(torch.equal(x, y) for x, y in zip(_outputs(a), _outputs(b)))
+    a.opt.grad_norm(), a.opt.update()                # a decision all the same: t moves once
+    assert a.opt.read_state()["t"] == 3
+    a.opt.grad_norm(), a.opt.step()                  # the norm to look at, then a step without a decision
+    a.opt.update()
+    assert a.opt.read_state()["t"] == 6
+
+
 def test_refusals():
     from zero_partitioned_mixed_replica_gb300 import binding as B
     from zero_partitioned_mixed_replica_gb300 import multi

@@ -185,6 +185,7 @@ class MultiAdamW:
         self.decide = (max_norm > 0 or not no_scaler) if decide is None else bool(decide)
         if not self.decide and (max_norm > 0 or dynamic_scale):
             raise ValueError("a step without the norm cannot clip or skip")
+        self._decided = False        # grad_norm was called since the last update
         self.state_bits, self.max_norm, self.seed = state_bits, float(max_norm), int(seed)
         self.beta1, self.beta2 = groups[0].beta1, groups[0].beta2
         self._hp = (B.zero_adamw_hp * len(groups))(*[B.zero_adamw_hp(lr=g.lr, eps=g.eps, weight_decay=g.weight_decay)
@@ -275,11 +276,17 @@ class MultiAdamW:
     def grad_norm(self) -> None:
         """The global norm and the step decision alone (one launch)."""
         self._norm()
+        self._decided = True
 
-    def update(self, flags: int = B.ZERO_MULTI_DECIDED) -> None:
-        """The update alone, after a decision (``grad_norm``) or, with
-        ``ZERO_MULTI_ADVANCE``, without one (one launch)."""
+    def update(self, flags: Optional[int] = None) -> None:
+        """The update alone (one launch): of the step that ``grad_norm`` has
+        decided (``ZERO_MULTI_DECIDED``), or of one without a decision
+        (``ZERO_MULTI_ADVANCE``), which is the default for an object with
+        ``decide=False`` unless ``grad_norm`` was called since its last update."""
+        if flags is None:
+            flags = B.ZERO_MULTI_DECIDED if self.decide or self._decided else B.ZERO_MULTI_ADVANCE
         self._update(flags)
+        self._decided = False
 
     def step(self) -> None:
         if self.decide:
@@ -287,6 +294,7 @@ class MultiAdamW:
             self._update(B.ZERO_MULTI_DECIDED)
         else:
             self._update(B.ZERO_MULTI_ADVANCE)
+            self._decided = False
 
     def capture(self) -> torch.cuda.CUDAGraph:
         """Record one step into a CUDA graph; replaying it runs one step, with
