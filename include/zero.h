@@ -702,7 +702,9 @@ enum {
                                 another decision (zero_grad_norm), combine with
                                 ZERO_MULTI_UNSCALED                            */
     ZERO_MULTI_ADVANCE = 1,  /* no norm: update with the constants of step t+1,
-                                clip 1, and advance t and beta^t (no skip)     */
+                                clip 1, and advance t and beta^t (no skip).
+                                Clears overflow; grad_norm stays that of the
+                                last decision                                  */
     ZERO_MULTI_UNSCALED = 2  /* the gradients carry no loss scale any more
                                 (e.g. reduced by zero_reduce_scatter)          */
 };

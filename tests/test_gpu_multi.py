@@ -423,6 +423,18 @@ def test_a_list_of_empty_tensors_still_advances():
         assert opt.read_state()["t"] == 2 and opt.read_state()["grad_norm"] == 0.0
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_step_without_the_norm_clears_the_last_decision(bits):
+    s = Setup([300, 5], "bf16", "bf16", bits, decide=False)
+    s.dg[7] = math.inf
+    s.opt.grad_norm()
+    assert s.opt.read_state()["overflow"] == 1
+    s.dg[7] = 0
+    s.opt.step()
+    st = s.opt.read_state()
+    assert (st["t"], st["overflow"], st["nonfinite"], st["apply"], st["skipped"]) == (1, 0, 0, 1, 1)
+
+
 def test_zero_gradients_move_nothing_but_the_decay():
     for bits in (32, 8):
         s = Setup([5000], "bf16", "bf16", bits, decide=False)

@@ -353,6 +353,8 @@ __device__ __forceinline__ void advance_step(const MultiArgs& a) {
     __threadfence();
     if (atomicInc(&a.t.counters[4], gridDim.x - 1) != gridDim.x - 1) return;
     zero_step_state* st = a.st;
+    st->nonfinite = 0;  // nothing was looked for
+    st->overflow = 0;
     st->clip_coef = 1.0f;
     st->apply = 1;
     st->t += 1;
