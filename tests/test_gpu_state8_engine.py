@@ -178,6 +178,42 @@ def test_checkpoints_cross_widths_and_partitions(tmp_path):
         assert bool(((got - want).abs() <= rel * want.abs() + least * top).all()), name
 
 
+def test_an_error_of_the_codec_is_not_lost(tmp_path, monkeypatch):
+    """Nothing is made to fail on the GPU: the error word that a kernel would set is set behind it."""
+    from zero_partitioned_mixed_replica_gb300 import binding as B
+    from zero_partitioned_mixed_replica_gb300 import multi
+    c = Case([3000, 500, 41], 2, 2, FMT_BF16)
+    eng = _engine(c)
+    eng.save_checkpoint(str(tmp_path))
+    opt = multi.MultiAdamW([torch.zeros(100, device="cuda")], [torch.zeros(100, device="cuda")], state_bits=8)
+    m, v = opt.states32()
+    opt.load_states(m, v)
+    assert opt.read_state()["error"] == 0 and eng.flat("m").any() == False and eng.read_state()["error"] == 0  # noqa: E712
+    seen = []
+
+    def after(call):
+        def run(self):
+            call(self)
+            self._list.error_word().fill_(4)
+            seen.append(B.zero_multi_device_error(self._list.M))
+        return run
+
+    monkeypatch.setattr(multi.StateCodec8, "decode", after(multi.StateCodec8.decode))
+    opt.states32()
+    assert opt.read_state()["error"] == 4
+    eng.flat("m")
+    assert eng.read_state()["error"] == 4
+    with pytest.raises(RuntimeError, match="8-bit states"):
+        eng.save_checkpoint(str(tmp_path / "other"))
+    monkeypatch.setattr(multi.StateCodec8, "encode", after(multi.StateCodec8.encode))
+    opt.state.zero_()
+    opt.load_states(m, v)
+    assert opt.read_state()["error"] == 4
+    with pytest.raises(RuntimeError, match="8-bit states"):
+        eng.load_checkpoint(str(tmp_path))
+    assert seen and set(seen) == {4}
+
+
 def test_refusals():
     from zero_partitioned_mixed_replica_gb300.engine import ZeroStep
     for kw in (dict(state_bits=16), dict(state_bits=8, fused=True), dict(state_bits=8, live_units=2, unit_of_tensor=[0])):

@@ -316,7 +316,9 @@ class ZeroStep:
         if self.state_bits == 32:
             return self.m, self.v
         m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
-        self._codec8(m, v).decode()
+        codec = self._codec8(m, v)
+        codec.decode()
+        codec.report(self.state)
         torch.cuda.current_stream(self.device).wait_stream(self._s())
         return m, v
 
@@ -491,7 +493,13 @@ class ZeroStep:
         are written as the fp32 values they stand for, so a checkpoint loads
         into engines of either width and any partition."""
         os.makedirs(path, exist_ok=True)
-        m, v = self.states32()
+        if self.state_bits == 32:
+            m, v = self.m, self.v
+        else:
+            m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
+            codec = self._codec8(m, v)
+            codec.decode()
+            codec.check()                    # rather no checkpoint than one with states that were not decoded
         torch.cuda.synchronize(self.device)
         p16 = self._shard16_rows_view()
 
@@ -576,8 +584,9 @@ class ZeroStep:
         self.state.copy_(torch.frombuffer(bytearray(st), dtype=torch.uint8))
         self._s().wait_stream(torch.cuda.current_stream(self.device))   # the uploads ran on the current stream
         if self.state_bits == 8:
-            self._codec8(m, v).encode()      # nearest 8-bit values
-            torch.cuda.synchronize(self.device)
+            codec = self._codec8(m, v)
+            codec.encode()                   # nearest 8-bit values
+            codec.check()
         if self.stage != 3:
             if self.shard16 is None:
                 shards = torch.stack([t.clone() for t in p16_rows])

@@ -82,6 +82,11 @@ class BoundList:
         self.info = B.zero_multi_query(self.M)
         self.workspace = torch.zeros(self.info.workspace_bytes, dtype=torch.uint8, device=device)
 
+    def error_word(self) -> torch.Tensor:
+        """Where the codec's kernels report errors: the fourth word of the
+        workspace, what zero_multi_device_error reads."""
+        return self.workspace[12:16].view(torch.int32)
+
     def bind(self, stream, **arrays):
         # the workspace's zero fill, and whatever made the tensors, ran on the current stream
         stream.wait_stream(torch.cuda.current_stream(self.workspace.device))
@@ -101,7 +106,8 @@ class StateCodec8:
     ones ``m8`` (float8_e4m3fn), ``v8`` (float8_e5m2), ``m8_scale`` and
     ``v8_scale`` (float8_e8m0fnu, one per 32 elements) of the same tensors:
     :meth:`encode` writes the second from the first, :meth:`decode` the first
-    from the second."""
+    from the second.  A kernel whose waits ran out leaves elements unwritten
+    and an error: :meth:`check` raises then, :meth:`report` hands it on."""
 
     def __init__(self, m, v, m8, m8_scale, v8, v8_scale, stream: Optional[torch.cuda.Stream] = None):
         if not len(m):
@@ -141,6 +147,19 @@ class StateCodec8:
         status = self._decode(self._M, _raw_stream(self._index) if self.stream is None else self.stream.cuda_stream)
         if status:
             B._check(status)
+
+    def check(self) -> None:
+        """Wait for the calls so far; RuntimeError if one of their kernels reported an error."""
+        with _device(self._index):
+            bits = B.zero_multi_device_error(self._list.M)
+        if bits:
+            raise RuntimeError("8-bit states: a codec kernel gave up waiting (error bits %d)" % bits)
+
+    def report(self, state: torch.Tensor) -> None:
+        """Add the errors of the calls so far to a device step state's, without waiting."""
+        at = B.zero_step_state.error.offset
+        with torch.cuda.stream(self._s()):
+            state[at:at + 4].view(torch.int32).bitwise_or_(self._list.error_word())
 
 
 class MultiAdamW:
@@ -321,7 +340,8 @@ class MultiAdamW:
 
     def states32(self):
         """(m, v) as lists of new fp32 tensors, e.g. for a checkpoint that an
-        optimizer with states of either width can resume from."""
+        optimizer with states of either width can resume from.  An error of
+        the decoding kernel shows in ``read_state()["error"]``."""
         cur = torch.cuda.current_stream(self.device)
         if self.state_bits == 32:
             cur.wait_stream(self._s())
@@ -329,7 +349,9 @@ class MultiAdamW:
             self._s().wait_stream(cur)       # the next step, on a stream of its own
             return copies
         m, v = (_slices(self.numels, torch.float32, self.device) for _ in range(2))
-        self._codec(m, v).decode()
+        codec = self._codec(m, v)
+        codec.decode()
+        codec.report(self.state)
         cur.wait_stream(self._s())
         return m, v
 
@@ -345,7 +367,9 @@ class MultiAdamW:
                     b.copy_(a)
             self._s().wait_stream(cur)
         else:
-            self._codec(m, v).encode()
+            codec = self._codec(m, v)
+            codec.encode()
+            codec.report(self.state)
             # the codec's workspace, and the caller's m and v, may be freed after this on the current stream
             torch.cuda.current_stream(self.device).wait_stream(self._s())
 
