@@ -178,6 +178,42 @@ def test_checkpoints_cross_widths_and_partitions(tmp_path):
         assert bool(((got - want).abs() <= rel * want.abs() + least * top).all()), name
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_loads_and_reads_around_steps_under_way_on_another_stream(tmp_path, bits):
+    c = CASES["zero2_bf16"]
+    L = c.layout()
+    stream = torch.cuda.Stream()
+    p0 = torch.from_numpy(c.master0(L))
+    p1 = torch.from_numpy(c.master0(L)) * 2
+    eng, ref = _engine(c, bits, stream=stream), _engine(c, bits)
+    for e in (eng, ref):
+        e.load_master(p0)
+        _feed(e, c, L, 1)
+    torch.cuda.synchronize()
+    ref.step()
+    ref.save_checkpoint(str(tmp_path))
+    want = {x: ref.flat(x) for x in ("master", "m", "v")}
+    hold = lambda: torch.cuda._sleep(20_000_000)  # noqa: E731
+
+    eng.step()                              # reads: the copies are held up, the next step is already issued
+    hold()
+    got = {x: eng.flat(x) for x in want}
+    eng.step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[x], want[x]) for x in want)
+    with torch.cuda.stream(stream):         # loads: the step before is held up
+        hold()
+    eng.step()
+    eng.load_checkpoint(str(tmp_path))
+    assert all(torch.equal(eng.flat(x), want[x]) for x in want)
+    with torch.cuda.stream(stream):
+        hold()
+    eng.step()
+    eng.load_master(p1.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(eng.flat("master").cpu(), p1) and not bool(eng.flat("m").any())
+
+
 def test_an_error_of_the_codec_is_not_lost(tmp_path, monkeypatch):
     """Nothing is made to fail on the GPU: the error word that a kernel would set is set behind it."""
     from zero_partitioned_mixed_replica_gb300 import binding as B

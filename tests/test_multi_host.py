@@ -189,3 +189,41 @@ def test_calls_go_to_the_device_of_the_tensors(monkeypatch):
     assert [n for n, _ in log] == ["zero_multi_grad_norm", "zero_multi_adamw", "zero_multi_adamw8", "zero_multi_encode8",
                                    "zero_multi_decode8", "bind"]
     assert {d for _, d in log} == {1} and current == [0]
+
+
+class Shards(Tensor):
+    """[N_d, S] on the current stream."""
+
+    shape = (1, 5)
+
+    def to(self, *a, **k):
+        return self
+
+    def view(self, *a):
+        return self
+
+    def zero_(self):
+        self.log.append("write")
+
+    def __getitem__(self, at):
+        return self
+
+
+@pytest.mark.parametrize("own_stream", [True, False])
+def test_the_engine_s_loads_and_reads_are_ordered_with_its_steps(monkeypatch, own_stream):
+    log = []
+    cur = Stream("current", log)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: cur)
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: Shards(log))
+    eng = engine.ZeroStep.__new__(engine.ZeroStep)
+    eng.device, eng.stream, eng.state_bits, eng.n_d = torch.device("cuda", 0), Stream("own", log) if own_stream else None, 32, 1
+    eng.info = type("Info", (), {"psi_pad": 5})
+    eng.units = [type("Unit", (), {"offset": 0, "shard": 5, "shard_base": 0})]
+    eng.master, eng.m, eng.v = Shards(log), Shards(log), Shards(log)
+    eng.shard16 = eng.params = eng.gshard = None
+    waits = ["current waits for own", "own waits for current"] if own_stream else []
+    eng.load_master(Shards(log))
+    assert log == waits[:1] + 3 * ["write"] + waits[1:]
+    log.clear()
+    eng.flat("master")
+    assert log == waits[:1] + ["write"] + waits[1:]

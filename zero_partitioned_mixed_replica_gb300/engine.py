@@ -207,6 +207,7 @@ class ZeroStep:
         if flat_master.dtype != torch.float32:
             raise ValueError("load_master takes the fp32 master, got %s" % flat_master.dtype)
         fm = flat_master.to(self.device)
+        torch.cuda.current_stream(self.device).wait_stream(self._s())   # a step under way on a stream of its own
         for u in self.units:
             for r in range(self.n_d):
                 lo = u.offset + r * u.shard
@@ -574,6 +575,7 @@ class ZeroStep:
                     host[k][do:do + n] = views[sr][k][so:so + n]
             return r, host
 
+        torch.cuda.current_stream(self.device).wait_stream(self._s())   # a step under way on a stream of its own
         m, v = (self.m, self.v) if self.state_bits == 32 else (torch.zeros_like(self.master), torch.zeros_like(self.master))
         with ThreadPoolExecutor(max_workers=min(16, self.n_d)) as ex:
             for r, host in ex.map(assemble, range(self.n_d)):
@@ -617,4 +619,5 @@ class ZeroStep:
             for r in range(self.n_d):
                 lo = u.offset + r * u.shard
                 out[lo:lo + u.shard].copy_(src[r, u.shard_base:u.shard_base + u.shard])
+        self._s().wait_stream(torch.cuda.current_stream(self.device))   # the next step, before it changes them
         return out
