@@ -178,6 +178,35 @@ def test_checkpoints_cross_widths_and_partitions(tmp_path):
         assert bool(((got - want).abs() <= rel * want.abs() + least * top).all()), name
 
 
+@pytest.mark.parametrize("n_d,elems", [(2, 1 << 18), (3, 400_001)])
+def test_checkpoints_of_8_bit_states_take_little_device_memory(tmp_path, monkeypatch, n_d, elems):
+    """The fp32 values go through pieces, not through whole copies of the states (8 bytes a parameter): with pieces of
+    65,536 bytes, less than a quarter of that."""
+    from zero_partitioned_mixed_replica_gb300 import engine
+    monkeypatch.setattr(engine, "STAGE_BYTES", 1 << 16)
+    c = Case([elems, 3001, 77], n_d, 2, FMT_BF16, grad_std=1e-2)
+    L = c.layout()
+    eng = _engine(c)
+    eng.load_master(torch.from_numpy(c.master0(L)))
+    _feed(eng, c, L, 1)
+    eng.step()
+    m, v = (x.cpu() for x in eng.states32())
+    whole = 8 * eng.master.numel()
+    other = _engine(c)
+    for call in (eng.save_checkpoint, other.load_checkpoint):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        call(str(tmp_path))
+        assert torch.cuda.max_memory_allocated() - before <= whole / 4
+    S = eng.info.shard_len
+    for r in range(n_d):
+        f32 = np.fromfile(tmp_path / ("rank%03d.bin" % r), np.float32, 3 * S)
+        assert np.array_equal(f32[S:2 * S], m[r].numpy()) and np.array_equal(f32[2 * S:], v[r].numpy())
+    for a, b in zip(other.states32(), (m, v)):
+        assert torch.equal(a.cpu(), b)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_loads_and_reads_around_steps_under_way_on_another_stream(tmp_path, bits):
     c = CASES["zero2_bf16"]

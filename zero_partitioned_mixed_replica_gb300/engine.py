@@ -39,6 +39,8 @@ import torch
 
 from . import binding as B
 
+STAGE_BYTES = 64 << 20      # of a checkpoint's copies between the device and the host; a multiple of 512
+
 TORCH_16 = {B.ZERO_BF16: torch.bfloat16, B.ZERO_FP16: torch.float16}
 
 
@@ -311,6 +313,30 @@ class ZeroStep:
         from . import multi
         return multi.StateCodec8(list(m), list(v), self.m_rows, self.m_scale_rows, self.v_rows, self.v_scale_rows, self.stream)
 
+    def _pieces(self):
+        """(begin, end) of a shard's pieces of STAGE_BYTES of fp32 states: checkpoints take 8-bit states
+        through them, without whole copies at 8 bytes a parameter."""
+        S, n = self.info.shard_len, STAGE_BYTES // 4
+        return [(a, min(S, a + n)) for a in range(0, S, n)]
+
+    def _piece_codec8(self, r: int, a: int, b: int, m: torch.Tensor, v: torch.Tensor):
+        """The 8-bit states a .. b of rank r (whole blocks) and fp32 ones, on the current stream."""
+        from . import multi
+        cut = slice(a // multi.BLOCK, -(-b // multi.BLOCK))
+        return multi.StateCodec8([m], [v], [self.m[r, a:b]], [self.m_scale[r, cut]], [self.v[r, a:b]], [self.v_scale[r, cut]])
+
+    def _decode_piece8(self, r: int, a: int, b: int):
+        m, v = (torch.empty(b - a, dtype=torch.float32, device=self.device) for _ in range(2))
+        codec = self._piece_codec8(r, a, b, m, v)
+        codec.decode()
+        codec.check()                        # rather no checkpoint than one with states that were not decoded
+        return m, v
+
+    def _encode_piece8(self, r: int, a: int, b: int, m: np.ndarray, v: np.ndarray):
+        codec = self._piece_codec8(r, a, b, *(torch.from_numpy(x).to(self.device) for x in (m, v)))
+        codec.encode()                       # nearest 8-bit values
+        codec.check()
+
     def states32(self):
         """(m, v) as fp32 [N_d, S] tensors: the states themselves, or, with
         8-bit states, new tensors of their values."""
@@ -494,17 +520,10 @@ class ZeroStep:
         are written as the fp32 values they stand for, so a checkpoint loads
         into engines of either width and any partition."""
         os.makedirs(path, exist_ok=True)
-        if self.state_bits == 32:
-            m, v = self.m, self.v
-        else:
-            m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
-            codec = self._codec8(m, v)
-            codec.decode()
-            codec.check()                    # rather no checkpoint than one with states that were not decoded
         torch.cuda.synchronize(self.device)
         p16 = self._shard16_rows_view()
 
-        chunk = 64 << 20                       # bytes per staged device-to-host copy
+        chunk = STAGE_BYTES
 
         def dump(r):
             # one pinned staging buffer per writer; the file gets the staged bytes as they are
@@ -512,13 +531,23 @@ class ZeroStep:
             view = stage.numpy()
             stream = torch.cuda.Stream(self.device)
             with open(os.path.join(path, "rank%03d.bin" % r), "wb") as f, torch.cuda.stream(stream):
-                for t in (self.master[r], m[r], v[r], p16[r].contiguous()):
+                def put(t):
                     flat = t.view(torch.uint8)
                     for off in range(0, flat.numel(), chunk):
                         n = min(chunk, flat.numel() - off)
                         stage[:n].copy_(flat[off:off + n], non_blocking=True)
                         stream.synchronize()
                         f.write(memoryview(view[:n]))
+
+                put(self.master[r])
+                if self.state_bits == 32:
+                    put(self.m[r])
+                    put(self.v[r])
+                else:
+                    for k in (0, 1):         # all of m, then all of v
+                        for a, b in self._pieces():
+                            put(self._decode_piece8(r, a, b)[k])
+                put(p16[r].contiguous())
             return 14 * self.info.shard_len
 
         with ThreadPoolExecutor(max_workers=min(16, self.n_d)) as ex:
@@ -576,19 +605,18 @@ class ZeroStep:
             return r, host
 
         torch.cuda.current_stream(self.device).wait_stream(self._s())   # a step under way on a stream of its own
-        m, v = (self.m, self.v) if self.state_bits == 32 else (torch.zeros_like(self.master), torch.zeros_like(self.master))
         with ThreadPoolExecutor(max_workers=min(16, self.n_d)) as ex:
             for r, host in ex.map(assemble, range(self.n_d)):
                 self.master[r].copy_(torch.from_numpy(host[0]))
-                m[r].copy_(torch.from_numpy(host[1]))
-                v[r].copy_(torch.from_numpy(host[2]))
+                if self.state_bits == 32:
+                    self.m[r].copy_(torch.from_numpy(host[1]))
+                    self.v[r].copy_(torch.from_numpy(host[2]))
+                else:
+                    for a, b in self._pieces():
+                        self._encode_piece8(r, a, b, host[1][a:b], host[2][a:b])
                 p16_rows[r].view(torch.int16).copy_(torch.from_numpy(host[3].view(np.int16)))
         self.state.copy_(torch.frombuffer(bytearray(st), dtype=torch.uint8))
         self._s().wait_stream(torch.cuda.current_stream(self.device))   # the uploads ran on the current stream
-        if self.state_bits == 8:
-            codec = self._codec8(m, v)
-            codec.encode()                   # nearest 8-bit values
-            codec.check()
         if self.stage != 3:
             if self.shard16 is None:
                 shards = torch.stack([t.clone() for t in p16_rows])
