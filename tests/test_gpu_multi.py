@@ -325,6 +325,76 @@ def test_codec_against_references(n):
         assert torch.equal(back.view(torch.int32), R.decode_ref(c, b).view(torch.int32))
 
 
+def _placed(x, off, mark):
+    """x at `off` elements behind a 256-byte boundary, between marks: (the buffer's bytes, the view)."""
+    buf = torch.full(((x.numel() + off + 64) * x.element_size(),), mark, dtype=torch.uint8, device="cuda")
+    view = buf[off * x.element_size():(off + x.numel()) * x.element_size()].view(x.dtype)
+    view.copy_(x)
+    return buf, view
+
+
+def _marks_stand(buf, view, off, mark):
+    a, b = off * view.element_size(), (off + view.numel()) * view.element_size()
+    return bool((buf[:a] == mark).all()) and bool((buf[b:] == mark).all())
+
+
+# distances of (m, v, codes of m, codes of v, scales of m, scales of v) from a boundary, in elements
+DISTANCES = [(1, 1, 0, 0, 0, 0), (3, 3, 0, 0, 0, 0), (4, 4, 0, 0, 0, 0), (0, 5, 0, 0, 0, 0), (0, 0, 1, 1, 0, 0), (0, 0, 8, 8, 0, 0),
+             (0, 0, 16, 0, 0, 0), (0, 0, 0, 7, 0, 0), (0, 0, 0, 0, 1, 1), (0, 0, 0, 0, 2, 0), (0, 0, 0, 0, 0, 3), (2, 2, 3, 5, 1, 2),
+             (7, 6, 15, 13, 3, 1)]
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 33, 2048, 5001])
+def test_codec_wherever_the_states_begin(n):
+    """What aligned states give, bit for bit, and nothing around them is touched."""
+    from zero_partitioned_mixed_replica_gb300 import multi
+    gen = torch.Generator("cuda").manual_seed(n)
+    m, v = torch.randn(n, generator=gen, device="cuda") * 3e-4, torch.rand(n, generator=gen, device="cuda") * 1e-6
+    nb = multi.scale_count(n)
+    zero = lambda k, dt: torch.zeros(k, dtype=torch.uint8, device="cuda").view(dt)  # noqa: E731
+    want = None
+    for d in [(0,) * 6] + DISTANCES:
+        arrays = [m, v, zero(n, multi.M8), zero(n, multi.V8), zero(nb, multi.SCALE8), zero(nb, multi.SCALE8)]
+        placed = [_placed(x, off, 0xA5) for x, off in zip(arrays, d)]
+        pm, pv, m8, v8, ms, vs = (view for _, view in placed)
+        codec = multi.StateCodec8([pm], [pv], [m8], [ms], [v8], [vs])
+        codec.encode()
+        assert torch.equal(pm, m) and torch.equal(pv, v)
+        pm.zero_(), pv.zero_()
+        codec.decode()
+        codec.check()
+        got = [x.contiguous().view(torch.uint8).clone() for x in (pm, pv, m8, v8, ms, vs)]
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), d
+        assert all(_marks_stand(*p, off, 0xA5) for p, off in zip(placed, d)), d
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 33, 2048, 5001])
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+def test_adamw8_wherever_the_states_begin(grad, n):
+    from zero_partitioned_mixed_replica_gb300 import multi
+    gen = torch.Generator("cuda").manual_seed(n)
+    r = lambda: torch.randn(n, generator=gen, device="cuda")  # noqa: E731
+    g, p, m, v = (r() * 1e-3).to(DT[grad]), r() * 0.02, r() * 3e-4, (r() ** 2 + 0.01) * 1e-6
+    nb = multi.scale_count(n)
+    zero = lambda k, dt: torch.zeros(k, dtype=torch.uint8, device="cuda").view(dt)  # noqa: E731
+    eight = [zero(n, multi.M8), zero(n, multi.V8), zero(nb, multi.SCALE8), zero(nb, multi.SCALE8)]
+    multi.StateCodec8([m], [v], [eight[0]], [eight[2]], [eight[1]], [eight[3]]).encode()
+    want = None
+    for d in [(0,) * 6] + [d for d in DISTANCES if any(d[2:])]:
+        for off in (0, 1, 3):                       # of the parameters, their copies and the gradients
+            placed = [_placed(x, o, 0xA5) for x, o in zip([p, p.bfloat16(), g] + eight, (off,) * 3 + d[2:])]
+            pp, out, pg, m8, v8, ms, vs = (view for _, view in placed)
+            opt = multi.MultiAdamW([pp], [pg], [out], state_bits=8, m=[m8], v=[v8], m_scale=[ms], v_scale=[vs], decide=False, seed=6)
+            opt.step()
+            opt.step()
+            assert opt.read_state()["error"] == 0
+            got = [x.contiguous().view(torch.uint8).clone() for x in (pp, out, m8, v8, ms, vs)]
+            want = want or got
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (d, off)
+            assert all(_marks_stand(*x, o, 0xA5) for x, o in zip(placed, (off,) * 3 + d[2:])), (d, off)
+
+
 def test_codec_of_values_that_are_not_finite():
     x = torch.ones(128)
     x[5], x[40] = math.inf, math.nan
