@@ -1302,7 +1302,6 @@ __global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_co
             const uint32_t chunks = (uint32_t)((r.numel + max(r.shift, r.gshift) + kChunk - 1) / kChunk) - (c - r.first_chunk);
             const uint32_t take = min(chunks, c1 - c);
             const int64_t end = min(r.numel, begin + (int64_t)take * kChunk);
-            constexpr bool vec = true;  // gshift puts the gradients on a boundary
             const uint64_t lim = (uint64_t)r.numel > t.slack ? (uint64_t)r.numel - t.slack : 0;
             auto add = [&](const float (&g)[8]) {
                 float q = __fmul_rn(g[0], g[0]);
@@ -1321,25 +1320,24 @@ __global__ void __launch_bounds__(kThreads, 8) multi_norm_kernel(const __grid_co
                 int e0, e1;
                 if (span8(t, r, i, e0, e1)) {
                     float g[8];
-                    load_grad<G>(r.grad, i, e0, e1, vec, g);
+                    load_grad<G>(r.grad, i, e0, e1, true, g);  // gshift puts the gradients on a boundary
                     add(g);
                 }
                 i += kStep;
             };
             if (begin < 0) one();  // the first vector is not whole
-            if (vec)
-                for (; i + (kUnroll - 1) * kStep + kVec <= end; i += kUnroll * kStep) {
-                    if (!in_bounds((uint64_t)i + (kUnroll - 1) * kStep + kVec, lim)) break;
-                    typename G::Raw q[kUnroll];
+            for (; i + (kUnroll - 1) * kStep + kVec <= end; i += kUnroll * kStep) {
+                if (!in_bounds((uint64_t)i + (kUnroll - 1) * kStep + kVec, lim)) break;
+                typename G::Raw q[kUnroll];
 #pragma unroll
-                    for (int u = 0; u < kUnroll; ++u) q[u] = G::raw(static_cast<const typename G::T*>(r.grad) + i + u * kStep);
+                for (int u = 0; u < kUnroll; ++u) q[u] = G::raw(static_cast<const typename G::T*>(r.grad) + i + u * kStep);
 #pragma unroll
-                    for (int u = 0; u < kUnroll; ++u) {
-                        float g[8];
-                        G::values(q[u], g);
-                        add(g);
-                    }
+                for (int u = 0; u < kUnroll; ++u) {
+                    float g[8];
+                    G::values(q[u], g);
+                    add(g);
                 }
+            }
             while (i < end) one();
             c += take;
         }
