@@ -563,7 +563,7 @@ __device__ __forceinline__ void ring_compute(int32_t* error, Stage* stage, Ring<
 // same bits here as in the flat buffer.  Bound by memory: 14 bytes read and 14
 // written per element with 16-bit gradients and copies.  GB300, 1.56e9
 // elements in 580 tensors: 6.16 ms, 7.1 TB/s (the copy that the roofline is
-// measured with: 6.77).  80K elements in 50 tensors: 3.4 us from a graph, the
+// measured with: 6.77).  80K elements in 50 tensors: 3.6 us from a graph, the
 // latency of launch, copies, constants, update and stores one after the other.
 // ----------------------------------------------------------------------------
 // A computing warp takes 256 elements of a tile, 8 consecutive ones per lane.
@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kThreads32, 2) multi_adamw_kernel(const __grid
 // onto one by a shift of the work, as in the 32-bit update: they are copied
 // from the boundary before, taken over by as many elements, and the results
 // turned round in shared memory so that neighbouring lanes store neighbouring
-// pairs (GB300, 91e6 elements in 150 tensors at odd offsets: 424 us, aligned 408;
+// pairs (GB300, 175e6 elements in 158 tensors at odd offsets: 423 us, aligned 408;
 // stored one by one 467, read by plain loads as well 588).  A tensor's last few
 // elements, and its first 16 if they are not on a boundary, are read by plain
 // loads.
@@ -1084,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_adamw8_kernel(const __grid
 
 // ----------------------------------------------------------------------------
 // 32-bit states into the 8-bit form and back: 10.06 bytes per element, bound by
-// memory.  GB300, 355e6 elements: encode 496 us (7.2 TB/s), decode 511 us (7.0
+// memory.  GB300, 355e6 elements: encode 497 us (7.2 TB/s), decode 510 us (7.0
 // TB/s; 621 with all CTAs that fit on an SM, 690 with two).
 // ----------------------------------------------------------------------------
 // Nearest codes (ties to even) of 16 values.
@@ -1238,7 +1238,7 @@ __global__ void __launch_bounds__(kThreads8, 4) multi_codec_kernel(const __grid_
 // (two_sum); pairs (sum, error) are combined by shuffles and, among the CTAs,
 // by the one that ends last.  The split into kSlices ranges is fixed, so the
 // result does not depend on the grid.  Bound by memory: GB300, 1.56e9 16-bit
-// gradients 433 us (7.2 TB/s read); 30.7e6 of them 15.5 us, of which 9 are the
+// gradients 433 us (7.2 TB/s read); 30.7e6 of them 15.7 us, of which 9 are the
 // bytes and the rest launch, first loads and the last CTA's sum.
 // ----------------------------------------------------------------------------
 // The step decision, as zero_grad_norm makes it: skip on overflow, else the clip
