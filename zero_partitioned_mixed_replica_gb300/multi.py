@@ -319,7 +319,8 @@ class MultiAdamW:
         """Record one step into a CUDA graph; replaying it runs one step, with
         the hyperparameters of the recording and the gradients of the last
         :meth:`rebind_grads`.  Replays and the object's other calls are
-        ordered like any work: on one stream, or by waits."""
+        ordered like any work: on one stream, or by waits.  The object and its
+        tensors must live as long as the graph."""
         g = torch.cuda.CUDAGraph()
         side = torch.cuda.Stream(self.device)
         side.wait_stream(torch.cuda.current_stream(self.device))
