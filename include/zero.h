@@ -757,6 +757,74 @@ zero_status_t zero_multi_decode8(const zero_multi* M, zero_stream_t stream);
  * report theirs (*bits = 0: none).  Synchronises the device. */
 zero_status_t zero_multi_device_error(const zero_multi* M, int32_t* bits);
 
+/* ------------------------------------------------------------------------ */
+/* A model's ends and norms: embedding, layer norm                             */
+/* ------------------------------------------------------------------------ */
+/* The operators whose weights are neither matrices of a block nor pointwise:
+ * a table looked up by token, and the norms between blocks (wte, ln_*, ln_f
+ * of the GPT-2 workloads).  Their weight gradients are written where the step
+ * reads them: as a tensor of a rank's flat 16-bit gradient replica, or of a
+ * zero_multi's list.  The pages have no counterpart (backward compute is the
+ * caller's there).
+ *
+ * Differences from the conventions above:
+ *   - Tensors need the natural alignment of their elements only (a tensor may
+ *     begin anywhere in a flat buffer), else ZERO_ERR_ALIGN; a workspace is
+ *     256-byte aligned as everywhere, its size is what the query gives, its
+ *     contents on entry do not matter and it may be used for anything else
+ *     when the call's kernels are done.  Calls that may overlap on the GPU
+ *     need workspaces of their own.
+ *   - dtype ZERO_BF16, ZERO_FP16 or ZERO_FP32: of activations and weights (one
+ *     type for both).  Weight gradients have it too, or are ZERO_FP32
+ *     (grad_dtype).  Sums are binary32 and rounded once, to nearest even.
+ *   - accumulate != 0 adds to the weight gradients that are there (micro-
+ *     batches, tied weights), with one rounding of the sum; 0 overwrites all of
+ *     them.
+ *   - Outputs do not overlap inputs or one another.
+ *   - n == 0 (or rows == 0) is allowed: pointers of empty arrays may be NULL,
+ *     and weight gradients are zeroed (or, accumulating, left alone).
+ *   - Same inputs, same bits: no sum depends on the order in which CTAs run,
+ *     on zero_set_max_ctas or on the GPU's SM count. */
+
+/* out[i] = round(scale * weight[ids[i]]), one binary32 product an element;
+ * weight [vocab, d], ids [n], out [n, d].  An id outside 0 .. vocab-1 (padding)
+ * gives a row of zeros.
+ * vocab 1 .. 2^31-2, d 1 .. 2^20, n 0 .. 2^31-1, scale finite, else ZERO_ERR_INVALID. */
+zero_status_t zero_embedding_forward(const void* weight, const int64_t* ids, int64_t vocab, int64_t d, int64_t n,
+                                     int32_t dtype, double scale, void* out, zero_stream_t stream);
+
+/* grad_weight[k] (+)= scale * sum of grad_out[i] over the i with ids[i] == k;
+ * grad_out [n, d] of dtype, grad_weight [vocab, d] of grad_dtype.  Ids outside
+ * 0 .. vocab-1 take no part.  Tokens are sorted by id (stable) and each id's
+ * rows added in that order, in fixed pieces. */
+zero_status_t zero_embedding_workspace(int64_t vocab, int64_t d, int64_t n, int64_t* bytes);
+zero_status_t zero_embedding_backward(const void* grad_out, const int64_t* ids, int64_t vocab, int64_t d, int64_t n,
+                                      int32_t dtype, int32_t grad_dtype, double scale, int32_t accumulate,
+                                      void* grad_weight, void* workspace, zero_stream_t stream);
+
+/* Layer norm of each row: mean and rstd = 1 / sqrt(var + eps) with var the
+ * mean of (x - mean)^2 (two passes over the row's registers), y = round((x -
+ * mean) * rstd * weight + bias).  x [rows, d] with x_stride elements between
+ * rows (>= d), y [rows, d], weight and bias [d] of dtype (bias may be NULL),
+ * mean and rstd [rows] binary32 for the backward pass (both may be NULL).
+ * rows 0 .. 2^31-1, d 1 .. ZERO_MAX_NORM_DIM, eps >= 0, else ZERO_ERR_INVALID. */
+#define ZERO_MAX_NORM_DIM 16384
+zero_status_t zero_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                                      int64_t rows, int64_t d, int32_t dtype, double eps, void* y, float* mean,
+                                      float* rstd, zero_stream_t stream);
+
+/* With u = (x - mean) * rstd and h = grad_y * weight: grad_x = round(rstd * (h -
+ * mean_d(h) - u * mean_d(h * u))), grad_weight (+)= sum over rows of grad_y * u,
+ * grad_bias (+)= sum over rows of grad_y (grad_bias may be NULL).  grad_y and
+ * x have row strides, grad_x [rows, d] has none.  Rows are added in fixed
+ * blocks, whose sums are added in order. */
+zero_status_t zero_layer_norm_workspace(int64_t rows, int64_t d, int64_t* bytes);
+zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, const void* x, int64_t x_stride,
+                                       const void* weight, const float* mean, const float* rstd, int64_t rows,
+                                       int64_t d, int32_t dtype, int32_t grad_dtype, int32_t accumulate,
+                                       void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                                       zero_stream_t stream);
+
 /* Cap on the CTAs of every later launch by this library (process-wide;
  * 0 = no cap: each kernel's own persistent grid, one full wave of CTAs or,
  * where that measured faster on GB300, fewer CTAs per SM).  For overlapping

@@ -40,6 +40,7 @@ ZERO_MAX_GROUPS = 16
 ZERO_MULTI_DECIDED = 0
 ZERO_MULTI_ADVANCE = 1
 ZERO_MULTI_UNSCALED = 2
+ZERO_MAX_NORM_DIM = 16384
 
 EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero_layout_unit",
             "zero_layout_tensor_offset", "zero_layout_destroy", "zero_state_init",
@@ -51,7 +52,8 @@ EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero
             "zero_last_error", "zero_launch_count", "zero_checked_build", "zero_bounds_violations",
             "zero_checked_set_slack", "zero_multi_init", "zero_multi_query", "zero_multi_destroy", "zero_multi_bind",
             "zero_multi_grad_norm", "zero_multi_adamw", "zero_multi_adamw8", "zero_multi_encode8",
-            "zero_multi_decode8", "zero_multi_device_error"]
+            "zero_multi_decode8", "zero_multi_device_error", "zero_embedding_forward", "zero_embedding_workspace",
+            "zero_embedding_backward", "zero_layer_norm_forward", "zero_layer_norm_workspace", "zero_layer_norm_backward"]
 ZERO_NOALLOC_MAX_ELEMS = 67108864
 
 
@@ -227,6 +229,12 @@ def lib():
         "zero_multi_encode8": [P, P],
         "zero_multi_decode8": [P, P],
         "zero_multi_device_error": [P, ctypes.POINTER(i32)],
+        "zero_embedding_forward": [P, P, i64, i64, i64, i32, dbl, P, P],
+        "zero_embedding_workspace": [i64, i64, i64, ctypes.POINTER(i64)],
+        "zero_embedding_backward": [P, P, i64, i64, i64, i32, i32, dbl, i32, P, P, P],
+        "zero_layer_norm_forward": [P, i64, P, P, i64, i64, i32, dbl, P, P, P, P],
+        "zero_layer_norm_workspace": [i64, i64, ctypes.POINTER(i64)],
+        "zero_layer_norm_backward": [P, i64, P, i64, P, P, P, i64, i64, i32, i32, i32, P, P, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -611,3 +619,38 @@ def zero_multi_device_error(M: Multi) -> int:
     bits = ctypes.c_int32(0)
     _check(lib().zero_multi_device_error(M, ctypes.byref(bits)))
     return int(bits.value)
+
+
+def zero_embedding_forward(weight, ids, vocab: int, d: int, n: int, dtype: int, scale: float, out, stream=None) -> None:
+    _check(lib().zero_embedding_forward(_addr(weight), _addr(ids), vocab, d, n, dtype, scale, _addr(out), _stream(stream)))
+
+
+def zero_embedding_workspace(vocab: int, d: int, n: int) -> int:
+    b = ctypes.c_int64()
+    _check(lib().zero_embedding_workspace(vocab, d, n, ctypes.byref(b)))
+    return b.value
+
+
+def zero_embedding_backward(grad_out, ids, vocab: int, d: int, n: int, dtype: int, grad_dtype: int, scale: float,
+                            accumulate: bool, grad_weight, workspace, stream=None) -> None:
+    _check(lib().zero_embedding_backward(_addr(grad_out), _addr(ids), vocab, d, n, dtype, grad_dtype, scale,
+                                         int(bool(accumulate)), _addr(grad_weight), _addr(workspace), _stream(stream)))
+
+
+def zero_layer_norm_forward(x, x_stride: int, weight, bias, rows: int, d: int, dtype: int, eps: float, y, mean, rstd,
+                            stream=None) -> None:
+    _check(lib().zero_layer_norm_forward(_addr(x), x_stride, _addr(weight), _addr(bias), rows, d, dtype, eps, _addr(y),
+                                         _addr(mean), _addr(rstd), _stream(stream)))
+
+
+def zero_layer_norm_workspace(rows: int, d: int) -> int:
+    b = ctypes.c_int64()
+    _check(lib().zero_layer_norm_workspace(rows, d, ctypes.byref(b)))
+    return b.value
+
+
+def zero_layer_norm_backward(grad_y, gy_stride: int, x, x_stride: int, weight, mean, rstd, rows: int, d: int, dtype: int,
+                             grad_dtype: int, accumulate: bool, grad_x, grad_weight, grad_bias, workspace, stream=None) -> None:
+    _check(lib().zero_layer_norm_backward(_addr(grad_y), gy_stride, _addr(x), x_stride, _addr(weight), _addr(mean),
+                                          _addr(rstd), rows, d, dtype, grad_dtype, int(bool(accumulate)), _addr(grad_x),
+                                          _addr(grad_weight), _addr(grad_bias), _addr(workspace), _stream(stream)))

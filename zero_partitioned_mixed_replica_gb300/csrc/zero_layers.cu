@@ -1,0 +1,955 @@
+// Embedding lookup and layer norm, forward and backward.
+//
+// All four move each element once or twice and compute a handful of
+// operations on it: they are bound by memory, and for few tokens by the
+// latency of a launch.  Rows are read in the widest pieces that every tensor
+// of the call allows (E elements: 16 bytes where all rows begin on a 16-byte
+// boundary; 4 bytes, or single elements, for tensors anywhere in a flat
+// buffer).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "zero_launch.h"
+
+namespace zk {
+
+namespace cg = cooperative_groups;
+
+struct Fp32 {
+    using S = float;
+};
+template <class F>
+struct Store {
+    using S = uint16_t;
+};
+template <>
+struct Store<Fp32> {
+    using S = float;
+};
+
+// E elements from p, widened; p is aligned to min(16, E * size) bytes.
+template <class F, int E>
+__device__ __forceinline__ void ld_e(const typename Store<F>::S* __restrict__ p, float (&o)[E]) {
+    if constexpr (sizeof(typename Store<F>::S) == 4) {
+        if constexpr (E % 4 == 0) {
+#pragma unroll
+            for (int k = 0; k < E / 4; ++k) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(p) + k);
+                o[4 * k] = x.x; o[4 * k + 1] = x.y; o[4 * k + 2] = x.z; o[4 * k + 3] = x.w;
+            }
+        } else if constexpr (E == 2) {
+            const float2 x = __ldg(reinterpret_cast<const float2*>(p));
+            o[0] = x.x; o[1] = x.y;
+        } else {
+            o[0] = __ldg(p);
+        }
+    } else if constexpr (E == 8) {
+        unpack8<F>(__ldg(reinterpret_cast<const uint4*>(p)), o);
+    } else if constexpr (E == 2) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
+        o[0] = F::lo(w);
+        o[1] = F::hi(w);
+    } else {
+        static_assert(E == 1, "8, 2 or 1 16-bit elements");
+        o[0] = F::dec1(__ldg(p));
+    }
+}
+
+template <class F, int E>
+__device__ __forceinline__ void st_e(typename Store<F>::S* p, const float (&o)[E]) {
+    if constexpr (sizeof(typename Store<F>::S) == 4) {
+        if constexpr (E % 4 == 0) {
+#pragma unroll
+            for (int k = 0; k < E / 4; ++k)
+                reinterpret_cast<float4*>(p)[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if constexpr (E == 2) {
+            *reinterpret_cast<float2*>(p) = make_float2(o[0], o[1]);
+        } else {
+            *p = o[0];
+        }
+    } else if constexpr (E == 8) {
+        *reinterpret_cast<uint4*>(p) = pack8<F>(o);
+    } else if constexpr (E == 2) {
+        *reinterpret_cast<uint32_t*>(p) = F::pack(o[0], o[1]);
+    } else {
+        *p = F::enc1(o[0]);
+    }
+}
+
+// What is already there, not through the read-only path: it is written by this launch.
+template <class F, int E>
+__device__ __forceinline__ void add_e(const typename Store<F>::S* p, float (&o)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if constexpr (sizeof(typename Store<F>::S) == 4)
+            o[e] = __fadd_rn(p[e], o[e]);
+        else
+            o[e] = __fadd_rn(F::dec1(p[e]), o[e]);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, m));
+    return x;
+}
+
+// ----------------------------------------------------------------------------
+// Embedding
+// ----------------------------------------------------------------------------
+struct EmbedArgs {
+    const void* weight;
+    const int64_t* ids;
+    void* out;
+    int64_t vocab, n;
+    uint32_t d, dv;      // elements and pieces of a row
+    int32_t lanes_log2;  // lanes of a warp that share a row
+    float scale;
+};
+
+// A row goes to 1, 2, .. 32 lanes of a warp, the fewest that cover it.
+template <class F, int E>
+__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
+    using S = typename Store<F>::S;
+    const uint32_t lanes = 1u << a.lanes_log2;
+    const uint32_t c0 = threadIdx.x & (lanes - 1);
+    const int64_t per_grid = ((int64_t)gridDim.x * kThreads) >> a.lanes_log2;
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> a.lanes_log2; i < a.n; i += per_grid) {
+        const int64_t id = __ldg(a.ids + i);
+        const bool inside = id >= 0 && id < a.vocab;
+        const S* src = static_cast<const S*>(a.weight) + (inside ? id : 0) * (int64_t)a.d;
+        S* dst = static_cast<S*>(a.out) + i * (int64_t)a.d;
+#pragma unroll 4
+        for (uint32_t c = c0; c < a.dv; c += lanes) {
+            float x[E] = {};
+            if (inside) {
+                ld_e<F, E>(src + (size_t)c * E, x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], a.scale);
+            }
+            st_e<F, E>(dst + (size_t)c * E, x);
+        }
+    }
+}
+
+// The tokens sorted by id, stable: a radix sort of (id, position) pairs in
+// 8-bit digits by one thread-block cluster, whose CTAs exchange their digit
+// counts through distributed shared memory; an id outside the vocabulary
+// becomes `vocab` and sorts behind all others.  The clusters behind the first
+// zero the gradient meanwhile.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+
+struct SortArgs {
+    const int64_t* ids;
+    uint64_t* pairs[2];  // id << 32 | position; the result is in pairs[passes & 1]
+    uint8_t* zero;       // zero_bytes of it are zeroed
+    int64_t zero_bytes;
+    int64_t vocab;
+    uint32_t n;
+    int32_t passes;
+};
+
+__device__ __forceinline__ uint64_t sort_pair(const SortArgs& a, int pass, uint32_t i) {
+    if (pass > 0) return a.pairs[pass & 1][i];
+    const int64_t id = __ldg(a.ids + i);
+    const uint64_t key = id >= 0 && id < a.vocab ? (uint64_t)id : (uint64_t)a.vocab;
+    return key << 32 | i;
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ SortArgs a) {
+    __shared__ uint32_t counts[kSortWarps][256];  // of a digit in a warp's tokens; then where the next one goes
+    __shared__ uint32_t total[256];               // of a digit in this CTA's tokens
+    __shared__ uint32_t scan[256];
+    cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t ctas = cluster.num_blocks(), rank = cluster.block_rank();
+    if (blockIdx.x >= ctas) {  // zero the gradient: bytes to a 16-byte boundary, vectors, bytes
+        const int64_t t = (int64_t)(blockIdx.x - ctas) * kSortThreads + threadIdx.x;
+        const int64_t step = (int64_t)(gridDim.x - ctas) * kSortThreads;
+        const int64_t head = min(a.zero_bytes, (int64_t)(-reinterpret_cast<intptr_t>(a.zero) & 15));
+        const int64_t vecs = (a.zero_bytes - head) / 16;
+        uint4* v = reinterpret_cast<uint4*>(a.zero + head);
+        for (int64_t i = t; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
+        if (t < head) a.zero[t] = 0;
+        if (head + vecs * 16 + t < a.zero_bytes) a.zero[head + vecs * 16 + t] = 0;   // fewer than 16
+        return;
+    }
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    // each warp has a contiguous stretch of whole 32s
+    const uint64_t per_warp = (((uint64_t)a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+    const uint32_t w0 = (uint32_t)min((uint64_t)a.n, (rank * kSortWarps + warp) * per_warp);
+    const uint32_t w1 = (uint32_t)min((uint64_t)a.n, w0 + per_warp);
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int shift = 32 + 8 * pass;
+        for (uint32_t d = lane; d < 256; d += 32) counts[warp][d] = 0;
+        __syncwarp();
+        for (uint32_t i = w0 + lane; i < w1; i += 32) atomicAdd(&counts[warp][(sort_pair(a, pass, i) >> shift) & 255], 1u);
+        __syncthreads();
+        uint32_t mine = 0;
+        if (threadIdx.x < 256) {
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = counts[w][threadIdx.x];
+                counts[w][threadIdx.x] = mine;
+                mine += c;
+            }
+            total[threadIdx.x] = mine;
+        }
+        cluster.sync();
+        uint32_t before = 0, all = 0;  // of this digit in the CTAs before this one, and in all
+        if (threadIdx.x < 256) {
+            for (uint32_t r = 0; r < ctas; ++r) {
+                const uint32_t c = cluster.map_shared_rank(total, r)[threadIdx.x];
+                before += r < rank ? c : 0;
+                all += c;
+            }
+            scan[threadIdx.x] = all;
+        }
+        __syncthreads();
+        for (int s = 1; s < 256; s <<= 1) {
+            const uint32_t x = threadIdx.x < 256 && threadIdx.x >= (uint32_t)s ? scan[threadIdx.x - s] : 0;
+            __syncthreads();
+            if (threadIdx.x < 256) scan[threadIdx.x] += x;
+            __syncthreads();
+        }
+        if (threadIdx.x < 256) {
+            const uint32_t base = scan[threadIdx.x] - all + before;
+            for (int w = 0; w < kSortWarps; ++w) counts[w][threadIdx.x] += base;
+        }
+        __syncthreads();
+        uint64_t* out = a.pairs[(pass + 1) & 1];
+        for (uint32_t i0 = w0; i0 < w1; i0 += 32) {  // in order: equal digits keep theirs
+            const uint32_t i = i0 + lane;
+            const bool on = i < w1;
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, on);
+            if (on) {
+                const uint64_t p = sort_pair(a, pass, i);
+                const uint32_t digit = (p >> shift) & 255;
+                const uint32_t same = __match_any_sync(live, digit);
+                const uint32_t at = counts[warp][digit];
+                __syncwarp(live);
+                if (lane == (uint32_t)(__ffs(same) - 1)) counts[warp][digit] = at + __popc(same);
+                out[at + __popc(same & ((1u << lane) - 1))] = p;
+            }
+            __syncwarp();
+        }
+        // the pairs, and the counts of all CTAs, before the next pass reads and overwrites them
+        __threadfence();
+        cluster.sync();
+    }
+}
+
+// The sorted tokens are cut into pieces of `piece`.  A group of threads adds
+// the rows of a piece's tokens, id after id.  What begins and ends in the piece
+// is a gradient's row; what reaches into another piece goes into a binary32
+// row of its own (slot 0: it came from the piece before; slot 1: it begins
+// here), which embed_join_kernel adds up.
+struct EmbedGradArgs {
+    const void* grad;
+    const uint64_t* pairs;
+    void* out;
+    float* parts;  // [pieces][2][d]
+    uint32_t n, pieces, d, dv, vocab;
+    int32_t piece;
+    int32_t group;  // threads of a piece
+    int32_t accumulate;
+    float scale;
+};
+
+template <class F, class O, int E>
+__device__ __forceinline__ void embed_row(const EmbedGradArgs& a, uint32_t id, uint32_t c, float (&x)[E]) {
+    typename Store<O>::S* p = static_cast<typename Store<O>::S*>(a.out) + (size_t)id * a.d + (size_t)c * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], a.scale);
+    if (a.accumulate) add_e<O, E>(p, x);
+    st_e<O, E>(p, x);
+}
+
+template <class F, class O, int E>
+__global__ void __launch_bounds__(kThreads) embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
+    using S = typename Store<F>::S;
+    const uint32_t per_cta = kThreads / a.group;
+    const uint32_t lane = threadIdx.x % a.group;
+    for (uint32_t q = blockIdx.x * per_cta + threadIdx.x / a.group; q < a.pieces; q += gridDim.x * per_cta) {
+        const uint32_t b = q * a.piece, e = min(a.n, b + a.piece);
+        const uint32_t id_before = b > 0 ? (uint32_t)(__ldg(a.pairs + b - 1) >> 32) : ~0u;
+        const uint32_t id_after = e < a.n ? (uint32_t)(__ldg(a.pairs + e) >> 32) : ~0u;
+        for (uint32_t c = lane; c < a.dv; c += a.group) {
+            float sum[E] = {};
+            uint32_t id = (uint32_t)(__ldg(a.pairs + b) >> 32);
+            bool first = true;  // the piece's first id
+            auto flush = [&](uint32_t next) {
+                if (id < a.vocab) {
+                    const bool came = first && id == id_before, goes = next == id;
+                    if (came || goes) {
+                        float* p = a.parts + ((size_t)q * 2 + (came ? 0 : 1)) * a.d + (size_t)c * E;
+#pragma unroll
+                        for (int k = 0; k < E; ++k) p[k] = sum[k];
+                    } else {
+                        embed_row<F, O, E>(a, id, c, sum);
+                    }
+                }
+                first = false;
+            };
+            for (uint32_t i = b; i < e; i += 4) {
+                uint64_t pair[4];
+                float x[4][E];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    pair[k] = i + k < e ? __ldg(a.pairs + i + k) : ~0ull;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if ((uint32_t)(pair[k] >> 32) < a.vocab)
+                        ld_e<F, E>(static_cast<const S*>(a.grad) + (size_t)(uint32_t)pair[k] * a.d + (size_t)c * E, x[k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t now = (uint32_t)(pair[k] >> 32);
+                    if (now < a.vocab) {
+                        if (now != id) {
+                            flush(now);
+                            id = now;
+#pragma unroll
+                            for (int j = 0; j < E; ++j) sum[j] = x[k][j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < E; ++j) sum[j] = __fadd_rn(sum[j], x[k][j]);
+                        }
+                    }
+                }
+            }
+            // behind the last row of an id in the vocabulary come only padding tokens, which flush nothing
+            flush(id_after);
+        }
+    }
+}
+
+// One CTA adds up the parts of an id whose rows begin in piece q and go on
+// behind it: slot 1 of q, slot 0 of the pieces after it.
+template <class F, class O, int E>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradArgs a) {
+    for (uint32_t q = blockIdx.x; q + 1 < a.pieces; q += gridDim.x) {
+        const uint32_t b = q * a.piece, e = b + a.piece;
+        const uint32_t id = (uint32_t)(__ldg(a.pairs + e) >> 32);
+        if (id >= a.vocab || (uint32_t)(__ldg(a.pairs + e - 1) >> 32) != id) continue;
+        if (b > 0 && (uint32_t)(__ldg(a.pairs + b - 1) >> 32) == id) continue;  // an earlier piece's
+        uint32_t lo = e, hi = a.n;  // the first place behind this id's tokens, in (lo, hi]
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if ((uint32_t)(__ldg(a.pairs + mid) >> 32) == id) lo = mid; else hi = mid;
+        }
+        const uint32_t last = lo / a.piece;
+        for (uint32_t c = threadIdx.x + blockIdx.y * kThreads; c < a.dv; c += kThreads * gridDim.y) {
+            float sum[E];
+            const float* p = a.parts + ((size_t)q * 2 + 1) * a.d + (size_t)c * E;
+#pragma unroll
+            for (int k = 0; k < E; ++k) sum[k] = p[k];
+#pragma unroll 4
+            for (uint32_t r = q + 1; r <= last; ++r) {
+                p = a.parts + (size_t)r * 2 * a.d + (size_t)c * E;
+#pragma unroll
+                for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], p[k]);
+            }
+            embed_row<F, O, E>(a, id, c, sum);
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------
+// Layer norm
+// ----------------------------------------------------------------------------
+// Sum over the threads that share a row: a warp, or the CTA.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float x, float* sh) {
+    x = warp_sum(x);
+    if constexpr (!WARP) {
+        const int warps = blockDim.x / 32;
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x / 32] = x;
+        __syncthreads();
+        x = warp_sum((int)(threadIdx.x & 31) < warps ? sh[threadIdx.x & 31] : 0.0f);
+        __syncthreads();
+    }
+    return x;
+}
+
+struct NormArgs {
+    const void* x;
+    const void* weight;
+    const void* bias;
+    void* y;
+    float* mean;
+    float* rstd;
+    int64_t rows, x_stride;
+    uint32_t d, dv;
+    float eps;
+};
+
+// A row stays in the registers of a warp or of a CTA, NV pieces a thread.
+template <class F, int E, int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? kThreads : 1024) norm_kernel(const __grid_constant__ NormArgs a) {
+    using S = typename Store<F>::S;
+    __shared__ float sh[32];
+    const uint32_t group = WARP ? 32 : blockDim.x;
+    const uint32_t lane = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t first = WARP ? ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32 : blockIdx.x;
+    const int64_t step = WARP ? (int64_t)gridDim.x * blockDim.x / 32 : gridDim.x;
+    const float d = (float)a.d;
+    for (int64_t row = first; row < a.rows; row += step) {
+        const S* src = static_cast<const S*>(a.x) + row * a.x_stride;
+        float x[NV][E];
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t c = lane + k * group;
+            if (c < a.dv) ld_e<F, E>(src + (size_t)c * E, x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (lane + k * group < a.dv)
+#pragma unroll
+                for (int e = 0; e < E; ++e) sum = __fadd_rn(sum, x[k][e]);
+        const float mean = __fdiv_rn(row_sum<WARP>(sum, sh), d);
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (lane + k * group < a.dv)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    x[k][e] = __fsub_rn(x[k][e], mean);
+                    sum = __fmaf_rn(x[k][e], x[k][e], sum);
+                }
+        const float var = __fdiv_rn(row_sum<WARP>(sum, sh), d);
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+        if (lane == 0 && a.mean) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        S* dst = static_cast<S*>(a.y) + row * (int64_t)a.d;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t c = lane + k * group;
+            if (c < a.dv) {
+                float w[E], b[E] = {};
+                ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)c * E, w);
+                if (a.bias) ld_e<F, E>(static_cast<const S*>(a.bias) + (size_t)c * E, b);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[k][e] = __fmaf_rn(__fmul_rn(x[k][e], rstd), w[e], b[e]);
+                st_e<F, E>(dst + (size_t)c * E, x[k]);
+            }
+        }
+    }
+}
+
+constexpr int64_t kNormBlocks = 456;   // blocks of rows, at most: 3 CTAs on each of 152 SMs
+
+struct NormGradArgs {
+    const void* gy;
+    const void* x;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    void* gx;
+    void* gw;
+    void* gb;
+    float* parts;  // [blocks][2][d]: sums of gy * u, of gy
+    int64_t rows, gy_stride, x_stride, per_block;
+    uint32_t d, dv;
+    int32_t blocks, accumulate;
+};
+
+// A CTA takes a block of rows, RI at a time.  The threads keep their columns'
+// sums for the weight and bias in registers; a row's two means are sums over
+// the CTA, for RI rows between two barriers.
+template <class F, int E, int NV, int RI>
+__global__ void __launch_bounds__(RI == 1 ? 1024 : 512) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
+    using S = typename Store<F>::S;
+    __shared__ float sh[2][2 * RI][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    float w[NV][E];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const uint32_t c = threadIdx.x + k * blockDim.x;
+        if (c < a.dv) ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)c * E, w[k]);
+    }
+    const float inv_d = __fdiv_rn(1.0f, (float)a.d);
+    int flip = 0;
+    for (int block = blockIdx.x; block < a.blocks; block += gridDim.x) {
+        float sw[NV][E] = {}, sb[NV][E] = {};
+        const int64_t r1 = min(a.rows, (block + 1) * a.per_block);
+        for (int64_t r0 = block * a.per_block; r0 < r1; r0 += RI, flip ^= 1) {
+            float u[RI][NV][E], g[RI][NV][E], rstd[RI], s[2 * RI];
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const int64_t row = r0 + i;
+                if (row < r1) {
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        const uint32_t c = threadIdx.x + k * blockDim.x;
+                        if (c < a.dv) {
+                            ld_e<F, E>(static_cast<const S*>(a.x) + row * a.x_stride + (size_t)c * E, u[i][k]);
+                            ld_e<F, E>(static_cast<const S*>(a.gy) + row * a.gy_stride + (size_t)c * E, g[i][k]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                s[2 * i] = s[2 * i + 1] = 0.0f;
+                if (r0 + i < r1) {
+                    const float mean = __ldg(a.mean + r0 + i);
+                    rstd[i] = __ldg(a.rstd + r0 + i);
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+                        if (threadIdx.x + k * blockDim.x < a.dv)
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                u[i][k][e] = __fmul_rn(__fsub_rn(u[i][k][e], mean), rstd[i]);
+                                sw[k][e] = __fmaf_rn(g[i][k][e], u[i][k][e], sw[k][e]);
+                                sb[k][e] = __fadd_rn(sb[k][e], g[i][k][e]);
+                                g[i][k][e] = __fmul_rn(g[i][k][e], w[k][e]);
+                                s[2 * i] = __fadd_rn(s[2 * i], g[i][k][e]);
+                                s[2 * i + 1] = __fmaf_rn(g[i][k][e], u[i][k][e], s[2 * i + 1]);
+                            }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * RI; ++i) {
+                s[i] = warp_sum(s[i]);
+                if (lane == 0) sh[flip][i][warp] = s[i];
+            }
+            __syncthreads();   // the other half of sh is written next: one barrier is enough
+#pragma unroll
+            for (int i = 0; i < 2 * RI; ++i)
+                s[i] = __fmul_rn(warp_sum(lane < warps ? sh[flip][i][lane] : 0.0f), inv_d);
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                if (r0 + i < r1) {
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        const uint32_t c = threadIdx.x + k * blockDim.x;
+                        if (c < a.dv) {
+                            float o[E];
+#pragma unroll
+                            for (int e = 0; e < E; ++e)
+                                o[e] = __fmul_rn(rstd[i], __fmaf_rn(-u[i][k][e], s[2 * i + 1], __fsub_rn(g[i][k][e], s[2 * i])));
+                            st_e<F, E>(static_cast<S*>(a.gx) + (r0 + i) * (int64_t)a.d + (size_t)c * E, o);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t c = threadIdx.x + k * blockDim.x;
+            if (c < a.dv) {
+                float* p = a.parts + (size_t)block * 2 * a.d + (size_t)c * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    p[e] = sw[k][e];
+                    p[a.d + e] = sb[k][e];
+                }
+            }
+        }
+    }
+}
+
+// The blocks' sums: 32 columns a CTA, each warp every 32nd block, the warps in order.
+template <class O>
+__global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormGradArgs a) {
+    using S = typename Store<O>::S;
+    __shared__ float sh[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const uint32_t per = (a.d + 31) / 32;
+    for (uint32_t t = blockIdx.x; t < 2 * per; t += gridDim.x) {
+        const bool bias = t >= per;
+        const uint32_t c = (t - (bias ? per : 0)) * 32 + lane;
+        float sum = 0.0f;
+        if (c < a.d)
+#pragma unroll 4
+            for (int b = warp; b < a.blocks; b += 32) sum = __fadd_rn(sum, a.parts[((size_t)b * 2 + bias) * a.d + c]);
+        sh[warp][lane] = sum;
+        __syncthreads();
+        S* p = static_cast<S*>(bias ? a.gb : a.gw);
+        if (warp == 0 && c < a.d && p) {
+            float o[1] = {0.0f};
+            for (int w = 0; w < 32; ++w) o[0] = __fadd_rn(o[0], sh[w][lane]);
+            if (a.accumulate) add_e<O, 1>(p + c, o);
+            st_e<O, 1>(p + c, o);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace zk
+
+using namespace zero_detail;
+
+namespace {
+
+int elem_size(int32_t dtype) { return dtype == ZERO_FP32 ? 4 : 2; }
+
+bool known(int32_t dtype) { return dtype == ZERO_BF16 || dtype == ZERO_FP16 || dtype == ZERO_FP32; }
+
+// A tensor's pointer: natural alignment.
+zero_status_t check_elem_ptr(const void* p, int size, const std::string& what) {
+    if (!p) return fail(ZERO_ERR_INVALID, what + ": NULL device pointer");
+    if (reinterpret_cast<uintptr_t>(p) % size) return fail(ZERO_ERR_ALIGN, what + ": not aligned to its elements");
+    return ZERO_OK;
+}
+
+// Elements of a piece: the widest that rows of d elements at these addresses
+// and strides allow.
+struct Piece {
+    int64_t bits = 0;  // addresses and strides in bytes, or-ed, of what is read or written in pieces
+    int64_t d;
+    int size;
+    explicit Piece(int64_t d_, int size_) : d(d_), size(size_) {}
+    // an array of `its` bytes an element, with rows `stride` elements apart
+    void add(const void* p, int its, int64_t stride) {
+        // in units of `size`: an array of wider elements needs 16 bytes at most
+        const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(p) | (stride * its);
+        bits |= its == size ? a : ((a & 15) == 0 ? 0 : (a & 7) == 0 ? 4 : size);
+    }
+    int elems() const {
+        const int wide = 16 / size;
+        if (d % wide == 0 && bits % 16 == 0) return wide;
+        if (size == 2 && d % 2 == 0 && bits % 4 == 0) return 2;
+        return 1;
+    }
+};
+
+#define ZL_E16(F, e, ...)                                                  \
+    do {                                                                   \
+        if ((e) == 8) { constexpr int E = 8; using T = F; __VA_ARGS__; }   \
+        else if ((e) == 2) { constexpr int E = 2; using T = F; __VA_ARGS__; } \
+        else { constexpr int E = 1; using T = F; __VA_ARGS__; }            \
+    } while (0)
+// T: the type, E: elements of a piece
+#define ZL_DISPATCH(dtype, e, ...)                                         \
+    do {                                                                   \
+        if ((dtype) == ZERO_BF16) ZL_E16(zk::Bf16, e, __VA_ARGS__);        \
+        else if ((dtype) == ZERO_FP16) ZL_E16(zk::Fp16, e, __VA_ARGS__);   \
+        else if ((e) == 4) { constexpr int E = 4; using T = zk::Fp32; __VA_ARGS__; } \
+        else { constexpr int E = 1; using T = zk::Fp32; __VA_ARGS__; }     \
+    } while (0)
+
+int capped(int64_t ctas) {
+    const int32_t cap = max_ctas();
+    if (cap > 0 && ctas > cap) ctas = cap;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, 0x7FFFFFFF));
+}
+
+constexpr int64_t kMaxVocab = 0x7FFFFFFE, kMaxRows = 0x7FFFFFFF, kMaxDim = 1 << 20;
+
+zero_status_t check_embedding(const char* what, int64_t vocab, int64_t d, int64_t n) {
+    if (vocab < 1 || vocab > kMaxVocab) return fail(ZERO_ERR_INVALID, std::string(what) + ": vocab must be 1 .. 2^31-2");
+    if (d < 1 || d > kMaxDim) return fail(ZERO_ERR_INVALID, std::string(what) + ": d must be 1 .. 2^20");
+    if (n < 0 || n > kMaxRows) return fail(ZERO_ERR_INVALID, std::string(what) + ": n must be 0 .. 2^31-1");
+    return ZERO_OK;
+}
+
+// Tokens of a piece of the sorted list: enough pieces to fill the GPU, and
+// long ones for long lists, whose frequent ids leave fewer parts.
+int64_t embed_piece(int64_t n) { return n <= 8192 ? 8 : n <= (1 << 20) ? 32 : 256; }
+
+struct EmbedWorkspace {
+    int64_t pairs0, pairs1, parts, bytes;
+    explicit EmbedWorkspace(int64_t d, int64_t n) {
+        const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+        const int64_t pieces = (n + embed_piece(n) - 1) / embed_piece(n);
+        pairs0 = 0;
+        pairs1 = up(n * 8);
+        parts = pairs1 + up(n * 8);
+        bytes = parts + up(pieces * 2 * d * 4) + 256;
+    }
+};
+
+}  // namespace
+
+extern "C" zero_status_t zero_embedding_forward(const void* weight, const int64_t* ids, int64_t vocab, int64_t d, int64_t n,
+                                                int32_t dtype, double scale, void* out, zero_stream_t stream) {
+    clear_error();
+    const char* what = "zero_embedding_forward";
+    zero_status_t rc = check_embedding(what, vocab, d, n);
+    if (rc != ZERO_OK) return rc;
+    if (!known(dtype)) return fail(ZERO_ERR_INVALID, "zero_embedding_forward: unknown dtype");
+    if (!std::isfinite(scale)) return fail(ZERO_ERR_INVALID, "zero_embedding_forward: scale must be finite");
+    if (n == 0) return ZERO_OK;
+    const int size = elem_size(dtype);
+    if ((rc = check_elem_ptr(weight, size, "zero_embedding_forward weight")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(ids, 8, "zero_embedding_forward ids")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(out, size, "zero_embedding_forward out")) != ZERO_OK) return rc;
+    Piece piece(d, size);
+    piece.add(weight, size, 0);
+    piece.add(out, size, 0);
+    const int e = piece.elems();
+    zk::EmbedArgs a{weight, ids, out, vocab, n, (uint32_t)d, (uint32_t)(d / e), 0, (float)scale};
+    while (a.lanes_log2 < 5 && (1u << a.lanes_log2) < a.dv) ++a.lanes_log2;
+    const int64_t ctas = ((n << a.lanes_log2) + zk::kThreads - 1) / zk::kThreads;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ZL_DISPATCH(dtype, e, zk::embed_kernel<T, E><<<capped(ctas), zk::kThreads, 0, s>>>(a));
+    return after_launch(what);
+}
+
+extern "C" zero_status_t zero_embedding_workspace(int64_t vocab, int64_t d, int64_t n, int64_t* bytes) {
+    clear_error();
+    const zero_status_t rc = check_embedding("zero_embedding_workspace", vocab, d, n);
+    if (rc != ZERO_OK) return rc;
+    if (!bytes) return fail(ZERO_ERR_INVALID, "zero_embedding_workspace: NULL bytes");
+    *bytes = EmbedWorkspace(d, n).bytes;
+    return ZERO_OK;
+}
+
+namespace {
+
+template <class F, class O, int E>
+zero_status_t launch_embed_grad(const zk::EmbedGradArgs& a, cudaStream_t s) {
+    const char* what = "zero_embedding_backward";
+    auto k = zk::embed_grad_kernel<F, O, E>;
+    const uint32_t per_cta = zk::kThreads / a.group;
+    k<<<persistent_grid(k, (a.pieces + per_cta - 1) / per_cta), zk::kThreads, 0, s>>>(a);
+    zero_status_t rc = after_launch(what);
+    if (rc != ZERO_OK || a.pieces < 2) return rc;
+    // few CTAs find something to add: pieces x column slices
+    const int64_t slices = std::min<int64_t>((a.dv + zk::kThreads - 1) / zk::kThreads, 64);
+    const dim3 grid((unsigned)capped(std::min<int64_t>(a.pieces - 1, 65535)), (unsigned)(max_ctas() > 0 ? 1 : slices));
+    zk::embed_join_kernel<F, O, E><<<grid, zk::kThreads, 0, s>>>(a);
+    return after_launch(what);
+}
+
+}  // namespace
+
+extern "C" zero_status_t zero_embedding_backward(const void* grad_out, const int64_t* ids, int64_t vocab, int64_t d,
+                                                 int64_t n, int32_t dtype, int32_t grad_dtype, double scale,
+                                                 int32_t accumulate, void* grad_weight, void* workspace,
+                                                 zero_stream_t stream) {
+    clear_error();
+    const char* what = "zero_embedding_backward";
+    zero_status_t rc = check_embedding(what, vocab, d, n);
+    if (rc != ZERO_OK) return rc;
+    if (!known(dtype)) return fail(ZERO_ERR_INVALID, "zero_embedding_backward: unknown dtype");
+    if (grad_dtype != dtype && grad_dtype != ZERO_FP32)
+        return fail(ZERO_ERR_INVALID, "zero_embedding_backward: grad_dtype must be dtype or ZERO_FP32");
+    if (!std::isfinite(scale)) return fail(ZERO_ERR_INVALID, "zero_embedding_backward: scale must be finite");
+    const int size = elem_size(dtype), gsize = elem_size(grad_dtype);
+    if ((rc = check_elem_ptr(grad_weight, gsize, "zero_embedding_backward grad_weight")) != ZERO_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (n == 0) {
+        if (accumulate) return ZERO_OK;
+        const cudaError_t err = cudaMemsetAsync(grad_weight, 0, (size_t)vocab * d * gsize, s);
+        return err == cudaSuccess ? ZERO_OK : fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(err));
+    }
+    if ((rc = check_elem_ptr(grad_out, size, "zero_embedding_backward grad_out")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(ids, 8, "zero_embedding_backward ids")) != ZERO_OK) return rc;
+    if ((rc = check_dev_ptr(workspace, "zero_embedding_backward workspace")) != ZERO_OK) return rc;
+    const EmbedWorkspace ws(d, n);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+
+    zk::SortArgs sa{};
+    sa.ids = ids;
+    sa.pairs[0] = reinterpret_cast<uint64_t*>(base + ws.pairs0);
+    sa.pairs[1] = reinterpret_cast<uint64_t*>(base + ws.pairs1);
+    sa.zero = static_cast<uint8_t*>(grad_weight);
+    sa.zero_bytes = accumulate ? 0 : vocab * d * gsize;
+    sa.vocab = vocab;
+    sa.n = (uint32_t)n;
+    sa.passes = 1;
+    while (sa.passes < 4 && (vocab >> (8 * sa.passes)) > 0) ++sa.passes;
+    const int32_t cap = max_ctas();
+    // the cluster that sorts: 8 CTAs, one for what one can sort as fast
+    int cluster = n <= 2048 ? 1 : 8;
+    while (cap > 0 && cluster > 1 && cluster > cap) cluster /= 2;
+    int64_t fill = sa.zero_bytes == 0 ? 0 : std::min<int64_t>((sa.zero_bytes / 16 / zk::kSortThreads + cluster) / cluster, 2 * 152 / cluster);
+    if (sa.zero_bytes > 0 && fill < 1) fill = 1;
+    if (cap > 0) fill = std::min<int64_t>(fill, std::max<int64_t>(1, cap / cluster - 1));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(cluster * (1 + (sa.zero_bytes > 0 ? fill : 0))));
+    cfg.blockDim = dim3(zk::kSortThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, zk::embed_sort_kernel, sa);
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(err));
+    }
+    if ((rc = after_launch(what)) != ZERO_OK) return rc;
+
+    Piece piece(d, size);
+    piece.add(grad_out, size, 0);
+    piece.add(grad_weight, gsize, 0);
+    const int e = piece.elems();
+    zk::EmbedGradArgs a{};
+    a.grad = grad_out;
+    a.pairs = sa.pairs[sa.passes & 1];
+    a.out = grad_weight;
+    a.parts = reinterpret_cast<float*>(base + ws.parts);
+    a.n = (uint32_t)n;
+    a.piece = (int32_t)embed_piece(n);
+    a.pieces = (uint32_t)((n + a.piece - 1) / a.piece);
+    a.d = (uint32_t)d;
+    a.dv = (uint32_t)(d / e);
+    a.vocab = (uint32_t)vocab;
+    a.group = 1;
+    while (a.group < zk::kThreads && (uint32_t)a.group < a.dv) a.group *= 2;
+    a.accumulate = accumulate != 0;
+    a.scale = (float)scale;
+    if (grad_dtype == dtype) ZL_DISPATCH(dtype, e, rc = launch_embed_grad<T, T, E>(a, s));
+    else ZL_DISPATCH(dtype, e, rc = launch_embed_grad<T, zk::Fp32, E>(a, s));
+    return rc;
+}
+
+// ----------------------------------------------------------------------------
+// Layer norm
+// ----------------------------------------------------------------------------
+namespace {
+
+zero_status_t check_norm(const char* what, int64_t rows, int64_t d) {
+    if (rows < 0 || rows > kMaxRows) return fail(ZERO_ERR_INVALID, std::string(what) + ": rows must be 0 .. 2^31-1");
+    if (d < 1 || d > ZERO_MAX_NORM_DIM) return fail(ZERO_ERR_INVALID, std::string(what) + ": d must be 1 .. ZERO_MAX_NORM_DIM");
+    return ZERO_OK;
+}
+
+template <class F, int E>
+void launch_norm(const zk::NormArgs& a, cudaStream_t s) {
+    // a warp keeps up to 64 elements a lane, a CTA's thread up to 16
+    constexpr int WIDE = E == 1 ? 32 : E == 2 ? 16 : E == 4 ? 8 : 8;
+    constexpr int HALF = WIDE / 2;
+    const auto warps = [&](auto kern) { kern<<<persistent_grid(kern, (a.rows + 7) / 8), zk::kThreads, 0, s>>>(a); };
+    if (a.dv <= 32u * HALF) return warps(zk::norm_kernel<F, E, HALF, true>);
+    if (a.dv <= 32u * WIDE) return warps(zk::norm_kernel<F, E, WIDE, true>);
+    constexpr int NV = 16 / E;
+    auto kern = zk::norm_kernel<F, E, NV, false>;
+    const int threads = (int)((a.dv + NV - 1) / NV + 31) / 32 * 32;
+    kern<<<persistent_grid(kern, a.rows, 0, threads), threads, 0, s>>>(a);
+}
+
+int64_t norm_rows_per_block(int64_t rows) {
+    const int64_t per = (rows + zk::kNormBlocks - 1) / zk::kNormBlocks;
+    return std::max<int64_t>(4, per);
+}
+
+template <class F, int E>
+void launch_norm_grad(const zk::NormGradArgs& a, cudaStream_t s) {
+    const auto go = [&](auto kern, int nv) {
+        const int threads = (int)((a.dv + nv - 1) / nv + 31) / 32 * 32;
+        kern<<<persistent_grid(kern, a.blocks, 0, threads), threads, 0, s>>>(a);
+    };
+    if constexpr (E >= 4) {
+        if (a.dv <= 512) return go(zk::norm_grad_kernel<F, E, 1, 4>, 1);
+        go(zk::norm_grad_kernel<F, E, E == 8 ? 2 : 4, 1>, E == 8 ? 2 : 4);
+    } else {
+        if (a.dv <= 1024u) return go(zk::norm_grad_kernel<F, E, 2, 4>, 2);
+        go(zk::norm_grad_kernel<F, E, 16 / E, 1>, 16 / E);
+    }
+}
+
+}  // namespace
+
+extern "C" zero_status_t zero_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                                                 int64_t rows, int64_t d, int32_t dtype, double eps, void* y, float* mean,
+                                                 float* rstd, zero_stream_t stream) {
+    clear_error();
+    const char* what = "zero_layer_norm_forward";
+    zero_status_t rc = check_norm(what, rows, d);
+    if (rc != ZERO_OK) return rc;
+    if (!known(dtype)) return fail(ZERO_ERR_INVALID, "zero_layer_norm_forward: unknown dtype");
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(ZERO_ERR_INVALID, "zero_layer_norm_forward: eps must be >= 0");
+    if (x_stride < d) return fail(ZERO_ERR_INVALID, "zero_layer_norm_forward: rows overlap (x_stride < d)");
+    if ((mean == nullptr) != (rstd == nullptr)) return fail(ZERO_ERR_INVALID, "zero_layer_norm_forward: mean and rstd go together");
+    if (rows == 0) return ZERO_OK;
+    const int size = elem_size(dtype);
+    if ((rc = check_elem_ptr(x, size, "zero_layer_norm_forward x")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(weight, size, "zero_layer_norm_forward weight")) != ZERO_OK) return rc;
+    if (bias && (rc = check_elem_ptr(bias, size, "zero_layer_norm_forward bias")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(y, size, "zero_layer_norm_forward y")) != ZERO_OK) return rc;
+    if (mean && ((rc = check_elem_ptr(mean, 4, "zero_layer_norm_forward mean")) != ZERO_OK ||
+                 (rc = check_elem_ptr(rstd, 4, "zero_layer_norm_forward rstd")) != ZERO_OK)) return rc;
+    Piece piece(d, size);
+    piece.add(x, size, rows > 1 ? x_stride : 0);
+    piece.add(weight, size, 0);
+    piece.add(bias, size, 0);
+    piece.add(y, size, 0);
+    const int e = piece.elems();
+    const zk::NormArgs a{x, weight, bias, y, mean, rstd, rows, x_stride, (uint32_t)d, (uint32_t)(d / e), (float)eps};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    ZL_DISPATCH(dtype, e, launch_norm<T, E>(a, s));
+    return after_launch(what);
+}
+
+extern "C" zero_status_t zero_layer_norm_workspace(int64_t rows, int64_t d, int64_t* bytes) {
+    clear_error();
+    const zero_status_t rc = check_norm("zero_layer_norm_workspace", rows, d);
+    if (rc != ZERO_OK) return rc;
+    if (!bytes) return fail(ZERO_ERR_INVALID, "zero_layer_norm_workspace: NULL bytes");
+    const int64_t per = norm_rows_per_block(rows);
+    *bytes = ((rows + per - 1) / per * 2 * d * 4 + 255) / 256 * 256 + 256;
+    return ZERO_OK;
+}
+
+extern "C" zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, const void* x, int64_t x_stride,
+                                                  const void* weight, const float* mean, const float* rstd, int64_t rows,
+                                                  int64_t d, int32_t dtype, int32_t grad_dtype, int32_t accumulate,
+                                                  void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                                                  zero_stream_t stream) {
+    clear_error();
+    const char* what = "zero_layer_norm_backward";
+    zero_status_t rc = check_norm(what, rows, d);
+    if (rc != ZERO_OK) return rc;
+    if (!known(dtype)) return fail(ZERO_ERR_INVALID, "zero_layer_norm_backward: unknown dtype");
+    if (grad_dtype != dtype && grad_dtype != ZERO_FP32)
+        return fail(ZERO_ERR_INVALID, "zero_layer_norm_backward: grad_dtype must be dtype or ZERO_FP32");
+    if (x_stride < d || gy_stride < d) return fail(ZERO_ERR_INVALID, "zero_layer_norm_backward: rows overlap (a stride < d)");
+    const int size = elem_size(dtype), gsize = elem_size(grad_dtype);
+    if ((rc = check_elem_ptr(grad_weight, gsize, "zero_layer_norm_backward grad_weight")) != ZERO_OK) return rc;
+    if (grad_bias && (rc = check_elem_ptr(grad_bias, gsize, "zero_layer_norm_backward grad_bias")) != ZERO_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        if (accumulate) return ZERO_OK;
+        cudaError_t err = cudaMemsetAsync(grad_weight, 0, (size_t)d * gsize, s);
+        if (err == cudaSuccess && grad_bias) err = cudaMemsetAsync(grad_bias, 0, (size_t)d * gsize, s);
+        return err == cudaSuccess ? ZERO_OK : fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(err));
+    }
+    if ((rc = check_elem_ptr(grad_y, size, "zero_layer_norm_backward grad_y")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(x, size, "zero_layer_norm_backward x")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(weight, size, "zero_layer_norm_backward weight")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(mean, 4, "zero_layer_norm_backward mean")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(rstd, 4, "zero_layer_norm_backward rstd")) != ZERO_OK) return rc;
+    if ((rc = check_elem_ptr(grad_x, size, "zero_layer_norm_backward grad_x")) != ZERO_OK) return rc;
+    if ((rc = check_dev_ptr(workspace, "zero_layer_norm_backward workspace")) != ZERO_OK) return rc;
+    Piece piece(d, size);
+    piece.add(x, size, rows > 1 ? x_stride : 0);
+    piece.add(grad_y, size, rows > 1 ? gy_stride : 0);
+    piece.add(weight, size, 0);
+    piece.add(grad_x, size, 0);
+    const int e = piece.elems();
+    zk::NormGradArgs a{};
+    a.gy = grad_y;
+    a.x = x;
+    a.weight = weight;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.gx = grad_x;
+    a.gw = grad_weight;
+    a.gb = grad_bias;
+    a.parts = static_cast<float*>(workspace);
+    a.rows = rows;
+    a.gy_stride = gy_stride;
+    a.x_stride = x_stride;
+    a.per_block = norm_rows_per_block(rows);
+    a.blocks = (int32_t)((rows + a.per_block - 1) / a.per_block);
+    a.d = (uint32_t)d;
+    a.dv = (uint32_t)(d / e);
+    a.accumulate = accumulate != 0;
+    ZL_DISPATCH(dtype, e, launch_norm_grad<T, E>(a, s));
+    if ((rc = after_launch(what)) != ZERO_OK) return rc;
+    const int join = capped(2 * ((d + 31) / 32));
+    if (grad_dtype == ZERO_FP32) zk::norm_join_kernel<zk::Fp32><<<join, 1024, 0, s>>>(a);
+    else if (grad_dtype == ZERO_BF16) zk::norm_join_kernel<zk::Bf16><<<join, 1024, 0, s>>>(a);
+    else zk::norm_join_kernel<zk::Fp16><<<join, 1024, 0, s>>>(a);
+    return after_launch(what);
+}
