@@ -825,6 +825,76 @@ zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, co
                                        void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
                                        zero_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Language-model head and loss                                                */
+/* ------------------------------------------------------------------------ */
+/* Softmax cross entropy of the logits hidden @ weight^T against a target per
+ * token, without keeping the logits: [n, vocab] of them (0.8 GB in 16 bits at
+ * 8192 tokens of GPT-2) never exist.  The forward call computes tiles of
+ * them in tensor memory and keeps each tile's row maximum and sum of
+ * exponentials; the backward call computes them again, piece of the
+ * vocabulary by piece, turns a piece into its gradient (16-bit, rounded once)
+ * and multiplies that with the weight and with the hidden states.
+ *   loss_i = log(sum_k exp(z_ik)) - z_i,target(i),  z_ik = hidden_i . weight_k
+ *   dz_ik = (exp(z_ik - lse_i) - [k == target(i)]) * share * scale
+ *   grad_hidden = dz @ weight,  grad_weight (+)= dz^T @ hidden
+ * share: 1 / (number of tokens that count) for ZERO_LOSS_MEAN, 1 for
+ * ZERO_LOSS_SUM.  A target outside 0 .. vocab-1 (padding) makes a token not
+ * count: its loss is 0, its row of grad_hidden zeros, its hidden state is
+ * read by no product (it may hold NaN).  With no token that counts, the
+ * loss and all gradients are zeros.
+ *
+ * hidden [n, d] with hidden_stride elements between rows (>= d), weight
+ * [vocab, d], of dtype ZERO_BF16 or ZERO_FP16; targets [n]; losses, lse [n] and
+ * stats [2] binary32: stats[0] is the mean (or sum) of the losses, stats[1]
+ * the share.  grad_hidden [n, d] and grad_weight [vocab, d] have dtype, and
+ * carry scale times *scale_dev (if not NULL, a binary32 on the device: the
+ * loss scale of a zero_step_state, or the gradient of the loss).  With
+ * accumulate != 0 grad_weight is added to, with one rounding of the sum.
+ * Products accumulate in binary32; dz is rounded to dtype before scale and
+ * share (fp16: times 2^14, so that small probabilities stay normal numbers),
+ * which are applied in binary32 to the sums.
+ *
+ * Tensors need the natural alignment of their elements; products are read by
+ * TMA, so a weight that does not begin on a 16-byte boundary, or whose d is
+ * not a multiple of 8, is copied into the workspace first.  The other
+ * differences from the conventions above are those of the embedding and the
+ * layer norm.  Kernels take whole SMs: zero_set_max_ctas caps their CTAs at the
+ * next even number. */
+enum { ZERO_LOSS_MEAN = 0, ZERO_LOSS_SUM = 1 };
+
+typedef struct zero_lm_loss_args {
+    int64_t n, d, vocab;      /* 0 .. 2^31-1, 1 .. 65536, 1 .. 2^31-2            */
+    int64_t hidden_stride;
+    int32_t dtype, reduction;
+    int64_t piece;            /* columns of dz that exist at a time in the backward
+                                 call; 0: chosen (up to 512 MiB of them); else
+                                 rounded up to a multiple of 256                */
+    const void* hidden;
+    const void* weight;
+    const int64_t* targets;
+    float* losses;            /* forward only                                  */
+    float* lse;               /* written by forward, read by backward          */
+    float* stats;
+    void* workspace;          /* forward_bytes or backward_bytes of the query  */
+    /* backward only */
+    double scale;
+    const float* scale_dev;   /* or NULL                                       */
+    void* grad_hidden;        /* or NULL: not computed                         */
+    void* grad_weight;        /* or NULL: not computed                         */
+    int32_t accumulate;
+} zero_lm_loss_args;
+
+/* Workspace sizes; reads the sizes, strides, dtype, piece and the weight's address. */
+zero_status_t zero_lm_loss_query(const zero_lm_loss_args* a, int64_t* forward_bytes, int64_t* backward_bytes);
+zero_status_t zero_lm_loss_forward(const zero_lm_loss_args* a, zero_stream_t stream);
+zero_status_t zero_lm_loss_backward(const zero_lm_loss_args* a, zero_stream_t stream);
+
+/* Errors that the last call's kernels reported in this workspace, with the
+ * bits of zero_step_state.error (*bits = 0: none).  Synchronises the device.
+ * A forward call that reports one has NaN in stats[0]. */
+zero_status_t zero_lm_loss_device_error(const void* workspace, int32_t* bits);
+
 /* Cap on the CTAs of every later launch by this library (process-wide;
  * 0 = no cap: each kernel's own persistent grid, one full wave of CTAs or,
  * where that measured faster on GB300, fewer CTAs per SM).  For overlapping

@@ -112,3 +112,101 @@ X, V, M = torch.zeros(3, 4), torch.zeros(4), torch.zeros(3)
 def test_python_refusals(call, word):
     with pytest.raises(ValueError, match=word):
         call()
+
+
+# -- language-model loss ---------------------------------------------------------------------------------
+def _loss(**kw):
+    a = dict(n=3, d=8, vocab=10, hidden_stride=8, dtype=B.ZERO_BF16, reduction=B.ZERO_LOSS_MEAN, piece=0, hidden=FAKE, weight=FAKE,
+             targets=FAKE, losses=FAKE, lse=FAKE, stats=FAKE, workspace=FAKE, scale=1.0, scale_dev=None, grad_hidden=FAKE,
+             grad_weight=FAKE, accumulate=0)
+    a.update(kw)
+    return B.zero_lm_loss_args(**a)
+
+
+LOSS_SIZES = [dict(n=-1), dict(n=2 ** 31), dict(d=0), dict(d=65537, hidden_stride=65537), dict(vocab=0), dict(vocab=2 ** 31 - 1),
+              dict(hidden_stride=7), dict(dtype=B.ZERO_FP32), dict(dtype=-1), dict(piece=-1)]
+
+
+@pytest.mark.parametrize("bad", LOSS_SIZES + [dict(reduction=2), dict(hidden=0), dict(weight=0), dict(targets=0), dict(losses=0),
+                                              dict(lse=0), dict(stats=0), dict(workspace=0)])
+def test_loss_forward_invalid(bad):
+    assert _status(B.zero_lm_loss_forward, _loss(**bad), 0) == B.ZERO_ERR_INVALID
+
+
+@pytest.mark.parametrize("bad", LOSS_SIZES + [dict(hidden=0), dict(weight=0), dict(targets=0), dict(lse=0), dict(stats=0),
+                                              dict(workspace=0), dict(scale=float("inf")), dict(scale=float("nan"))])
+def test_loss_backward_invalid(bad):
+    assert _status(B.zero_lm_loss_backward, _loss(**bad), 0) == B.ZERO_ERR_INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(hidden=FAKE + 1), dict(weight=FAKE + 1), dict(targets=FAKE + 4), dict(lse=FAKE + 2),
+                                 dict(stats=FAKE + 2), dict(workspace=FAKE + 16)])
+def test_loss_misaligned(bad):
+    assert _status(B.zero_lm_loss_forward, _loss(**bad), 0) == B.ZERO_ERR_ALIGN
+    assert _status(B.zero_lm_loss_backward, _loss(**bad), 0) == B.ZERO_ERR_ALIGN
+
+
+@pytest.mark.parametrize("bad", [dict(scale_dev=FAKE + 1), dict(grad_hidden=FAKE + 1), dict(grad_weight=FAKE + 1)])
+def test_loss_backward_misaligned(bad):
+    assert _status(B.zero_lm_loss_backward, _loss(**bad), 0) == B.ZERO_ERR_ALIGN
+
+
+def test_loss_queries():
+    lib = B.lib()
+    for fn in (lib.zero_lm_loss_forward, lib.zero_lm_loss_backward):
+        assert fn(None, None) == B.ZERO_ERR_INVALID
+    assert lib.zero_lm_loss_query(None, None, None) == B.ZERO_ERR_INVALID
+    assert _status(B.zero_lm_loss_query, _loss(vocab=0)) == B.ZERO_ERR_INVALID
+    f, b = B.zero_lm_loss_query(_loss(n=8192, d=1600, vocab=50257, hidden_stride=1600))
+    assert f % 256 == 0 and b % 256 == 0
+    assert f < 64 << 20 and b < 800 << 20            # the logits alone would be 824 MB in 16 bits
+    # bounded whatever the vocabulary, less with a smaller piece, and a copy of a weight that TMA cannot read
+    assert B.zero_lm_loss_query(_loss(n=8192, d=1600, vocab=10 ** 6, hidden_stride=1600))[1] < 800 << 20
+    assert B.zero_lm_loss_query(_loss(n=8192, d=1600, vocab=50257, hidden_stride=1600, piece=256))[1] < 128 << 20
+    assert B.zero_lm_loss_query(_loss(weight=FAKE + 2))[0] > B.zero_lm_loss_query(_loss())[0]
+    assert B.zero_lm_loss_query(_loss(n=0))[0] > 0
+    assert lib.zero_lm_loss_device_error(None, None) == B.ZERO_ERR_INVALID
+    assert _status(B.zero_lm_loss_device_error, 0) == B.ZERO_ERR_INVALID
+    assert _status(B.zero_lm_loss_device_error, FAKE + 8) == B.ZERO_ERR_ALIGN
+    B.zero_lm_loss_backward(_loss(grad_hidden=None, grad_weight=None), 0)      # nothing asked for
+
+
+def test_loss_struct_matches_the_header(tmp_path):
+    import ctypes
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cls = B.zero_lm_loss_args
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "zero.h"', "int main(void) {",
+             'printf("size %zu\\n", sizeof(zero_lm_loss_args));']
+    lines += ['printf("%s %%zu\\n", offsetof(zero_lm_loss_args, %s));' % (f[0], f[0]) for f in cls._fields_]
+    lines += ['printf("%s %%d\\n", (int)%s);' % (c, c) for c in ("ZERO_MAX_NORM_DIM", "ZERO_LOSS_MEAN", "ZERO_LOSS_SUM")]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines + ["return 0;", "}"]))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
+    got = dict(x.split() for x in subprocess.run([str(exe)], capture_output=True, text=True).stdout.splitlines())
+    assert int(got["size"]) == ctypes.sizeof(cls)
+    for f in cls._fields_:
+        assert int(got[f[0]]) == getattr(cls, f[0]).offset, f[0]
+    for c in ("ZERO_MAX_NORM_DIM", "ZERO_LOSS_MEAN", "ZERO_LOSS_SUM"):
+        assert int(got[c]) == getattr(B, c), c
+
+
+H, HW = torch.zeros(3, 4, dtype=torch.bfloat16), torch.zeros(10, 4, dtype=torch.bfloat16)
+SAVED = (torch.zeros(3), torch.zeros(2))
+
+
+@pytest.mark.parametrize("call,word", [
+    (lambda: L.lm_loss_forward(H, HW, IDS, reduction="none"), "reduction"),
+    (lambda: L.lm_loss_forward(H, HW[0], IDS), "weight"),
+    (lambda: L.lm_loss_forward(H, HW.t(), IDS), "contiguous"),
+    (lambda: L.lm_loss_forward(H.float(), HW.float(), IDS), "hidden"),
+    (lambda: L.lm_loss_forward(H, HW.half(), IDS), "weight"),
+    (lambda: L.lm_loss_forward(H, HW, IDS.int()), "int64"),
+    (lambda: L.lm_loss_forward(H, HW, IDS[:2]), "targets"),
+    (lambda: L.lm_loss_forward(H[:, :3], HW, IDS), "hidden"),
+    (lambda: L.lm_loss_forward(H, HW, IDS), "CUDA"),
+    (lambda: L.lm_loss(H, HW, IDS), "CUDA")])
+def test_loss_python_refusals(call, word):
+    with pytest.raises(ValueError, match=word):
+        call()

@@ -41,6 +41,8 @@ ZERO_MULTI_DECIDED = 0
 ZERO_MULTI_ADVANCE = 1
 ZERO_MULTI_UNSCALED = 2
 ZERO_MAX_NORM_DIM = 16384
+ZERO_LOSS_MEAN = 0
+ZERO_LOSS_SUM = 1
 
 EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero_layout_unit",
             "zero_layout_tensor_offset", "zero_layout_destroy", "zero_state_init",
@@ -53,7 +55,8 @@ EXPORTED = ["zero_layout_init", "zero_layout_query", "zero_layout_bucket", "zero
             "zero_checked_set_slack", "zero_multi_init", "zero_multi_query", "zero_multi_destroy", "zero_multi_bind",
             "zero_multi_grad_norm", "zero_multi_adamw", "zero_multi_adamw8", "zero_multi_encode8",
             "zero_multi_decode8", "zero_multi_device_error", "zero_embedding_forward", "zero_embedding_workspace",
-            "zero_embedding_backward", "zero_layer_norm_forward", "zero_layer_norm_workspace", "zero_layer_norm_backward"]
+            "zero_embedding_backward", "zero_layer_norm_forward", "zero_layer_norm_workspace", "zero_layer_norm_backward",
+            "zero_lm_loss_query", "zero_lm_loss_forward", "zero_lm_loss_backward", "zero_lm_loss_device_error"]
 ZERO_NOALLOC_MAX_ELEMS = 67108864
 
 
@@ -115,6 +118,14 @@ class zero_multi_arrays(ctypes.Structure):
 class zero_multi_info(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("n_tensors", "n_groups", "grad_dtype", "param_dtype")] +
                 [(n, ctypes.c_int64) for n in ("numel", "n_chunks", "state8_bytes", "workspace_bytes")])
+
+
+class zero_lm_loss_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("n", "d", "vocab", "hidden_stride")] +
+                [(n, ctypes.c_int32) for n in ("dtype", "reduction")] + [("piece", ctypes.c_int64)] +
+                [(n, ctypes.c_void_p) for n in ("hidden", "weight", "targets", "losses", "lse", "stats", "workspace")] +
+                [("scale", ctypes.c_double)] +
+                [(n, ctypes.c_void_p) for n in ("scale_dev", "grad_hidden", "grad_weight")] + [("accumulate", ctypes.c_int32)])
 
 
 ZERO_UNIT_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
@@ -233,6 +244,10 @@ def lib():
         "zero_embedding_workspace": [i64, i64, i64, ctypes.POINTER(i64)],
         "zero_embedding_backward": [P, P, i64, i64, i64, i32, i32, dbl, i32, P, P, P],
         "zero_layer_norm_forward": [P, i64, P, P, i64, i64, i32, dbl, P, P, P, P],
+        "zero_lm_loss_query": [ctypes.POINTER(zero_lm_loss_args), ctypes.POINTER(i64), ctypes.POINTER(i64)],
+        "zero_lm_loss_forward": [ctypes.POINTER(zero_lm_loss_args), P],
+        "zero_lm_loss_backward": [ctypes.POINTER(zero_lm_loss_args), P],
+        "zero_lm_loss_device_error": [P, ctypes.POINTER(i32)],
         "zero_layer_norm_workspace": [i64, i64, ctypes.POINTER(i64)],
         "zero_layer_norm_backward": [P, i64, P, i64, P, P, P, i64, i64, i32, i32, i32, P, P, P, P, P],
     }
@@ -654,3 +669,25 @@ def zero_layer_norm_backward(grad_y, gy_stride: int, x, x_stride: int, weight, m
     _check(lib().zero_layer_norm_backward(_addr(grad_y), gy_stride, _addr(x), x_stride, _addr(weight), _addr(mean),
                                           _addr(rstd), rows, d, dtype, grad_dtype, int(bool(accumulate)), _addr(grad_x),
                                           _addr(grad_weight), _addr(grad_bias), _addr(workspace), _stream(stream)))
+
+
+def zero_lm_loss_query(args: zero_lm_loss_args):
+    """(forward, backward) workspace bytes."""
+    f, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().zero_lm_loss_query(ctypes.byref(args), ctypes.byref(f), ctypes.byref(b)))
+    return f.value, b.value
+
+
+def zero_lm_loss_forward(args: zero_lm_loss_args, stream=None) -> None:
+    _check(lib().zero_lm_loss_forward(ctypes.byref(args), _stream(stream)))
+
+
+def zero_lm_loss_backward(args: zero_lm_loss_args, stream=None) -> None:
+    _check(lib().zero_lm_loss_backward(ctypes.byref(args), _stream(stream)))
+
+
+def zero_lm_loss_device_error(workspace) -> int:
+    """Errors that the last call's kernels reported (0: none); synchronises the device."""
+    bits = ctypes.c_int32(0)
+    _check(lib().zero_lm_loss_device_error(_addr(workspace), ctypes.byref(bits)))
+    return int(bits.value)

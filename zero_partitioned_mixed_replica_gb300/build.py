@@ -25,8 +25,9 @@ OBJ_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libzero_checked.so")
 
 SOURCES = ["zero_layout.cpp", "zero_rs.cu", "zero_adamw.cu", "zero_norm.cu", "zero_gather.cu",
-           "zero_noalloc.cu", "zero_accum.cu", "zero_multi.cu", "zero_layers.cu", "zero_exec.cpp"]
-HEADERS = ["zero_internal.h", "zero_device.cuh", "zero_launch.h"]
+           "zero_noalloc.cu", "zero_accum.cu", "zero_multi.cu", "zero_layers.cu", "zero_lm_loss.cu",
+           "zero_exec.cpp"]
+HEADERS = ["zero_internal.h", "zero_device.cuh", "zero_launch.h", "zero_tc.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no contraction of a*b+c on the device; the host compiler gets

@@ -191,6 +191,26 @@ class ZeroStep:
     def _s(self):
         return self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
 
+    def tensor_view(self, row: torch.Tensor, tensor: int, shape: Optional[Sequence[int]] = None) -> torch.Tensor:
+        """Tensor ``tensor`` of the layout in a flat buffer of Psi_pad elements
+        (``grads[r]``, ``params[r]``, a master as ``load_master`` takes it): a
+        view, in ``shape`` if given.  Where a backward pass leaves a weight's
+        gradient, and a forward pass finds the weight."""
+        if row.dim() != 1 or row.numel() != self.info.psi_pad:
+            raise ValueError("tensor_view takes a flat buffer of Psi_pad = %d elements" % self.info.psi_pad)
+        if not 0 <= tensor < len(self.numels):
+            raise ValueError("tensor must be 0 .. %d" % (len(self.numels) - 1))
+        at = self.tensor_offsets[tensor]
+        flat = row[at:at + self.numels[tensor]]
+        return flat if shape is None else flat.view(*shape)
+
+    @property
+    def loss_scale(self) -> torch.Tensor:
+        """The current loss scale as a one-element float32 view of the device
+        step state, for a backward pass that is not to wait for the host."""
+        at = B.zero_step_state.loss_scale.offset
+        return self.state[at:at + 4].view(torch.float32)
+
     # -- initialisation (plumbing, not part of the step) -------------------------
     def reset_state(self):
         # after the work on the current stream (the buffers' zero fill, at construction), when

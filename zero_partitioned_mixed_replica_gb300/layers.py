@@ -1,5 +1,5 @@
-"""The operators at a model's ends and between its blocks: embedding and layer
-norm, with their gradients.
+"""The operators at a model's ends and between its blocks: embedding, layer
+norm, and the language-model head with its loss, with their gradients.
 
 A step of :class:`.engine.ZeroStep` or :class:`.multi.MultiAdamW` begins where
 backward has left the weight gradients: in a rank's flat 16-bit replica, or in
@@ -7,10 +7,10 @@ a list of tensors.  The ``*_backward`` functions here write them there, into
 any tensor that the caller gives (``engine.tensor_view(engine.grads[r], t,
 shape)``), overwriting it or adding to it; what else they return is new.
 
-Each operator comes in two forms.  ``embedding_forward`` / ``embedding_backward``
-and ``layer_norm_forward`` / ``layer_norm_backward`` are the library's calls:
-nothing is recorded, and they can be captured into a CUDA graph.
-:func:`embedding` and :func:`layer_norm` are differentiable by torch's autograd.
+Each operator comes in two forms.  The ``*_forward`` and ``*_backward`` functions
+are the library's calls: nothing is recorded, and they can be captured into a
+CUDA graph.  :func:`embedding`, :func:`layer_norm` and :func:`lm_loss` are
+differentiable by torch's autograd.
 
 All of them run on torch's current stream of the tensors' device and allocate
 their workspace from torch's allocator for the call.  Inputs may have any
@@ -21,7 +21,7 @@ place are contiguous.  Formulas, ranges and what happens at their edges:
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -249,3 +249,111 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     """y of :func:`layer_norm_forward`, differentiable in x, weight and bias."""
     _no_capture(x, weight, bias)
     return _LayerNorm.apply(x, weight, bias, eps)
+
+
+# -- language-model head and loss ------------------------------------------------------------------------
+_REDUCTION = {"mean": B.ZERO_LOSS_MEAN, "sum": B.ZERO_LOSS_SUM}
+
+
+def _loss_args(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, piece: int):
+    """(checked arguments, the tensors that they point to)."""
+    if weight.dim() != 2:
+        raise ValueError("weight: shape %s (need vocab x d)" % _shape(weight))
+    _check_weight("weight", weight, weight.shape)
+    if hidden.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("hidden: dtype %s (need torch.bfloat16 or torch.float16)" % hidden.dtype)
+    _check_dtype("weight", weight, hidden.dtype)
+    _check_ids("targets", targets)
+    vocab, d = weight.shape
+    _check_last("hidden", hidden, d)
+    if hidden.shape[:-1] != targets.shape:
+        raise ValueError("targets: shape %s (need %s)" % (_shape(targets), "x".join(map(str, hidden.shape[:-1]))))
+    _check_on(weight.device, weight=weight, hidden=hidden, targets=targets)
+    rows, stride = _rows(hidden, d)
+    flat = targets.contiguous()
+    a = B.zero_lm_loss_args(n=rows.shape[0], d=d, vocab=vocab, hidden_stride=stride, dtype=DTYPE[hidden.dtype], piece=piece,
+                            hidden=rows.data_ptr(), weight=weight.data_ptr(), targets=flat.data_ptr(), scale=1.0)
+    return a, (rows, flat)
+
+
+def lm_loss_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, reduction: str = "mean"):
+    """(loss, losses, saved): the cross entropy of softmax(hidden @ weight.T)
+    against ``targets``, without the logits in memory.  hidden [..., d] and
+    weight [vocab, d] are bf16 or fp16, targets int64 of hidden's leading
+    shape; a target outside 0 .. vocab-1 makes a token not count.  ``loss``
+    is the mean over the tokens that count (or the sum; 0 without any),
+    ``losses`` has a value for each token, both float32; ``saved`` is for
+    :func:`lm_loss_backward`."""
+    if reduction not in _REDUCTION:
+        raise ValueError("reduction must be 'mean' or 'sum'")
+    dev = weight.device
+    a, keep = _loss_args(hidden, weight, targets, 0)
+    with _device(dev.index):
+        out = torch.empty((2, *targets.shape), dtype=torch.float32, device=dev)
+        stats = torch.empty(2, dtype=torch.float32, device=dev)
+        ws = _bytes(B.zero_lm_loss_query(a)[0], dev)
+        a.reduction = _REDUCTION[reduction]
+        a.losses, a.lse, a.stats, a.workspace = out[0].data_ptr(), out[1].data_ptr(), stats.data_ptr(), ws.data_ptr()
+        B.zero_lm_loss_forward(a, _raw_stream(dev.index))
+    return stats[0], out[0], (out[1], stats)
+
+
+def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, saved,
+                     grad_weight: Optional[torch.Tensor] = None, scale: Union[float, torch.Tensor] = 1.0,
+                     accumulate: bool = False, need_hidden: bool = True, piece: int = 0) -> Optional[torch.Tensor]:
+    """The gradient of ``loss`` times ``scale``: hidden's is returned (None
+    without ``need_hidden``), the weight's goes into ``grad_weight`` [vocab, d]
+    of its dtype, overwritten or, with ``accumulate``, added to.  ``scale`` is
+    a number or a float32 CUDA tensor of one element that is read when the
+    kernels run: a loss scale (``MultiAdamW.state_fields()["loss_scale"]``,
+    ``ZeroStep.loss_scale``) or the gradient of ``loss``.  ``piece`` columns of
+    the vocabulary are in memory at a time (0: chosen)."""
+    dev = weight.device
+    a, keep = _loss_args(hidden, weight, targets, piece)
+    lse, stats = saved
+    _check_weight("saved[0]", lse, targets.shape)
+    _check_weight("saved[1]", stats, (2,))
+    for name, t in (("saved[0]", lse), ("saved[1]", stats)):
+        _check_dtype(name, t, torch.float32)
+    if grad_weight is not None:
+        _check_weight("grad_weight", grad_weight, weight.shape)
+        _check_dtype("grad_weight", grad_weight, weight.dtype)
+    if isinstance(scale, torch.Tensor):
+        if scale.dtype != torch.float32 or scale.numel() != 1:
+            raise ValueError("scale: a number or a float32 tensor of one element")
+        a.scale_dev = scale.data_ptr()
+    else:
+        a.scale = scale
+    _check_on(dev, lse=lse, stats=stats, grad_weight=grad_weight, scale=scale if isinstance(scale, torch.Tensor) else None)
+    with _device(dev.index):
+        grad_hidden = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev) if need_hidden else None
+        ws = _bytes(B.zero_lm_loss_query(a)[1], dev)
+        a.lse, a.stats, a.workspace = lse.data_ptr(), stats.data_ptr(), ws.data_ptr()
+        a.grad_hidden = grad_hidden.data_ptr() if need_hidden else None
+        a.grad_weight = grad_weight.data_ptr() if grad_weight is not None else None
+        a.accumulate = int(bool(accumulate))
+        B.zero_lm_loss_backward(a, _raw_stream(dev.index))
+    return grad_hidden
+
+
+class _LmLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, reduction):
+        loss, _, (lse, stats) = lm_loss_forward(hidden, weight, targets, reduction)
+        ctx.save_for_backward(hidden, weight, targets, lse, stats)
+        return loss.clone()         # stats is kept: what becomes of the loss does not reach it
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        hidden, weight, targets, lse, stats = ctx.saved_tensors
+        need_hidden, need_weight = ctx.needs_input_grad[:2]
+        gw = torch.empty_like(weight) if need_weight else None
+        gh = lm_loss_backward(hidden, weight, targets, (lse, stats), gw, scale=grad.contiguous(), need_hidden=need_hidden)
+        return gh, gw, None, None
+
+
+def lm_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, reduction: str = "mean") -> torch.Tensor:
+    """``loss`` of :func:`lm_loss_forward`, differentiable in hidden and weight."""
+    _no_capture(hidden, weight)
+    return _LmLoss.apply(hidden, weight, targets, reduction)
