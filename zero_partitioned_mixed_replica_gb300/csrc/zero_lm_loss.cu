@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "zero_launch.h"
 #include "zero_tc.cuh"
@@ -23,11 +24,13 @@
 namespace zk {
 
 constexpr int kTileK = 64;            // of K in a stage: 128 bytes
-constexpr int kMmThreads = 192;       // warps 0-3: accumulator, 4: loads, 5: products
+constexpr int kEpiWarps = 8;          // two for each quarter of the accumulator's rows, half of the columns each
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kTileWarp = 10;
+constexpr int kMmThreads = 32 * 11;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows of 64
 constexpr int kTileN = 256;           // columns of a tile, at most
 
-enum { EPI_STATS = 0, EPI_DZ = 1, EPI_PART = 2, EPI_OUT = 3 };
+enum { MM_STATS = 0, MM_DZ = 1, MM_GRADS = 2 };
 enum { ROWS_M = 1, ROWS_K = 2 };  // which extent is the number of tokens that count
 
 // The workspace begins with what the kernels share.
@@ -38,33 +41,49 @@ struct LossHead {
     int32_t pad;
 };
 
-struct MmArgs {
-    LossHead* head;
+// One product C = A B^T, A [m, k] and B [n, k].  The last tile of a row is as
+// narrow as what is left, in steps of 16 columns: at d = 1600 six tiles of 256
+// and one of 64 take 0.89 of the time of seven of 240, whose loads (32 KB for
+// 480 cycles of products) pass what an SM can take in (about 60 bytes a cycle).
+struct MmProblem {
     int32_t rows_in;          // ROWS_M or ROWS_K
-    int64_t m, n, k;          // extents (the one of rows_in at most: head->count says how many)
+    int64_t m, n, k;          // extents (the one of rows_in at most: head->count says how many); m == 0: no product
     int32_t bn;               // columns of a tile, a multiple of 16
     int32_t splits;           // of K
     int32_t m_group;          // row tiles that follow one another while the columns stay; 0: columns first
     int32_t n_off, k_off;     // where B's rows and K begin
-    uint32_t idesc;
-    // epilogue
-    const int32_t* target;    // STATS, DZ: of each row
-    const int32_t* row_of;    // DZ: the token of each row
+    uint32_t idesc;           // without the columns
+};
+
+struct MmMaps {
+    CUtensorMap a[2], b[2];
+};
+
+struct MmArgs {
+    LossHead* head;
+    uint32_t* next;           // tiles dealt behind the first of each cluster; 0 before the launch
+    MmProblem p[2];           // GRADS: dz @ weight, dz^T @ hidden; else the first alone
+    // STATS, DZ
+    const int32_t* target;    // of each row
+    const int32_t* row_of;    // the token of each row
     const float* lse;         // DZ: by token
-    float2* parts;            // STATS: [column tile][part_rows] row maximum, sum of exponentials
-    int64_t part_rows;
+    float2* parts;            // STATS: [row][part_ld] maximum and sum of exponentials of half a tile's columns
+    int64_t part_ld;
     float* z_target;          // STATS: the target's logit
-    uint16_t* dz;             // DZ: [rows][ld]
-    int64_t ld;
+    uint16_t* dz;             // DZ: [rows][dz_ld]
+    int64_t dz_ld;
     float dz_scale;
-    float* part;              // PART: [split][split_rows][ld]
-    int64_t split_rows;
-    uint16_t* out;            // OUT: [m][ld]
+    // GRADS
+    float* part;              // binary32 sums of dz @ weight: [split][split_rows][part_cols]
+    int64_t split_rows, part_cols;
+    uint16_t* gh;             // not NULL: the last sums go there, at row row_of[row], instead
+    uint16_t* gw;             // rows of the piece
+    int64_t d;
     float scale;
     const float* scale_dev;
     const float* share;
-    int32_t add;              // PART, OUT: to what is there
-    int32_t vec;              // OUT: rows begin on 32-byte boundaries, ld % 16 == 0
+    int32_t part_add, gw_add; // to what is there
+    int32_t gw_vec;           // rows begin on 32-byte boundaries, d % 16 == 0
 };
 
 template <int CG>
@@ -73,44 +92,92 @@ struct MmShape {
     static constexpr int kB = 2 * kBoxBytes / CG;
     static constexpr int kStages = CG == 2 ? 6 : 4;
     static constexpr int kOps = kStages * (kA + kB);
-    static constexpr int kBytes = 1024 + kOps + 4 * 32 * 33 * 4 + 256;   // alignment, operands, transposition, barriers
+    static constexpr int kTurn = kEpiWarps * 32 * 17 * 4;       // transposition
+    static constexpr int kSync = 512;                           // barriers, tiles dealt
+    static constexpr int kBytes = 1024 + kOps + kTurn + kSync;  // and alignment
 };
 
-struct MmTile {
-    int32_t m, n, kb0, kb1;   // row tile, column tile, blocks of kTileK
+struct alignas(16) MmTile {
+    int32_t p;                // problem, or -1: no more tiles
+    int32_t m, n, split;      // row tile, column tile
+    int32_t kb0, kb1;         // blocks of kTileK
+    int32_t width, pad;       // columns that exist
 };
 
-__device__ __forceinline__ MmTile mm_tile(const MmArgs& a, int64_t t, int64_t tm, int64_t tn, int32_t kblocks) {
-    const int64_t tiles = tm * tn;
-    const int32_t split = (int32_t)(t / tiles);
-    t -= split * tiles;
-    MmTile r;
-    if (a.m_group > 0) {
-        const int64_t g = t / (a.m_group * tn), in = t - g * a.m_group * tn;
-        const int64_t rows = min((int64_t)a.m_group, tm - g * a.m_group);
-        r.n = (int32_t)(in / rows);
-        r.m = (int32_t)(g * a.m_group + in - r.n * rows);
-    } else {
-        r.m = (int32_t)(t / tn);
-        r.n = (int32_t)(t - r.m * tn);
+// Extents of one product, with the tokens that count.
+template <int CG>
+struct MmExtent {
+    int64_t tm, tn, tiles;
+    int32_t kblocks;
+
+    __device__ MmExtent(const MmProblem& p, int64_t count) {
+        tm = ((p.rows_in == ROWS_M ? min(count, p.m) : p.m) + 128 * CG - 1) / (128 * CG);
+        tn = p.m > 0 ? (p.n + p.bn - 1) / p.bn : 0;
+        kblocks = (int32_t)(((p.rows_in == ROWS_K ? min(count, p.k) : p.k) + kTileK - 1) / kTileK);
+        tiles = tm * tn * p.splits;
     }
-    r.kb0 = (int32_t)((int64_t)kblocks * split / a.splits);
-    r.kb1 = (int32_t)((int64_t)kblocks * (split + 1) / a.splits);
-    return r;
-}
+    __device__ MmTile tile(const MmProblem& p, int64_t t) const {
+        MmTile r;
+        const int64_t one = tm * tn;
+        r.split = (int32_t)(t / one);
+        t -= r.split * one;
+        if (p.m_group > 0) {
+            const int64_t g = t / (p.m_group * tn), in = t - g * p.m_group * tn;
+            const int64_t rows = min((int64_t)p.m_group, tm - g * p.m_group);
+            r.n = (int32_t)(in / rows);
+            r.m = (int32_t)(g * p.m_group + in - r.n * rows);
+        } else {
+            r.m = (int32_t)(t / tn);
+            r.n = (int32_t)(t - r.m * tn);
+        }
+        r.kb0 = (int32_t)((int64_t)kblocks * r.split / p.splits);
+        r.kb1 = (int32_t)((int64_t)kblocks * (r.split + 1) / p.splits);
+        r.width = (int32_t)min((int64_t)p.bn, p.n - (int64_t)r.n * p.bn);
+        r.pad = 0;
+        return r;
+    }
+};
+
+// The products of a launch: one, or (MM_GRADS) two.
+template <int CG, int MODE>
+struct MmGrid {
+    MmExtent<CG> e0, e1;
+    bool second;   // comes first: long tiles before short ones, so that short ones end the launch
+
+    __device__ MmGrid(const MmArgs& a) : e0(a.p[0], a.head->count), e1(a.p[MODE == MM_GRADS], a.head->count) {
+        second = MODE == MM_GRADS && e1.kblocks > e0.kblocks / a.p[0].splits;
+    }
+    __device__ int64_t all() const { return MODE == MM_GRADS ? e0.tiles + e1.tiles : e0.tiles; }
+    __device__ MmTile tile(const MmArgs& a, int64_t t) const {
+        if constexpr (MODE == MM_GRADS) {
+            const int64_t lead = second ? e1.tiles : e0.tiles;
+            const bool p1 = (t < lead) == second;
+            if (t >= lead) t -= lead;
+            MmTile r = p1 ? e1.tile(a.p[1], t) : e0.tile(a.p[0], t);
+            r.p = p1;
+            return r;
+        } else {
+            MmTile r = e0.tile(a.p[0], t);
+            r.p = 0;
+            return r;
+        }
+    }
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Row maximum and sum of exponentials of 32 columns, into (m, s).  The difference is taken before the product with
 // log2(e): exact near the maximum, however far that is from zero.
-__device__ __forceinline__ void stats_chunk(float (&v)[32], float& m, float& s) {
-    float top = v[0];
+__device__ __forceinline__ void stats_chunk(const float (&v)[32], float& m, float& s) {
+    float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int j = 1; j < 32; ++j) top = fmaxf(top, v[j]);
-    const float next = fmaxf(m, top);
-    constexpr float kLog2e = 1.4426950408889634f;
+    for (int j = 4; j < 32; ++j) t4[j & 3] = fmaxf(t4[j & 3], v[j]);
+    const float next = fmaxf(m, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
     if (next == -INFINITY) {   // nothing but -inf so far, or NaN, which the maximum passes over
+        bool nan = false;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (v[j] != v[j]) s = v[j];
+        for (int j = 0; j < 32; ++j) nan |= v[j] != v[j];
+        if (nan) s = NAN;
         return;
     }
     s = __fmul_rn(s, ex2(__fmul_rn(__fsub_rn(m, next), kLog2e)));
@@ -121,71 +188,81 @@ __device__ __forceinline__ void stats_chunk(float (&v)[32], float& m, float& s) 
     m = next;
 }
 
-// out (+)= f * v for 32 columns of 32 rows of a warp; `left`: columns that exist.
+// 32 columns of a row, rounded, to p (32-byte aligned), as far as `left` (a multiple of 16) columns exist.
 template <class F>
-__device__ __forceinline__ void out_chunk(const MmArgs& a, float f, float (&v)[32], int64_t row, bool row_on, int64_t col,
-                                          int left, float (*sh)[33]) {
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[32], int left, bool add) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
-    if (a.vec) {
-        if (!row_on) return;
-        uint16_t* p = a.out + row * a.ld + col;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (h * 16 >= left) break;   // ld % 16 == 0: halves are whole
+    for (int h = 0; h < 2; ++h) {
+        if (h * 16 < left) {
             uint32_t w[8];
-            if (a.add) {
+            if (add) {
                 ld8w(p + h * 16, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[h * 16 + 2 * j] = __fadd_rn(v[h * 16 + 2 * j], F::lo(w[j]));
-                    v[h * 16 + 2 * j + 1] = __fadd_rn(v[h * 16 + 2 * j + 1], F::hi(w[j]));
-                }
-            }
+                for (int j = 0; j < 8; ++j)
+                    w[j] = F::pack(__fadd_rn(v[h * 16 + 2 * j], F::lo(w[j])), __fadd_rn(v[h * 16 + 2 * j + 1], F::hi(w[j])));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = F::pack(v[h * 16 + 2 * j], v[h * 16 + 2 * j + 1]);
+                for (int j = 0; j < 8; ++j) w[j] = F::pack(v[h * 16 + 2 * j], v[h * 16 + 2 * j + 1]);
+            }
             st8w(p + h * 16, w);
         }
-        return;
     }
-    // rows that begin anywhere: through shared memory, a row's 32 columns at a time
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) sh[lane][j] = v[j];
-    __syncwarp();
-    const uint32_t on = __ballot_sync(0xFFFFFFFFu, row_on);
-    for (int r = 0; r < 32; ++r) {
-        if ((on >> r & 1) && lane < left) {
-            uint16_t* p = a.out + (row - lane + r) * a.ld + col + lane;
-            float x = sh[r][lane];
-            if (a.add) x = __fadd_rn(x, F::dec1(*p));
-            *p = F::enc1(x);
-        }
-    }
-    __syncwarp();
 }
 
-// C = A B^T of A [m, k] and B [n, k] in tiles of (128 CG) x bn, persistent.
-// The loads run up to kStages blocks of K ahead of the products; two
-// accumulators take turns, so that the epilogue of a tile runs under the next
-// tile's products.
-template <int CG, bool A_MN, bool B_MN, int EPI, class F>
-__global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant__ CUtensorMap map_a,
-                                                           const __grid_constant__ CUtensorMap map_b,
-                                                           const __grid_constant__ MmArgs a) {
+// The same for rows that begin anywhere: through shared memory, two rows of 16 columns at a time.  p: the first lane's row.
+template <class F>
+__device__ __forceinline__ void store_turned(uint16_t* p, int64_t ld, uint32_t rows_on, const float (&v)[32], int left, bool add,
+                                             float (*sh)[17]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sh[lane][j] = v[h * 16 + j];
+        __syncwarp();
+        const int c = h * 16 + (lane & 15);
+#pragma unroll 4
+        for (int r = lane >> 4; r < 32; r += 2) {
+            if ((rows_on >> r & 1) && c < left) {
+                uint16_t* q = p + r * ld + c;
+                float x = sh[r][lane & 15];
+                if (add) x = __fadd_rn(x, F::dec1(*q));
+                *q = F::enc1(x);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// The products of a launch, in tiles of (128 CG) x bn, persistent.  One warp
+// deals tiles from a counter (SMs differ in speed by a seventh under a power
+// limit, and tiles of two products in length), one loads blocks of K, up to
+// kStages ahead, one issues the products, eight take the accumulator; two
+// accumulators take turns, so that a tile's epilogue runs under the next tile's
+// products.  MM_GRADS runs both products with dz, whose tiles fill one
+// another's last round.
+template <int CG, int MODE, class F>
+__global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
     using Shape = MmShape<CG>;
     constexpr int ST = Shape::kStages;
+    constexpr bool B_MN = MODE == MM_GRADS;
+    // tiles dealt before they are begun: short tiles (logits, d of K) hide the counter's latency, long ones stay balanced
+    constexpr int RING = MODE == MM_GRADS ? 2 : 3;
     extern __shared__ uint8_t raw[];
     uint8_t* ops = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
-    float(*sh)[32][33] = reinterpret_cast<float(*)[32][33]>(ops + Shape::kOps);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ops + Shape::kOps + 4 * 32 * 33 * 4);
-    uint64_t* full = bars;             // [ST] in the leader: a block of both CTAs has landed
-    uint64_t* empty = full + ST;       // [ST] a block has been read by the products
-    uint64_t* acc_full = empty + ST;   // [2] a tile's products are done
+    float(*sh)[32][17] = reinterpret_cast<float(*)[32][17]>(ops + Shape::kOps);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ops + Shape::kOps + Shape::kTurn);
+    uint64_t* full = bars;               // [ST] in the leader: a block of both CTAs has landed
+    uint64_t* empty = full + ST;         // [ST] a block has been read by the products
+    uint64_t* acc_full = empty + ST;     // [2] a tile's products are done
     uint64_t* acc_empty = acc_full + 2;  // [2] in the leader: the epilogues have read the accumulator
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    uint64_t* tile_full = acc_empty + 2; // [RING] a tile has been dealt
+    uint64_t* tile_empty = tile_full + RING;  // [RING] in the leader: all roles of both CTAs know it
+    MmTile* ring = reinterpret_cast<MmTile*>(bars + 24);   // [RING]
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ring + RING);
+    static_assert(2 * ST + 4 + 2 * RING <= 24 && 24 * 8 + sizeof(MmTile) * RING + 4 <= Shape::kSync, "what the roles share");
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const auto leader = [](uint64_t* bar) { return CG == 2 ? map_rank(smem_u32(bar), 0) : smem_u32(bar); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -194,67 +271,129 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4 * CG);
+            mbar_init(acc_empty + i, kEpiWarps * CG);
+        }
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(tile_full + i, 1);
+            mbar_init(tile_empty + i, CG * (kEpiWarps + 1) + 1);
         }
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc<CG>(tmem_at, 512);
-    if (warp == 4 && lane == 0) {
-        prefetch_map(&map_a);
-        prefetch_map(&map_b);
+    if (warp == kMmaWarp) tmem_alloc<CG>(tmem_at, 512);
+    if (warp == kLoadWarp && lane == 0) {
+        for (int i = 0; i <= (MODE == MM_GRADS); ++i) {
+            prefetch_map(&maps.a[i]);
+            prefetch_map(&maps.b[i]);
+        }
     }
     tc_fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_barrier();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
-
-    const int32_t count = a.head->count;
-    const int64_t m_rows = a.rows_in == ROWS_M ? min((int64_t)count, a.m) : a.m;
-    const int64_t k_cols = a.rows_in == ROWS_K ? min((int64_t)count, a.k) : a.k;
-    const int64_t tm = (m_rows + 128 * CG - 1) / (128 * CG), tn = (a.n + a.bn - 1) / a.bn;
-    const int32_t kblocks = (int32_t)((k_cols + kTileK - 1) / kTileK);
-    const int64_t tiles = tm * tn * a.splits;
-    const int64_t t0 = blockIdx.x / CG, step = gridDim.x / CG;
     bool ok = true;   // of this thread's waits
+    // the next tile; for one thread of a role
+    int tile_slot = 0;
+    uint32_t tile_phase = 0;
+    const auto next_tile = [&]() -> MmTile {
+        MmTile t;
+        t.p = -1;
+        ok = mbar_wait_cluster(tile_full + tile_slot, tile_phase);
+        if (!ok) return t;
+        const uint32_t at = smem_u32(ring + tile_slot);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(t.p), "=r"(t.m), "=r"(t.n), "=r"(t.split) : "r"(at) : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(t.kb0), "=r"(t.kb1), "=r"(t.width), "=r"(t.pad) : "r"(at + 16) : "memory");
+        mbar_arrive_remote(leader(tile_empty + tile_slot));
+        if (++tile_slot == RING) {
+            tile_slot = 0;
+            tile_phase ^= 1;
+        }
+        return t;
+    };
 
-    if (warp == 4) {
+    if (warp == kTileWarp) {
+        if (lane == 0 && rank == 0) {
+            const MmGrid<CG, MODE> grid(a);
+            const int64_t tiles = grid.all();
+            int64_t t = blockIdx.x / CG;
+            for (;;) {
+                ok = mbar_wait_bounded(tile_empty + tile_slot, tile_phase ^ 1);
+                if (!ok) break;
+                MmTile w;
+                w.p = -1;
+                w.m = w.n = w.split = w.kb0 = w.kb1 = w.width = w.pad = 0;
+                if (t < tiles) w = grid.tile(a, t);
+#pragma unroll
+                for (int r = 0; r < CG; ++r) {
+                    const uint32_t to = CG == 2 ? map_rank(smem_u32(ring + tile_slot), r) : smem_u32(ring + tile_slot);
+                    const uint32_t bar = CG == 2 ? map_rank(smem_u32(tile_full + tile_slot), r) : smem_u32(tile_full + tile_slot);
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w.p), "r"(w.m), "r"(w.n), "r"(w.split) : "memory");
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16), "r"(w.kb0), "r"(w.kb1), "r"(w.width), "r"(w.pad) : "memory");
+                    mbar_arrive_cluster(bar);
+                }
+                if (w.p < 0) break;
+                if (++tile_slot == RING) {
+                    tile_slot = 0;
+                    tile_phase ^= 1;
+                }
+                t = gridDim.x / CG + (int64_t)atomicAdd(a.next, 1u);
+            }
+        }
+    } else if (warp == kLoadWarp) {
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            for (int64_t t = t0; t < tiles && ok; t += step) {
-                const MmTile w = mm_tile(a, t, tm, tn, kblocks);
+            const uint32_t full0 = leader(full), ops0 = smem_u32(ops);
+            // one tile's blocks; what differs between the products is known at compile time
+            const auto load = [&](auto a_mn_, const MmTile& w, const CUtensorMap* map_a, const CUtensorMap* map_b, const MmProblem& p) {
+                constexpr bool A_MN = decltype(a_mn_)::value;
                 const int32_t ma = w.m * 128 * CG + (int32_t)rank * 128;
-                const int32_t nb = w.n * a.bn + (int32_t)rank * (a.bn / CG) + a.n_off;
+                // logits: a box of bn / CG rows of the weight; else boxes of 64 columns, as many as the tile has
+                const int32_t cols = B_MN ? (w.width + 15) / 16 * 16 / CG : p.bn / CG, k_off = p.k_off;
+                const int32_t nb = w.n * p.bn + (int32_t)rank * cols + p.n_off;
+                const int32_t boxes = (cols + 63) / 64;
+                const uint32_t bytes = CG * (Shape::kA + (B_MN ? boxes * 8192 : cols * 128));
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    ok = mbar_wait_cluster(empty + stage, phase ^ 1);
+                    ok = mbar_wait_bounded(empty + stage, phase ^ 1);
                     if (!ok) break;
-                    const uint32_t bar = CG == 2 ? map_rank(smem_u32(full + stage), 0) : smem_u32(full + stage);
-                    if (rank == 0) mbar_arrive_expect_tx(full + stage, CG * (Shape::kA + Shape::kB));
-                    const uint32_t sa = smem_u32(ops) + stage * (Shape::kA + Shape::kB), sb = sa + Shape::kA;
+                    const uint32_t bar = full0 + stage * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
+                    const uint32_t sa = ops0 + stage * (Shape::kA + Shape::kB), sb = sa + Shape::kA;
                     const int32_t k = kb * kTileK;
                     if constexpr (A_MN) {
-                        tma_load<CG>(sa, &map_a, ma, k, bar);
-                        tma_load<CG>(sa + 8192, &map_a, ma + 64, k, bar);
+                        tma_load<CG>(sa, map_a, ma, k, bar);
+                        tma_load<CG>(sa + 8192, map_a, ma + 64, k, bar);
                     } else {
-                        tma_load<CG>(sa, &map_a, k, ma, bar);
+                        tma_load<CG>(sa, map_a, k, ma, bar);
                     }
                     if constexpr (B_MN) {
 #pragma unroll
-                        for (int j = 0; j < 4 / CG; ++j) tma_load<CG>(sb + j * 8192, &map_b, nb + 64 * j, k + a.k_off, bar);
+                        for (int j = 0; j < Shape::kB / 8192; ++j)
+                            if (j < boxes) tma_load<CG>(sb + j * 8192, map_b, nb + 64 * j, k + k_off, bar);
                     } else {
-                        tma_load<CG>(sb, &map_b, k + a.k_off, nb, bar);
+                        tma_load<CG>(sb, map_b, k + k_off, nb, bar);
                     }
                     if (++stage == ST) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
+            };
+            for (MmTile w; (w = next_tile()).p >= 0;) {
+                if constexpr (MODE == MM_GRADS) {
+                    if (w.p == 0) load(std::false_type{}, w, &maps.a[0], &maps.b[0], a.p[0]);
+                    else load(std::true_type{}, w, &maps.a[1], &maps.b[1], a.p[1]);
+                } else {
+                    load(std::false_type{}, w, &maps.a[0], &maps.b[0], a.p[0]);
+                }
+                if (!ok) break;
             }
             // until the products have read what was loaded, here and in the other CTA: neither may end before
-            for (int i = 0; i < ST; ++i) {   // places never filled are free
+            // (places never filled are free)
+            const bool all = ok;
+            for (int i = 0; i < ST; ++i) {
                 bool read = false;
-                for (int tries = 0; tries < (ok ? 1 : kDrainTries) && !read; ++tries) read = mbar_wait_cluster(empty + stage, phase ^ 1);
+                for (int tries = 0; tries < (all ? 1 : kDrainTries) && !read; ++tries) read = mbar_wait_bounded(empty + stage, phase ^ 1);
                 ok = ok && read;
                 if (++stage == ST) {
                     stage = 0;
@@ -262,26 +401,22 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                 }
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == kMmaWarp) {
         if (lane == 0 && rank == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            int64_t done = 0;   // tiles
-            for (int64_t t = t0; t < tiles && ok; t += step) {
-                const MmTile w = mm_tile(a, t, tm, tn, kblocks);
-                if (w.kb0 == w.kb1) continue;
-                const int buf = (int)(done & 1);
-                ok = mbar_wait_cluster(acc_empty + buf, (uint32_t)((done >> 1) & 1) ^ 1);
-                tc_fence_after();
-                for (int32_t kb = w.kb0; kb < w.kb1 && ok; ++kb) {
-                    ok = mbar_wait_cluster(full + stage, phase);
+            int64_t done = 0;   // accumulators
+            const auto multiply = [&](auto a_mn_, const MmTile& w, uint32_t idesc, uint32_t acc) {
+                constexpr bool A_MN = decltype(a_mn_)::value;
+                const uint64_t da0 = operand_desc(smem_u32(ops), A_MN), db0 = operand_desc(smem_u32(ops) + Shape::kA, B_MN);
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    ok = mbar_wait_bounded(full + stage, phase);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(ops) + stage * (Shape::kA + Shape::kB);
-                    const uint64_t da = operand_desc(sa, A_MN), db = operand_desc(sa + Shape::kA, B_MN);
+                    const uint64_t at = stage * ((Shape::kA + Shape::kB) >> 4);
 #pragma unroll
                     for (int j = 0; j < kTileK / 16; ++j)
-                        tc_mma<CG>(tmem + buf * kTileN, da + j * (A_MN ? kStepMN : kStepK), db + j * (B_MN ? kStepMN : kStepK), a.idesc,
+                        tc_mma<CG>(acc, da0 + at + j * (A_MN ? kStepMN : kStepK), db0 + at + j * (B_MN ? kStepMN : kStepK), idesc,
                                    kb > w.kb0 || j > 0);
                     tc_commit<CG>(empty + stage);
                     if (++stage == ST) {
@@ -289,38 +424,67 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                         phase ^= 1;
                     }
                 }
-                if (ok) tc_commit<CG>(acc_full + buf);
+            };
+            for (MmTile w; (w = next_tile()).p >= 0;) {
+                if (w.kb0 == w.kb1) continue;
+                // the columns: of the last tile no more than there are (logits: what the box has loaded beyond them does no harm)
+                const uint32_t columns = (uint32_t)(B_MN ? (w.width + 15) / 16 * 16 : a.p[0].bn) >> 3 << 17;
+                const int buf = (int)(done & 1);
+                ok = mbar_wait_bounded(acc_empty + buf, (uint32_t)((done >> 1) & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                if constexpr (MODE == MM_GRADS) {
+                    if (w.p == 0) multiply(std::false_type{}, w, a.p[0].idesc | columns, tmem + buf * kTileN);
+                    else multiply(std::true_type{}, w, a.p[1].idesc | columns, tmem + buf * kTileN);
+                } else {
+                    multiply(std::false_type{}, w, a.p[0].idesc | columns, tmem + buf * kTileN);
+                }
+                if (!ok) break;
+                tc_commit<CG>(acc_full + buf);
                 ++done;
             }
         }
     } else {
+        const int half = warp >> 2;   // of the columns; a warp reads the rows of its quarter, warp % 4
         int64_t done = 0;
+        const int64_t rows0 = min((int64_t)a.head->count, a.p[0].m), rows1 = a.p[1].m;
         float f = a.scale;
-        if constexpr (EPI == EPI_OUT) {
+        if constexpr (MODE == MM_GRADS) {
             f = __fmul_rn(f, *a.share);
             if (a.scale_dev) f = __fmul_rn(f, *a.scale_dev);
         }
-        for (int64_t t = t0; t < tiles && ok; t += step) {
-            const MmTile w = mm_tile(a, t, tm, tn, kblocks);
+        for (;;) {
+            MmTile w;
+            w.p = -1;
+            if (lane == 0) w = next_tile();
+            w.p = __shfl_sync(0xFFFFFFFFu, w.p, 0);
+            if (w.p < 0) break;
+            w.m = __shfl_sync(0xFFFFFFFFu, w.m, 0);
+            w.n = __shfl_sync(0xFFFFFFFFu, w.n, 0);
+            w.split = __shfl_sync(0xFFFFFFFFu, w.split, 0);
+            w.kb0 = __shfl_sync(0xFFFFFFFFu, w.kb0, 0);
+            w.kb1 = __shfl_sync(0xFFFFFFFFu, w.kb1, 0);
+            w.width = __shfl_sync(0xFFFFFFFFu, w.width, 0);
+            const MmProblem& p = a.p[w.p];
             const bool any = w.kb0 < w.kb1;   // without a token that counts the sums are zeros
             const int buf = (int)(done & 1);
-            const int64_t row = (int64_t)w.m * 128 * CG + rank * 128 + warp * 32 + lane;
-            const int64_t n0 = (int64_t)w.n * a.bn;
-            const int width = (int)min((int64_t)a.bn, a.n - n0);
+            const int64_t row0 = (int64_t)w.m * 128 * CG + rank * 128 + (warp & 3) * 32, row = row0 + lane;
+            const bool row_on = row < (w.p == 0 ? rows0 : rows1);
+            const int64_t n0 = (int64_t)w.n * p.bn;
+            const int c0 = half * 128, c1 = half == 0 ? min(w.width, 128) : w.width;
             if (any) {
-                ok = mbar_wait_cluster(acc_full + buf, (uint32_t)(done >> 1) & 1);
+                ok = mbar_wait_bounded(acc_full + buf, (uint32_t)(done >> 1) & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
             }
-            const uint32_t at = tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16);
+            const uint32_t at = tmem + buf * kTileN + ((uint32_t)((warp & 3) * 32) << 16);
             [[maybe_unused]] float top = -INFINITY, sum = 0.0f, lse = 0.0f;
             [[maybe_unused]] int target = -1;
-            const bool row_on = row < m_rows;
-            if constexpr (EPI == EPI_STATS || EPI == EPI_DZ)
-                if (row_on) target = a.target[row] - (int)n0 - (EPI == EPI_DZ ? a.n_off : 0);
-            if constexpr (EPI == EPI_DZ) lse = row_on ? a.lse[a.row_of[row]] : 0.0f;
-            for (int c = 0; c < width; c += 32) {
+            if constexpr (MODE != MM_GRADS)
+                if (row_on) target = a.target[row] - (int)n0 - p.n_off;
+            if constexpr (MODE == MM_DZ) lse = row_on ? a.lse[a.row_of[row]] : 0.0f;
+            for (int c = c0; c < c1; c += 32) {
                 float v[32];
                 if (any) {
                     uint32_t u[32];
@@ -332,71 +496,85 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 }
-                const int left = width - c;
-                if constexpr (EPI == EPI_STATS) {
+                const int left = c1 - c;
+                if constexpr (MODE == MM_STATS) {
                     if (left < 32) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j >= left) v[j] = -INFINITY;
                     }
-                    if (target >= c && target < c + 32) {
+                    if (target >= c && target < min(c + 32, c1)) {
+                        // predicated stores: of a choice among registers the compiler makes an array in local memory
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j == target - c) a.z_target[row] = v[j];
+                            asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %0, %1;\n\t@p st.global.f32 [%2], %3;\n\t}" ::"r"(target - c), "r"(j),
+                                         "l"(a.z_target + row), "f"(v[j])
+                                         : "memory");
                     }
                     stats_chunk(v, top, sum);
-                } else if constexpr (EPI == EPI_DZ) {
+                } else if constexpr (MODE == MM_DZ) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = ex2(__fmul_rn(__fsub_rn(v[j], lse), 1.4426950408889634f));
-                    if (target >= c && target < c + 32) {
+                    for (int j = 0; j < 32; ++j) v[j] = ex2(__fmul_rn(__fsub_rn(v[j], lse), kLog2e));
+                    if (target >= c && target < min(c + 32, c1)) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j == target - c) v[j] = __fsub_rn(v[j], 1.0f);
+                        for (int j = 0; j < 32; ++j) v[j] = __fsub_rn(v[j], j == target - c ? 1.0f : 0.0f);
                     }
                     if (left < 32) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j >= left) v[j] = 0.0f;
                     }
-                    uint32_t u[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        u[j] = row_on ? F::pack(__fmul_rn(v[2 * j], a.dz_scale), __fmul_rn(v[2 * j + 1], a.dz_scale)) : 0u;
-                    uint16_t* p = a.dz + row * a.ld + n0 + c;
-                    st8w(p, u);
-                    st8w(p + 16, u + 8);
-                } else if constexpr (EPI == EPI_PART) {
+                    for (int j = 0; j < 32; ++j) v[j] = row_on ? __fmul_rn(v[j], a.dz_scale) : 0.0f;
+                    store_row<F>(a.dz + row * a.dz_ld + n0 + c, v, left, false);   // 16 columns at a time: bn % 16 == 0
+                } else if (w.p == 0) {
                     if (row_on) {
-                        float* p = a.part + ((t / (tm * tn)) * a.split_rows + row) * a.ld + n0 + c;
+                        float* q = a.part + (w.split * a.split_rows + row) * a.part_cols + n0 + c;
+                        if (a.part_add) {
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            if (h * 8 >= left) break;   // ld % 8 == 0
-                            uint32_t u[8];
-                            if (a.add) {
-                                ld8w(p + h * 8, u);
+                            for (int h = 0; h < 4; ++h) {
+                                if (h * 8 < left) {   // part_cols % 8 == 0
+                                    uint32_t u[8];
+                                    ld8w(q + h * 8, u);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) v[h * 8 + j] = __fadd_rn(v[h * 8 + j], __uint_as_float(u[j]));
+                                    for (int j = 0; j < 8; ++j) v[h * 8 + j] = __fadd_rn(v[h * 8 + j], __uint_as_float(u[j]));
+                                }
                             }
+                        }
+                        if (a.gh) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[h * 8 + j]);
-                            st8w(p + h * 8, u);
+                            for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
+                            store_row<F>(a.gh + a.row_of[row] * a.d + n0 + c, v, left, false);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                if (h * 8 < left) {
+                                    uint32_t u[8];
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[h * 8 + j]);
+                                    st8w(q + h * 8, u);
+                                }
+                            }
                         }
                     }
                 } else {
-                    out_chunk<F>(a, f, v, row, row_on, n0 + c, left, sh[warp]);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
+                    if (a.gw_vec) {
+                        if (row_on) store_row<F>(a.gw + row * a.d + n0 + c, v, left, a.gw_add);
+                    } else {
+                        store_turned<F>(a.gw + row0 * a.d + n0 + c, a.d, __ballot_sync(0xFFFFFFFFu, row_on), v, left, a.gw_add, sh[warp]);
+                    }
                 }
             }
             if (any) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_cluster(map_rank(smem_u32(acc_empty + buf), 0));
-                    else mbar_arrive_cluster(smem_u32(acc_empty + buf));
-                }
+                if (lane == 0) mbar_arrive_remote(leader(acc_empty + buf));
                 ++done;
             }
-            if constexpr (EPI == EPI_STATS)
-                if (row_on) a.parts[w.n * a.part_rows + row] = make_float2(top, sum);
+            if constexpr (MODE == MM_STATS)
+                if (row_on) a.parts[row * a.part_ld + 2 * w.n + half] = make_float2(top, sum);
         }
     }
     if (!ok) atomicOr(&a.head->error, ZERO_DEVERR_WAIT_TIMEOUT);
@@ -404,44 +582,104 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
     __syncthreads();
     if constexpr (CG == 2) cluster_barrier();
     tc_fence_after();
-    if (warp == 5) tmem_free<CG>(tmem, 512);
+    if (warp == kMmaWarp) tmem_free<CG>(tmem, 512);
 }
 
 // ----------------------------------------------------------------------------
-// Which tokens count
+// Which tokens count, and their hidden states
 // ----------------------------------------------------------------------------
 struct PickArgs {
     LossHead* head;
+    uint32_t* next;     // counters of the products' launches, zeroed
+    int32_t nexts;
     const int64_t* targets;
     int32_t* slot;      // by token: its place among those that count, or -1
     int32_t* token;     // by place
     int32_t* target;    // by place
     float* losses;      // zeroed for tokens that do not count, and lse (NULL: left alone)
     float* lse;
+    uint16_t* zero;     // [n][d], the same (NULL: left alone)
+    const uint16_t* src;  // hidden states, src_stride apart
+    uint16_t* dst;      // by place, dst_stride apart, `rows` of them
+    int64_t src_stride, dst_stride, rows;
     int64_t vocab;
-    uint32_t n;
+    uint32_t n, d, per_cta;
 };
 
-// One CTA walks the targets in order.
-__global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ PickArgs a) {
-    __shared__ uint32_t warps[32];
+constexpr int kPickThreads = 512;
+
+template <int E>
+__device__ __forceinline__ void copy_row(uint16_t* dst, const uint16_t* src, uint32_t d, uint32_t at, uint32_t step) {
+    if constexpr (E == 8) {
+#pragma unroll 8
+        for (uint32_t c = at; c < d / 8; c += step)
+            reinterpret_cast<uint4*>(dst)[c] = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll 8
+        for (uint32_t c = at; c < d; c += step) dst[c] = src ? __ldg(src + c) : (uint16_t)0;
+    }
+}
+
+// A CTA has per_cta tokens.  It counts those before them that count (every CTA
+// reads all targets: 64 KB at 8192 tokens), places its own, and copies their
+// rows, a warp each; behind the last one come zeros up to a whole tile.
+template <int E>
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ PickArgs a) {
+    constexpr int W = kPickThreads / 32;
+    __shared__ uint32_t sums[2][W];
+    __shared__ int32_t place[kPickThreads];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    uint32_t base = 0;
-    for (uint32_t i0 = 0; i0 < a.n; i0 += 1024) {
-        const uint32_t i = i0 + threadIdx.x;
-        const int64_t t = i < a.n ? a.targets[i] : -1;
-        const bool on = t >= 0 && t < a.vocab;
-        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, on);
-        if (lane == 0) warps[warp] = __popc(vote);
-        __syncthreads();
-        uint32_t before = lane < warp ? warps[lane] : 0, all = warps[lane];
+    const auto counts = [&](int64_t t) { return t >= 0 && t < a.vocab; };
+    const uint32_t b0 = (uint32_t)min((uint64_t)a.n, (uint64_t)blockIdx.x * a.per_cta);
+    const uint32_t b1 = (uint32_t)min((uint64_t)a.n, (uint64_t)b0 + a.per_cta);
+    uint32_t before = 0, all = 0;
+#pragma unroll 8
+    for (uint64_t i = threadIdx.x; i < a.n; i += kPickThreads) {
+        const bool on = counts(__ldg(a.targets + i));
+        all += on;
+        before += on && i < b0;
+    }
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) {
-            before += __shfl_xor_sync(0xFFFFFFFFu, before, s);
-            all += __shfl_xor_sync(0xFFFFFFFFu, all, s);
+    for (int s = 16; s > 0; s >>= 1) {
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, s);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, s);
+    }
+    if (lane == 0) {
+        sums[0][warp] = before;
+        sums[1][warp] = all;
+    }
+    __syncthreads();
+    before = all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        before += sums[0][w];
+        all += sums[1][w];
+    }
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) {
+            a.head->error = 0;
+            a.head->count = (int32_t)all;
+            a.head->ticket = 0;
         }
-        const uint32_t at = base + before + __popc(vote & ((1u << lane) - 1));
-        if (i < a.n) {
+        for (int i = threadIdx.x; i < a.nexts; i += kPickThreads) a.next[i] = 0;
+    }
+    for (uint32_t i0 = b0; i0 < b1; i0 += kPickThreads) {
+        const uint32_t i = i0 + threadIdx.x;
+        const int64_t t = i < b1 ? __ldg(a.targets + i) : -1;
+        const bool on = counts(t);
+        const uint32_t vote = __ballot_sync(0xFFFFFFFFu, on);
+        __syncthreads();       // sums and place have been read
+        if (lane == 0) sums[0][warp] = __popc(vote);
+        __syncthreads();
+        uint32_t at = before, in_all = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            at += w < warp ? sums[0][w] : 0;
+            in_all += sums[0][w];
+        }
+        at += __popc(vote & ((1u << lane) - 1));
+        place[threadIdx.x] = on ? (int32_t)at : -1;
+        if (i < b1) {
             a.slot[i] = on ? (int32_t)at : -1;
             if (on) {
                 a.token[at] = (int32_t)i;
@@ -451,46 +689,33 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
                 a.lse[i] = 0.0f;
             }
         }
-        base += all;
+        before += in_all;
         __syncthreads();
+        const uint32_t tokens = min((uint32_t)kPickThreads, b1 - i0);
+        for (uint32_t j = warp; j < tokens; j += W) {
+            const int32_t to = place[j];
+            if (to >= 0)
+                copy_row<E>(a.dst + to * a.dst_stride, a.src + (int64_t)(i0 + j) * a.src_stride, a.d, lane, 32);
+            else if (a.zero)
+                copy_row<1>(a.zero + (int64_t)(i0 + j) * a.d, nullptr, a.d, lane, 32);
+        }
     }
-    if (threadIdx.x == 0) {
-        a.head->error = 0;
-        a.head->count = (int32_t)base;
-        a.head->ticket = 0;
-    }
+    const int64_t end = min(a.rows, ((int64_t)all + 255) / 256 * 256);
+    for (int64_t r = all + blockIdx.x; r < end; r += gridDim.x) copy_row<E>(a.dst + r * a.dst_stride, nullptr, a.d, threadIdx.x, kPickThreads);
 }
 
-struct GatherRows {
-    const LossHead* head;   // NULL: all rows, in place
-    const int32_t* token;
+// A matrix of rows x d, elements in a row next to one another, into rows `ld` apart.
+struct CopyArgs {
     const uint16_t* src;
     uint16_t* dst;
-    int64_t src_stride, dst_stride, rows;   // rows: of dst
+    int64_t rows, ld;
     uint32_t d;
 };
 
-// Rows of d 16-bit elements, a warp each; what is behind the tokens that count
-// becomes zeros, up to a whole tile.
-template <int E>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ GatherRows a) {
-    const int lane = threadIdx.x & 31;
-    int64_t count = a.rows, end = a.rows;
-    if (a.head) {
-        count = a.head->count;
-        end = min(a.rows, (count + 255) / 256 * 256);
-    }
+__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
     const int64_t step = (int64_t)gridDim.x * kThreads / 32;
-    for (int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; r < end; r += step) {
-        const uint16_t* src = a.src + (r >= count ? 0 : a.head ? a.token[r] : r) * a.src_stride;
-        uint16_t* dst = a.dst + r * a.dst_stride;
-        if constexpr (E == 8) {
-            for (uint32_t c = lane; c < a.d / 8; c += 32)
-                reinterpret_cast<uint4*>(dst)[c] = r < count ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-        } else {
-            for (uint32_t c = lane; c < a.d; c += 32) dst[c] = r < count ? __ldg(src + c) : (uint16_t)0;
-        }
-    }
+    for (int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; r < a.rows; r += step)
+        copy_row<1>(a.dst + r * a.ld, a.src + r * (int64_t)a.d, a.d, threadIdx.x & 31, 32);
 }
 
 // ----------------------------------------------------------------------------
@@ -498,8 +723,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 // ----------------------------------------------------------------------------
 struct LossArgs {
     LossHead* head;
-    const float2* parts;   // [tiles][rows]
-    int64_t rows;
+    const float2* parts;   // [row][tiles]
+    int64_t ld;
     int32_t tiles, blocks, reduction;
     const float* z_target;
     const int32_t* token;
@@ -509,48 +734,49 @@ struct LossArgs {
     double* block_sums;
 };
 
-// 32 tokens a block: 8 threads for each join every 8th tile, then one another
-// in order.  The last CTA to end adds the blocks' sums, in order.
+constexpr int kLossRows = kThreads / 32;
+
+// A warp for each token, kLossRows of them a block: the maximum of its parts,
+// then the sum at that maximum.  The last CTA to end adds the blocks' sums, in
+// order.
 __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ LossArgs a) {
-    __shared__ float2 sh[8][33];
     __shared__ double sums[kThreads];
     __shared__ bool last;
-    constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-    const int lane = threadIdx.x & 31, part = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const int32_t count = a.head->count;
     for (int block = blockIdx.x; block < a.blocks; block += gridDim.x) {
-        const int64_t row = (int64_t)block * 32 + lane;
-        float m = -INFINITY, s = 0.0f;
-        const auto join = [&](float2 p) {   // into (m, s)
-            const float next = fmaxf(m, p.x);
-            if (next == -INFINITY) {
-                s = __fadd_rn(s, p.y);      // 0, or NaN
-                return;
-            }
-            s = __fadd_rn(__fmul_rn(s, ex2(__fmul_rn(__fsub_rn(m, next), kLog2e))),
-                          __fmul_rn(p.y, ex2(__fmul_rn(__fsub_rn(p.x, next), kLog2e))));
-            m = next;
-        };
-        if (row < count)
-#pragma unroll 4
-            for (int t = part; t < a.tiles; t += 8) join(a.parts[(int64_t)t * a.rows + row]);
-        sh[part][lane] = make_float2(m, s);
-        __syncthreads();
+        const int64_t row = (int64_t)block * kLossRows + warp;
         double loss = 0.0;
-        if (part == 0) {
-            if (row < count) {
-                for (int p = 1; p < 8; ++p) join(sh[p][lane]);
-                // log(sum exp(z)) - z_target = ln 2 (log2 s) + (m - z_target): exact where the target is the maximum
-                const float ln_s = __fmul_rn(log2f(s), kLn2);
-                const float one = __fadd_rn(__fsub_rn(m, a.z_target[row]), ln_s);
+        if (row < count) {
+            const float2* p = a.parts + row * a.ld;
+            float m = -INFINITY, s = 0.0f;
+#pragma unroll 4
+            for (int t = lane; t < a.tiles; t += 32) m = fmaxf(m, __ldg(p + t).x);
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
+#pragma unroll 4
+            for (int t = lane; t < a.tiles; t += 32) {
+                const float2 x = __ldg(p + t);
+                // all -inf: the sums are zeros, or NaN
+                s = __fadd_rn(s, m == -INFINITY ? x.y : __fmul_rn(x.y, ex2(__fmul_rn(__fsub_rn(x.x, m), kLog2e))));
+            }
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, k));
+            // log(sum exp(z)) - z_target = (m - z_target) + ln 2 log2(s): exact where the target is the maximum
+            const float ln_s = __fmul_rn(log2f(s), kLn2);
+            const float one = __fadd_rn(__fsub_rn(m, a.z_target[row]), ln_s);
+            if (lane == 0) {
                 const int32_t i = a.token[row];
                 a.losses[i] = one;
                 a.lse[i] = __fadd_rn(m, ln_s);
-                loss = one;
             }
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) loss = __dadd_rn(loss, __shfl_xor_sync(0xFFFFFFFFu, loss, k));
-            if (lane == 0) a.block_sums[block] = loss;
+            loss = one;
+        }
+        if (lane == 0) sums[warp] = loss;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kLossRows; ++w) loss = __dadd_rn(loss, sums[w]);
+            a.block_sums[block] = loss;
         }
         __syncthreads();
     }
@@ -562,6 +788,7 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ 
     __syncthreads();
     if (!last) return;
     double sum = 0.0;
+#pragma unroll 4
     for (int b = threadIdx.x; b < a.blocks; b += kThreads) sum = __dadd_rn(sum, __ldcg(a.block_sums + b));
     sums[threadIdx.x] = sum;
     __syncthreads();
@@ -654,21 +881,35 @@ zero_status_t make_map(CUtensorMap* map, bool bf16, const void* base, int64_t ro
     return ZERO_OK;
 }
 
-// A matrix operand: rows x cols at ld; k_inner: K runs along the rows (K-major).
+// A matrix operand: rows x cols at ld, read in boxes of box_rows x 64.
 struct Operand {
     const void* base;
     int64_t rows, cols, ld;
+    int box_rows;
 };
 
-template <int CG, bool A_MN, bool B_MN, int EPI, class F>
-zero_status_t launch_mm(const Operand& oa, const Operand& ob, zk::MmArgs a, int64_t max_tiles, cudaStream_t s, const char* what) {
+// Tiles of a launch at most (all tokens counting).
+template <int CG>
+int64_t most_tiles(const zk::MmProblem& p) {
+    return p.m > 0 ? (p.m + 128 * CG - 1) / (128 * CG) * ((p.n + p.bn - 1) / p.bn) * p.splits : 0;
+}
+
+template <int CG, int MODE, class F>
+zero_status_t launch_mm(const Operand* oa, const Operand* ob, zk::MmArgs a, cudaStream_t s, const char* what) {
     constexpr bool bf16 = std::is_same<F, zk::Bf16>::value;
-    CUtensorMap ma, mb;
-    zero_status_t rc = make_map(&ma, bf16, oa.base, oa.rows, oa.cols, oa.ld, A_MN ? 64 : 128);
-    if (rc == ZERO_OK) rc = make_map(&mb, bf16, ob.base, ob.rows, ob.cols, ob.ld, B_MN ? 64 : 256 / CG);
-    if (rc != ZERO_OK) return rc;
-    a.idesc = zk::instr_desc(bf16, A_MN, B_MN, 128 * CG, a.bn);
-    auto kern = zk::mm_kernel<CG, A_MN, B_MN, EPI, F>;
+    zk::MmMaps maps{};
+    for (int i = 0; i < 2; ++i) {
+        zk::MmProblem& p = a.p[i];
+        if (p.m == 0) {
+            p.splits = p.bn = 1;
+            continue;
+        }
+        zero_status_t rc = make_map(&maps.a[i], bf16, oa[i].base, oa[i].rows, oa[i].cols, oa[i].ld, oa[i].box_rows);
+        if (rc == ZERO_OK) rc = make_map(&maps.b[i], bf16, ob[i].base, ob[i].rows, ob[i].cols, ob[i].ld, ob[i].box_rows);
+        if (rc != ZERO_OK) return rc;
+        p.idesc = zk::instr_desc(bf16, MODE == zk::MM_GRADS && i == 1, MODE == zk::MM_GRADS, 128 * CG, 0);
+    }
+    auto kern = zk::mm_kernel<CG, MODE, F>;
     constexpr int smem = zk::MmShape<CG>::kBytes;
     static std::atomic<uint64_t> allowed{0};   // by device
     int dev = 0;
@@ -681,7 +922,7 @@ zero_status_t launch_mm(const Operand& oa, const Operand& ob, zk::MmArgs a, int6
     int64_t groups = std::max(1, sm_count() / CG);
     const int32_t cap = max_ctas();
     if (cap > 0) groups = std::min<int64_t>(groups, (cap + CG - 1) / CG);
-    groups = std::max<int64_t>(1, std::min(groups, max_tiles));
+    groups = std::max<int64_t>(1, std::min(groups, most_tiles<CG>(a.p[0]) + most_tiles<CG>(a.p[1])));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(groups * CG));
     cfg.blockDim = dim3(zk::kMmThreads);
@@ -693,7 +934,7 @@ zero_status_t launch_mm(const Operand& oa, const Operand& ob, zk::MmArgs a, int6
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps, a);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
@@ -701,20 +942,41 @@ zero_status_t launch_mm(const Operand& oa, const Operand& ob, zk::MmArgs a, int6
     return after_launch(what);
 }
 
+constexpr int64_t kSlots = 152;   // SMs of a GB300: what the splits of work are made for
+
+int cta_group(int64_t n) { return n <= 128 ? 1 : 2; }
+
+// Columns of a tile: as few tiles as there are at 256, of one width.
+int32_t even_tile(int64_t n) {
+    const int64_t tiles = (n + zk::kTileN - 1) / zk::kTileN;
+    return (int32_t)std::min<int64_t>(zk::kTileN, up((n + tiles - 1) / tiles, 16));
+}
+
+// Columns of a tile of logits.  Few tokens: the weight's read bounds the time,
+// and what the busiest SM has of it: rounds of tiles times their width.
+int32_t logit_tile(int64_t n, int64_t vocab) {
+    const int64_t cg = cta_group(n), slots = kSlots / cg, rows = (n + 128 * cg - 1) / (128 * cg);
+    const auto cost = [&](int64_t bn) { return ((vocab + bn - 1) / bn * rows + slots - 1) / slots * bn; };
+    int64_t best = even_tile(vocab);
+    if ((vocab + best - 1) / best * rows < 8 * slots)
+        for (int64_t bn = zk::kTileN; bn >= 96; bn -= 16)
+            if (cost(bn) < cost(best)) best = bn;
+    return (int32_t)best;
+}
+
 // Sizes and places of one call's workspace.
 struct LossPlan {
-    int64_t n256, ldh, ldw, vocab_tiles;
+    int64_t n256, ldh, ldw, part_ld;
     bool copy_weight;
+    int32_t logit_bn, d_bn;
     int64_t piece, pieces, splits, ldo;
     // offsets: of both calls, of the forward, of the backward
-    int64_t slot, token, target, hidden, weight, common;
+    int64_t next, slot, token, target, hidden, weight;
     int64_t z_target, parts, sums, forward;
     int64_t dz, part, backward;
 };
 
 constexpr int64_t kPieceBytes = 512 << 20;
-
-int cta_group(int64_t n) { return n <= 128 ? 1 : 2; }
 
 LossPlan make_plan(const zero_lm_loss_args* a) {
     LossPlan p{};
@@ -722,7 +984,8 @@ LossPlan make_plan(const zero_lm_loss_args* a) {
     p.ldh = up(a->d, 8);
     p.copy_weight = (reinterpret_cast<uintptr_t>(a->weight) & 15) || a->d % 8;
     p.ldw = p.copy_weight ? p.ldh : a->d;
-    p.vocab_tiles = (a->vocab + zk::kTileN - 1) / zk::kTileN;
+    p.logit_bn = logit_tile(a->n, a->vocab);
+    p.part_ld = 2 * ((a->vocab + p.logit_bn - 1) / p.logit_bn);
     // dz columns at a time: few and long pieces read and write the binary32 sums of grad_hidden less often
     const int64_t all = up(a->vocab, 256);
     p.piece = a->piece > 0 ? std::min(all, up(std::min(a->piece, all), 256))
@@ -731,23 +994,28 @@ LossPlan make_plan(const zero_lm_loss_args* a) {
     p.piece = up((a->vocab + p.pieces - 1) / p.pieces, 256);   // of one size
     p.pieces = (a->vocab + p.piece - 1) / p.piece;
     p.ldo = up(a->d, 8);
-    // grad_hidden sums over the vocabulary: in parts, where its tiles alone would leave SMs idle
-    const int cg = cta_group(a->n);
-    const int64_t tiles = (p.n256 / 256) * (cg == 2 ? 1 : 1) * ((a->d + 255) / 256), slots = 152 / cg;
-    p.splits = std::max<int64_t>(1, std::min<int64_t>({slots / std::max<int64_t>(tiles, 1), p.piece / 512, 64}));
+    p.d_bn = (int32_t)std::min<int64_t>(zk::kTileN, up(a->d, 16));
+    // dz @ weight sums over the piece, dz^T @ hidden over the tokens, in one launch.  The first in parts, so that a tile of
+    // it is at most a quarter of what an SM has to do.
+    const int64_t cg = cta_group(a->n), slots = kSlots / cg, columns = (a->d + p.d_bn - 1) / p.d_bn;
+    const int64_t tiles0 = (a->n + 128 * cg - 1) / (128 * cg) * columns, kb0 = (p.piece + 63) / 64;
+    const int64_t tiles1 = (p.piece + 128 * cg - 1) / (128 * cg) * columns, kb1 = (a->n + 63) / 64;
+    const int64_t share = std::max<int64_t>(8, (tiles0 * kb0 + tiles1 * kb1) / slots / 4);
+    p.splits = std::max<int64_t>(1, std::min<int64_t>({(kb0 + share - 1) / share, 32, (64 << 20) / (p.n256 * p.ldo * 4)}));
     int64_t at = 256;
     const auto take = [&](int64_t bytes) { const int64_t o = at; at += up(bytes, 256); return o; };
+    p.next = take(4 * (2 * p.pieces + 1));
     p.slot = take(4 * a->n);
     p.token = take(4 * a->n);
     p.target = take(4 * a->n);
     p.hidden = take(p.n256 * p.ldh * 2);
     p.weight = p.copy_weight ? take(a->vocab * p.ldw * 2) : 0;
-    p.common = at;
+    const int64_t common = at;
     p.z_target = take(4 * a->n);
-    p.parts = take(p.vocab_tiles * p.n256 * 8);
-    p.sums = take((a->n + 31) / 32 * 8 + 8);
+    p.parts = take(p.part_ld * a->n * 8);
+    p.sums = take((a->n + zk::kLossRows - 1) / zk::kLossRows * 8 + 8);
     p.forward = at;
-    at = p.common;
+    at = common;
     p.dz = take(p.n256 * p.piece * 2);
     p.part = take(p.splits * p.n256 * p.ldo * 4);
     p.backward = at;
@@ -780,68 +1048,80 @@ zero_status_t launch_rows(Kernel kern, int64_t rows, const Args& a, cudaStream_t
     return after_launch(what);
 }
 
+bool direct_grad_hidden(const zero_lm_loss_args* a, const LossPlan& p) {
+    return a->grad_hidden && p.splits == 1 && (reinterpret_cast<uintptr_t>(a->grad_hidden) & 31) == 0 && a->d % 16 == 0;
+}
+
 // What both calls begin with: the tokens that count, their hidden states, and a weight that TMA can read.
 zero_status_t gather_inputs(const zero_lm_loss_args* a, const LossPlan& p, bool forward, cudaStream_t s, const char* what) {
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-    zk::PickArgs pick{};
-    pick.head = reinterpret_cast<zk::LossHead*>(ws);
-    pick.targets = a->targets;
-    pick.slot = reinterpret_cast<int32_t*>(ws + p.slot);
-    pick.token = reinterpret_cast<int32_t*>(ws + p.token);
-    pick.target = reinterpret_cast<int32_t*>(ws + p.target);
-    pick.losses = forward ? a->losses : nullptr;
-    pick.lse = forward ? a->lse : nullptr;
-    pick.vocab = a->vocab;
-    pick.n = (uint32_t)a->n;
-    zk::pick_kernel<<<1, 1024, 0, s>>>(pick);
-    zero_status_t rc = after_launch(what);
-    if (rc != ZERO_OK) return rc;
-    zk::GatherRows g{};
-    g.head = pick.head;
-    g.token = pick.token;
-    g.src = static_cast<const uint16_t*>(a->hidden);
-    g.dst = reinterpret_cast<uint16_t*>(ws + p.hidden);
-    g.src_stride = a->hidden_stride;
-    g.dst_stride = p.ldh;
-    g.rows = p.n256;
-    g.d = (uint32_t)a->d;
+    zk::PickArgs k{};
+    k.head = reinterpret_cast<zk::LossHead*>(ws);
+    k.next = reinterpret_cast<uint32_t*>(ws + p.next);
+    k.nexts = (int32_t)(2 * p.pieces + 1);
+    k.targets = a->targets;
+    k.slot = reinterpret_cast<int32_t*>(ws + p.slot);
+    k.token = reinterpret_cast<int32_t*>(ws + p.token);
+    k.target = reinterpret_cast<int32_t*>(ws + p.target);
+    k.losses = forward ? a->losses : nullptr;
+    k.lse = forward ? a->lse : nullptr;
+    k.zero = !forward && direct_grad_hidden(a, p) ? static_cast<uint16_t*>(a->grad_hidden) : nullptr;
+    k.src = static_cast<const uint16_t*>(a->hidden);
+    k.dst = reinterpret_cast<uint16_t*>(ws + p.hidden);
+    k.src_stride = a->hidden_stride;
+    k.dst_stride = p.ldh;
+    k.rows = p.n256;
+    k.vocab = a->vocab;
+    k.n = (uint32_t)a->n;
+    k.d = (uint32_t)a->d;
     const bool wide = !(reinterpret_cast<uintptr_t>(a->hidden) & 15) && a->d % 8 == 0 && (a->hidden_stride % 8 == 0 || a->n == 1);
-    rc = wide ? launch_rows(zk::rows_kernel<8>, p.n256, g, s, what) : launch_rows(zk::rows_kernel<1>, p.n256, g, s, what);
+    const auto kern = wide ? zk::pick_kernel<8> : zk::pick_kernel<1>;
+    const int grid = persistent_grid(kern, std::min<int64_t>((a->n + 15) / 16, 2 * kSlots), 0, zk::kPickThreads);
+    k.per_cta = (uint32_t)((a->n + grid - 1) / grid);
+    kern<<<grid, zk::kPickThreads, 0, s>>>(k);
+    const zero_status_t rc = after_launch(what);
     if (rc != ZERO_OK || !p.copy_weight) return rc;
-    zk::GatherRows w{};
-    w.src = static_cast<const uint16_t*>(a->weight);
-    w.dst = reinterpret_cast<uint16_t*>(ws + p.weight);
-    w.src_stride = a->d;
-    w.dst_stride = p.ldw;
-    w.rows = a->vocab;
-    w.d = (uint32_t)a->d;
-    return launch_rows(zk::rows_kernel<1>, a->vocab, w, s, what);
+    const zk::CopyArgs w{static_cast<const uint16_t*>(a->weight), reinterpret_cast<uint16_t*>(ws + p.weight), a->vocab, p.ldw, (uint32_t)a->d};
+    return launch_rows(zk::copy_kernel, a->vocab, w, s, what);
 }
 
-// Columns of an output tile: as few tiles as there are at 256, of one width.
-int32_t even_tile(int64_t n) {
-    const int64_t tiles = (n + zk::kTileN - 1) / zk::kTileN;
-    return (int32_t)std::min<int64_t>(zk::kTileN, up((n + tiles - 1) / tiles, 16));
+zk::MmArgs mm_args(const zero_lm_loss_args* a, const LossPlan& p) {
+    uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+    zk::MmArgs m{};
+    m.head = reinterpret_cast<zk::LossHead*>(ws);
+    m.next = reinterpret_cast<uint32_t*>(ws + p.next);
+    m.target = reinterpret_cast<const int32_t*>(ws + p.target);
+    m.row_of = reinterpret_cast<const int32_t*>(ws + p.token);
+    m.lse = a->lse;
+    m.d = a->d;
+    return m;
+}
+
+// hidden @ weight^T for `cols` columns of the vocabulary from v0 on.
+template <int CG>
+zk::MmProblem logits_of(const zero_lm_loss_args* a, int64_t v0, int64_t cols, int32_t bn) {
+    zk::MmProblem p{};
+    p.rows_in = zk::ROWS_M;
+    p.m = a->n;
+    p.n = cols;
+    p.k = a->d;
+    p.bn = bn;
+    p.splits = 1;
+    p.m_group = 32;   // 32 tiles of hidden states stay in L2 while the weight streams by
+    p.n_off = (int32_t)v0;
+    return p;
 }
 
 template <int CG, class F>
 zero_status_t run_forward(const zero_lm_loss_args* a, const LossPlan& p, const void* weight, cudaStream_t s, const char* what) {
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-    const Operand h{ws + p.hidden, p.n256, a->d, p.ldh}, w{weight, a->vocab, a->d, p.ldw};
-    zk::MmArgs m{};
-    m.head = reinterpret_cast<zk::LossHead*>(ws);
-    m.rows_in = zk::ROWS_M;
-    m.m = a->n;
-    m.n = a->vocab;
-    m.k = a->d;
-    m.bn = zk::kTileN;
-    m.splits = 1;
-    m.m_group = 32;
-    m.target = reinterpret_cast<const int32_t*>(ws + p.target);
+    const Operand h{ws + p.hidden, p.n256, a->d, p.ldh, 128}, w{weight, a->vocab, a->d, p.ldw, p.logit_bn / CG};
+    zk::MmArgs m = mm_args(a, p);
+    m.p[0] = logits_of<CG>(a, 0, a->vocab, p.logit_bn);
     m.parts = reinterpret_cast<float2*>(ws + p.parts);
-    m.part_rows = p.n256;
+    m.part_ld = p.part_ld;
     m.z_target = reinterpret_cast<float*>(ws + p.z_target);
-    return launch_mm<CG, false, false, zk::EPI_STATS, F>(h, w, m, (p.n256 / 128) * p.vocab_tiles, s, what);
+    return launch_mm<CG, zk::MM_STATS, F>(&h, &w, m, s, what);
 }
 
 template <int CG, class F>
@@ -849,70 +1129,64 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
     constexpr bool bf16 = std::is_same<F, zk::Bf16>::value;
     const float up_by = bf16 ? 1.0f : 16384.0f;   // of dz: fp16's normal numbers end at 2^-14
-    zk::MmArgs base{};
-    base.head = reinterpret_cast<zk::LossHead*>(ws);
+    const bool direct = direct_grad_hidden(a, p);
+    zk::MmArgs base = mm_args(a, p);
+    base.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
+    base.dz_ld = p.piece;
+    base.dz_scale = up_by;
+    base.part = reinterpret_cast<float*>(ws + p.part);
+    base.split_rows = p.n256;
+    base.part_cols = p.ldo;
     base.scale = (float)a->scale / up_by;
     base.scale_dev = a->scale_dev;
     base.share = a->stats + 1;
-    base.splits = 1;
+    base.gw_add = a->accumulate != 0;
+    base.gw_vec = (reinterpret_cast<uintptr_t>(a->grad_weight) & 31) == 0 && a->d % 16 == 0;
     zero_status_t rc = ZERO_OK;
-    for (int64_t v0 = 0, i = 0; v0 < a->vocab; v0 += p.piece, ++i) {
-        const int64_t cols = std::min(p.piece, a->vocab - v0);
-        const Operand h{ws + p.hidden, p.n256, a->d, p.ldh}, w{weight, a->vocab, a->d, p.ldw};
-        const Operand dz{ws + p.dz, p.n256, cols, p.piece};
-        zk::MmArgs m = base;     // the logits of the piece, and their gradient
-        m.rows_in = zk::ROWS_M;
-        m.m = a->n;
-        m.n = cols;
-        m.k = a->d;
-        m.bn = zk::kTileN;
-        m.m_group = 32;
-        m.n_off = (int32_t)v0;
-        m.target = reinterpret_cast<const int32_t*>(ws + p.target);
-        m.row_of = reinterpret_cast<const int32_t*>(ws + p.token);
-        m.lse = a->lse;
-        m.dz = reinterpret_cast<uint16_t*>(ws + p.dz);
-        m.ld = p.piece;
-        m.dz_scale = up_by;
-        rc = launch_mm<CG, false, false, zk::EPI_DZ, F>(h, w, m, (p.n256 / 128) * ((cols + 255) / 256), s, what);
-        if (rc != ZERO_OK) return rc;
-        if (a->grad_hidden) {    // dz @ weight: K is the piece
-            m = base;
-            m.rows_in = zk::ROWS_M;
-            m.m = a->n;
-            m.n = a->d;
-            m.k = cols;
-            m.bn = even_tile(a->d);
-            m.k_off = (int32_t)v0;
-            m.splits = (int32_t)p.splits;
-            m.part = reinterpret_cast<float*>(ws + p.part);
-            m.split_rows = p.n256;
-            m.ld = p.ldo;
-            m.add = i > 0;
-            rc = launch_mm<CG, false, true, zk::EPI_PART, F>(dz, w, m, (p.n256 / 128) * ((a->d + m.bn - 1) / m.bn) * p.splits, s, what);
+    for (int64_t i = 0; i < p.pieces; ++i) {
+        const int64_t v0 = i * p.piece, cols = std::min(p.piece, a->vocab - v0);
+        const int32_t bn = std::min<int32_t>(p.logit_bn, even_tile(cols));
+        {   // the logits of the piece, and their gradient
+            const Operand h{ws + p.hidden, p.n256, a->d, p.ldh, 128}, w{weight, a->vocab, a->d, p.ldw, bn / CG};
+            zk::MmArgs m = base;
+            m.next += 2 * i;
+            m.p[0] = logits_of<CG>(a, v0, cols, bn);
+            rc = launch_mm<CG, zk::MM_DZ, F>(&h, &w, m, s, what);
             if (rc != ZERO_OK) return rc;
+        }
+        const Operand oa[2] = {{ws + p.dz, p.n256, cols, p.piece, 128}, {ws + p.dz, p.n256, cols, p.piece, 64}};
+        const Operand ob[2] = {{weight, a->vocab, a->d, p.ldw, 64}, {ws + p.hidden, p.n256, a->d, p.ldh, 64}};
+        zk::MmArgs m = base;
+        m.next += 2 * i + 1;
+        if (a->grad_hidden) {    // dz @ weight: K is the piece
+            m.p[0].rows_in = zk::ROWS_M;
+            m.p[0].m = a->n;
+            m.p[0].n = a->d;
+            m.p[0].k = cols;
+            m.p[0].bn = p.d_bn;
+            m.p[0].k_off = (int32_t)v0;
+            m.p[0].splits = (int32_t)p.splits;
+            m.part_add = i > 0;
+            m.gh = direct && i == p.pieces - 1 ? static_cast<uint16_t*>(a->grad_hidden) : nullptr;
         }
         if (a->grad_weight) {    // dz^T @ hidden: K is the tokens that count
-            m = base;
-            m.rows_in = zk::ROWS_K;
-            m.m = cols;
-            m.n = a->d;
-            m.k = a->n;
-            m.bn = even_tile(a->d);
-            m.out = static_cast<uint16_t*>(a->grad_weight) + v0 * a->d;
-            m.ld = a->d;
-            m.add = a->accumulate != 0;
-            m.vec = (reinterpret_cast<uintptr_t>(a->grad_weight) & 31) == 0 && a->d % 16 == 0;
-            rc = launch_mm<2, true, true, zk::EPI_OUT, F>(dz, h, m, ((cols + 255) / 256) * ((a->d + m.bn - 1) / m.bn), s, what);
-            if (rc != ZERO_OK) return rc;
+            m.p[1].rows_in = zk::ROWS_K;
+            m.p[1].m = cols;
+            m.p[1].n = a->d;
+            m.p[1].k = a->n;
+            m.p[1].bn = p.d_bn;
+            m.p[1].splits = 1;
+            m.gw = static_cast<uint16_t*>(a->grad_weight) + v0 * a->d;
         }
+        rc = launch_mm<CG, zk::MM_GRADS, F>(oa, ob, m, s, what);
+        if (rc != ZERO_OK) return rc;
     }
-    if (!a->grad_hidden) return ZERO_OK;
+    if (!a->grad_hidden || direct) return ZERO_OK;
     zk::FinishArgs f{};
-    f.part = reinterpret_cast<const float*>(ws + p.part);
+    f.part = base.part;
     f.slot = reinterpret_cast<const int32_t*>(ws + p.slot);
     f.out = static_cast<uint16_t*>(a->grad_hidden);
-    f.share = a->stats + 1;
+    f.share = base.share;
     f.scale_dev = a->scale_dev;
     f.n = a->n;
     f.split_rows = p.n256;
@@ -920,6 +1194,7 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
     f.d = (uint32_t)a->d;
     f.splits = (int32_t)p.splits;
     f.scale = base.scale;
+    if (a->n == 0) return ZERO_OK;
     const bool wide = !(reinterpret_cast<uintptr_t>(a->grad_hidden) & 15) && a->d % 8 == 0;
     return wide ? launch_rows(zk::finish_kernel<F, 8>, a->n, f, s, what) : launch_rows(zk::finish_kernel<F, 1>, a->n, f, s, what);
 }
@@ -961,9 +1236,9 @@ extern "C" zero_status_t zero_lm_loss_forward(const zero_lm_loss_args* a, zero_s
     zk::LossArgs l{};
     l.head = reinterpret_cast<zk::LossHead*>(ws);
     l.parts = reinterpret_cast<const float2*>(ws + p.parts);
-    l.rows = p.n256;
-    l.tiles = (int32_t)p.vocab_tiles;
-    l.blocks = (int32_t)((a->n + 31) / 32);
+    l.ld = p.part_ld;
+    l.tiles = (int32_t)p.part_ld;
+    l.blocks = (int32_t)((a->n + zk::kLossRows - 1) / zk::kLossRows);
     l.reduction = a->reduction;
     l.z_target = reinterpret_cast<const float*>(ws + p.z_target);
     l.token = reinterpret_cast<const int32_t*>(ws + p.token);
