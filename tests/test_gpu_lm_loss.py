@@ -346,8 +346,9 @@ def test_captured_replayed_and_on_two_streams():
 
 def test_no_errors_reported():
     h, w, t = inputs(50, 64, 300, BF)
-    a, keep = L._loss_args(h, w, t, 0)
-    ws = torch.empty(B.zero_lm_loss_query(a)[0], dtype=torch.uint8, device="cuda")
+    a, (need, _), keep = L._loss_args(h, w, t)
+    assert need == B.zero_lm_loss_query(a)[0]
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     out, stats = torch.empty(2, 50, device="cuda"), torch.empty(2, device="cuda")
     a.losses, a.lse, a.stats, a.workspace = out[0].data_ptr(), out[1].data_ptr(), stats.data_ptr(), ws.data_ptr()
     B.zero_lm_loss_forward(a)

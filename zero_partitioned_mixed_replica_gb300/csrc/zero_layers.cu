@@ -9,6 +9,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "zero_launch.h"
@@ -55,6 +56,74 @@ __device__ __forceinline__ void ld_e(const typename Store<F>::S* __restrict__ p,
         static_assert(E == 1, "8, 2 or 1 16-bit elements");
         o[0] = F::dec1(__ldg(p));
     }
+}
+
+// The same as it lies in memory, to be widened where it is used: half the registers.
+template <class F, int E>
+struct Raw {
+    using S = typename Store<F>::S;
+    static constexpr int kWords = E * (int)sizeof(S) >= 4 ? E * (int)sizeof(S) / 4 : 1;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const S* __restrict__ p) {
+        if constexpr (kWords == 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else {
+            static_assert(kWords == 1, "16, 4 or 2 bytes");
+            if constexpr (E * sizeof(S) == 4) w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            else w[0] = __ldg(p);
+        }
+    }
+    // from shared memory, 16 bytes
+    __device__ __forceinline__ void load_shared(const uint8_t* p) {
+        static_assert(kWords == 4, "16 bytes");
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    }
+    __device__ __forceinline__ void get(float (&o)[E]) const {
+        if constexpr (sizeof(S) == 4) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) o[k] = __uint_as_float(w[k]);
+        } else if constexpr (E == 1) {
+            o[0] = F::dec1((uint16_t)w[0]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
+                o[2 * k] = F::lo(w[k]);
+                o[2 * k + 1] = F::hi(w[k]);
+            }
+        }
+    }
+};
+
+// Wait for the kernels before this one in the stream: it may have begun while they end.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Two binary32 operations in one instruction, each rounded to nearest.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
 template <class F, int E>
@@ -271,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) embed_grad_kernel(const __grid_const
     using S = typename Store<F>::S;
     const uint32_t per_cta = kThreads / a.group;
     const uint32_t lane = threadIdx.x % a.group;
+    grid_wait();
     for (uint32_t q = blockIdx.x * per_cta + threadIdx.x / a.group; q < a.pieces; q += gridDim.x * per_cta) {
         const uint32_t b = q * a.piece, e = min(a.n, b + a.piece);
         const uint32_t id_before = b > 0 ? (uint32_t)(__ldg(a.pairs + b - 1) >> 32) : ~0u;
@@ -292,28 +362,30 @@ __global__ void __launch_bounds__(kThreads) embed_grad_kernel(const __grid_const
                 }
                 first = false;
             };
-            for (uint32_t i = b; i < e; i += 4) {
-                uint64_t pair[4];
-                float x[4][E];
+            for (uint32_t i = b; i < e; i += 8) {
+                uint64_t pair[8];
+                Raw<F, E> raw[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 8; ++k)
                     pair[k] = i + k < e ? __ldg(a.pairs + i + k) : ~0ull;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 8; ++k)
                     if ((uint32_t)(pair[k] >> 32) < a.vocab)
-                        ld_e<F, E>(static_cast<const S*>(a.grad) + (size_t)(uint32_t)pair[k] * a.d + (size_t)c * E, x[k]);
+                        raw[k].load(static_cast<const S*>(a.grad) + (size_t)(uint32_t)pair[k] * a.d + (size_t)c * E);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const uint32_t now = (uint32_t)(pair[k] >> 32);
                     if (now < a.vocab) {
+                        float x[E];
+                        raw[k].get(x);
                         if (now != id) {
                             flush(now);
                             id = now;
 #pragma unroll
-                            for (int j = 0; j < E; ++j) sum[j] = x[k][j];
+                            for (int j = 0; j < E; ++j) sum[j] = x[j];
                         } else {
 #pragma unroll
-                            for (int j = 0; j < E; ++j) sum[j] = __fadd_rn(sum[j], x[k][j]);
+                            for (int j = 0; j < E; ++j) sum[j] = __fadd_rn(sum[j], x[j]);
                         }
                     }
                 }
@@ -324,10 +396,16 @@ __global__ void __launch_bounds__(kThreads) embed_grad_kernel(const __grid_const
     }
 }
 
-// One CTA adds up the parts of an id whose rows begin in piece q and go on
-// behind it: slot 1 of q, slot 0 of the pieces after it.
+// Adds up the parts of an id whose rows begin in piece q and go on behind it:
+// slot 1 of q, slot 0 of the pieces after it.  The warps of a CTA take every
+// eighth part of 32 pieces of columns, and are added in order (the first token
+// of a Zipf-distributed text is in a hundred pieces).
 template <class F, class O, int E>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradArgs a) {
+    constexpr int W = kThreads / 32;
+    __shared__ float sh[W][32 * E];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    grid_wait();
     for (uint32_t q = blockIdx.x; q + 1 < a.pieces; q += gridDim.x) {
         const uint32_t b = q * a.piece, e = b + a.piece;
         const uint32_t id = (uint32_t)(__ldg(a.pairs + e) >> 32);
@@ -338,19 +416,28 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
             const uint32_t mid = lo + (hi - lo) / 2;
             if ((uint32_t)(__ldg(a.pairs + mid) >> 32) == id) lo = mid; else hi = mid;
         }
-        const uint32_t last = lo / a.piece;
-        for (uint32_t c = threadIdx.x + blockIdx.y * kThreads; c < a.dv; c += kThreads * gridDim.y) {
-            float sum[E];
-            const float* p = a.parts + ((size_t)q * 2 + 1) * a.d + (size_t)c * E;
-#pragma unroll
-            for (int k = 0; k < E; ++k) sum[k] = p[k];
+        const uint32_t parts = lo / a.piece - q + 1;
+        for (uint32_t c0 = blockIdx.y * 32; c0 < a.dv; c0 += 32 * gridDim.y) {
+            const uint32_t c = c0 + lane;
+            float sum[E] = {};
+            if (c < a.dv) {
 #pragma unroll 4
-            for (uint32_t r = q + 1; r <= last; ++r) {
-                p = a.parts + (size_t)r * 2 * a.d + (size_t)c * E;
+                for (uint32_t r = warp; r < parts; r += W) {
+                    const float* p = a.parts + ((size_t)(q + r) * 2 + (r == 0)) * a.d + (size_t)c * E;
 #pragma unroll
-                for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], p[k]);
+                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], p[k]);
+                }
             }
-            embed_row<F, O, E>(a, id, c, sum);
+#pragma unroll
+            for (int k = 0; k < E; ++k) sh[warp][lane * E + k] = sum[k];
+            __syncthreads();
+            if (warp == 0 && c < a.dv) {
+                for (uint32_t w = 1; w < min((uint32_t)W, parts); ++w)
+#pragma unroll
+                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], sh[w][lane * E + k]);
+                embed_row<F, O, E>(a, id, c, sum);
+            }
+            __syncthreads();
         }
     }
 }
@@ -440,7 +527,74 @@ __global__ void __launch_bounds__(WARP ? kThreads : 1024) norm_kernel(const __gr
     }
 }
 
+// The same with 16-byte pieces, a warp a row: the row stays in registers as it
+// lies in memory, so that twice as many rows are under way.
+template <class F, int NV>
+__global__ void __launch_bounds__(kThreads) norm_warp_kernel(const __grid_constant__ NormArgs a) {
+    using S = typename Store<F>::S;
+    constexpr int E = 16 / (int)sizeof(S);
+    const uint32_t lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+    const float d = (float)a.d;
+    for (int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; row < a.rows; row += step) {
+        const S* src = static_cast<const S*>(a.x) + row * a.x_stride;
+        Raw<F, E> raw[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (lane + k * 32 < a.dv) raw[k].load(src + (size_t)(lane + k * 32) * E);
+        F2 sum = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (lane + k * 32 < a.dv) {
+                float x[E];
+                raw[k].get(x);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) sum = add2(sum, f2(x[e], x[e + 1]));
+            }
+        float lo, hi;
+        split(sum, lo, hi);
+        const float mean = __fdiv_rn(warp_sum(__fadd_rn(lo, hi)), d);
+        const F2 minus = f2(-mean, -mean);
+        sum = f2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (lane + k * 32 < a.dv) {
+                float x[E];
+                raw[k].get(x);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const F2 t = add2(f2(x[e], x[e + 1]), minus);
+                    sum = fma2(t, t, sum);
+                }
+            }
+        split(sum, lo, hi);
+        const float var = __fdiv_rn(warp_sum(__fadd_rn(lo, hi)), d);
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+        if (lane == 0 && a.mean) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        const F2 by = f2(rstd, rstd);
+        S* dst = static_cast<S*>(a.y) + row * (int64_t)a.d;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t c = lane + k * 32;
+            if (c < a.dv) {
+                float x[E], w[E], b[E] = {};
+                raw[k].get(x);
+                ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)c * E, w);
+                if (a.bias) ld_e<F, E>(static_cast<const S*>(a.bias) + (size_t)c * E, b);
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    split(fma2(mul2(add2(f2(x[e], x[e + 1]), minus), by), f2(w[e], w[e + 1]), f2(b[e], b[e + 1])), x[e], x[e + 1]);
+                st_e<F, E>(dst + (size_t)c * E, x);
+            }
+        }
+    }
+}
+
 constexpr int64_t kNormBlocks = 456;   // blocks of rows, at most: 3 CTAs on each of 152 SMs
+constexpr int64_t kRingBlocks = 152;   // and of the kernel with a ring, which fills an SM
 
 struct NormGradArgs {
     const void* gy;
@@ -553,6 +707,185 @@ __global__ void __launch_bounds__(RI == 1 ? 1024 : 512) norm_grad_kernel(const _
     }
 }
 
+// The same where rows are read in 16-byte pieces.  A team of G warps takes a
+// row, 8 / G teams a CTA; a thread keeps NV pieces of columns, at most 64
+// columns, and their sums for the weight and bias in registers for all its
+// rows.  Rows come through a ring of bulk copies in shared memory, which are
+// under way while a team computes: 8 warps alone could not keep enough loads
+// in flight (3.5 times the time, with loads into registers and one barrier
+// for 4 rows).  A row's two means need it twice: from shared memory, as
+// registers are full.
+struct RingShape {
+    int32_t stages;
+    uint32_t row_bytes, weight_at, bars_at;
+};
+
+template <int G>
+__device__ __forceinline__ void team_barrier(int team) {
+    if constexpr (G == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(G * 32) : "memory");
+}
+
+template <class F, int NV, int G>
+__global__ void __launch_bounds__(kThreads, 1) norm_ring_kernel(const __grid_constant__ NormGradArgs a,
+                                                                const __grid_constant__ RingShape shape) {
+    using S = typename Store<F>::S;
+    constexpr int E = 16 / (int)sizeof(S), T = kThreads / 32 / G;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float sh[2][T][G][2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, team = warp / G, part = warp % G;
+    const uint32_t tid = part * 32 + lane;   // in the team
+    const uint32_t row_bytes = shape.row_bytes;
+    const int ST = shape.stages;
+    uint8_t* ring = smem + (size_t)team * ST * 2 * row_bytes;   // [stage][x, gy][row]
+    uint8_t* weight = smem + shape.weight_at;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + shape.bars_at) + team * ST;
+    for (uint32_t c = threadIdx.x; c < a.dv; c += kThreads)
+        reinterpret_cast<uint4*>(weight)[c] = __ldg(reinterpret_cast<const uint4*>(a.weight) + c);
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) mbar_init(full + i, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const float inv_d = __fdiv_rn(1.0f, (float)a.d);
+    bool ok = true;
+    int stage = 0, fill = 0, flip = 0, under_way = 0;
+    uint32_t phase = 0;
+    for (int block = blockIdx.x; block < a.blocks; block += gridDim.x) {
+        const int64_t r0 = block * a.per_block + team, r1 = min(a.rows, (block + 1) * a.per_block);
+        F2 sw[NV][E / 2], sb[NV][E / 2];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) sw[k][e] = sb[k][e] = f2(0.0f, 0.0f);
+        const auto request = [&](int64_t row) {   // one thread of the team
+            mbar_arrive_expect_tx(full + fill, 2 * row_bytes);
+            bulk_g2s(ring + (size_t)fill * 2 * row_bytes, static_cast<const S*>(a.x) + row * a.x_stride, row_bytes, full + fill);
+            bulk_g2s(ring + (size_t)(fill * 2 + 1) * row_bytes, static_cast<const S*>(a.gy) + row * a.gy_stride, row_bytes, full + fill);
+            if (++fill == ST) fill = 0;
+            ++under_way;
+        };
+        if (tid == 0 && ok)
+            for (int i = 0; i < ST; ++i)
+                if (r0 + i * T < r1) request(r0 + i * T);
+        for (int64_t row = r0; row < r1; row += T, flip ^= 1) {
+            const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
+            if (ok) ok = mbar_wait_bounded(full + stage, phase);
+            if (ok) --under_way;
+            // a copy that does not come: NaN in what this thread computes, and so in the weight's gradient
+            const float scale = ok ? rstd : NAN;
+            const F2 minus = f2(-mean, -mean), by = f2(scale, scale);
+            const uint8_t* xs = ring + (size_t)stage * 2 * row_bytes;
+            const uint8_t* gs = xs + row_bytes;
+            F2 s1 = f2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const uint32_t c = tid + k * 32 * G;
+                if (c < a.dv) {
+                    Raw<F, E> rx, rg, rw;
+                    rx.load_shared(xs + c * 16);
+                    rg.load_shared(gs + c * 16);
+                    rw.load_shared(weight + c * 16);
+                    float x[E], g[E], w[E];
+                    rx.get(x);
+                    rg.get(g);
+                    rw.get(w);
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const F2 u = mul2(add2(f2(x[e], x[e + 1]), minus), by), gg = f2(g[e], g[e + 1]);
+                        sw[k][e / 2] = fma2(gg, u, sw[k][e / 2]);
+                        sb[k][e / 2] = add2(sb[k][e / 2], gg);
+                        const F2 h = mul2(gg, f2(w[e], w[e + 1]));
+                        s1 = add2(s1, h);
+                        s2 = fma2(h, u, s2);
+                    }
+                }
+            }
+            float lo, hi, m1, m2;
+            split(s1, lo, hi);
+            m1 = warp_sum(__fadd_rn(lo, hi));
+            split(s2, lo, hi);
+            m2 = warp_sum(__fadd_rn(lo, hi));
+            if constexpr (G > 1) {
+                if (lane == 0) {
+                    sh[flip][team][part][0] = m1;
+                    sh[flip][team][part][1] = m2;
+                }
+                team_barrier<G>(team);   // the other half of sh is written next
+                m1 = m2 = 0.0f;
+#pragma unroll
+                for (int p = 0; p < G; ++p) {
+                    m1 = __fadd_rn(m1, sh[flip][team][p][0]);
+                    m2 = __fadd_rn(m2, sh[flip][team][p][1]);
+                }
+            }
+            m1 = __fmul_rn(m1, inv_d);
+            m2 = -__fmul_rn(m2, inv_d);
+            const F2 less = f2(-m1, -m1), along = f2(m2, m2);
+            S* dst = static_cast<S*>(a.gx) + row * (int64_t)a.d;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const uint32_t c = tid + k * 32 * G;
+                if (c < a.dv) {
+                    Raw<F, E> rx, rg, rw;
+                    rx.load_shared(xs + c * 16);
+                    rg.load_shared(gs + c * 16);
+                    rw.load_shared(weight + c * 16);
+                    float x[E], g[E], w[E];
+                    rx.get(x);
+                    rg.get(g);
+                    rw.get(w);
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const F2 u = mul2(add2(f2(x[e], x[e + 1]), minus), by), h = mul2(f2(g[e], g[e + 1]), f2(w[e], w[e + 1]));
+                        split(mul2(by, fma2(u, along, add2(h, less))), x[e], x[e + 1]);
+                    }
+                    st_e<F, E>(dst + (size_t)c * E, x);
+                }
+            }
+            team_barrier<G>(team);   // the stage has been read
+            if (tid == 0 && ok && row + (int64_t)ST * T < r1) request(row + (int64_t)ST * T);
+            if (ok && ++stage == ST) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (!ok && tid == 0) {   // the copies still under way write to shared memory: not beyond the CTA's end
+            for (; under_way > 0; --under_way) {
+                for (int tries = 0; tries < kDrainTries && !mbar_wait_bounded(full + stage, phase); ++tries) {}
+                if (++stage == ST) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // the teams' sums, in order, through the ring
+        __syncthreads();
+        float* sums = reinterpret_cast<float*>(smem);   // [team][2][d]
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t c = tid + k * 32 * G;
+            if (c < a.dv) {
+                float* p = sums + (size_t)team * 2 * a.d + (size_t)c * E;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    split(sw[k][e], p[2 * e], p[2 * e + 1]);
+                    split(sb[k][e], p[a.d + 2 * e], p[a.d + 2 * e + 1]);
+                }
+            }
+        }
+        __syncthreads();
+        for (uint32_t c = threadIdx.x; c < 2 * a.d; c += kThreads) {
+            float sum = sums[c];
+#pragma unroll
+            for (int t = 1; t < T; ++t) sum = __fadd_rn(sum, sums[(size_t)t * 2 * a.d + c]);
+            a.parts[(size_t)block * 2 * a.d + c] = sum;
+        }
+        fence_proxy_async_smem();   // copies of the next block write where these were
+        __syncthreads();
+    }
+}
+
 // The blocks' sums: 32 columns a CTA, each warp every 32nd block, the warps in order.
 template <class O>
 __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormGradArgs a) {
@@ -560,6 +893,7 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
     __shared__ float sh[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const uint32_t per = (a.d + 31) / 32;
+    grid_wait();
     for (uint32_t t = blockIdx.x; t < 2 * per; t += gridDim.x) {
         const bool bias = t >= per;
         const uint32_t c = (t - (bias ? per : 0)) * 32 + lane;
@@ -639,6 +973,27 @@ int capped(int64_t ctas) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, 0x7FFFFFFF));
 }
 
+// A launch that may begin while the stream's last kernel ends (grid_wait).
+template <class... P, class... A>
+zero_status_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const char* what, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    }
+    return after_launch(what);
+}
+
 constexpr int64_t kMaxVocab = 0x7FFFFFFE, kMaxRows = 0x7FFFFFFF, kMaxDim = 1 << 20;
 
 zero_status_t check_embedding(const char* what, int64_t vocab, int64_t d, int64_t n) {
@@ -707,14 +1062,12 @@ zero_status_t launch_embed_grad(const zk::EmbedGradArgs& a, cudaStream_t s) {
     const char* what = "zero_embedding_backward";
     auto k = zk::embed_grad_kernel<F, O, E>;
     const uint32_t per_cta = zk::kThreads / a.group;
-    k<<<persistent_grid(k, (a.pieces + per_cta - 1) / per_cta), zk::kThreads, 0, s>>>(a);
-    zero_status_t rc = after_launch(what);
+    zero_status_t rc = launch_after(k, dim3((unsigned)persistent_grid(k, (a.pieces + per_cta - 1) / per_cta)), zk::kThreads, 0, s, what, a);
     if (rc != ZERO_OK || a.pieces < 2) return rc;
     // few CTAs find something to add: pieces x column slices
-    const int64_t slices = std::min<int64_t>((a.dv + zk::kThreads - 1) / zk::kThreads, 64);
-    const dim3 grid((unsigned)capped(std::min<int64_t>(a.pieces - 1, 65535)), (unsigned)(max_ctas() > 0 ? 1 : slices));
-    zk::embed_join_kernel<F, O, E><<<grid, zk::kThreads, 0, s>>>(a);
-    return after_launch(what);
+    const dim3 grid((unsigned)capped(std::min<int64_t>(a.pieces - 1, 65535)),
+                    (unsigned)(max_ctas() > 0 ? 1 : std::min<int64_t>((a.dv + 31) / 32, 64)));
+    return launch_after(zk::embed_join_kernel<F, O, E>, grid, zk::kThreads, 0, s, what, a);
 }
 
 }  // namespace
@@ -817,34 +1170,73 @@ zero_status_t check_norm(const char* what, int64_t rows, int64_t d) {
 template <class F, int E>
 void launch_norm(const zk::NormArgs& a, cudaStream_t s) {
     // a warp keeps up to 64 elements a lane, a CTA's thread up to 16
-    constexpr int WIDE = E == 1 ? 32 : E == 2 ? 16 : E == 4 ? 8 : 8;
-    constexpr int HALF = WIDE / 2;
     const auto warps = [&](auto kern) { kern<<<persistent_grid(kern, (a.rows + 7) / 8), zk::kThreads, 0, s>>>(a); };
-    if (a.dv <= 32u * HALF) return warps(zk::norm_kernel<F, E, HALF, true>);
-    if (a.dv <= 32u * WIDE) return warps(zk::norm_kernel<F, E, WIDE, true>);
+    if constexpr (E >= 4) {
+        constexpr int B = 8 / E;   // twice as many pieces of half the elements
+        if (a.dv <= 32u * 1 * B) return warps(zk::norm_warp_kernel<F, 1 * B>);
+        if (a.dv <= 32u * 2 * B) return warps(zk::norm_warp_kernel<F, 2 * B>);
+        if (a.dv <= 32u * 3 * B) return warps(zk::norm_warp_kernel<F, 3 * B>);
+        if (a.dv <= 32u * 4 * B) return warps(zk::norm_warp_kernel<F, 4 * B>);
+        if (a.dv <= 32u * 6 * B) return warps(zk::norm_warp_kernel<F, 6 * B>);
+        if (a.dv <= 32u * 8 * B) return warps(zk::norm_warp_kernel<F, 8 * B>);
+    } else {
+        constexpr int WIDE = E == 1 ? 32 : 16;
+        if (a.dv <= 32u * WIDE) return warps(zk::norm_kernel<F, E, WIDE, true>);
+    }
     constexpr int NV = 16 / E;
     auto kern = zk::norm_kernel<F, E, NV, false>;
     const int threads = (int)((a.dv + NV - 1) / NV + 31) / 32 * 32;
     kern<<<persistent_grid(kern, a.rows, 0, threads), threads, 0, s>>>(a);
 }
 
-int64_t norm_rows_per_block(int64_t rows) {
-    const int64_t per = (rows + zk::kNormBlocks - 1) / zk::kNormBlocks;
-    return std::max<int64_t>(4, per);
+// Rows of a block: of the kernel with a ring, and of the others.
+int64_t norm_rows_per_block(int64_t rows, bool ring) {
+    const int64_t most = ring ? zk::kRingBlocks : zk::kNormBlocks;
+    return std::max<int64_t>(ring ? 1 : 4, (rows + most - 1) / most);
+}
+
+template <class F, int NV, int G>
+zero_status_t launch_norm_ring(const zk::NormGradArgs& a, cudaStream_t s, const char* what) {
+    constexpr int T = zk::kThreads / 32 / G;
+    constexpr int64_t kMost = 232448 - 1024;   // of the 227 KB of shared memory a CTA may have, 1 KB is for static arrays
+    zk::RingShape r{};
+    r.row_bytes = a.d * sizeof(typename zk::Store<F>::S);
+    r.stages = (int32_t)std::max<int64_t>(1, std::min<int64_t>(4, (kMost - r.row_bytes - 512) / (T * 2 * (int64_t)r.row_bytes)));
+    const int64_t ring = (int64_t)T * r.stages * 2 * r.row_bytes, sums = (int64_t)T * 2 * a.d * 4;
+    r.weight_at = (uint32_t)((std::max(ring, sums) + 127) / 128 * 128);
+    r.bars_at = (r.weight_at + r.row_bytes + 127) / 128 * 128;
+    const int smem = (int)(r.bars_at + T * r.stages * 8);
+    auto kern = zk::norm_ring_kernel<F, NV, G>;
+    static std::atomic<uint64_t> allowed{0};   // by device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) != cudaSuccess) return after_launch(what);
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    kern<<<capped(std::min<int64_t>(a.blocks, std::max(1, sm_count()))), zk::kThreads, smem, s>>>(a, r);
+    return after_launch(what);
 }
 
 template <class F, int E>
-void launch_norm_grad(const zk::NormGradArgs& a, cudaStream_t s) {
-    const auto go = [&](auto kern, int nv) {
-        const int threads = (int)((a.dv + nv - 1) / nv + 31) / 32 * 32;
-        kern<<<persistent_grid(kern, a.blocks, 0, threads), threads, 0, s>>>(a);
-    };
+zero_status_t launch_norm_grad(const zk::NormGradArgs& a, cudaStream_t s, const char* what) {
     if constexpr (E >= 4) {
-        if (a.dv <= 512) return go(zk::norm_grad_kernel<F, E, 1, 4>, 1);
-        go(zk::norm_grad_kernel<F, E, E == 8 ? 2 : 4, 1>, E == 8 ? 2 : 4);
+        constexpr int B = 8 / E;
+        if (a.dv <= 32u * 2 * B) return launch_norm_ring<F, 2 * B, 1>(a, s, what);
+        if (a.dv <= 32u * 4 * B) return launch_norm_ring<F, 4 * B, 1>(a, s, what);
+        if (a.dv <= 32u * 8 * B) return launch_norm_ring<F, 8 * B, 1>(a, s, what);
+        if (a.dv <= 64u * 8 * B) return launch_norm_ring<F, 8 * B, 2>(a, s, what);
+        if (a.dv <= 128u * 8 * B) return launch_norm_ring<F, 8 * B, 4>(a, s, what);
+        return launch_norm_ring<F, 8 * B, 8>(a, s, what);
     } else {
+        const auto go = [&](auto kern, int nv) {
+            const int threads = (int)((a.dv + nv - 1) / nv + 31) / 32 * 32;
+            kern<<<persistent_grid(kern, a.blocks, 0, threads), threads, 0, s>>>(a);
+            return after_launch(what);
+        };
         if (a.dv <= 1024u) return go(zk::norm_grad_kernel<F, E, 2, 4>, 2);
-        go(zk::norm_grad_kernel<F, E, 16 / E, 1>, 16 / E);
+        return go(zk::norm_grad_kernel<F, E, 16 / E, 1>, 16 / E);
     }
 }
 
@@ -886,8 +1278,8 @@ extern "C" zero_status_t zero_layer_norm_workspace(int64_t rows, int64_t d, int6
     const zero_status_t rc = check_norm("zero_layer_norm_workspace", rows, d);
     if (rc != ZERO_OK) return rc;
     if (!bytes) return fail(ZERO_ERR_INVALID, "zero_layer_norm_workspace: NULL bytes");
-    const int64_t per = norm_rows_per_block(rows);
-    *bytes = ((rows + per - 1) / per * 2 * d * 4 + 255) / 256 * 256 + 256;
+    const int64_t per = norm_rows_per_block(rows, false), ring = norm_rows_per_block(rows, true);
+    *bytes = (std::max((rows + per - 1) / per, (rows + ring - 1) / ring) * 2 * d * 4 + 255) / 256 * 256 + 256;
     return ZERO_OK;
 }
 
@@ -940,16 +1332,15 @@ extern "C" zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy
     a.rows = rows;
     a.gy_stride = gy_stride;
     a.x_stride = x_stride;
-    a.per_block = norm_rows_per_block(rows);
+    a.per_block = norm_rows_per_block(rows, e * size == 16);
     a.blocks = (int32_t)((rows + a.per_block - 1) / a.per_block);
     a.d = (uint32_t)d;
     a.dv = (uint32_t)(d / e);
     a.accumulate = accumulate != 0;
-    ZL_DISPATCH(dtype, e, launch_norm_grad<T, E>(a, s));
-    if ((rc = after_launch(what)) != ZERO_OK) return rc;
-    const int join = capped(2 * ((d + 31) / 32));
-    if (grad_dtype == ZERO_FP32) zk::norm_join_kernel<zk::Fp32><<<join, 1024, 0, s>>>(a);
-    else if (grad_dtype == ZERO_BF16) zk::norm_join_kernel<zk::Bf16><<<join, 1024, 0, s>>>(a);
-    else zk::norm_join_kernel<zk::Fp16><<<join, 1024, 0, s>>>(a);
-    return after_launch(what);
+    ZL_DISPATCH(dtype, e, rc = (launch_norm_grad<T, E>(a, s, what)));
+    if (rc != ZERO_OK) return rc;
+    const dim3 join((unsigned)capped(2 * ((d + 31) / 32)));
+    if (grad_dtype == ZERO_FP32) return launch_after(zk::norm_join_kernel<zk::Fp32>, join, 1024, 0, s, what, a);
+    if (grad_dtype == ZERO_BF16) return launch_after(zk::norm_join_kernel<zk::Bf16>, join, 1024, 0, s, what, a);
+    return launch_after(zk::norm_join_kernel<zk::Fp16>, join, 1024, 0, s, what, a);
 }

@@ -21,15 +21,20 @@ place are contiguous.  Formulas, ranges and what happens at their edges:
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional, Tuple, Union
 
 import torch
 
 from . import binding as B
 from .multi import _GRAD as DTYPE
-from .multi import _device, _raw_stream
+from .multi import _current_device, _raw_stream
+
+_FP32 = torch.float32
 
 
+# A short call costs the host more than the GPU: each function looks at its arguments in one condition, and only where
+# that does not hold says which one is wrong.
 def _shape(t: torch.Tensor) -> str:
     return "x".join(map(str, t.shape)) or "scalar"
 
@@ -41,12 +46,9 @@ def _check_on(device: torch.device, **tensors) -> None:
             raise ValueError("%s is on %s: the call's tensors are on one CUDA device" % (name, t.device))
 
 
-def _check_dtype(name: str, t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> None:
-    if dtype is None:
-        if t.dtype not in DTYPE:
-            raise ValueError("%s: dtype %s (need %s)" % (name, t.dtype, "/".join(map(str, DTYPE))))
-    elif t.dtype != dtype:
-        raise ValueError("%s: dtype %s (need %s)" % (name, t.dtype, dtype))
+def _check_dtype(name: str, t: torch.Tensor, *dtypes: torch.dtype) -> None:
+    if t.dtype not in (dtypes or DTYPE):
+        raise ValueError("%s: dtype %s (need %s)" % (name, t.dtype, " or ".join(map(str, dtypes or DTYPE))))
 
 
 def _check_weight(name: str, t: torch.Tensor, shape) -> None:
@@ -56,23 +58,9 @@ def _check_weight(name: str, t: torch.Tensor, shape) -> None:
         raise ValueError("%s is not contiguous" % name)
 
 
-def _check_grad(name: str, t: torch.Tensor, shape, dtype: torch.dtype) -> None:
-    _check_weight(name, t, shape)
-    if t.dtype != dtype and t.dtype != torch.float32:
-        raise ValueError("%s: dtype %s (need %s or torch.float32)" % (name, t.dtype, dtype))
-
-
-def _rows(t: torch.Tensor, d: int) -> Tuple[torch.Tensor, int]:
-    """(t as rows of d, elements between rows); a copy where t is not evenly
-    spaced rows of contiguous elements."""
-    if t.dim() != 2:
-        t = t.reshape(-1, d)
-    if t.is_contiguous() or t.shape[0] == 0:
-        return t, d
-    stride = d if t.shape[0] <= 1 else t.stride(0)
-    if (d > 1 and t.stride(1) != 1) or stride < d:
-        return t.contiguous(), d
-    return t, stride
+def _check_dims(name: str, t: torch.Tensor, dims: int) -> None:
+    if t.dim() != dims:
+        raise ValueError("%s: shape %s (need %s)" % (name, _shape(t), "vocab x d" if dims == 2 else "one dimension"))
 
 
 def _check_last(name: str, t: torch.Tensor, d: int) -> None:
@@ -80,13 +68,27 @@ def _check_last(name: str, t: torch.Tensor, d: int) -> None:
         raise ValueError("%s: shape %s (need %d in the last dimension)" % (name, _shape(t), d))
 
 
-def _check_ids(name: str, ids: torch.Tensor) -> None:
-    if ids.dtype != torch.int64:
-        raise ValueError("%s: dtype %s (need torch.int64)" % (name, ids.dtype))
+def _like(t: Optional[torch.Tensor], shape, dtype, index) -> bool:
+    return t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous())
 
 
-def _bytes(n: int, device) -> torch.Tensor:
-    return torch.empty(n, dtype=torch.uint8, device=device)
+def _rows(t: torch.Tensor, d: int) -> Tuple[torch.Tensor, int]:
+    """(t as rows of d, elements between rows); a copy where t is not evenly
+    spaced rows of contiguous elements."""
+    if t.is_contiguous():
+        return t, d
+    if t.dim() != 2:
+        t = t.reshape(-1, d)
+        if t.is_contiguous():
+            return t, d
+    stride = d if t.shape[0] <= 1 else t.stride(0)
+    if (d > 1 and t.stride(1) != 1) or stride < d:
+        return t.contiguous(), d
+    return t, stride
+
+
+_embedding_workspace = lru_cache(maxsize=256)(B.zero_embedding_workspace)
+_norm_workspace = lru_cache(maxsize=256)(B.zero_layer_norm_workspace)
 
 
 def _no_capture(*tensors) -> None:
@@ -102,18 +104,24 @@ def embedding_forward(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.
     """``scale * weight[ids]``: weight [vocab, d], ids int64 of any shape; a
     new tensor of ids' shape with d behind it.  An id outside 0 .. vocab-1
     (padding) gives zeros."""
-    if weight.dim() != 2:
-        raise ValueError("weight: shape %s (need vocab x d)" % _shape(weight))
-    _check_weight("weight", weight, weight.shape)
-    _check_dtype("weight", weight)
-    _check_ids("ids", ids)
-    dev = weight.device
-    _check_on(dev, weight=weight, ids=ids)
+    index, code = weight.get_device(), DTYPE.get(weight.dtype)
+    if not (index >= 0 and code is not None and weight.dim() == 2 and weight.is_contiguous() and ids.dtype is torch.int64 and
+            ids.get_device() == index):
+        _check_dims("weight", weight, 2)
+        _check_weight("weight", weight, weight.shape)
+        _check_dtype("weight", weight)
+        _check_dtype("ids", ids, torch.int64)
+        _check_on(weight.device, weight=weight, ids=ids)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return embedding_forward(weight, ids, scale)
     vocab, d = weight.shape
-    with _device(dev.index):
-        flat = ids.contiguous()
-        out = torch.empty((*ids.shape, d), dtype=weight.dtype, device=dev)
-        B.zero_embedding_forward(weight, flat, vocab, d, flat.numel(), DTYPE[weight.dtype], scale, out, _raw_stream(dev.index))
+    flat = ids.contiguous()
+    out = weight.new_empty((*ids.shape, d))
+    status = B.lib().zero_embedding_forward(weight.data_ptr(), flat.data_ptr(), vocab, d, flat.numel(), code, scale,
+                                            out.data_ptr(), _raw_stream(index))
+    if status:
+        B._check(status)
     return out
 
 
@@ -123,21 +131,30 @@ def embedding_backward(grad_out: torch.Tensor, ids: torch.Tensor, grad_weight: t
     or float32): row k gets ``scale`` times the sum of the rows of
     ``grad_out`` whose id is k, the others zeros; with ``accumulate`` that is
     added to what is there.  The same inputs give the same bits."""
-    if grad_weight.dim() != 2:
-        raise ValueError("grad_weight: shape %s (need vocab x d)" % _shape(grad_weight))
+    index, dtype = grad_weight.get_device(), grad_out.dtype
+    code, to = DTYPE.get(dtype), grad_weight.dtype
+    if not (index >= 0 and code is not None and grad_weight.dim() == 2 and grad_weight.is_contiguous() and
+            (to is dtype or to is _FP32) and ids.dtype is torch.int64 and ids.get_device() == index and
+            grad_out.get_device() == index and grad_out.shape == (*ids.shape, grad_weight.shape[1])):
+        _check_dims("grad_weight", grad_weight, 2)
+        _check_dtype("grad_out", grad_out)
+        _check_weight("grad_weight", grad_weight, grad_weight.shape)
+        _check_dtype("grad_weight", grad_weight, dtype, _FP32)
+        _check_dtype("ids", ids, torch.int64)
+        if tuple(grad_out.shape) != (*ids.shape, grad_weight.shape[1]):
+            raise ValueError("grad_out: shape %s (need %s)" % (_shape(grad_out), "x".join(map(str, (*ids.shape, grad_weight.shape[1])))))
+        _check_on(grad_weight.device, grad_weight=grad_weight, grad_out=grad_out, ids=ids)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return embedding_backward(grad_out, ids, grad_weight, scale, accumulate)
     vocab, d = grad_weight.shape
-    _check_dtype("grad_out", grad_out)
-    _check_grad("grad_weight", grad_weight, grad_weight.shape, grad_out.dtype)
-    _check_ids("ids", ids)
-    if tuple(grad_out.shape) != (*ids.shape, d):
-        raise ValueError("grad_out: shape %s (need %s)" % (_shape(grad_out), "x".join(map(str, (*ids.shape, d)))))
-    dev = grad_weight.device
-    _check_on(dev, grad_weight=grad_weight, grad_out=grad_out, ids=ids)
-    with _device(dev.index):
-        g, flat = grad_out.contiguous(), ids.contiguous()
-        ws = _bytes(B.zero_embedding_workspace(vocab, d, flat.numel()), dev)
-        B.zero_embedding_backward(g, flat, vocab, d, flat.numel(), DTYPE[g.dtype], DTYPE[grad_weight.dtype], scale,
-                                  accumulate, grad_weight, ws, _raw_stream(dev.index))
+    g, flat = grad_out.contiguous(), ids.contiguous()
+    n = flat.numel()
+    ws = torch.empty(_embedding_workspace(vocab, d, n), dtype=torch.uint8, device=index)
+    status = B.lib().zero_embedding_backward(g.data_ptr(), flat.data_ptr(), vocab, d, n, code, DTYPE[to], scale, 1 if accumulate else 0,
+                                             grad_weight.data_ptr(), ws.data_ptr(), _raw_stream(index))
+    if status:
+        B._check(status)
     return grad_weight
 
 
@@ -168,24 +185,29 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
     """(y, mean, rstd): ``y = (x - mean) * rstd * weight + bias`` over the last
     dimension; mean and rstd are float32, one per row, for
     :func:`layer_norm_backward`.  All tensors have one dtype."""
-    _check_dtype("x", x)
-    if weight.dim() != 1:
-        raise ValueError("weight: shape %s (need one dimension)" % _shape(weight))
-    d = weight.shape[0]
-    _check_last("x", x, d)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _check_weight(name, t, (d,))
-            _check_dtype(name, t, x.dtype)
-    dev = x.device
-    _check_on(dev, x=x, weight=weight, bias=bias)
-    with _device(dev.index):
-        rows, stride = _rows(x, d)
-        n = rows.shape[0]
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
-        mean, rstd = stats[0], stats[1]
-        B.zero_layer_norm_forward(rows, stride, weight, bias, n, d, DTYPE[x.dtype], eps, y, mean, rstd, _raw_stream(dev.index))
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    code, per_row, last = DTYPE.get(dtype), shape[:-1], shape[-1:]
+    if not (index >= 0 and code is not None and len(last) == 1 and _like(weight, last, dtype, index) and _like(bias, last, dtype, index)):
+        _check_dtype("x", x)
+        _check_dims("weight", weight, 1)
+        _check_last("x", x, weight.shape[0])
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None:
+                _check_weight(name, t, last)
+                _check_dtype(name, t, dtype)
+        _check_on(x.device, x=x, weight=weight, bias=bias)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return layer_norm_forward(x, weight, bias, eps)
+    d = last[0]
+    rows, stride = _rows(x, d)
+    y = x.new_empty(shape)
+    mean, rstd = x.new_empty(per_row, dtype=_FP32), x.new_empty(per_row, dtype=_FP32)
+    status = B.lib().zero_layer_norm_forward(rows.data_ptr(), stride, weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                                             mean.numel(), d, code, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                             _raw_stream(index))
+    if status:
+        B._check(status)
     return y, mean, rstd
 
 
@@ -196,35 +218,43 @@ def layer_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Ten
     ``grad_weight`` and ``grad_bias`` [d] (x's dtype or float32, one for both),
     overwritten or, with ``accumulate``, added to.  mean and rstd are
     :func:`layer_norm_forward`'s."""
-    _check_dtype("x", x)
-    _check_dtype("grad_y", grad_y, x.dtype)
-    if weight.dim() != 1:
-        raise ValueError("weight: shape %s (need one dimension)" % _shape(weight))
-    d = weight.shape[0]
-    _check_last("x", x, d)
-    if grad_y.shape != x.shape:
-        raise ValueError("grad_y: shape %s (need %s)" % (_shape(grad_y), _shape(x)))
-    _check_weight("weight", weight, (d,))
-    _check_dtype("weight", weight, x.dtype)
-    _check_grad("grad_weight", grad_weight, (d,), x.dtype)
-    if grad_bias is not None:
-        _check_grad("grad_bias", grad_bias, (d,), x.dtype)
-        if grad_bias.dtype != grad_weight.dtype:
-            raise ValueError("grad_bias: dtype %s (need grad_weight's %s)" % (grad_bias.dtype, grad_weight.dtype))
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _check_weight(name, t, x.shape[:-1])
-        _check_dtype(name, t, torch.float32)
-    dev = x.device
-    _check_on(dev, x=x, grad_y=grad_y, weight=weight, mean=mean, rstd=rstd, grad_weight=grad_weight, grad_bias=grad_bias)
-    with _device(dev.index):
-        rows, stride = _rows(x, d)
-        g, g_stride = _rows(grad_y, d)
-        n = rows.shape[0]
-        grad_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        ws = _bytes(B.zero_layer_norm_workspace(n, d), dev)
-        B.zero_layer_norm_backward(g, g_stride, rows, stride, weight, mean, rstd, n, d, DTYPE[x.dtype],
-                                   DTYPE[grad_weight.dtype], accumulate, grad_x, grad_weight, grad_bias, ws,
-                                   _raw_stream(dev.index))
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    code, per_row, last, to = DTYPE.get(dtype), shape[:-1], shape[-1:], grad_weight.dtype
+    if not (index >= 0 and code is not None and len(last) == 1 and grad_y.shape == shape and grad_y.dtype is dtype and
+            grad_y.get_device() == index and _like(weight, last, dtype, index) and (to is dtype or to is _FP32) and
+            _like(grad_weight, last, to, index) and _like(grad_bias, last, to, index) and _like(mean, per_row, _FP32, index) and
+            _like(rstd, per_row, _FP32, index)):
+        _check_dtype("x", x)
+        _check_dtype("grad_y", grad_y, dtype)
+        _check_dims("weight", weight, 1)
+        _check_last("x", x, weight.shape[0])
+        if grad_y.shape != shape:
+            raise ValueError("grad_y: shape %s (need %s)" % (_shape(grad_y), _shape(x)))
+        _check_weight("weight", weight, last)
+        _check_dtype("weight", weight, dtype)
+        _check_weight("grad_weight", grad_weight, last)
+        _check_dtype("grad_weight", grad_weight, dtype, _FP32)
+        if grad_bias is not None:
+            _check_weight("grad_bias", grad_bias, last)
+            _check_dtype("grad_bias", grad_bias, to)
+        for name, t in (("mean", mean), ("rstd", rstd)):
+            _check_weight(name, t, per_row)
+            _check_dtype(name, t, _FP32)
+        _check_on(x.device, x=x, grad_y=grad_y, weight=weight, mean=mean, rstd=rstd, grad_weight=grad_weight, grad_bias=grad_bias)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return layer_norm_backward(grad_y, x, weight, mean, rstd, grad_weight, grad_bias, accumulate)
+    d, n = last[0], mean.numel()
+    rows, stride = _rows(x, d)
+    g, g_stride = _rows(grad_y, d)
+    grad_x = x.new_empty(shape)
+    ws = torch.empty(_norm_workspace(n, d), dtype=torch.uint8, device=index)
+    status = B.lib().zero_layer_norm_backward(g.data_ptr(), g_stride, rows.data_ptr(), stride, weight.data_ptr(), mean.data_ptr(),
+                                              rstd.data_ptr(), n, d, code, DTYPE[to], 1 if accumulate else 0, grad_x.data_ptr(),
+                                              grad_weight.data_ptr(), None if grad_bias is None else grad_bias.data_ptr(),
+                                              ws.data_ptr(), _raw_stream(index))
+    if status:
+        B._check(status)
     return grad_x
 
 
@@ -253,27 +283,40 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
 
 # -- language-model head and loss ------------------------------------------------------------------------
 _REDUCTION = {"mean": B.ZERO_LOSS_MEAN, "sum": B.ZERO_LOSS_SUM}
+_LOSS_DTYPE = {torch.bfloat16: B.ZERO_BF16, torch.float16: B.ZERO_FP16}
 
 
-def _loss_args(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, piece: int):
-    """(checked arguments, the tensors that they point to)."""
-    if weight.dim() != 2:
-        raise ValueError("weight: shape %s (need vocab x d)" % _shape(weight))
+@lru_cache(maxsize=256)
+def _loss_workspace(n: int, d: int, vocab: int, dtype: int, piece: int, weight_at: int) -> Tuple[int, int]:
+    return B.zero_lm_loss_query(B.zero_lm_loss_args(n=n, d=d, vocab=vocab, hidden_stride=d, dtype=dtype, piece=piece, weight=256 + weight_at))
+
+
+def _check_loss(hidden, weight, targets) -> None:
+    _check_dims("weight", weight, 2)
     _check_weight("weight", weight, weight.shape)
-    if hidden.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("hidden: dtype %s (need torch.bfloat16 or torch.float16)" % hidden.dtype)
+    _check_dtype("hidden", hidden, *_LOSS_DTYPE)
     _check_dtype("weight", weight, hidden.dtype)
-    _check_ids("targets", targets)
-    vocab, d = weight.shape
-    _check_last("hidden", hidden, d)
+    _check_dtype("targets", targets, torch.int64)
+    _check_last("hidden", hidden, weight.shape[1])
     if hidden.shape[:-1] != targets.shape:
         raise ValueError("targets: shape %s (need %s)" % (_shape(targets), "x".join(map(str, hidden.shape[:-1]))))
     _check_on(weight.device, weight=weight, hidden=hidden, targets=targets)
+
+
+def _loss_args(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, piece: int = 0):
+    """(arguments without outputs, their workspaces' sizes, tensors that they point to)."""
+    index, dtype = weight.get_device(), hidden.dtype
+    code = _LOSS_DTYPE.get(dtype)
+    if not (index >= 0 and code is not None and weight.dtype is dtype and weight.dim() == 2 and weight.is_contiguous() and
+            targets.dtype is torch.int64 and hidden.get_device() == index and targets.get_device() == index and
+            hidden.shape == (*targets.shape, weight.shape[1])):
+        _check_loss(hidden, weight, targets)
+    vocab, d = weight.shape
     rows, stride = _rows(hidden, d)
     flat = targets.contiguous()
-    a = B.zero_lm_loss_args(n=rows.shape[0], d=d, vocab=vocab, hidden_stride=stride, dtype=DTYPE[hidden.dtype], piece=piece,
-                            hidden=rows.data_ptr(), weight=weight.data_ptr(), targets=flat.data_ptr(), scale=1.0)
-    return a, (rows, flat)
+    n, at = flat.numel(), weight.data_ptr()
+    a = B.zero_lm_loss_args(n, d, vocab, stride, code, 0, piece, rows.data_ptr(), at, flat.data_ptr(), scale=1.0)
+    return a, _loss_workspace(n, d, vocab, code, piece, at & 255), (rows, flat)
 
 
 def lm_loss_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, reduction: str = "mean"):
@@ -286,16 +329,20 @@ def lm_loss_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.T
     :func:`lm_loss_backward`."""
     if reduction not in _REDUCTION:
         raise ValueError("reduction must be 'mean' or 'sum'")
-    dev = weight.device
-    a, keep = _loss_args(hidden, weight, targets, 0)
-    with _device(dev.index):
-        out = torch.empty((2, *targets.shape), dtype=torch.float32, device=dev)
-        stats = torch.empty(2, dtype=torch.float32, device=dev)
-        ws = _bytes(B.zero_lm_loss_query(a)[0], dev)
-        a.reduction = _REDUCTION[reduction]
-        a.losses, a.lse, a.stats, a.workspace = out[0].data_ptr(), out[1].data_ptr(), stats.data_ptr(), ws.data_ptr()
-        B.zero_lm_loss_forward(a, _raw_stream(dev.index))
-    return stats[0], out[0], (out[1], stats)
+    a, (need, _), keep = _loss_args(hidden, weight, targets)
+    index = weight.get_device()
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return lm_loss_forward(hidden, weight, targets, reduction)
+    losses, lse = (hidden.new_empty(targets.shape, dtype=_FP32) for _ in range(2))
+    stats = hidden.new_empty(2, dtype=_FP32)
+    ws = torch.empty(need, dtype=torch.uint8, device=index)
+    a.reduction = _REDUCTION[reduction]
+    a.losses, a.lse, a.stats, a.workspace = losses.data_ptr(), lse.data_ptr(), stats.data_ptr(), ws.data_ptr()
+    status = B.lib().zero_lm_loss_forward(a, _raw_stream(index))
+    if status:
+        B._check(status)
+    return stats[0], losses, (lse, stats)
 
 
 def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, saved,
@@ -308,31 +355,36 @@ def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
     kernels run: a loss scale (``MultiAdamW.state_fields()["loss_scale"]``,
     ``ZeroStep.loss_scale``) or the gradient of ``loss``.  ``piece`` columns of
     the vocabulary are in memory at a time (0: chosen)."""
-    dev = weight.device
-    a, keep = _loss_args(hidden, weight, targets, piece)
-    lse, stats = saved
-    _check_weight("saved[0]", lse, targets.shape)
-    _check_weight("saved[1]", stats, (2,))
-    for name, t in (("saved[0]", lse), ("saved[1]", stats)):
-        _check_dtype(name, t, torch.float32)
-    if grad_weight is not None:
-        _check_weight("grad_weight", grad_weight, weight.shape)
-        _check_dtype("grad_weight", grad_weight, weight.dtype)
-    if isinstance(scale, torch.Tensor):
-        if scale.dtype != torch.float32 or scale.numel() != 1:
-            raise ValueError("scale: a number or a float32 tensor of one element")
+    a, (_, need), keep = _loss_args(hidden, weight, targets, piece)
+    index, (lse, stats) = weight.get_device(), saved
+    by_tensor = isinstance(scale, torch.Tensor)
+    if by_tensor and (scale.dtype is not _FP32 or scale.numel() != 1):
+        raise ValueError("scale: a number or a float32 tensor of one element")
+    if not (_like(lse, targets.shape, _FP32, index) and _like(stats, (2,), _FP32, index) and
+            _like(grad_weight, weight.shape, weight.dtype, index) and (not by_tensor or scale.get_device() == index)):
+        for name, t, shape in (("saved[0]", lse, targets.shape), ("saved[1]", stats, (2,))):
+            _check_weight(name, t, shape)
+            _check_dtype(name, t, _FP32)
+        if grad_weight is not None:
+            _check_weight("grad_weight", grad_weight, weight.shape)
+            _check_dtype("grad_weight", grad_weight, weight.dtype)
+        _check_on(weight.device, lse=lse, stats=stats, grad_weight=grad_weight, scale=scale if by_tensor else None)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return lm_loss_backward(hidden, weight, targets, saved, grad_weight, scale, accumulate, need_hidden, piece)
+    grad_hidden = hidden.new_empty(hidden.shape) if need_hidden else None
+    ws = torch.empty(need, dtype=torch.uint8, device=index)
+    if by_tensor:
         a.scale_dev = scale.data_ptr()
     else:
         a.scale = scale
-    _check_on(dev, lse=lse, stats=stats, grad_weight=grad_weight, scale=scale if isinstance(scale, torch.Tensor) else None)
-    with _device(dev.index):
-        grad_hidden = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev) if need_hidden else None
-        ws = _bytes(B.zero_lm_loss_query(a)[1], dev)
-        a.lse, a.stats, a.workspace = lse.data_ptr(), stats.data_ptr(), ws.data_ptr()
-        a.grad_hidden = grad_hidden.data_ptr() if need_hidden else None
-        a.grad_weight = grad_weight.data_ptr() if grad_weight is not None else None
-        a.accumulate = int(bool(accumulate))
-        B.zero_lm_loss_backward(a, _raw_stream(dev.index))
+    a.lse, a.stats, a.workspace = lse.data_ptr(), stats.data_ptr(), ws.data_ptr()
+    a.grad_hidden = grad_hidden.data_ptr() if need_hidden else None
+    a.grad_weight = grad_weight.data_ptr() if grad_weight is not None else None
+    a.accumulate = 1 if accumulate else 0
+    status = B.lib().zero_lm_loss_backward(a, _raw_stream(index))
+    if status:
+        B._check(status)
     return grad_hidden
 
 
