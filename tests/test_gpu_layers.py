@@ -108,10 +108,10 @@ def test_embedding_backward(vocab, d, n, dtype, shift, fp32_grad):
         assert torch.equal(L.embedding_backward(go, ids, gw, scale=0.75), first), cap
 
 
-@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 8192, 8193, 50001])
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 2048, 2049, 8192, 8193, 50001, 98304, 98305, 200003])
 @pytest.mark.parametrize("kind", ["one id", "none", "two alternating", "sorted", "each once"])
 def test_embedding_backward_token_orders(n, kind):
-    vocab = 70000
+    vocab = max(70000, n)
     go = torch.randn(n, 24, generator=gen(3), device="cuda")
     i = torch.arange(n, device="cuda")
     ids = {"one id": torch.full((n,), 69999, device="cuda"), "none": torch.full((n,), -100, device="cuda"),

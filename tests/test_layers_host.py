@@ -193,7 +193,6 @@ def test_loss_struct_matches_the_header(tmp_path):
 
 
 H, HW = torch.zeros(3, 4, dtype=torch.bfloat16), torch.zeros(10, 4, dtype=torch.bfloat16)
-SAVED = (torch.zeros(3), torch.zeros(2))
 
 
 @pytest.mark.parametrize("call,word", [

@@ -75,12 +75,6 @@ struct Raw {
             else w[0] = __ldg(p);
         }
     }
-    // from shared memory, 16 bytes
-    __device__ __forceinline__ void load_shared(const uint8_t* p) {
-        static_assert(kWords == 4, "16 bytes");
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    }
     __device__ __forceinline__ void get(float (&o)[E]) const {
         if constexpr (sizeof(S) == 4) {
 #pragma unroll
@@ -207,8 +201,12 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
 // 8-bit digits by one thread-block cluster, whose CTAs exchange their digit
 // counts through distributed shared memory; an id outside the vocabulary
 // becomes `vocab` and sorts behind all others.  The clusters behind the first
-// zero the gradient meanwhile.
+// zero the gradient meanwhile.  SHARED: the pairs stay in the cluster's shared
+// memory between the passes; under the zeroing's traffic a trip to memory takes
+// 2 us, and a pass of the other form, for more tokens than that holds, makes
+// three.
 constexpr int kSortThreads = 1024;
+constexpr uint32_t kPairsPad = 16;   // entries behind the pairs, which are read 4 at a time and 4 ahead
 constexpr int kSortWarps = kSortThreads / 32;
 
 struct SortArgs {
@@ -218,98 +216,140 @@ struct SortArgs {
     int64_t zero_bytes;
     int64_t vocab;
     uint32_t n;
+    uint32_t per_warp;   // tokens of a warp, next to one another: a multiple of 32
     int32_t passes;
 };
 
-__device__ __forceinline__ uint64_t sort_pair(const SortArgs& a, int pass, uint32_t i) {
-    if (pass > 0) return a.pairs[pass & 1][i];
+__device__ __forceinline__ uint64_t id_pair(const SortArgs& a, uint32_t i) {
     const int64_t id = __ldg(a.ids + i);
     const uint64_t key = id >= 0 && id < a.vocab ? (uint64_t)id : (uint64_t)a.vocab;
     return key << 32 | i;
 }
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ SortArgs a) {
-    __shared__ uint32_t counts[kSortWarps][256];  // of a digit in a warp's tokens; then where the next one goes
-    __shared__ uint32_t total[256];               // of a digit in this CTA's tokens
-    __shared__ uint32_t scan[256];
+    extern __shared__ __align__(16) uint64_t held[];   // SHARED: [2][pairs of a CTA]
+    __shared__ __align__(128) uint32_t counts[kSortWarps][256];  // of a digit in a warp's tokens; then where the next one goes
+    __shared__ uint32_t total[256];                    // of a digit in this CTA's tokens
+    __shared__ uint32_t warp_total[8];
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ctas = cluster.num_blocks(), rank = cluster.block_rank();
-    if (blockIdx.x >= ctas) {  // zero the gradient: bytes to a 16-byte boundary, vectors, bytes
+    if (blockIdx.x >= ctas) {  // zero the gradient: bytes to a 16-byte boundary, 32 KB of zeros over and over, bytes
         const int64_t t = (int64_t)(blockIdx.x - ctas) * kSortThreads + threadIdx.x;
-        const int64_t step = (int64_t)(gridDim.x - ctas) * kSortThreads;
         const int64_t head = min(a.zero_bytes, (int64_t)(-reinterpret_cast<intptr_t>(a.zero) & 15));
-        const int64_t vecs = (a.zero_bytes - head) / 16;
-        uint4* v = reinterpret_cast<uint4*>(a.zero + head);
-        for (int64_t i = t; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
+        const int64_t whole = (a.zero_bytes - head) / 16 * 16, tail = head + whole;
         if (t < head) a.zero[t] = 0;
-        if (head + vecs * 16 + t < a.zero_bytes) a.zero[head + vecs * 16 + t] = 0;   // fewer than 16
+        if (tail + t < a.zero_bytes) a.zero[tail + t] = 0;   // fewer than 16
+        for (uint32_t i = threadIdx.x; i < kSortWarps * 256; i += kSortThreads) counts[0][i] = 0;
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int64_t at = (int64_t)(blockIdx.x - ctas) * (int64_t)sizeof counts; at < whole; at += (int64_t)(gridDim.x - ctas) * (int64_t)sizeof counts)
+                bulk_s2g(a.zero + head + at, counts, (uint32_t)min(whole - at, (int64_t)sizeof counts));
+            bulk_commit();
+            bulk_wait_all<0>();
+        }
         return;
     }
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    // each warp has a contiguous stretch of whole 32s
-    const uint64_t per_warp = (((uint64_t)a.n + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
-    const uint32_t w0 = (uint32_t)min((uint64_t)a.n, (rank * kSortWarps + warp) * per_warp);
-    const uint32_t w1 = (uint32_t)min((uint64_t)a.n, w0 + per_warp);
+    if (rank == 0 && threadIdx.x < kPairsPad) a.pairs[a.passes & 1][(uint64_t)a.n + threadIdx.x] = ~0ull;
+    const uint32_t per_cta = kSortWarps * a.per_warp, cta0 = rank * per_cta;   // at most n + 2^15
+    const uint32_t w0 = min(a.n, cta0 + warp * a.per_warp), w1 = min(a.n, w0 + a.per_warp);
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = 32 + 8 * pass;
+        uint64_t* mine = held + (SHARED ? (size_t)(pass & 1) * per_cta : 0);
+        // 8 of a lane's pairs at a time: the counter and the ranks below go one after another
+        const auto load8 = [&](uint32_t i0, uint64_t (&p)[8]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t i = i0 + k * 32 + lane;
+                p[k] = i >= w1 ? 0 : pass == 0 ? id_pair(a, i) : SHARED ? mine[i - cta0] : a.pairs[pass & 1][i];
+            }
+        };
         for (uint32_t d = lane; d < 256; d += 32) counts[warp][d] = 0;
         __syncwarp();
-        for (uint32_t i = w0 + lane; i < w1; i += 32) atomicAdd(&counts[warp][(sort_pair(a, pass, i) >> shift) & 255], 1u);
+        uint64_t p[8];
+        for (uint32_t i0 = w0; i0 < w1; i0 += 256) {
+            load8(i0, p);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + k * 32 + lane < w1) atomicAdd(&counts[warp][(p[k] >> shift) & 255], 1u);
+        }
         __syncthreads();
-        uint32_t mine = 0;
         if (threadIdx.x < 256) {
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = counts[w][threadIdx.x];
-                counts[w][threadIdx.x] = mine;
-                mine += c;
-            }
-            total[threadIdx.x] = mine;
+            uint32_t in_cta = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) in_cta += counts[w][threadIdx.x];
+            total[threadIdx.x] = in_cta;
         }
         cluster.sync();
-        uint32_t before = 0, all = 0;  // of this digit in the CTAs before this one, and in all
+        uint32_t before = 0, all = 0, scan = 0;  // of this digit in the CTAs before this one, and in all; of the digits up to it
         if (threadIdx.x < 256) {
-            for (uint32_t r = 0; r < ctas; ++r) {
-                const uint32_t c = cluster.map_shared_rank(total, r)[threadIdx.x];
+#pragma unroll
+            for (uint32_t r = 0; r < 8; ++r) {   // ctas is 8 at most
+                const uint32_t c = r < ctas ? cluster.map_shared_rank(total, r)[threadIdx.x] : 0;
                 before += r < rank ? c : 0;
                 all += c;
             }
-            scan[threadIdx.x] = all;
-        }
-        __syncthreads();
-        for (int s = 1; s < 256; s <<= 1) {
-            const uint32_t x = threadIdx.x < 256 && threadIdx.x >= (uint32_t)s ? scan[threadIdx.x - s] : 0;
-            __syncthreads();
-            if (threadIdx.x < 256) scan[threadIdx.x] += x;
-            __syncthreads();
-        }
-        if (threadIdx.x < 256) {
-            const uint32_t base = scan[threadIdx.x] - all + before;
-            for (int w = 0; w < kSortWarps; ++w) counts[w][threadIdx.x] += base;
-        }
-        __syncthreads();
-        uint64_t* out = a.pairs[(pass + 1) & 1];
-        for (uint32_t i0 = w0; i0 < w1; i0 += 32) {  // in order: equal digits keep theirs
-            const uint32_t i = i0 + lane;
-            const bool on = i < w1;
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, on);
-            if (on) {
-                const uint64_t p = sort_pair(a, pass, i);
-                const uint32_t digit = (p >> shift) & 255;
-                const uint32_t same = __match_any_sync(live, digit);
-                const uint32_t at = counts[warp][digit];
-                __syncwarp(live);
-                if (lane == (uint32_t)(__ffs(same) - 1)) counts[warp][digit] = at + __popc(same);
-                out[at + __popc(same & ((1u << lane) - 1))] = p;
+            scan = all;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, scan, s);
+                if (lane >= (uint32_t)s) scan += x;
             }
-            __syncwarp();
+            if (lane == 31) warp_total[warp] = scan;
+        }
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            uint32_t base = scan - all + before;
+#pragma unroll
+            for (uint32_t w = 0; w < 8; ++w) base += w < warp ? warp_total[w] : 0;
+#pragma unroll
+            for (int w0 = 0; w0 < kSortWarps; w0 += 16) {   // loads before stores, which the compiler keeps in order
+                uint32_t c[16];
+#pragma unroll
+                for (int w = 0; w < 16; ++w) c[w] = counts[w0 + w][threadIdx.x];
+#pragma unroll
+                for (int w = 0; w < 16; ++w) {
+                    counts[w0 + w][threadIdx.x] = base;
+                    base += c[w];
+                }
+            }
+        }
+        __syncthreads();
+        const bool to_memory = !SHARED || pass + 1 == a.passes;
+        uint64_t* out = a.pairs[(pass + 1) & 1];
+        for (uint32_t i0 = w0; i0 < w1; i0 += 256) {  // in order: equal digits keep theirs
+            if (i0 > w0 || a.per_warp > 256) load8(i0, p);   // else they are there from the count
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool on = i0 + k * 32 + lane < w1;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, on);
+                if (on) {
+                    const uint32_t digit = (p[k] >> shift) & 255;
+                    const uint32_t same = __match_any_sync(live, digit);
+                    const uint32_t at = counts[warp][digit];
+                    __syncwarp(live);
+                    if (lane == (uint32_t)(__ffs(same) - 1)) counts[warp][digit] = at + __popc(same);
+                    const uint32_t to = at + __popc(same & ((1u << lane) - 1));
+                    if (to_memory) {
+                        out[to] = p[k];
+                    } else {
+                        const uint32_t cta = to / per_cta;
+                        uint64_t* there = cluster.map_shared_rank(held, cta);
+                        there[(size_t)((pass + 1) & 1) * per_cta + (to - cta * per_cta)] = p[k];
+                    }
+                }
+                __syncwarp();
+            }
         }
         // the pairs, and the counts of all CTAs, before the next pass reads and overwrites them
-        __threadfence();
+        if (to_memory) __threadfence();
         cluster.sync();
     }
 }
 
-// The sorted tokens are cut into pieces of `piece`.  A group of threads adds
+// The sorted tokens are cut into pieces of `piece` (a multiple of 8).  Lanes add
 // the rows of a piece's tokens, id after id.  What begins and ends in the piece
 // is a gradient's row; what reaches into another piece goes into a binary32
 // row of its own (slot 0: it came from the piece before; slot 1: it begins
@@ -321,7 +361,6 @@ struct EmbedGradArgs {
     float* parts;  // [pieces][2][d]
     uint32_t n, pieces, d, dv, vocab;
     int32_t piece;
-    int32_t group;  // threads of a piece
     int32_t accumulate;
     float scale;
 };
@@ -335,110 +374,146 @@ __device__ __forceinline__ void embed_row(const EmbedGradArgs& a, uint32_t id, u
     st_e<O, E>(p, x);
 }
 
-template <class F, class O, int E>
-__global__ void __launch_bounds__(kThreads) embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
+// LANES lanes of a warp have a piece and as many of its columns: a whole warp
+// where rows are wide, so that warps of one piece are next to one another and
+// none waits for another.  4 rows are under way at a time in each of 32 warps: 8
+// rows in the 16 to 24 warps that their registers allow took 1.5 times as long.
+template <class F, class O, int E, int LANES>
+__global__ void __launch_bounds__(kThreads, 4) embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
     using S = typename Store<F>::S;
-    const uint32_t per_cta = kThreads / a.group;
-    const uint32_t lane = threadIdx.x % a.group;
+    const uint32_t lane = threadIdx.x & (LANES - 1);
+    const uint32_t slices = (a.dv + LANES - 1) / LANES;
+    const uint64_t items = (uint64_t)a.pieces * slices, step = (uint64_t)gridDim.x * (kThreads / LANES);
     grid_wait();
-    for (uint32_t q = blockIdx.x * per_cta + threadIdx.x / a.group; q < a.pieces; q += gridDim.x * per_cta) {
+    for (uint64_t item = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / LANES; item < items; item += step) {
+        const uint32_t q = (uint32_t)(item / slices), c = (uint32_t)(item - (uint64_t)q * slices) * LANES + lane;
         const uint32_t b = q * a.piece, e = min(a.n, b + a.piece);
+        const bool on = c < a.dv;
         const uint32_t id_before = b > 0 ? (uint32_t)(__ldg(a.pairs + b - 1) >> 32) : ~0u;
         const uint32_t id_after = e < a.n ? (uint32_t)(__ldg(a.pairs + e) >> 32) : ~0u;
-        for (uint32_t c = lane; c < a.dv; c += a.group) {
-            float sum[E] = {};
-            uint32_t id = (uint32_t)(__ldg(a.pairs + b) >> 32);
-            bool first = true;  // the piece's first id
-            auto flush = [&](uint32_t next) {
-                if (id < a.vocab) {
-                    const bool came = first && id == id_before, goes = next == id;
-                    if (came || goes) {
-                        float* p = a.parts + ((size_t)q * 2 + (came ? 0 : 1)) * a.d + (size_t)c * E;
+        // (position, id) of 4 tokens; behind the last one lie kPairsPad that are none
+        uint4 pairs[2];
 #pragma unroll
-                        for (int k = 0; k < E; ++k) p[k] = sum[k];
-                    } else {
-                        embed_row<F, O, E>(a, id, c, sum);
-                    }
+        for (int k = 0; k < 2; ++k) pairs[k] = __ldg(reinterpret_cast<const uint4*>(a.pairs + b) + k);
+        float sum[E] = {};
+        uint32_t id = pairs[0].y;
+        bool first = true;  // the piece's first id
+        const auto flush = [&](uint32_t next) {
+            if (on && id < a.vocab) {
+                const bool came = first && id == id_before, goes = next == id;
+                if (came || goes) {
+                    float* p = a.parts + ((size_t)q * 2 + (came ? 0 : 1)) * a.d + (size_t)c * E;
+#pragma unroll
+                    for (int k = 0; k < E; ++k) p[k] = sum[k];
+                } else {
+                    embed_row<F, O, E>(a, id, c, sum);
                 }
-                first = false;
-            };
-            for (uint32_t i = b; i < e; i += 8) {
-                uint64_t pair[8];
-                Raw<F, E> raw[8];
+            }
+            first = false;
+        };
+        const S* column = static_cast<const S*>(a.grad) + (on ? (size_t)c * E : 0);
+        for (uint32_t i = b; i < e; i += 4) {
+            Raw<F, E> raw[4];
+            uint32_t ids[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    pair[k] = i + k < e ? __ldg(a.pairs + i + k) : ~0ull;
+            for (int k = 0; k < 4; ++k) {
+                ids[k] = k & 1 ? pairs[k / 2].w : pairs[k / 2].y;
+                if (ids[k] < a.vocab) raw[k].load(column + (size_t)(k & 1 ? pairs[k / 2].z : pairs[k / 2].x) * a.d);
+            }
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if ((uint32_t)(pair[k] >> 32) < a.vocab)
-                        raw[k].load(static_cast<const S*>(a.grad) + (size_t)(uint32_t)pair[k] * a.d + (size_t)c * E);
+            for (int k = 0; k < 2; ++k) pairs[k] = __ldg(reinterpret_cast<const uint4*>(a.pairs + i + 4) + k);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t now = (uint32_t)(pair[k] >> 32);
-                    if (now < a.vocab) {
-                        float x[E];
-                        raw[k].get(x);
-                        if (now != id) {
-                            flush(now);
-                            id = now;
+            for (int k = 0; k < 4; ++k) {
+                if (ids[k] < a.vocab) {
+                    float x[E];
+                    raw[k].get(x);
+                    if (ids[k] != id) {
+                        flush(ids[k]);
+                        id = ids[k];
 #pragma unroll
-                            for (int j = 0; j < E; ++j) sum[j] = x[j];
-                        } else {
+                        for (int j = 0; j < E; ++j) sum[j] = x[j];
+                    } else if constexpr (E > 1) {
 #pragma unroll
-                            for (int j = 0; j < E; ++j) sum[j] = __fadd_rn(sum[j], x[j]);
-                        }
+                        for (int j = 0; j < E; j += 2) split(add2(f2(sum[j], sum[j + 1]), f2(x[j], x[j + 1])), sum[j], sum[j + 1]);
+                    } else {
+                        sum[0] = __fadd_rn(sum[0], x[0]);
                     }
                 }
             }
-            // behind the last row of an id in the vocabulary come only padding tokens, which flush nothing
-            flush(id_after);
         }
+        // behind the last row of an id in the vocabulary come only padding tokens, which flush nothing
+        flush(id_after);
     }
 }
 
 // Adds up the parts of an id whose rows begin in piece q and go on behind it:
-// slot 1 of q, slot 0 of the pieces after it.  The warps of a CTA take every
-// eighth part of 32 pieces of columns, and are added in order (the first token
-// of a Zipf-distributed text is in a hundred pieces).
+// slot 1 of q, slot 0 of the pieces after it.  A warp looks at a piece; what has
+// more than 8 parts is added by the CTA, a warp every eighth of them, and the
+// warps in order (the first token of a Zipf-distributed text is in a hundred
+// pieces).
 template <class F, class O, int E>
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedGradArgs a) {
-    constexpr int W = kThreads / 32;
+    constexpr uint32_t W = kThreads / 32;
     __shared__ float sh[W][32 * E];
+    __shared__ uint32_t parts_of[W], id_of[W];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     grid_wait();
-    for (uint32_t q = blockIdx.x; q + 1 < a.pieces; q += gridDim.x) {
-        const uint32_t b = q * a.piece, e = b + a.piece;
-        const uint32_t id = (uint32_t)(__ldg(a.pairs + e) >> 32);
-        if (id >= a.vocab || (uint32_t)(__ldg(a.pairs + e - 1) >> 32) != id) continue;
-        if (b > 0 && (uint32_t)(__ldg(a.pairs + b - 1) >> 32) == id) continue;  // an earlier piece's
-        uint32_t lo = e, hi = a.n;  // the first place behind this id's tokens, in (lo, hi]
-        while (hi - lo > 1) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if ((uint32_t)(__ldg(a.pairs + mid) >> 32) == id) lo = mid; else hi = mid;
+    for (uint32_t q0 = blockIdx.x * W; q0 + 1 < a.pieces; q0 += gridDim.x * W) {
+        const uint32_t q = q0 + warp;
+        uint32_t parts = 0, id = 0;
+        if (q + 1 < a.pieces) {
+            const uint32_t b = q * a.piece, e = b + a.piece;
+            id = (uint32_t)(__ldg(a.pairs + e) >> 32);
+            const uint32_t last = (uint32_t)(__ldg(a.pairs + e - 1) >> 32), before = b > 0 ? (uint32_t)(__ldg(a.pairs + b - 1) >> 32) : ~0u;
+            if (id < a.vocab && last == id && before != id) {   // else nothing goes on here, or it is an earlier piece's
+                uint32_t lo = e, hi = a.n;  // a place with this id, one behind its last: 32 probes at a time
+                while (hi - lo > 1) {
+                    const uint32_t at = lo + (uint32_t)((uint64_t)(hi - lo) * (lane + 1) / 33);
+                    const uint32_t same = __popc(__ballot_sync(0xFFFFFFFFu, (uint32_t)(__ldg(a.pairs + at) >> 32) == id));
+                    const uint32_t from = lo, width = hi - lo;
+                    if (same > 0) lo = from + (uint32_t)((uint64_t)width * same / 33);
+                    if (same < 32) hi = max(lo + 1, from + (uint32_t)((uint64_t)width * (same + 1) / 33));
+                }
+                parts = lo / a.piece - q + 1;
+            }
         }
-        const uint32_t parts = lo / a.piece - q + 1;
+        if (lane == 0) {
+            parts_of[warp] = parts;
+            id_of[warp] = id;
+        }
+        __syncthreads();
         for (uint32_t c0 = blockIdx.y * 32; c0 < a.dv; c0 += 32 * gridDim.y) {
             const uint32_t c = c0 + lane;
-            float sum[E] = {};
-            if (c < a.dv) {
+            const auto add = [&](uint32_t from, uint32_t r0, uint32_t count, uint32_t by, float (&sum)[E]) {
 #pragma unroll 4
-                for (uint32_t r = warp; r < parts; r += W) {
-                    const float* p = a.parts + ((size_t)(q + r) * 2 + (r == 0)) * a.d + (size_t)c * E;
+                for (uint32_t r = r0; r < count; r += by) {
+                    const float* p = a.parts + ((size_t)(from + r) * 2 + (r == 0)) * a.d + (size_t)c * E;
 #pragma unroll
                     for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], p[k]);
                 }
-            }
-#pragma unroll
-            for (int k = 0; k < E; ++k) sh[warp][lane * E + k] = sum[k];
-            __syncthreads();
-            if (warp == 0 && c < a.dv) {
-                for (uint32_t w = 1; w < min((uint32_t)W, parts); ++w)
-#pragma unroll
-                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], sh[w][lane * E + k]);
+            };
+            if (parts > 0 && parts <= W && c < a.dv) {
+                float sum[E] = {};
+                add(q, 0, parts, 1, sum);
                 embed_row<F, O, E>(a, id, c, sum);
             }
-            __syncthreads();
+            for (uint32_t o = 0; o < W; ++o) {
+                if (parts_of[o] <= W) continue;
+                float sum[E] = {};
+                if (c < a.dv) add(q0 + o, warp, parts_of[o], W, sum);
+#pragma unroll
+                for (int k = 0; k < E; ++k) sh[warp][lane * E + k] = sum[k];
+                __syncthreads();
+                if (warp == 0 && c < a.dv) {
+                    for (uint32_t w = 1; w < W; ++w)
+#pragma unroll
+                        for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], sh[w][lane * E + k]);
+                    embed_row<F, O, E>(a, id_of[o], c, sum);
+                }
+                __syncthreads();
+            }
         }
+        __syncthreads();   // parts_of has been read
     }
 }
 
@@ -530,7 +605,7 @@ __global__ void __launch_bounds__(WARP ? kThreads : 1024) norm_kernel(const __gr
 // The same with 16-byte pieces, a warp a row: the row stays in registers as it
 // lies in memory, so that twice as many rows are under way.
 template <class F, int NV>
-__global__ void __launch_bounds__(kThreads) norm_warp_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(typename Store<F>::S) == 2 ? 4 : 2) norm_warp_kernel(const __grid_constant__ NormArgs a) {
     using S = typename Store<F>::S;
     constexpr int E = 16 / (int)sizeof(S);
     const uint32_t lane = threadIdx.x & 31;
@@ -593,8 +668,7 @@ __global__ void __launch_bounds__(kThreads) norm_warp_kernel(const __grid_consta
     }
 }
 
-constexpr int64_t kNormBlocks = 456;   // blocks of rows, at most: 3 CTAs on each of 152 SMs
-constexpr int64_t kRingBlocks = 152;   // and of the kernel with a ring, which fills an SM
+constexpr int64_t kNormBlocks = 152;   // blocks of rows, at most: a CTA on each SM
 
 struct NormGradArgs {
     const void* gy;
@@ -611,277 +685,197 @@ struct NormGradArgs {
     int32_t blocks, accumulate;
 };
 
-// A CTA takes a block of rows, RI at a time.  The threads keep their columns'
-// sums for the weight and bias in registers; a row's two means are sums over
-// the CTA, for RI rows between two barriers.
-template <class F, int E, int NV, int RI>
-__global__ void __launch_bounds__(RI == 1 ? 1024 : 512) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
-    using S = typename Store<F>::S;
-    __shared__ float sh[2][2 * RI][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    float w[NV][E];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const uint32_t c = threadIdx.x + k * blockDim.x;
-        if (c < a.dv) ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)c * E, w[k]);
-    }
-    const float inv_d = __fdiv_rn(1.0f, (float)a.d);
-    int flip = 0;
-    for (int block = blockIdx.x; block < a.blocks; block += gridDim.x) {
-        float sw[NV][E] = {}, sb[NV][E] = {};
-        const int64_t r1 = min(a.rows, (block + 1) * a.per_block);
-        for (int64_t r0 = block * a.per_block; r0 < r1; r0 += RI, flip ^= 1) {
-            float u[RI][NV][E], g[RI][NV][E], rstd[RI], s[2 * RI];
-#pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                const int64_t row = r0 + i;
-                if (row < r1) {
-#pragma unroll
-                    for (int k = 0; k < NV; ++k) {
-                        const uint32_t c = threadIdx.x + k * blockDim.x;
-                        if (c < a.dv) {
-                            ld_e<F, E>(static_cast<const S*>(a.x) + row * a.x_stride + (size_t)c * E, u[i][k]);
-                            ld_e<F, E>(static_cast<const S*>(a.gy) + row * a.gy_stride + (size_t)c * E, g[i][k]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                s[2 * i] = s[2 * i + 1] = 0.0f;
-                if (r0 + i < r1) {
-                    const float mean = __ldg(a.mean + r0 + i);
-                    rstd[i] = __ldg(a.rstd + r0 + i);
-#pragma unroll
-                    for (int k = 0; k < NV; ++k)
-                        if (threadIdx.x + k * blockDim.x < a.dv)
-#pragma unroll
-                            for (int e = 0; e < E; ++e) {
-                                u[i][k][e] = __fmul_rn(__fsub_rn(u[i][k][e], mean), rstd[i]);
-                                sw[k][e] = __fmaf_rn(g[i][k][e], u[i][k][e], sw[k][e]);
-                                sb[k][e] = __fadd_rn(sb[k][e], g[i][k][e]);
-                                g[i][k][e] = __fmul_rn(g[i][k][e], w[k][e]);
-                                s[2 * i] = __fadd_rn(s[2 * i], g[i][k][e]);
-                                s[2 * i + 1] = __fmaf_rn(g[i][k][e], u[i][k][e], s[2 * i + 1]);
-                            }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * RI; ++i) {
-                s[i] = warp_sum(s[i]);
-                if (lane == 0) sh[flip][i][warp] = s[i];
-            }
-            __syncthreads();   // the other half of sh is written next: one barrier is enough
-#pragma unroll
-            for (int i = 0; i < 2 * RI; ++i)
-                s[i] = __fmul_rn(warp_sum(lane < warps ? sh[flip][i][lane] : 0.0f), inv_d);
-#pragma unroll
-            for (int i = 0; i < RI; ++i) {
-                if (r0 + i < r1) {
-#pragma unroll
-                    for (int k = 0; k < NV; ++k) {
-                        const uint32_t c = threadIdx.x + k * blockDim.x;
-                        if (c < a.dv) {
-                            float o[E];
-#pragma unroll
-                            for (int e = 0; e < E; ++e)
-                                o[e] = __fmul_rn(rstd[i], __fmaf_rn(-u[i][k][e], s[2 * i + 1], __fsub_rn(g[i][k][e], s[2 * i])));
-                            st_e<F, E>(static_cast<S*>(a.gx) + (r0 + i) * (int64_t)a.d + (size_t)c * E, o);
-                        }
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const uint32_t c = threadIdx.x + k * blockDim.x;
-            if (c < a.dv) {
-                float* p = a.parts + (size_t)block * 2 * a.d + (size_t)c * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    p[e] = sw[k][e];
-                    p[a.d + e] = sb[k][e];
-                }
-            }
-        }
-    }
-}
-
-// The same where rows are read in 16-byte pieces.  A team of G warps takes a
-// row, 8 / G teams a CTA; a thread keeps NV pieces of columns, at most 64
-// columns, and their sums for the weight and bias in registers for all its
-// rows.  Rows come through a ring of bulk copies in shared memory, which are
-// under way while a team computes: 8 warps alone could not keep enough loads
-// in flight (3.5 times the time, with loads into registers and one barrier
-// for 4 rows).  A row's two means need it twice: from shared memory, as
-// registers are full.
-struct RingShape {
-    int32_t stages;
-    uint32_t row_bytes, weight_at, bars_at;
-};
-
 template <int G>
 __device__ __forceinline__ void team_barrier(int team) {
     if constexpr (G == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(G * 32) : "memory");
 }
 
-template <class F, int NV, int G>
-__global__ void __launch_bounds__(kThreads, 1) norm_ring_kernel(const __grid_constant__ NormGradArgs a,
-                                                                const __grid_constant__ RingShape shape) {
+// A CTA takes a block of rows, a team of G warps a row.  A thread keeps NV
+// pieces of columns, and for all its rows their sums for the weight and bias,
+// in registers; between the two passes over a row also x - mean and gy * weight
+// (KEEP: up to 32 columns), while the next row's loads are under way.  What the
+// time goes to are instructions (half of the issue slots; 54% of the memory's
+// rate at 32768 x 1600 bf16, 67 us): widening, and 9 operations an element, two
+// elements at a time.  16 columns and 16 warps: 32 columns and 8 warps issue a
+// fifth less and take 71 us; the weight in registers as well leaves 12 warps and
+// 77 us; rows through a ring of bulk copies in shared memory take 65 us.
+template <class F, int E, int NV, int G, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     using S = typename Store<F>::S;
-    constexpr int E = 16 / (int)sizeof(S), T = kThreads / 32 / G;
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int T = THREADS / 32 / G, C = NV * E;
+    constexpr bool KEEP = C <= 32;
+    static_assert(T * G * 32 == THREADS && C % 2 == 0, "whole teams, pairs of columns");
+    extern __shared__ __align__(16) float sums[];   // [team][2][d]
     __shared__ float sh[2][T][G][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, team = warp / G, part = warp % G;
-    const uint32_t tid = part * 32 + lane;   // in the team
-    const uint32_t row_bytes = shape.row_bytes;
-    const int ST = shape.stages;
-    uint8_t* ring = smem + (size_t)team * ST * 2 * row_bytes;   // [stage][x, gy][row]
-    uint8_t* weight = smem + shape.weight_at;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + shape.bars_at) + team * ST;
-    for (uint32_t c = threadIdx.x; c < a.dv; c += kThreads)
-        reinterpret_cast<uint4*>(weight)[c] = __ldg(reinterpret_cast<const uint4*>(a.weight) + c);
-    if (tid == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(full + i, 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
+    const uint32_t tid = part * 32 + lane;          // in the team
     const float inv_d = __fdiv_rn(1.0f, (float)a.d);
-    bool ok = true;
-    int stage = 0, fill = 0, flip = 0, under_way = 0;
-    uint32_t phase = 0;
+    // does the warp, does this lane have a piece k
+    const auto any = [&](int k) { return part * 32 + k * 32 * G < a.dv; };
+    const auto mine = [&](int k) { return tid + k * 32 * G < a.dv; };
+    int flip = 0;
     for (int block = blockIdx.x; block < a.blocks; block += gridDim.x) {
         const int64_t r0 = block * a.per_block + team, r1 = min(a.rows, (block + 1) * a.per_block);
-        F2 sw[NV][E / 2], sb[NV][E / 2];
+        F2 sw[C / 2], sb[C / 2];
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) sw[k][e] = sb[k][e] = f2(0.0f, 0.0f);
-        const auto request = [&](int64_t row) {   // one thread of the team
-            mbar_arrive_expect_tx(full + fill, 2 * row_bytes);
-            bulk_g2s(ring + (size_t)fill * 2 * row_bytes, static_cast<const S*>(a.x) + row * a.x_stride, row_bytes, full + fill);
-            bulk_g2s(ring + (size_t)(fill * 2 + 1) * row_bytes, static_cast<const S*>(a.gy) + row * a.gy_stride, row_bytes, full + fill);
-            if (++fill == ST) fill = 0;
-            ++under_way;
+        for (int j = 0; j < C / 2; ++j) sw[j] = sb[j] = f2(0.0f, 0.0f);
+        const S* x_at = static_cast<const S*>(a.x) + (size_t)tid * E;
+        const S* g_at = static_cast<const S*>(a.gy) + (size_t)tid * E;
+        Raw<F, E> rx[KEEP ? NV : 1], rg[KEEP ? NV : 1];
+        float next_mean = 0.0f, next_rstd = 0.0f;
+        const auto load = [&](int k, int at, int64_t row) {
+            rx[at].load(x_at + row * a.x_stride + k * 32 * G * E);
+            rg[at].load(g_at + row * a.gy_stride + k * 32 * G * E);
         };
-        if (tid == 0 && ok)
-            for (int i = 0; i < ST; ++i)
-                if (r0 + i * T < r1) request(r0 + i * T);
+        if (r0 < r1) {
+            next_mean = __ldg(a.mean + r0);
+            next_rstd = __ldg(a.rstd + r0);
+            if constexpr (KEEP)
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (mine(k)) load(k, k, r0);
+        }
         for (int64_t row = r0; row < r1; row += T, flip ^= 1) {
-            const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
-            if (ok) ok = mbar_wait_bounded(full + stage, phase);
-            if (ok) --under_way;
-            // a copy that does not come: NaN in what this thread computes, and so in the weight's gradient
-            const float scale = ok ? rstd : NAN;
-            const F2 minus = f2(-mean, -mean), by = f2(scale, scale);
-            const uint8_t* xs = ring + (size_t)stage * 2 * row_bytes;
-            const uint8_t* gs = xs + row_bytes;
+            const float mean = next_mean, rstd = next_rstd;
+            const bool more = row + T < r1;
+            if (more) {
+                next_mean = __ldg(a.mean + row + T);
+                next_rstd = __ldg(a.rstd + row + T);
+            }
+            const F2 minus = f2(-mean, -mean), by = f2(rstd, rstd);
             F2 s1 = f2(0.0f, 0.0f), s2 = s1;
+            // c = x - mean, h = gy * w: the sums of h, h c, gy c / std and gy
+            [[maybe_unused]] F2 cs[KEEP ? C / 2 : 1], hs[KEEP ? C / 2 : 1];
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const uint32_t c = tid + k * 32 * G;
-                if (c < a.dv) {
-                    Raw<F, E> rx, rg, rw;
-                    rx.load_shared(xs + c * 16);
-                    rg.load_shared(gs + c * 16);
-                    rw.load_shared(weight + c * 16);
-                    float x[E], g[E], w[E];
-                    rx.get(x);
-                    rg.get(g);
-                    rw.get(w);
+                if (any(k)) {
+                    float x[E] = {}, g[E] = {}, w[E] = {};   // zeros behind the row: they add nothing
+                    if (mine(k)) {
+                        if constexpr (!KEEP) load(k, 0, row);
+                        rx[KEEP ? k : 0].get(x);
+                        rg[KEEP ? k : 0].get(g);
+                        ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)(tid + k * 32 * G) * E, w);
+                        if constexpr (KEEP)
+                            if (more) load(k, k, row + T);
+                    }
+                    if constexpr (E > 1) {
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const F2 u = mul2(add2(f2(x[e], x[e + 1]), minus), by), gg = f2(g[e], g[e + 1]);
-                        sw[k][e / 2] = fma2(gg, u, sw[k][e / 2]);
-                        sb[k][e / 2] = add2(sb[k][e / 2], gg);
-                        const F2 h = mul2(gg, f2(w[e], w[e + 1]));
-                        s1 = add2(s1, h);
-                        s2 = fma2(h, u, s2);
+                        for (int e = 0; e < E; e += 2) {
+                            const int j = (k * E + e) / 2;
+                            const F2 c = add2(f2(x[e], x[e + 1]), minus), gg = f2(g[e], g[e + 1]);
+                            sw[j] = fma2(mul2(gg, by), c, sw[j]);
+                            sb[j] = add2(sb[j], gg);
+                            const F2 h = mul2(gg, f2(w[e], w[e + 1]));
+                            s1 = add2(s1, h);
+                            s2 = fma2(h, c, s2);
+                            if constexpr (KEEP) {
+                                cs[j] = c;
+                                hs[j] = h;
+                            }
+                        }
+                    } else {   // single elements: one of a pair, the other half idle
+                        const bool odd = k & 1;
+                        const int j = k / 2;
+                        const auto put = [odd](F2 old, float v) {
+                            float lo, hi;
+                            split(old, lo, hi);
+                            return odd ? f2(lo, v) : f2(v, hi);
+                        };
+                        const float c = __fsub_rn(x[0], mean), h = __fmul_rn(g[0], w[0]);
+                        float lo, hi;
+                        split(sw[j], lo, hi);
+                        sw[j] = put(sw[j], __fmaf_rn(__fmul_rn(g[0], rstd), c, odd ? hi : lo));
+                        split(sb[j], lo, hi);
+                        sb[j] = put(sb[j], __fadd_rn(odd ? hi : lo, g[0]));
+                        s1 = add2(s1, f2(h, 0.0f));
+                        s2 = fma2(f2(h, 0.0f), f2(c, 0.0f), s2);
+                        if constexpr (KEEP) {
+                            cs[j] = put(cs[j], c);
+                            hs[j] = put(hs[j], h);
+                        }
                     }
                 }
             }
             float lo, hi, m1, m2;
             split(s1, lo, hi);
-            m1 = warp_sum(__fadd_rn(lo, hi));
+            m1 = __fadd_rn(lo, hi);
             split(s2, lo, hi);
-            m2 = warp_sum(__fadd_rn(lo, hi));
+            m2 = __fadd_rn(lo, hi);
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) {
+                m1 = __fadd_rn(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, s));
+                m2 = __fadd_rn(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, s));
+            }
             if constexpr (G > 1) {
                 if (lane == 0) {
                     sh[flip][team][part][0] = m1;
                     sh[flip][team][part][1] = m2;
                 }
                 team_barrier<G>(team);   // the other half of sh is written next
-                m1 = m2 = 0.0f;
+                m1 = sh[flip][team][0][0];
+                m2 = sh[flip][team][0][1];
 #pragma unroll
-                for (int p = 0; p < G; ++p) {
+                for (int p = 1; p < G; ++p) {
                     m1 = __fadd_rn(m1, sh[flip][team][p][0]);
                     m2 = __fadd_rn(m2, sh[flip][team][p][1]);
                 }
             }
-            m1 = __fmul_rn(m1, inv_d);
-            m2 = -__fmul_rn(m2, inv_d);
-            const F2 less = f2(-m1, -m1), along = f2(m2, m2);
-            S* dst = static_cast<S*>(a.gx) + row * (int64_t)a.d;
+            // grad_x = h / std - c mean(h c) / std^3 - mean(h) / std
+            const float l = -__fmul_rn(rstd, __fmul_rn(m1, inv_d));
+            const float k3 = -__fmul_rn(__fmul_rn(rstd, rstd), __fmul_rn(rstd, __fmul_rn(m2, inv_d)));
+            const F2 less = f2(l, l), along = f2(k3, k3);
+            S* dst = static_cast<S*>(a.gx) + row * (int64_t)a.d + (size_t)tid * E;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const uint32_t c = tid + k * 32 * G;
-                if (c < a.dv) {
-                    Raw<F, E> rx, rg, rw;
-                    rx.load_shared(xs + c * 16);
-                    rg.load_shared(gs + c * 16);
-                    rw.load_shared(weight + c * 16);
-                    float x[E], g[E], w[E];
-                    rx.get(x);
-                    rg.get(g);
-                    rw.get(w);
+                if (mine(k)) {
+                    float o[E];
+                    if constexpr (!KEEP) {
+                        load(k, 0, row);
+                        float x[E], g[E], w[E];
+                        rx[0].get(x);
+                        rg[0].get(g);
+                        ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)(tid + k * 32 * G) * E, w);
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const F2 u = mul2(add2(f2(x[e], x[e + 1]), minus), by), h = mul2(f2(g[e], g[e + 1]), f2(w[e], w[e + 1]));
-                        split(mul2(by, fma2(u, along, add2(h, less))), x[e], x[e + 1]);
+                        for (int e = 0; e < E; ++e)
+                            o[e] = __fmaf_rn(__fsub_rn(x[e], mean), k3, __fmaf_rn(__fmul_rn(g[e], w[e]), rstd, l));
+                    } else if constexpr (E > 1) {
+#pragma unroll
+                        for (int e = 0; e < E; e += 2) {
+                            const int j = (k * E + e) / 2;
+                            split(fma2(cs[j], along, fma2(hs[j], by, less)), o[e], o[e + 1]);
+                        }
+                    } else {
+                        split(fma2(cs[k / 2], along, fma2(hs[k / 2], by, less)), lo, hi);
+                        o[0] = k & 1 ? hi : lo;
                     }
-                    st_e<F, E>(dst + (size_t)c * E, x);
-                }
-            }
-            team_barrier<G>(team);   // the stage has been read
-            if (tid == 0 && ok && row + (int64_t)ST * T < r1) request(row + (int64_t)ST * T);
-            if (ok && ++stage == ST) {
-                stage = 0;
-                phase ^= 1;
-            }
-        }
-        if (!ok && tid == 0) {   // the copies still under way write to shared memory: not beyond the CTA's end
-            for (; under_way > 0; --under_way) {
-                for (int tries = 0; tries < kDrainTries && !mbar_wait_bounded(full + stage, phase); ++tries) {}
-                if (++stage == ST) {
-                    stage = 0;
-                    phase ^= 1;
+                    st_e<F, E>(dst + k * 32 * G * E, o);
                 }
             }
         }
-        // the teams' sums, in order, through the ring
+        // the teams' sums, in order
         __syncthreads();
-        float* sums = reinterpret_cast<float*>(smem);   // [team][2][d]
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const uint32_t c = tid + k * 32 * G;
-            if (c < a.dv) {
-                float* p = sums + (size_t)team * 2 * a.d + (size_t)c * E;
+            if (mine(k)) {
+                float* p = sums + (size_t)team * 2 * a.d + (size_t)(tid + k * 32 * G) * E;
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    split(sw[k][e], p[2 * e], p[2 * e + 1]);
-                    split(sb[k][e], p[a.d + 2 * e], p[a.d + 2 * e + 1]);
+                for (int e = 0; e < E; ++e) {
+                    float lo, hi;
+                    split(sw[(k * E + e) / 2], lo, hi);
+                    p[e] = (k * E + e) & 1 ? hi : lo;
+                    split(sb[(k * E + e) / 2], lo, hi);
+                    p[a.d + e] = (k * E + e) & 1 ? hi : lo;
                 }
             }
         }
         __syncthreads();
-        for (uint32_t c = threadIdx.x; c < 2 * a.d; c += kThreads) {
+        for (uint32_t c = threadIdx.x; c < 2 * a.d; c += THREADS) {
             float sum = sums[c];
 #pragma unroll
             for (int t = 1; t < T; ++t) sum = __fadd_rn(sum, sums[(size_t)t * 2 * a.d + c]);
             a.parts[(size_t)block * 2 * a.d + c] = sum;
         }
-        fence_proxy_async_smem();   // copies of the next block write where these were
         __syncthreads();
     }
 }
@@ -1003,18 +997,33 @@ zero_status_t check_embedding(const char* what, int64_t vocab, int64_t d, int64_
     return ZERO_OK;
 }
 
-// Tokens of a piece of the sorted list: enough pieces to fill the GPU, and
-// long ones for long lists, whose frequent ids leave fewer parts.
-int64_t embed_piece(int64_t n) { return n <= 8192 ? 8 : n <= (1 << 20) ? 32 : 256; }
+// Tokens of a piece of the sorted list: few tokens in small pieces, to fill the
+// GPU; many in long ones, whose frequent ids leave fewer parts; between, of 16,
+// 24 and 32 what fills the last round of 152 SMs with 32 warps best (32768
+// tokens of 1600: pieces of 24, 28 us, and of 32, 34 us).
+int64_t embed_piece(int64_t d, int64_t n) {
+    if (n <= 8192) return 8;
+    if (n > (1 << 20)) return 256;
+    const int64_t slices = (d + 255) / 256;
+    int64_t best = 32, least = INT64_MAX;
+    for (int64_t p = 32; p >= 16; p -= 8) {
+        const int64_t cost = ((n + p - 1) / p * slices + 152 * 32 - 1) / (152 * 32) * p;
+        if (cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
+}
 
 struct EmbedWorkspace {
     int64_t pairs0, pairs1, parts, bytes;
     explicit EmbedWorkspace(int64_t d, int64_t n) {
         const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-        const int64_t pieces = (n + embed_piece(n) - 1) / embed_piece(n);
+        const int64_t pieces = (n + embed_piece(d, n) - 1) / embed_piece(d, n);
         pairs0 = 0;
-        pairs1 = up(n * 8);
-        parts = pairs1 + up(n * 8);
+        pairs1 = up((n + zk::kPairsPad) * 8);
+        parts = 2 * pairs1;
         bytes = parts + up(pieces * 2 * d * 4) + 256;
     }
 };
@@ -1060,14 +1069,39 @@ namespace {
 template <class F, class O, int E>
 zero_status_t launch_embed_grad(const zk::EmbedGradArgs& a, cudaStream_t s) {
     const char* what = "zero_embedding_backward";
-    auto k = zk::embed_grad_kernel<F, O, E>;
-    const uint32_t per_cta = zk::kThreads / a.group;
-    zero_status_t rc = launch_after(k, dim3((unsigned)persistent_grid(k, (a.pieces + per_cta - 1) / per_cta)), zk::kThreads, 0, s, what, a);
+    // narrow rows: 8 lanes a piece
+    const auto go = [&](auto k, int64_t lanes) {
+        const int64_t items = a.pieces * (((int64_t)a.dv + lanes - 1) / lanes);
+        return launch_after(k, dim3((unsigned)persistent_grid(k, (items * lanes + zk::kThreads - 1) / zk::kThreads)), zk::kThreads, 0, s, what, a);
+    };
+    const zero_status_t rc = a.dv > 16 ? go(zk::embed_grad_kernel<F, O, E, 32>, 32) : go(zk::embed_grad_kernel<F, O, E, 8>, 8);
     if (rc != ZERO_OK || a.pieces < 2) return rc;
     // few CTAs find something to add: pieces x column slices
-    const dim3 grid((unsigned)capped(std::min<int64_t>(a.pieces - 1, 65535)),
+    const dim3 grid((unsigned)capped(std::min<int64_t>((a.pieces + 6) / 8, 65535)),
                     (unsigned)(max_ctas() > 0 ? 1 : std::min<int64_t>((a.dv + 31) / 32, 64)));
     return launch_after(zk::embed_join_kernel<F, O, E>, grid, zk::kThreads, 0, s, what, a);
+}
+
+}  // namespace
+
+namespace {
+
+// Clusters of the sort that run at once: a CTA of 1024 threads fills an SM's registers, whatever shared memory it asks for.
+int64_t resident_clusters(void (*kern)(zk::SortArgs), cudaLaunchConfig_t cfg, int cluster, bool shared) {
+    static std::atomic<int> known[64][9][2];   // by device, size and form; zero-initialised (static storage)
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    std::atomic<int>& at = known[dev][cluster][shared];
+    n = at.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 2) {
+            cudaGetLastError();
+            n = 2;
+        }
+        at.store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 }  // namespace
@@ -1112,12 +1146,25 @@ extern "C" zero_status_t zero_embedding_backward(const void* grad_out, const int
     // the cluster that sorts: 8 CTAs, one for what one can sort as fast
     int cluster = n <= 2048 ? 1 : 8;
     while (cap > 0 && cluster > 1 && cluster > cap) cluster /= 2;
-    int64_t fill = sa.zero_bytes == 0 ? 0 : std::min<int64_t>((sa.zero_bytes / 16 / zk::kSortThreads + cluster) / cluster, 2 * 152 / cluster);
-    if (sa.zero_bytes > 0 && fill < 1) fill = 1;
-    if (cap > 0) fill = std::min<int64_t>(fill, std::max<int64_t>(1, cap / cluster - 1));
+    const int64_t warps = (int64_t)cluster * zk::kSortWarps;
+    sa.per_warp = (uint32_t)((n + warps * 32 - 1) / (warps * 32) * 32);
+    constexpr int64_t kMost = 192 << 10;   // of shared memory for the pairs: 98304 tokens in 8 CTAs
+    const int64_t held = 2 * zk::kSortWarps * (int64_t)sa.per_warp * 8;
+    const bool shared = held <= kMost;
+    const auto kern = shared ? zk::embed_sort_kernel<true> : zk::embed_sort_kernel<false>;
+    if (shared && held > (8 << 10)) {
+        static std::atomic<uint64_t> allowed{0};   // by device
+        int dev = 0;
+        cudaGetDevice(&dev);
+        const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+        if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) != cudaSuccess) return after_launch(what);
+            allowed.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(cluster * (1 + (sa.zero_bytes > 0 ? fill : 0))));
     cfg.blockDim = dim3(zk::kSortThreads);
+    cfg.dynamicSmemBytes = shared ? (size_t)held : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1125,7 +1172,15 @@ extern "C" zero_status_t zero_embedding_backward(const void* grad_out, const int
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, zk::embed_sort_kernel, sa);
+    // the clusters that zero: as many as run at once with the one that sorts (clusters of 8 do not fill every GPC: of 19, two
+    // began when others had ended, and the launch took twice as long)
+    cfg.gridDim = dim3((unsigned)cluster);
+    if (sa.zero_bytes > 0) {
+        int64_t fill = std::min<int64_t>((sa.zero_bytes / 32768 + cluster) / cluster, resident_clusters(kern, cfg, cluster, shared) - 1);
+        if (cap > 0) fill = std::min<int64_t>(fill, cap / cluster - 1);
+        cfg.gridDim = dim3((unsigned)(cluster * (1 + std::max<int64_t>(1, fill))));
+    }
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, sa);
     if (err != cudaSuccess) {
         cudaGetLastError();
         return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(err));
@@ -1142,13 +1197,11 @@ extern "C" zero_status_t zero_embedding_backward(const void* grad_out, const int
     a.out = grad_weight;
     a.parts = reinterpret_cast<float*>(base + ws.parts);
     a.n = (uint32_t)n;
-    a.piece = (int32_t)embed_piece(n);
+    a.piece = (int32_t)embed_piece(d, n);
     a.pieces = (uint32_t)((n + a.piece - 1) / a.piece);
     a.d = (uint32_t)d;
     a.dv = (uint32_t)(d / e);
     a.vocab = (uint32_t)vocab;
-    a.group = 1;
-    while (a.group < zk::kThreads && (uint32_t)a.group < a.dv) a.group *= 2;
     a.accumulate = accumulate != 0;
     a.scale = (float)scale;
     if (grad_dtype == dtype) ZL_DISPATCH(dtype, e, rc = launch_embed_grad<T, T, E>(a, s));
@@ -1173,12 +1226,17 @@ void launch_norm(const zk::NormArgs& a, cudaStream_t s) {
     const auto warps = [&](auto kern) { kern<<<persistent_grid(kern, (a.rows + 7) / 8), zk::kThreads, 0, s>>>(a); };
     if constexpr (E >= 4) {
         constexpr int B = 8 / E;   // twice as many pieces of half the elements
-        if (a.dv <= 32u * 1 * B) return warps(zk::norm_warp_kernel<F, 1 * B>);
-        if (a.dv <= 32u * 2 * B) return warps(zk::norm_warp_kernel<F, 2 * B>);
-        if (a.dv <= 32u * 3 * B) return warps(zk::norm_warp_kernel<F, 3 * B>);
-        if (a.dv <= 32u * 4 * B) return warps(zk::norm_warp_kernel<F, 4 * B>);
-        if (a.dv <= 32u * 6 * B) return warps(zk::norm_warp_kernel<F, 6 * B>);
-        if (a.dv <= 32u * 8 * B) return warps(zk::norm_warp_kernel<F, 8 * B>);
+        switch ((a.dv + 32 * B - 1) / (32 * B)) {
+            case 1: return warps(zk::norm_warp_kernel<F, 1 * B>);
+            case 2: return warps(zk::norm_warp_kernel<F, 2 * B>);
+            case 3: return warps(zk::norm_warp_kernel<F, 3 * B>);
+            case 4: return warps(zk::norm_warp_kernel<F, 4 * B>);
+            case 5: return warps(zk::norm_warp_kernel<F, 5 * B>);
+            case 6: return warps(zk::norm_warp_kernel<F, 6 * B>);
+            case 7: return warps(zk::norm_warp_kernel<F, 7 * B>);
+            case 8: return warps(zk::norm_warp_kernel<F, 8 * B>);
+            default: break;
+        }
     } else {
         constexpr int WIDE = E == 1 ? 32 : 16;
         if (a.dv <= 32u * WIDE) return warps(zk::norm_kernel<F, E, WIDE, true>);
@@ -1189,55 +1247,35 @@ void launch_norm(const zk::NormArgs& a, cudaStream_t s) {
     kern<<<persistent_grid(kern, a.rows, 0, threads), threads, 0, s>>>(a);
 }
 
-// Rows of a block: of the kernel with a ring, and of the others.
-int64_t norm_rows_per_block(int64_t rows, bool ring) {
-    const int64_t most = ring ? zk::kRingBlocks : zk::kNormBlocks;
-    return std::max<int64_t>(ring ? 1 : 4, (rows + most - 1) / most);
-}
+int64_t norm_rows_per_block(int64_t rows) { return std::max<int64_t>(1, (rows + zk::kNormBlocks - 1) / zk::kNormBlocks); }
 
-template <class F, int NV, int G>
-zero_status_t launch_norm_ring(const zk::NormGradArgs& a, cudaStream_t s, const char* what) {
-    constexpr int T = zk::kThreads / 32 / G;
-    constexpr int64_t kMost = 232448 - 1024;   // of the 227 KB of shared memory a CTA may have, 1 KB is for static arrays
-    zk::RingShape r{};
-    r.row_bytes = a.d * sizeof(typename zk::Store<F>::S);
-    r.stages = (int32_t)std::max<int64_t>(1, std::min<int64_t>(4, (kMost - r.row_bytes - 512) / (T * 2 * (int64_t)r.row_bytes)));
-    const int64_t ring = (int64_t)T * r.stages * 2 * r.row_bytes, sums = (int64_t)T * 2 * a.d * 4;
-    r.weight_at = (uint32_t)((std::max(ring, sums) + 127) / 128 * 128);
-    r.bars_at = (r.weight_at + r.row_bytes + 127) / 128 * 128;
-    const int smem = (int)(r.bars_at + T * r.stages * 8);
-    auto kern = zk::norm_ring_kernel<F, NV, G>;
+template <class F, int E, int NV, int G, int THREADS>
+zero_status_t launch_norm_team(const zk::NormGradArgs& a, cudaStream_t s, const char* what) {
+    const int smem = THREADS / 32 / G * 2 * (int)a.d * 4;   // 128 KB at most
+    auto kern = zk::norm_grad_kernel<F, E, NV, G, THREADS>;
     static std::atomic<uint64_t> allowed{0};   // by device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
     if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) != cudaSuccess) return after_launch(what);
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 131072) != cudaSuccess) return after_launch(what);
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    kern<<<capped(std::min<int64_t>(a.blocks, std::max(1, sm_count()))), zk::kThreads, smem, s>>>(a, r);
+    kern<<<capped(std::min<int64_t>(a.blocks, std::max(1, sm_count()))), THREADS, smem, s>>>(a);
     return after_launch(what);
 }
 
+// 16 columns a thread and as many warps a row as that takes; more columns a thread above 4096.
 template <class F, int E>
 zero_status_t launch_norm_grad(const zk::NormGradArgs& a, cudaStream_t s, const char* what) {
-    if constexpr (E >= 4) {
-        constexpr int B = 8 / E;
-        if (a.dv <= 32u * 2 * B) return launch_norm_ring<F, 2 * B, 1>(a, s, what);
-        if (a.dv <= 32u * 4 * B) return launch_norm_ring<F, 4 * B, 1>(a, s, what);
-        if (a.dv <= 32u * 8 * B) return launch_norm_ring<F, 8 * B, 1>(a, s, what);
-        if (a.dv <= 64u * 8 * B) return launch_norm_ring<F, 8 * B, 2>(a, s, what);
-        if (a.dv <= 128u * 8 * B) return launch_norm_ring<F, 8 * B, 4>(a, s, what);
-        return launch_norm_ring<F, 8 * B, 8>(a, s, what);
-    } else {
-        const auto go = [&](auto kern, int nv) {
-            const int threads = (int)((a.dv + nv - 1) / nv + 31) / 32 * 32;
-            kern<<<persistent_grid(kern, a.blocks, 0, threads), threads, 0, s>>>(a);
-            return after_launch(what);
-        };
-        if (a.dv <= 1024u) return go(zk::norm_grad_kernel<F, E, 2, 4>, 2);
-        return go(zk::norm_grad_kernel<F, E, 16 / E, 1>, 16 / E);
-    }
+    constexpr int B = 16 / E;
+    if (a.dv <= 16u * B) return launch_norm_team<F, E, B / 2, 1, 512>(a, s, what);
+    if (a.dv <= 32u * B) return launch_norm_team<F, E, B, 1, 512>(a, s, what);
+    if (a.dv <= 64u * B) return launch_norm_team<F, E, B, 2, 512>(a, s, what);
+    if (a.dv <= 128u * B) return launch_norm_team<F, E, B, 4, 512>(a, s, what);
+    if (a.dv <= 256u * B) return launch_norm_team<F, E, B, 8, 512>(a, s, what);
+    if (a.dv <= 512u * B) return launch_norm_team<F, E, 2 * B, 8, 256>(a, s, what);
+    return launch_norm_team<F, E, 4 * B, 8, 256>(a, s, what);
 }
 
 }  // namespace
@@ -1278,8 +1316,8 @@ extern "C" zero_status_t zero_layer_norm_workspace(int64_t rows, int64_t d, int6
     const zero_status_t rc = check_norm("zero_layer_norm_workspace", rows, d);
     if (rc != ZERO_OK) return rc;
     if (!bytes) return fail(ZERO_ERR_INVALID, "zero_layer_norm_workspace: NULL bytes");
-    const int64_t per = norm_rows_per_block(rows, false), ring = norm_rows_per_block(rows, true);
-    *bytes = (std::max((rows + per - 1) / per, (rows + ring - 1) / ring) * 2 * d * 4 + 255) / 256 * 256 + 256;
+    const int64_t per = norm_rows_per_block(rows);
+    *bytes = ((rows + per - 1) / per * 2 * d * 4 + 255) / 256 * 256 + 256;
     return ZERO_OK;
 }
 
@@ -1332,7 +1370,7 @@ extern "C" zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy
     a.rows = rows;
     a.gy_stride = gy_stride;
     a.x_stride = x_stride;
-    a.per_block = norm_rows_per_block(rows, e * size == 16);
+    a.per_block = norm_rows_per_block(rows);
     a.blocks = (int32_t)((rows + a.per_block - 1) / a.per_block);
     a.d = (uint32_t)d;
     a.dv = (uint32_t)(d / e);

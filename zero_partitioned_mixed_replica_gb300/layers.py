@@ -326,7 +326,7 @@ def lm_loss_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.T
     shape; a target outside 0 .. vocab-1 makes a token not count.  ``loss``
     is the mean over the tokens that count (or the sum; 0 without any),
     ``losses`` has a value for each token, both float32; ``saved`` is for
-    :func:`lm_loss_backward`."""
+    :func:`lm_loss_backward` (``loss`` is a view of it)."""
     if reduction not in _REDUCTION:
         raise ValueError("reduction must be 'mean' or 'sum'")
     a, (need, _), keep = _loss_args(hidden, weight, targets)
@@ -334,15 +334,16 @@ def lm_loss_forward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.T
     if _current_device() != index:
         with torch.cuda.device(index):
             return lm_loss_forward(hidden, weight, targets, reduction)
-    losses, lse = (hidden.new_empty(targets.shape, dtype=_FP32) for _ in range(2))
-    stats = hidden.new_empty(2, dtype=_FP32)
+    losses = hidden.new_empty(targets.shape, dtype=_FP32)
+    saved = hidden.new_empty(2 + a.n, dtype=_FP32)       # loss, share, log of each token's sum of exponentials
     ws = torch.empty(need, dtype=torch.uint8, device=index)
+    at = saved.data_ptr()
     a.reduction = _REDUCTION[reduction]
-    a.losses, a.lse, a.stats, a.workspace = losses.data_ptr(), lse.data_ptr(), stats.data_ptr(), ws.data_ptr()
+    a.losses, a.lse, a.stats, a.workspace = losses.data_ptr(), at + 8, at, ws.data_ptr()
     status = B.lib().zero_lm_loss_forward(a, _raw_stream(index))
     if status:
         B._check(status)
-    return stats[0], losses, (lse, stats)
+    return saved[0], losses, saved
 
 
 def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, saved,
@@ -356,19 +357,18 @@ def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
     ``ZeroStep.loss_scale``) or the gradient of ``loss``.  ``piece`` columns of
     the vocabulary are in memory at a time (0: chosen)."""
     a, (_, need), keep = _loss_args(hidden, weight, targets, piece)
-    index, (lse, stats) = weight.get_device(), saved
+    index = weight.get_device()
     by_tensor = isinstance(scale, torch.Tensor)
     if by_tensor and (scale.dtype is not _FP32 or scale.numel() != 1):
         raise ValueError("scale: a number or a float32 tensor of one element")
-    if not (_like(lse, targets.shape, _FP32, index) and _like(stats, (2,), _FP32, index) and
-            _like(grad_weight, weight.shape, weight.dtype, index) and (not by_tensor or scale.get_device() == index)):
-        for name, t, shape in (("saved[0]", lse, targets.shape), ("saved[1]", stats, (2,))):
-            _check_weight(name, t, shape)
-            _check_dtype(name, t, _FP32)
+    if not (_like(saved, (2 + a.n,), _FP32, index) and _like(grad_weight, weight.shape, weight.dtype, index) and
+            (not by_tensor or scale.get_device() == index)):
+        _check_weight("saved", saved, (2 + a.n,))
+        _check_dtype("saved", saved, _FP32)
         if grad_weight is not None:
             _check_weight("grad_weight", grad_weight, weight.shape)
             _check_dtype("grad_weight", grad_weight, weight.dtype)
-        _check_on(weight.device, lse=lse, stats=stats, grad_weight=grad_weight, scale=scale if by_tensor else None)
+        _check_on(weight.device, saved=saved, grad_weight=grad_weight, scale=scale if by_tensor else None)
     if _current_device() != index:
         with torch.cuda.device(index):
             return lm_loss_backward(hidden, weight, targets, saved, grad_weight, scale, accumulate, need_hidden, piece)
@@ -378,7 +378,7 @@ def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
         a.scale_dev = scale.data_ptr()
     else:
         a.scale = scale
-    a.lse, a.stats, a.workspace = lse.data_ptr(), stats.data_ptr(), ws.data_ptr()
+    a.lse, a.stats, a.workspace = saved.data_ptr() + 8, saved.data_ptr(), ws.data_ptr()
     a.grad_hidden = grad_hidden.data_ptr() if need_hidden else None
     a.grad_weight = grad_weight.data_ptr() if grad_weight is not None else None
     a.accumulate = 1 if accumulate else 0
@@ -391,17 +391,17 @@ def lm_loss_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.
 class _LmLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, targets, reduction):
-        loss, _, (lse, stats) = lm_loss_forward(hidden, weight, targets, reduction)
-        ctx.save_for_backward(hidden, weight, targets, lse, stats)
-        return loss.clone()         # stats is kept: what becomes of the loss does not reach it
+        loss, _, saved = lm_loss_forward(hidden, weight, targets, reduction)
+        ctx.save_for_backward(hidden, weight, targets, saved)
+        return loss.clone()         # saved is kept: what becomes of the loss does not reach it
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        hidden, weight, targets, lse, stats = ctx.saved_tensors
+        hidden, weight, targets, saved = ctx.saved_tensors
         need_hidden, need_weight = ctx.needs_input_grad[:2]
         gw = torch.empty_like(weight) if need_weight else None
-        gh = lm_loss_backward(hidden, weight, targets, (lse, stats), gw, scale=grad.contiguous(), need_hidden=need_hidden)
+        gh = lm_loss_backward(hidden, weight, targets, saved, gw, scale=grad.contiguous(), need_hidden=need_hidden)
         return gh, gw, None, None
 
 
