@@ -436,6 +436,13 @@ __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Launches that overlap at their ends (zero_detail::launch_after): a kernel may
+// begin when every CTA of the one before it in the stream has begun and called
+// grid_release, and waits in grid_wait until that one has ended and its writes
+// are there, before it touches memory that others write.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------
 // Kernel arguments (passed by value as __grid_constant__ parameters).
 // Vector indices count 8-element vectors of the flat buffer (32-bit: the

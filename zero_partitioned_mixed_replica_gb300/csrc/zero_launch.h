@@ -82,6 +82,27 @@ inline zero_status_t after_launch(const char* what) {
     return ZERO_OK;
 }
 
+// A launch that may begin while the stream's last kernel ends (grid_wait).
+template <class... P, class... A>
+inline zero_status_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const char* what, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+    }
+    return after_launch(what);
+}
+
 // The extents a launch's accesses are checked against (bounds-checked
 // builds; the normal build carries them unused): from the layout, each
 // shortened by the test hook's slack.  out_elems: each 16-bit output's size.

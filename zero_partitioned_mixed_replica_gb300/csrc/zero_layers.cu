@@ -91,9 +91,6 @@ struct Raw {
     }
 };
 
-// Wait for the kernels before this one in the stream: it may have begun while they end.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Two binary32 operations in one instruction, each rounded to nearest.
 struct F2 {
     uint64_t v;
@@ -232,6 +229,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
     __shared__ __align__(128) uint32_t counts[kSortWarps][256];  // of a digit in a warp's tokens; then where the next one goes
     __shared__ uint32_t total[256];                    // of a digit in this CTA's tokens
     __shared__ uint32_t warp_total[8];
+    grid_release();
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ctas = cluster.num_blocks(), rank = cluster.block_rank();
     if (blockIdx.x >= ctas) {  // zero the gradient: bytes to a 16-byte boundary, 32 KB of zeros over and over, bytes
@@ -385,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 4) embed_grad_kernel(const __grid_co
     const uint32_t slices = (a.dv + LANES - 1) / LANES;
     const uint64_t items = (uint64_t)a.pieces * slices, step = (uint64_t)gridDim.x * (kThreads / LANES);
     grid_wait();
+    grid_release();
     for (uint64_t item = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / LANES; item < items; item += step) {
         const uint32_t q = (uint32_t)(item / slices), c = (uint32_t)(item - (uint64_t)q * slices) * LANES + lane;
         const uint32_t b = q * a.piece, e = min(a.n, b + a.piece);
@@ -710,6 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
     __shared__ float sh[2][T][G][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, team = warp / G, part = warp % G;
     const uint32_t tid = part * 32 + lane;          // in the team
+    grid_release();
     const float inv_d = __fdiv_rn(1.0f, (float)a.d);
     // does the warp, does this lane have a piece k
     const auto any = [&](int k) { return part * 32 + k * 32 * G < a.dv; };
@@ -965,27 +965,6 @@ int capped(int64_t ctas) {
     const int32_t cap = max_ctas();
     if (cap > 0 && ctas > cap) ctas = cap;
     return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, 0x7FFFFFFF));
-}
-
-// A launch that may begin while the stream's last kernel ends (grid_wait).
-template <class... P, class... A>
-zero_status_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const char* what, const A&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail(ZERO_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-    }
-    return after_launch(what);
 }
 
 constexpr int64_t kMaxVocab = 0x7FFFFFFE, kMaxRows = 0x7FFFFFFF, kMaxDim = 1 << 20;

@@ -55,12 +55,14 @@ struct MmProblem {
     uint32_t idesc;           // without the columns
 };
 
+
 struct MmMaps {
     CUtensorMap a[2], b[2];
 };
 
 struct MmArgs {
     LossHead* head;
+    int32_t stages, b_bytes;  // b_bytes: of a widest tile's B in a stage of one CTA
     uint32_t* next;           // tiles dealt behind the first of each cluster; 0 before the launch
     MmProblem p[2];           // GRADS: dz @ weight, dz^T @ hidden; else the first alone
     // STATS, DZ
@@ -86,12 +88,10 @@ struct MmArgs {
     int32_t gw_vec;           // rows begin on 32-byte boundaries, d % 16 == 0
 };
 
-template <int CG>
+constexpr int kMaxStages = 8;
 struct MmShape {
-    static constexpr int kA = kBoxBytes;                        // bytes of A and B in a stage
-    static constexpr int kB = 2 * kBoxBytes / CG;
-    static constexpr int kStages = CG == 2 ? 6 : 4;
-    static constexpr int kOps = kStages * (kA + kB);
+    static constexpr int kA = kBoxBytes;                        // bytes of A in a stage; B has b_bytes
+    static constexpr int kOps = 12 * kBoxBytes;                 // of all stages: 6 of 256 rows between two CTAs, 4 of one's
     static constexpr int kTurn = kEpiWarps * 32 * 17 * 4;       // transposition
     static constexpr int kSync = 512;                           // barriers, tiles dealt
     static constexpr int kBytes = 1024 + kOps + kTurn + kSync;  // and alignment
@@ -242,8 +242,9 @@ __device__ __forceinline__ void store_turned(uint16_t* p, int64_t ld, uint32_t r
 // another's last round.
 template <int CG, int MODE, class F>
 __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
-    using Shape = MmShape<CG>;
-    constexpr int ST = Shape::kStages;
+    using Shape = MmShape;
+    const int ST = a.stages;
+    const uint32_t stage_bytes = Shape::kA + a.b_bytes;
     constexpr bool B_MN = MODE == MM_GRADS;
     // tiles dealt before they are begun: short tiles (logits, d of K) hide the counter's latency, long ones stay balanced
     constexpr int RING = MODE == MM_GRADS ? 2 : 3;
@@ -252,14 +253,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
     float(*sh)[32][17] = reinterpret_cast<float(*)[32][17]>(ops + Shape::kOps);
     uint64_t* bars = reinterpret_cast<uint64_t*>(ops + Shape::kOps + Shape::kTurn);
     uint64_t* full = bars;               // [ST] in the leader: a block of both CTAs has landed
-    uint64_t* empty = full + ST;         // [ST] a block has been read by the products
-    uint64_t* acc_full = empty + ST;     // [2] a tile's products are done
+    uint64_t* empty = full + kMaxStages; // [ST] a block has been read by the products
+    uint64_t* acc_full = empty + kMaxStages;  // [2] a tile's products are done
     uint64_t* acc_empty = acc_full + 2;  // [2] in the leader: the epilogues have read the accumulator
     uint64_t* tile_full = acc_empty + 2; // [RING] a tile has been dealt
     uint64_t* tile_empty = tile_full + RING;  // [RING] in the leader: all roles of both CTAs know it
-    MmTile* ring = reinterpret_cast<MmTile*>(bars + 24);   // [RING]
+    MmTile* ring = reinterpret_cast<MmTile*>(bars + 28);   // [RING]
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ring + RING);
-    static_assert(2 * ST + 4 + 2 * RING <= 24 && 24 * 8 + sizeof(MmTile) * RING + 4 <= Shape::kSync, "what the roles share");
+    static_assert(2 * kMaxStages + 4 + 2 * RING <= 28 && 28 * 8 + sizeof(MmTile) * RING + 4 <= Shape::kSync, "what the roles share");
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const auto leader = [](uint64_t* bar) { return CG == 2 ? map_rank(smem_u32(bar), 0) : smem_u32(bar); };
@@ -291,6 +292,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
     if constexpr (CG == 2) cluster_barrier();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
+    grid_wait();      // what is above ran while the kernel before this one ended
+    grid_release();
     bool ok = true;   // of this thread's waits
     // the next tile; for one thread of a role
     int tile_slot = 0;
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                     if (!ok) break;
                     const uint32_t bar = full0 + stage * 8;
                     if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
-                    const uint32_t sa = ops0 + stage * (Shape::kA + Shape::kB), sb = sa + Shape::kA;
+                    const uint32_t sa = ops0 + stage * stage_bytes, sb = sa + Shape::kA;
                     const int32_t k = kb * kTileK;
                     if constexpr (A_MN) {
                         tma_load<CG>(sa, map_a, ma, k, bar);
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                     }
                     if constexpr (B_MN) {
 #pragma unroll
-                        for (int j = 0; j < Shape::kB / 8192; ++j)
+                        for (int j = 0; j < 4 / CG; ++j)
                             if (j < boxes) tma_load<CG>(sb + j * 8192, map_b, nb + 64 * j, k + k_off, bar);
                     } else {
                         tma_load<CG>(sb, map_b, k + k_off, nb, bar);
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                     ok = mbar_wait_bounded(full + stage, phase);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t at = stage * ((Shape::kA + Shape::kB) >> 4);
+                    const uint64_t at = (uint64_t)(stage * (stage_bytes >> 4));
 #pragma unroll
                     for (int j = 0; j < kTileK / 16; ++j)
                         tc_mma<CG>(acc, da0 + at + j * (A_MN ? kStepMN : kStepK), db0 + at + j * (B_MN ? kStepMN : kStepK), idesc,
@@ -629,6 +632,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     __shared__ uint32_t sums[2][W];
     __shared__ int32_t place[kPickThreads];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    grid_release();
     const auto counts = [&](int64_t t) { return t >= 0 && t < a.vocab; };
     const uint32_t b0 = (uint32_t)min((uint64_t)a.n, (uint64_t)blockIdx.x * a.per_cta);
     const uint32_t b1 = (uint32_t)min((uint64_t)a.n, (uint64_t)b0 + a.per_cta);
@@ -743,6 +747,7 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ 
     __shared__ double sums[kThreads];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    grid_wait();
     const int32_t count = a.head->count;
     for (int block = blockIdx.x; block < a.blocks; block += gridDim.x) {
         const int64_t row = (int64_t)block * kLossRows + warp;
@@ -819,6 +824,7 @@ struct FinishArgs {
 template <class F, int E>
 __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant__ FinishArgs a) {
     const int lane = threadIdx.x & 31;
+    grid_wait();
     float f = __fmul_rn(a.scale, *a.share);
     if (a.scale_dev) f = __fmul_rn(f, *a.scale_dev);
     const int64_t step = (int64_t)gridDim.x * kThreads / 32;
@@ -909,8 +915,11 @@ zero_status_t launch_mm(const Operand* oa, const Operand* ob, zk::MmArgs a, cuda
         if (rc != ZERO_OK) return rc;
         p.idesc = zk::instr_desc(bf16, MODE == zk::MM_GRADS && i == 1, MODE == zk::MM_GRADS, 128 * CG, 0);
     }
+    // B of a stage: the box of a logits' tile, or boxes of 64 columns; 1024 bytes are a group of the swizzle
+    a.b_bytes = MODE == zk::MM_GRADS ? 2 * zk::kBoxBytes / CG : (int32_t)up(a.p[0].bn / CG * 128, 1024);
+    a.stages = std::min(zk::kMaxStages, zk::MmShape::kOps / (zk::MmShape::kA + a.b_bytes));
     auto kern = zk::mm_kernel<CG, MODE, F>;
-    constexpr int smem = zk::MmShape<CG>::kBytes;
+    constexpr int smem = zk::MmShape::kBytes;
     static std::atomic<uint64_t> allowed{0};   // by device
     int dev = 0;
     cudaGetDevice(&dev);
@@ -928,12 +937,14 @@ zero_status_t launch_mm(const Operand* oa, const Operand* ob, zk::MmArgs a, cuda
     cfg.blockDim = dim3(zk::kMmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps, a);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -996,11 +1007,11 @@ LossPlan make_plan(const zero_lm_loss_args* a) {
     p.ldo = up(a->d, 8);
     p.d_bn = (int32_t)std::min<int64_t>(zk::kTileN, up(a->d, 16));
     // dz @ weight sums over the piece, dz^T @ hidden over the tokens, in one launch.  The first in parts, so that a tile of
-    // it is at most a quarter of what an SM has to do.
+    // it is at most half of what an SM has to do.
     const int64_t cg = cta_group(a->n), slots = kSlots / cg, columns = (a->d + p.d_bn - 1) / p.d_bn;
     const int64_t tiles0 = (a->n + 128 * cg - 1) / (128 * cg) * columns, kb0 = (p.piece + 63) / 64;
     const int64_t tiles1 = (p.piece + 128 * cg - 1) / (128 * cg) * columns, kb1 = (a->n + 63) / 64;
-    const int64_t share = std::max<int64_t>(8, (tiles0 * kb0 + tiles1 * kb1) / slots / 4);
+    const int64_t share = std::max<int64_t>(8, (tiles0 * kb0 + tiles1 * kb1) / slots / 2);
     p.splits = std::max<int64_t>(1, std::min<int64_t>({(kb0 + share - 1) / share, 32, (64 << 20) / (p.n256 * p.ldo * 4)}));
     int64_t at = 256;
     const auto take = [&](int64_t bytes) { const int64_t o = at; at += up(bytes, 256); return o; };
@@ -1196,7 +1207,8 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
     f.scale = base.scale;
     if (a->n == 0) return ZERO_OK;
     const bool wide = !(reinterpret_cast<uintptr_t>(a->grad_hidden) & 15) && a->d % 8 == 0;
-    return wide ? launch_rows(zk::finish_kernel<F, 8>, a->n, f, s, what) : launch_rows(zk::finish_kernel<F, 1>, a->n, f, s, what);
+    const auto kern = wide ? zk::finish_kernel<F, 8> : zk::finish_kernel<F, 1>;
+    return launch_after(kern, dim3((unsigned)persistent_grid(kern, (a->n + 7) / 8)), zk::kThreads, 0, s, what, f);
 }
 
 }  // namespace
@@ -1246,8 +1258,7 @@ extern "C" zero_status_t zero_lm_loss_forward(const zero_lm_loss_args* a, zero_s
     l.lse = a->lse;
     l.stats = a->stats;
     l.block_sums = reinterpret_cast<double*>(ws + p.sums);
-    zk::loss_kernel<<<persistent_grid(zk::loss_kernel, std::max(1, l.blocks)), zk::kThreads, 0, s>>>(l);
-    return after_launch(what);
+    return launch_after(zk::loss_kernel, dim3((unsigned)persistent_grid(zk::loss_kernel, std::max(1, l.blocks))), zk::kThreads, 0, s, what, l);
 }
 
 extern "C" zero_status_t zero_lm_loss_backward(const zero_lm_loss_args* a, zero_stream_t stream) {

@@ -83,7 +83,6 @@ struct MultiArgs {
 // The kernels are launched so that they may begin while the kernel before them
 // in the stream ends; what that kernel wrote is read after grid_wait() only.
 // The rows and the chunk map are read before it (multi_reset_kernel).
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------
 // Binding
