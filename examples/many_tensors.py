@@ -1,13 +1,14 @@
 """Train a small next-token model whose parameters stay where torch put them.
 
-    python examples/many_tensors.py [--steps 200] [--state-bits 8]
+    python examples/many_tensors.py [--steps 200] [--state-bits 8] [--operators]
 
 The parameters are bf16 tensors of a few hundred to a few ten thousand
 elements with fp32 masters; one MultiAdamW step updates all of them: global
 norm and clip, then AdamW with weight decay on the matrices only.  With
 --state-bits 8, m and v take 2.06 bytes a parameter instead of 8.  Half way the
 states go out as fp32 (a checkpoint's form) and into a second optimizer that
-goes on.
+goes on.  With --operators the package's embedding and language-model loss
+take the place of torch's lookup and of the head's product and cross entropy.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from zero_partitioned_mixed_replica_gb300 import layers  # noqa: E402
 from zero_partitioned_mixed_replica_gb300.engine import AdamW  # noqa: E402
 from zero_partitioned_mixed_replica_gb300.multi import MultiAdamW  # noqa: E402
 
@@ -33,14 +35,21 @@ def parameters(gen):
     return made
 
 
-def loss_of(p, x, y):
-    h = p["embed"][x].float()
+def block(p, h):
     h = h + torch.relu(h @ p["in"].float() + p["in_bias"].float()) @ p["out"].float()
-    h = h / (h.square().mean(-1, keepdim=True) + 1e-5).sqrt() * p["norm"].float()
-    return torch.nn.functional.cross_entropy(h @ p["head"].float(), y)
+    return h / (h.square().mean(-1, keepdim=True) + 1e-5).sqrt() * p["norm"].float()
 
 
-def train(steps=200, state_bits=32, seed=0, batch=512, say=print):
+def loss_of(p, x, y):
+    return torch.nn.functional.cross_entropy(block(p, p["embed"][x].float()) @ p["head"].float(), y)
+
+
+def loss_of_operators(p, x, y):
+    h = block(p, layers.embedding(p["embed"], x).float())
+    return layers.lm_loss(h.bfloat16(), p["head"].t().contiguous(), y)
+
+
+def train(steps=200, state_bits=32, seed=0, batch=512, operators=False, say=print):
     """Losses of a run whose optimizer is replaced half way by one with the same states."""
     gen = torch.Generator("cuda").manual_seed(seed)
     master = parameters(gen)
@@ -64,7 +73,7 @@ def train(steps=200, state_bits=32, seed=0, batch=512, say=print):
             opt.load_states(m, v)
             opt.resume_at(t)
         x = torch.randint(VOCAB, (batch,), generator=gen, device="cuda")
-        loss = loss_of(model, x, rule[x])
+        loss = (loss_of_operators if operators else loss_of)(model, x, rule[x])
         for g, n in zip(torch.autograd.grad(loss, [model[n] for n in names]), range(len(names))):
             grads[n].copy_(g)
         opt.step()
@@ -80,5 +89,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--state-bits", type=int, default=8, choices=[8, 32])
+    ap.add_argument("--operators", action="store_true")
     a = ap.parse_args()
-    train(a.steps, a.state_bits)
+    train(a.steps, a.state_bits, operators=a.operators)

@@ -789,14 +789,16 @@ zero_status_t zero_multi_device_error(const zero_multi* M, int32_t* bits);
 /* out[i] = round(scale * weight[ids[i]]), one binary32 product an element;
  * weight [vocab, d], ids [n], out [n, d].  An id outside 0 .. vocab-1 (padding)
  * gives a row of zeros.
- * vocab 1 .. 2^31-2, d 1 .. 2^20, n 0 .. 2^31-1, scale finite, else ZERO_ERR_INVALID. */
+ * vocab 1 .. 2^31-2, d 1 .. 2^20, n 0 .. 2^31-1, scale finite in binary32,
+ * else ZERO_ERR_INVALID. */
 zero_status_t zero_embedding_forward(const void* weight, const int64_t* ids, int64_t vocab, int64_t d, int64_t n,
                                      int32_t dtype, double scale, void* out, zero_stream_t stream);
 
 /* grad_weight[k] (+)= scale * sum of grad_out[i] over the i with ids[i] == k;
  * grad_out [n, d] of dtype, grad_weight [vocab, d] of grad_dtype.  Ids outside
  * 0 .. vocab-1 take no part.  Tokens are sorted by id (stable) and each id's
- * rows added in that order, in fixed pieces. */
+ * rows added in that order, in fixed pieces.  Three launches, the first of two
+ * CTAs at least (one sorts, one zeroes). */
 zero_status_t zero_embedding_workspace(int64_t vocab, int64_t d, int64_t n, int64_t* bytes);
 zero_status_t zero_embedding_backward(const void* grad_out, const int64_t* ids, int64_t vocab, int64_t d, int64_t n,
                                       int32_t dtype, int32_t grad_dtype, double scale, int32_t accumulate,
@@ -842,7 +844,8 @@ zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, co
  * ZERO_LOSS_SUM.  A target outside 0 .. vocab-1 (padding) makes a token not
  * count: its loss is 0, its row of grad_hidden zeros, its hidden state is
  * read by no product (it may hold NaN).  With no token that counts, the
- * loss and all gradients are zeros.
+ * loss and all gradients are zeros.  A logit that is NaN or +inf makes its
+ * token's loss NaN.
  *
  * hidden [n, d] with hidden_stride elements between rows (>= d), weight
  * [vocab, d], of dtype ZERO_BF16 or ZERO_FP16; targets [n]; losses, lse [n] and
@@ -864,7 +867,7 @@ zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, co
 enum { ZERO_LOSS_MEAN = 0, ZERO_LOSS_SUM = 1 };
 
 typedef struct zero_lm_loss_args {
-    int64_t n, d, vocab;      /* 0 .. 2^31-1, 1 .. 65536, 1 .. 2^31-2            */
+    int64_t n, d, vocab;      /* 0 .. 2^30, 1 .. 65536, 1 .. 2^30                */
     int64_t hidden_stride;
     int32_t dtype, reduction;
     int64_t piece;            /* columns of dz that exist at a time in the backward
@@ -892,7 +895,9 @@ zero_status_t zero_lm_loss_backward(const zero_lm_loss_args* a, zero_stream_t st
 
 /* Errors that the last call's kernels reported in this workspace, with the
  * bits of zero_step_state.error (*bits = 0: none).  Synchronises the device.
- * A forward call that reports one has NaN in stats[0]. */
+ * A forward call that reports one has NaN in stats[0], a backward call in the
+ * first rows of its gradients, so that a step with a norm and a decision is
+ * skipped. */
 zero_status_t zero_lm_loss_device_error(const void* workspace, int32_t* bits);
 
 /* Cap on the CTAs of every later launch by this library (process-wide;
@@ -919,7 +924,9 @@ int64_t zero_launch_count(int32_t reset);
  * Psi_pad / 32; a rank index: N_d).  An access outside is skipped, never
  * made, and counted; nothing traps.  This stands in for a memory checker
  * ("the kernel reads and writes only inside the buffers the header
- * promises").  The normal build compiles the checks out.
+ * promises").  The normal build compiles the checks out.  The kernels of the
+ * embedding, layer norm and loss have no such checks: every row, column and id
+ * is compared with its bound there in every build.
  *   zero_checked_build: 1 for a checked build, 0 otherwise.
  *   zero_bounds_violations: *count = accesses skipped on the current device
  *     since the last reset (0 in a normal build); reset != 0 zeroes the count.

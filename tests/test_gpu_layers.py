@@ -346,6 +346,7 @@ def test_captured_and_replayed_with_other_inputs():
             assert torch.equal(a, e)
     wg = w.clone().requires_grad_()
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        ids.add_(0)
         with pytest.raises(RuntimeError, match="capture"):
             L.embedding(wg, ids)
 

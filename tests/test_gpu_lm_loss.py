@@ -340,6 +340,7 @@ def test_captured_replayed_and_on_two_streams():
             assert torch.equal(a, e)
     x = h.clone().requires_grad_()
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        t.add_(0)
         with pytest.raises(RuntimeError, match="capture"):
             L.lm_loss(x, w, t)
 

@@ -29,7 +29,7 @@ NORM_GRAD = dict(grad_y=FAKE, gy_stride=4, x=FAKE, x_stride=4, weight=FAKE, mean
                  dtype=B.ZERO_FP16, grad_dtype=B.ZERO_FP32, accumulate=True, grad_x=FAKE, grad_weight=FAKE, grad_bias=FAKE,
                  workspace=FAKE, stream=0)
 SIZES = [dict(vocab=0), dict(vocab=2 ** 31 - 1), dict(d=0), dict(d=2 ** 20 + 1), dict(n=-1), dict(n=2 ** 31), dict(dtype=3),
-         dict(dtype=-1), dict(scale=float("nan")), dict(scale=float("inf"))]
+         dict(dtype=-1), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e300)]
 ROWS = [dict(rows=-1), dict(rows=2 ** 31), dict(d=0), dict(d=B.ZERO_MAX_NORM_DIM + 1, x_stride=1 << 20), dict(dtype=7), dict(x_stride=3)]
 
 
@@ -123,7 +123,7 @@ def _loss(**kw):
     return B.zero_lm_loss_args(**a)
 
 
-LOSS_SIZES = [dict(n=-1), dict(n=2 ** 31), dict(d=0), dict(d=65537, hidden_stride=65537), dict(vocab=0), dict(vocab=2 ** 31 - 1),
+LOSS_SIZES = [dict(n=-1), dict(n=2 ** 30 + 1), dict(d=0), dict(d=65537, hidden_stride=65537), dict(vocab=0), dict(vocab=2 ** 30 + 1),
               dict(hidden_stride=7), dict(dtype=B.ZERO_FP32), dict(dtype=-1), dict(piece=-1)]
 
 
@@ -134,7 +134,7 @@ def test_loss_forward_invalid(bad):
 
 
 @pytest.mark.parametrize("bad", LOSS_SIZES + [dict(hidden=0), dict(weight=0), dict(targets=0), dict(lse=0), dict(stats=0),
-                                              dict(workspace=0), dict(scale=float("inf")), dict(scale=float("nan"))])
+                                              dict(workspace=0), dict(scale=float("inf")), dict(scale=float("nan")), dict(scale=-1e39)])
 def test_loss_backward_invalid(bad):
     assert _status(B.zero_lm_loss_backward, _loss(**bad), 0) == B.ZERO_ERR_INVALID
 

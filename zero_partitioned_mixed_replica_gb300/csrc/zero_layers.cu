@@ -138,15 +138,22 @@ __device__ __forceinline__ void st_e(typename Store<F>::S* p, const float (&o)[E
     }
 }
 
-// What is already there, not through the read-only path: it is written by this launch.
+// What is already there, added; not through the read-only path: this launch writes it.
 template <class F, int E>
 __device__ __forceinline__ void add_e(const typename Store<F>::S* p, float (&o)[E]) {
+    if constexpr (sizeof(typename Store<F>::S) == 2 && E == 8) {
+        float old[8];
+        unpack8<F>(*reinterpret_cast<const uint4*>(p), old);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if constexpr (sizeof(typename Store<F>::S) == 4)
-            o[e] = __fadd_rn(p[e], o[e]);
-        else
-            o[e] = __fadd_rn(F::dec1(p[e]), o[e]);
+        for (int e = 0; e < 8; ++e) o[e] = __fadd_rn(old[e], o[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if constexpr (sizeof(typename Store<F>::S) == 4)
+                o[e] = __fadd_rn(p[e], o[e]);
+            else
+                o[e] = __fadd_rn(F::dec1(p[e]), o[e]);
+        }
     }
 }
 
@@ -1016,7 +1023,7 @@ extern "C" zero_status_t zero_embedding_forward(const void* weight, const int64_
     zero_status_t rc = check_embedding(what, vocab, d, n);
     if (rc != ZERO_OK) return rc;
     if (!known(dtype)) return fail(ZERO_ERR_INVALID, "zero_embedding_forward: unknown dtype");
-    if (!std::isfinite(scale)) return fail(ZERO_ERR_INVALID, "zero_embedding_forward: scale must be finite");
+    if (!std::isfinite((float)scale)) return fail(ZERO_ERR_INVALID, "zero_embedding_forward: scale must be finite in binary32");
     if (n == 0) return ZERO_OK;
     const int size = elem_size(dtype);
     if ((rc = check_elem_ptr(weight, size, "zero_embedding_forward weight")) != ZERO_OK) return rc;
@@ -1096,7 +1103,7 @@ extern "C" zero_status_t zero_embedding_backward(const void* grad_out, const int
     if (!known(dtype)) return fail(ZERO_ERR_INVALID, "zero_embedding_backward: unknown dtype");
     if (grad_dtype != dtype && grad_dtype != ZERO_FP32)
         return fail(ZERO_ERR_INVALID, "zero_embedding_backward: grad_dtype must be dtype or ZERO_FP32");
-    if (!std::isfinite(scale)) return fail(ZERO_ERR_INVALID, "zero_embedding_backward: scale must be finite");
+    if (!std::isfinite((float)scale)) return fail(ZERO_ERR_INVALID, "zero_embedding_backward: scale must be finite in binary32");
     const int size = elem_size(dtype), gsize = elem_size(grad_dtype);
     if ((rc = check_elem_ptr(grad_weight, gsize, "zero_embedding_backward grad_weight")) != ZERO_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -848,6 +848,25 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
     }
 }
 
+// After a backward call whose kernels gave up waiting the gradients are not
+// whole: NaN in their first rows makes the step that reads them skip.
+struct VerdictArgs {
+    const LossHead* head;
+    uint16_t* gh;
+    uint16_t* gw;
+    uint32_t d;
+    uint16_t nan;
+};
+
+__global__ void __launch_bounds__(32) verdict_kernel(const __grid_constant__ VerdictArgs a) {
+    grid_wait();
+    if (a.head->error == 0) return;
+    for (uint32_t c = threadIdx.x; c < a.d; c += 32) {
+        if (a.gh) a.gh[c] = a.nan;
+        if (a.gw) a.gw[c] = a.nan;
+    }
+}
+
 }  // namespace zk
 
 using namespace zero_detail;
@@ -1036,9 +1055,10 @@ LossPlan make_plan(const zero_lm_loss_args* a) {
 zero_status_t check_sizes(const char* what, const zero_lm_loss_args* a) {
     const std::string w = what;
     if (!a) return fail(ZERO_ERR_INVALID, w + ": NULL arguments");
-    if (a->n < 0 || a->n > 0x7FFFFFFF) return fail(ZERO_ERR_INVALID, w + ": n must be 0 .. 2^31-1");
+    constexpr int64_t kMost = 1 << 30;   // coordinates of tiles are 32-bit
+    if (a->n < 0 || a->n > kMost) return fail(ZERO_ERR_INVALID, w + ": n must be 0 .. 2^30");
     if (a->d < 1 || a->d > 65536) return fail(ZERO_ERR_INVALID, w + ": d must be 1 .. 65536");
-    if (a->vocab < 1 || a->vocab > 0x7FFFFFFE) return fail(ZERO_ERR_INVALID, w + ": vocab must be 1 .. 2^31-2");
+    if (a->vocab < 1 || a->vocab > kMost) return fail(ZERO_ERR_INVALID, w + ": vocab must be 1 .. 2^30");
     if (a->hidden_stride < a->d) return fail(ZERO_ERR_INVALID, w + ": rows overlap (hidden_stride < d)");
     if (a->dtype != ZERO_BF16 && a->dtype != ZERO_FP16) return fail(ZERO_ERR_INVALID, w + ": dtype must be ZERO_BF16 or ZERO_FP16");
     if (a->piece < 0) return fail(ZERO_ERR_INVALID, w + ": piece must be >= 0");
@@ -1192,23 +1212,27 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
         rc = launch_mm<CG, zk::MM_GRADS, F>(oa, ob, m, s, what);
         if (rc != ZERO_OK) return rc;
     }
-    if (!a->grad_hidden || direct) return ZERO_OK;
-    zk::FinishArgs f{};
-    f.part = base.part;
-    f.slot = reinterpret_cast<const int32_t*>(ws + p.slot);
-    f.out = static_cast<uint16_t*>(a->grad_hidden);
-    f.share = base.share;
-    f.scale_dev = a->scale_dev;
-    f.n = a->n;
-    f.split_rows = p.n256;
-    f.ld = p.ldo;
-    f.d = (uint32_t)a->d;
-    f.splits = (int32_t)p.splits;
-    f.scale = base.scale;
-    if (a->n == 0) return ZERO_OK;
-    const bool wide = !(reinterpret_cast<uintptr_t>(a->grad_hidden) & 15) && a->d % 8 == 0;
-    const auto kern = wide ? zk::finish_kernel<F, 8> : zk::finish_kernel<F, 1>;
-    return launch_after(kern, dim3((unsigned)persistent_grid(kern, (a->n + 7) / 8)), zk::kThreads, 0, s, what, f);
+    if (a->grad_hidden && !direct && a->n > 0) {
+        zk::FinishArgs f{};
+        f.part = base.part;
+        f.slot = reinterpret_cast<const int32_t*>(ws + p.slot);
+        f.out = static_cast<uint16_t*>(a->grad_hidden);
+        f.share = base.share;
+        f.scale_dev = a->scale_dev;
+        f.n = a->n;
+        f.split_rows = p.n256;
+        f.ld = p.ldo;
+        f.d = (uint32_t)a->d;
+        f.splits = (int32_t)p.splits;
+        f.scale = base.scale;
+        const bool wide = !(reinterpret_cast<uintptr_t>(a->grad_hidden) & 15) && a->d % 8 == 0;
+        const auto kern = wide ? zk::finish_kernel<F, 8> : zk::finish_kernel<F, 1>;
+        rc = launch_after(kern, dim3((unsigned)persistent_grid(kern, (a->n + 7) / 8)), zk::kThreads, 0, s, what, f);
+        if (rc != ZERO_OK) return rc;
+    }
+    const zk::VerdictArgs v{base.head, a->n > 0 ? static_cast<uint16_t*>(a->grad_hidden) : nullptr, static_cast<uint16_t*>(a->grad_weight),
+                            (uint32_t)a->d, (uint16_t)(bf16 ? 0x7FC0 : 0x7E00)};
+    return launch_after(zk::verdict_kernel, dim3(1), 32, 0, s, what, v);
 }
 
 }  // namespace
@@ -1266,7 +1290,7 @@ extern "C" zero_status_t zero_lm_loss_backward(const zero_lm_loss_args* a, zero_
     const char* what = "zero_lm_loss_backward";
     zero_status_t rc = check_sizes(what, a);
     if (rc != ZERO_OK) return rc;
-    if (!std::isfinite(a->scale)) return fail(ZERO_ERR_INVALID, std::string(what) + ": scale must be finite");
+    if (!std::isfinite((float)a->scale)) return fail(ZERO_ERR_INVALID, std::string(what) + ": scale must be finite in binary32");
     if ((rc = check_at(a->stats, 4, what, "stats")) != ZERO_OK) return rc;
     if (a->n > 0 && ((rc = check_at(a->hidden, 2, what, "hidden")) != ZERO_OK || (rc = check_at(a->targets, 8, what, "targets")) != ZERO_OK ||
                      (rc = check_at(a->lse, 4, what, "lse")) != ZERO_OK))
