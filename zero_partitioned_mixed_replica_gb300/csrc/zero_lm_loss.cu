@@ -10,7 +10,7 @@
 // written and twice read, everything else stays in L2 (129 MB): the products
 // bound the time, at the measured 1.9 PFLOP/s of a burst.
 //
-// Tokens that do not count are taken out first: `gather` copies the others'
+// Tokens that do not count are taken out first: pick_kernel copies the others'
 // hidden states next to one another (rows of 16-byte multiples, which TMA
 // wants), so that padding costs nothing and cannot spoil a sum.
 #include <algorithm>
@@ -54,7 +54,6 @@ struct MmProblem {
     int32_t n_off, k_off;     // where B's rows and K begin
     uint32_t idesc;           // without the columns
 };
-
 
 struct MmMaps {
     CUtensorMap a[2], b[2];
@@ -235,8 +234,8 @@ __device__ __forceinline__ void store_turned(uint16_t* p, int64_t ld, uint32_t r
 
 // The products of a launch, in tiles of (128 CG) x bn, persistent.  One warp
 // deals tiles from a counter (SMs differ in speed by a seventh under a power
-// limit, and tiles of two products in length), one loads blocks of K, up to
-// kStages ahead, one issues the products, eight take the accumulator; two
+// limit, and tiles of two products in length), one loads blocks of K, six ahead
+// for whole tiles, one issues the products, eight take the accumulator; two
 // accumulators take turns, so that a tile's epilogue runs under the next tile's
 // products.  MM_GRADS runs both products with dz, whose tiles fill one
 // another's last round.
@@ -283,6 +282,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
     if (warp == kMmaWarp) tmem_alloc<CG>(tmem_at, 512);
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i <= (MODE == MM_GRADS); ++i) {
+            if (a.p[i].m == 0) continue;
             prefetch_map(&maps.a[i]);
             prefetch_map(&maps.b[i]);
         }
