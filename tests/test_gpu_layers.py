@@ -57,7 +57,8 @@ def close(got, exact, tol):
 
 # -- embedding -------------------------------------------------------------------------------------------
 TABLES = [(1, 1, 1, BF, 0), (5, 3, 7, BF, 1), (97, 64, 512, BF, 0), (257, 8, 1000, HF, 0), (50257, 768, 1023, BF, 0),
-          (1000, 1600, 300, HF, 5), (300, 33, 2500, FP, 0), (65536, 16, 70000, FP, 2), (40, 4104, 64, BF, 8), (33, 1001, 9000, HF, 3)]
+          (1000, 1600, 300, HF, 5), (300, 33, 2500, FP, 0), (65536, 16, 70000, FP, 2), (40, 4104, 64, BF, 8), (33, 1001, 9000, HF, 3),
+          (7, 70000, 40, HF, 0), (5, 70001, 20, BF, 1)]
 
 
 @pytest.mark.parametrize("vocab,d,n,dtype,shift", TABLES)
@@ -290,6 +291,23 @@ def test_layer_norm_gradient_against_differences():
             args[0][j], args[1][j] = t + one, t - one
             diff = (f(*args[0]) - f(*args[1])) / float((args[0][j] - args[1][j]).double().sum())
             assert abs(float(diff) - float(grad.view(-1)[k])) <= noise + curve
+
+
+def test_without_leading_dimensions():
+    g = gen(11)
+    w, x = torch.randn(9, 40, generator=g, device="cuda"), torch.randn(1, 40, generator=g, device="cuda")
+    one = torch.tensor(4, device="cuda")
+    assert torch.equal(L.embedding_forward(w, one), w[4])
+    gw = torch.empty_like(w)
+    L.embedding_backward(x[0], one, gw)
+    assert torch.equal(gw[4], x[0]) and int((gw != 0).any(1).sum()) == 1
+    y, mean, rstd = L.layer_norm_forward(x, w[0], w[1])
+    y0, mean0, rstd0 = L.layer_norm_forward(x[0], w[0], w[1])
+    assert torch.equal(y0, y[0]) and mean0.shape == () and torch.equal(rstd0, rstd[0])
+    a, b = torch.empty(40, device="cuda"), torch.empty(40, device="cuda")
+    gx = L.layer_norm_backward(y, x, w[0], mean, rstd, a, b)
+    first = a.clone()
+    assert torch.equal(L.layer_norm_backward(y0, x[0], w[0], mean0, rstd0, a, b), gx[0]) and torch.equal(a, first)
 
 
 # -- how they are called ----------------------------------------------------------------------------------

@@ -89,7 +89,8 @@ def close(got, want, tol):
 CASES = [(1, 8, 16, BF, 0), (3, 7, 5, HF, 0), (2, 64, 1, BF, 0), (37, 64, 97, BF, 0), (64, 128, 256, BF, 0), (128, 72, 300, HF, 0),
          (129, 65, 257, BF, 0), (255, 768, 1000, BF, 0), (256, 256, 512, HF, 0), (300, 1600, 2011, BF, 0), (513, 264, 3001, HF, 5),
          (700, 100, 999, BF, 1), (1023, 136, 50257, BF, 0), (64, 4104, 513, HF, 8), (2048, 512, 4096, BF, 0), (5000, 48, 64, HF, 0),
-         (40, 33, 70001, BF, 3), (9, 1, 33, HF, 0), (2500, 1000, 8191, BF, 0)]
+         (40, 33, 70001, BF, 3), (9, 1, 33, HF, 0), (2500, 1000, 8191, BF, 0), (70000, 16, 300, BF, 0), (5, 65536, 50, BF, 0),
+         (200, 1600, 700, HF, 1), (130, 31, 513, BF, 7)]
 
 
 @pytest.mark.parametrize("n,d,vocab,dtype,shift", CASES)
@@ -132,6 +133,28 @@ def test_pieces_of_the_vocabulary(piece):
     gw = torch.full_like(w, NAN)
     close(L.lm_loss_backward(h, w, t, saved, gw, piece=piece), want[2], tol[2])
     close(gw, want[3], tol[3])
+
+
+def test_pieces_with_sums_in_memory_until_the_last():
+    # enough tokens that grad_hidden is not summed in parts: its binary32 sums pass from piece to piece, and the last rounds
+    for dtype in (BF, HF):
+        h, w, t = inputs(3000, 256, 3000, dtype)
+        want, tol = exact(h, w, t, 64.0)
+        _, _, saved = L.lm_loss_forward(h, w, t)
+        gw = torch.full_like(w, NAN)
+        close(L.lm_loss_backward(h, w, t, saved, gw, scale=64.0, piece=512), want[2], tol[2])
+        close(gw, want[3], tol[3])
+
+
+def test_one_token_without_leading_dimensions():
+    h, w, t = inputs(1, 64, 100, BF)
+    loss, losses, saved = L.lm_loss_forward(h, w, t)
+    gw = torch.empty_like(w)
+    gh = L.lm_loss_backward(h, w, t, saved, gw)
+    first = gw.clone()
+    loss0, losses0, saved0 = L.lm_loss_forward(h[0], w, t[0])
+    assert losses0.shape == () and torch.equal(loss0, loss) and torch.equal(losses0, losses[0])
+    assert torch.equal(L.lm_loss_backward(h[0], w, t[0], saved0, gw), gh[0]) and torch.equal(gw, first)
 
 
 @pytest.mark.parametrize("n", [1, 5, 128, 300])

@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     for (int64_t r = all + blockIdx.x; r < end; r += gridDim.x) copy_row<E>(a.dst + r * a.dst_stride, nullptr, a.d, threadIdx.x, kPickThreads);
 }
 
-// A matrix of rows x d, elements in a row next to one another, into rows `ld` apart.
+// A matrix of rows x d, elements next to one another from anywhere on, into
+// rows `ld` apart that begin on 16-byte boundaries.
 struct CopyArgs {
     const uint16_t* src;
     uint16_t* dst;
@@ -716,10 +717,27 @@ struct CopyArgs {
     uint32_t d;
 };
 
+// 8 elements a lane, from 5 aligned words shifted by 0 or 16 bits.  Words behind
+// the matrix are not read; what a row's last piece has of the next row lies
+// between d and ld, which no product reads.
 __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+    const uint32_t lane = threadIdx.x & 31, pieces = (a.d + 7) / 8;
     const int64_t step = (int64_t)gridDim.x * kThreads / 32;
-    for (int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; r < a.rows; r += step)
-        copy_row<1>(a.dst + r * a.ld, a.src + r * (int64_t)a.d, a.d, threadIdx.x & 31, 32);
+    const uintptr_t end = reinterpret_cast<uintptr_t>(a.src + a.rows * (int64_t)a.d);
+    for (int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; r < a.rows; r += step) {
+        const uint16_t* src = a.src + r * (int64_t)a.d;
+        uint4* dst = reinterpret_cast<uint4*>(a.dst + r * a.ld);
+#pragma unroll 2
+        for (uint32_t c = lane; c < pieces; c += 32) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(src + (size_t)c * 8), word = at & ~(uintptr_t)3;
+            uint32_t w[5];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) w[k] = word + 4 * k < end ? __ldg(reinterpret_cast<const uint32_t*>(word) + k) : 0u;
+            const uint32_t shift = (uint32_t)(at & 3) * 8;
+            dst[c] = make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift), __funnelshift_r(w[2], w[3], shift),
+                                __funnelshift_r(w[3], w[4], shift));
+        }
+    }
 }
 
 // ----------------------------------------------------------------------------
