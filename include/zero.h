@@ -784,7 +784,9 @@ zero_status_t zero_multi_device_error(const zero_multi* M, int32_t* bits);
  *   - n == 0 (or rows == 0) is allowed: pointers of empty arrays may be NULL,
  *     and weight gradients are zeroed (or, accumulating, left alone).
  *   - Same inputs, same bits: no sum depends on the order in which CTAs run,
- *     on zero_set_max_ctas or on the GPU's SM count. */
+ *     on zero_set_max_ctas or on the GPU's SM count.  (A layer norm's sums over
+ *     a row go by the width of the pieces that its tensors' addresses and
+ *     strides allow: elsewhere in memory the last bits may differ.) */
 
 /* out[i] = round(scale * weight[ids[i]]), one binary32 product an element;
  * weight [vocab, d], ids [n], out [n, d].  An id outside 0 .. vocab-1 (padding)
