@@ -105,6 +105,18 @@ __device__ __forceinline__ uint4 pack8(const float (&p)[8]) {
     return r;
 }
 
+// F::pack in one conversion.
+__device__ __forceinline__ uint32_t pack_pair(Bf16, float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+__device__ __forceinline__ uint32_t pack_pair(Fp16, float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
 // ----------------------------------------------------------------------------
 // Memory access: every big buffer is streamed once per step.
 // ----------------------------------------------------------------------------

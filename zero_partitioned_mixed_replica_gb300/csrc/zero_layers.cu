@@ -130,9 +130,10 @@ __device__ __forceinline__ void st_e(typename Store<F>::S* p, const float (&o)[E
             *p = o[0];
         }
     } else if constexpr (E == 8) {
-        *reinterpret_cast<uint4*>(p) = pack8<F>(o);
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_pair(F{}, o[0], o[1]), pack_pair(F{}, o[2], o[3]), pack_pair(F{}, o[4], o[5]),
+                                                  pack_pair(F{}, o[6], o[7]));
     } else if constexpr (E == 2) {
-        *reinterpret_cast<uint32_t*>(p) = F::pack(o[0], o[1]);
+        *reinterpret_cast<uint32_t*>(p) = pack_pair(F{}, o[0], o[1]);
     } else {
         *p = F::enc1(o[0]);
     }

@@ -198,10 +198,10 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[32], int
                 ld8w(p + h * 16, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    w[j] = F::pack(__fadd_rn(v[h * 16 + 2 * j], F::lo(w[j])), __fadd_rn(v[h * 16 + 2 * j + 1], F::hi(w[j])));
+                    w[j] = pack_pair(F{}, __fadd_rn(v[h * 16 + 2 * j], F::lo(w[j])), __fadd_rn(v[h * 16 + 2 * j + 1], F::hi(w[j])));
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = F::pack(v[h * 16 + 2 * j], v[h * 16 + 2 * j + 1]);
+                for (int j = 0; j < 8; ++j) w[j] = pack_pair(F{}, v[h * 16 + 2 * j], v[h * 16 + 2 * j + 1]);
             }
             st8w(p + h * 16, w);
         }
@@ -860,7 +860,8 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], f);
             }
-            if constexpr (E == 8) *reinterpret_cast<uint4*>(dst + c) = pack8<F>(x);
+            if constexpr (E == 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack_pair(F{}, x[0], x[1]), pack_pair(F{}, x[2], x[3]), pack_pair(F{}, x[4], x[5]),
+                                                                              pack_pair(F{}, x[6], x[7]));
             else dst[c] = F::enc1(x[0]);
         }
     }
