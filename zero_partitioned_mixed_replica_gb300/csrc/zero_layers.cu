@@ -410,9 +410,7 @@ __global__ void __launch_bounds__(kThreads, 4) embed_grad_kernel(const __grid_co
             if (on && id < a.vocab) {
                 const bool came = first && id == id_before, goes = next == id;
                 if (came || goes) {
-                    float* p = a.parts + ((size_t)q * 2 + (came ? 0 : 1)) * a.d + (size_t)c * E;
-#pragma unroll
-                    for (int k = 0; k < E; ++k) p[k] = sum[k];
+                    st_e<Fp32, E>(a.parts + ((size_t)q * 2 + (came ? 0 : 1)) * a.d + (size_t)c * E, sum);
                 } else {
                     embed_row<F, O, E>(a, id, c, sum);
                 }
@@ -495,9 +493,10 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
             const auto add = [&](uint32_t from, uint32_t r0, uint32_t count, uint32_t by, float (&sum)[E]) {
 #pragma unroll 4
                 for (uint32_t r = r0; r < count; r += by) {
-                    const float* p = a.parts + ((size_t)(from + r) * 2 + (r == 0)) * a.d + (size_t)c * E;
+                    float x[E];
+                    ld_e<Fp32, E>(a.parts + ((size_t)(from + r) * 2 + (r == 0)) * a.d + (size_t)c * E, x);
 #pragma unroll
-                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], p[k]);
+                    for (int k = 0; k < E; ++k) sum[k] = __fadd_rn(sum[k], x[k]);
                 }
             };
             if (parts > 0 && parts <= W && c < a.dv) {
@@ -612,7 +611,7 @@ __global__ void __launch_bounds__(WARP ? kThreads : 1024) norm_kernel(const __gr
 
 // The same with 16-byte pieces, a warp a row: the row stays in registers as it
 // lies in memory, so that 32 warps of an SM have one under way.  32768 x 1600
-// bf16: 39 us, 5.4 TB/s (of 6.7), two thirds of the issue slots in
+// bf16: 37 us, 5.7 TB/s (of 6.7), two thirds of the issue slots in
 // use; 18 warps with rows widened to binary32 took 50 us, 24 that
 // load a row ahead 41.
 template <class F, int NV>
@@ -706,11 +705,12 @@ __device__ __forceinline__ void team_barrier(int team) {
 // pieces of columns, and for all its rows their sums for the weight and bias,
 // in registers; between the two passes over a row also x - mean and gy * weight
 // (KEEP: up to 32 columns), while the next row's loads are under way.  What the
-// time goes to are instructions (half of the issue slots; 54% of the memory's
-// rate at 32768 x 1600 bf16, 67 us): widening, and 9 operations an element, two
+// time goes to are instructions (half of the issue slots; 55% of the memory's
+// rate at 32768 x 1600 bf16, 65 us): widening, and 9 operations an element, two
 // elements at a time.  16 columns and 16 warps: 32 columns and 8 warps issue a
 // fifth less and take 71 us; the weight in registers as well leaves 12 warps and
-// 77 us; rows through a ring of bulk copies in shared memory take 65 us.
+// 77 us; rows through a ring of bulk copies in shared memory took 65 us where this
+// form took 67.
 template <class F, int E, int NV, int G, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     using S = typename Store<F>::S;
@@ -991,7 +991,7 @@ zero_status_t check_embedding(const char* what, int64_t vocab, int64_t d, int64_
 // Tokens of a piece of the sorted list: few tokens in small pieces, to fill the
 // GPU; many in long ones, whose frequent ids leave fewer parts; between, of 16,
 // 24 and 32 what fills the last round of 152 SMs with 32 warps best (32768
-// tokens of 1600: pieces of 24, 28 us, and of 32, 34 us).
+// tokens of 1600: pieces of 24, 26 us, and of 32, 32 us).
 int64_t embed_piece(int64_t d, int64_t n) {
     if (n <= 8192) return 8;
     if (n > (1 << 20)) return 256;

@@ -852,10 +852,17 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
         for (uint32_t c = lane * E; c < a.d; c += 32 * E) {
             float x[E] = {};
             if (at >= 0) {
+#pragma unroll 4
                 for (int s = 0; s < a.splits; ++s) {
                     const float* p = a.part + (s * a.split_rows + at) * a.ld + c;
+                    if constexpr (E == 8) {   // ld % 8 == 0
+                        const float4 u = __ldcs(reinterpret_cast<const float4*>(p)), v = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+                        const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[e] = __fadd_rn(x[e], p[e]);
+                        for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(x[e], y[e]);
+                    } else {
+                        x[0] = __fadd_rn(x[0], *p);
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], f);
