@@ -873,8 +873,8 @@ typedef struct zero_lm_loss_args {
     int64_t hidden_stride;
     int32_t dtype, reduction;
     int64_t piece;            /* columns of dz that exist at a time in the backward
-                                 call; 0: chosen (up to 512 MiB of them); else
-                                 rounded up to a multiple of 256                */
+                                 call; 0: chosen (512 MiB of them, or 4096
+                                 columns); else rounded up to a multiple of 256 */
     const void* hidden;
     const void* weight;
     const int64_t* targets;
