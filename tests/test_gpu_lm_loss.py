@@ -39,14 +39,14 @@ def inputs(n, d, vocab, dtype, shift=0, padded=0.3, lean=6.0, seed=0):
     return h, w, t
 
 
-def exact(h, w, t, scale, share=None):
-    """(loss, losses, grad_hidden, grad_weight) in 64 bits and what each may be off."""
+def exact(h, w, t, scale, share=None, terms=None):
+    """(loss, losses, grad_hidden, grad_weight) in 64 bits and what each may be off; `terms` of a logit are added one after another."""
     dtype, (n, d), vocab = h.dtype, h.shape, w.shape[0]
     on = (t >= 0) & (t < vocab)
     hd = torch.where(on[:, None], h.double(), 0.0)
     wd = w.double()
     z = hd @ wd.t()
-    ez = (2 * d * U * (hd.abs() @ wd.abs().t())).amax(1, keepdim=True)       # of a row's logits
+    ez = (2 * (terms or d) * U * (hd.abs() @ wd.abs().t())).amax(1, keepdim=True)       # of a row's logits
     lse = z.logsumexp(1, keepdim=True)
     at = torch.where(on, t, 0)[:, None]
     zt = z.gather(1, at)
@@ -91,6 +91,21 @@ CASES = [(1, 8, 16, BF, 0), (3, 7, 5, HF, 0), (2, 64, 1, BF, 0), (37, 64, 97, BF
          (700, 100, 999, BF, 1), (1023, 136, 50257, BF, 0), (64, 4104, 513, HF, 8), (2048, 512, 4096, BF, 0), (5000, 48, 64, HF, 0),
          (40, 33, 70001, BF, 3), (9, 1, 33, HF, 0), (2500, 1000, 8191, BF, 0), (70000, 16, 300, BF, 0), (5, 65536, 50, BF, 0),
          (200, 1600, 700, HF, 1), (130, 31, 513, BF, 7)]
+
+
+@pytest.mark.parametrize("n,d,vocab,dtype", [(1, 512, 100, BF), (128, 513, 300, HF), (37, 1024, 1001, BF), (5, 1032, 65, HF), (100, 4100, 2050, BF),
+                                             (3, 16383, 129, BF), (7, 65536, 200, HF)])
+def test_few_tokens_add_a_logit_in_runs(n, d, vocab, dtype):
+    """Up to 128 tokens: the tensor cores add up to 512 terms, then the d / 512 (or fewer) sums, of alike lengths, are added."""
+    h, w, t = inputs(n, d, vocab, dtype)
+    want, tol = exact(h, w, t, 1.0, terms=512 + -(-d // 512))
+    loss, losses, saved = L.lm_loss_forward(h, w, t)
+    close(losses, want[1], tol[1])
+    close(loss, want[0], tol[0])
+    gw = torch.empty_like(w)
+    gh = L.lm_loss_backward(h, w, t, saved, gw)
+    close(gh, want[2], tol[2])
+    close(gw, want[3], tol[3])
 
 
 @pytest.mark.parametrize("n,d,vocab,dtype,shift", CASES)

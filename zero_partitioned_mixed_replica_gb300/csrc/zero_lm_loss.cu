@@ -29,6 +29,8 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kTileWarp = 10;
 constexpr int kMmThreads = 32 * 11;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows of 64
 constexpr int kTileN = 256;           // columns of a tile, at most
+constexpr int kRun = 8;               // blocks of K that the tensor cores add up of a logit for few tokens, at most (MmTile)
+constexpr int kFewN = 128;            // columns of a tile of logits then, at most
 
 enum { MM_STATS = 0, MM_DZ = 1, MM_GRADS = 2 };
 enum { ROWS_M = 1, ROWS_K = 2 };  // which extent is the number of tokens that count
@@ -96,11 +98,19 @@ struct MmShape {
     static constexpr int kBytes = 1024 + kOps + kTurn + kSync;  // and alignment
 };
 
+// The tensor cores cut the sums that they keep instead of rounding them: errors
+// of one sign, 1e-6 of a logit over 2000 of K.  For up to 128 tokens (CG = 1),
+// whose losses no mean over many smooths and whose products wait for the
+// weight, they add a logit's K in runs of up to 512, and the runs are added in
+// registers: losses off by up to 1.8e-6 relatively before, below 1e-6 since, in
+// the same time (a forward call of 37 x 768 x 50257: 40.9 us before, 40.1
+// since).  Tiles are then kFewN wide: for more tokens a thread would hold 128
+// sums of a tile twice as wide, which spills.
 struct alignas(16) MmTile {
     int32_t p;                // problem, or -1: no more tiles
     int32_t m, n, split;      // row tile, column tile
     int32_t kb0, kb1;         // blocks of kTileK
-    int32_t width, pad;       // columns that exist
+    int32_t width, run;       // columns that exist; blocks of a run
 };
 
 // Extents of one product, with the tokens that count.
@@ -132,7 +142,7 @@ struct MmExtent {
         r.kb0 = (int32_t)((int64_t)kblocks * r.split / p.splits);
         r.kb1 = (int32_t)((int64_t)kblocks * (r.split + 1) / p.splits);
         r.width = (int32_t)min((int64_t)p.bn, p.n - (int64_t)r.n * p.bn);
-        r.pad = 0;
+        r.run = 0;
         return r;
     }
 };
@@ -154,10 +164,13 @@ struct MmGrid {
             if (t >= lead) t -= lead;
             MmTile r = p1 ? e1.tile(a.p[1], t) : e0.tile(a.p[0], t);
             r.p = p1;
+            r.run = max(1, r.kb1 - r.kb0);
             return r;
         } else {
             MmTile r = e0.tile(a.p[0], t);
             r.p = 0;
+            const int32_t blocks = r.kb1 - r.kb0, runs = CG == 1 ? (blocks + kRun - 1) / kRun : 1;   // of about one length
+            r.run = (blocks + runs - 1) / runs;
             return r;
         }
     }
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
         if (!ok) return t;
         const uint32_t at = smem_u32(ring + tile_slot);
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(t.p), "=r"(t.m), "=r"(t.n), "=r"(t.split) : "r"(at) : "memory");
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(t.kb0), "=r"(t.kb1), "=r"(t.width), "=r"(t.pad) : "r"(at + 16) : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(t.kb0), "=r"(t.kb1), "=r"(t.width), "=r"(t.run) : "r"(at + 16) : "memory");
         mbar_arrive_remote(leader(tile_empty + tile_slot));
         if (++tile_slot == RING) {
             tile_slot = 0;
@@ -324,14 +337,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                 if (!ok) break;
                 MmTile w;
                 w.p = -1;
-                w.m = w.n = w.split = w.kb0 = w.kb1 = w.width = w.pad = 0;
+                w.m = w.n = w.split = w.kb0 = w.kb1 = w.width = w.run = 0;
                 if (t < tiles) w = grid.tile(a, t);
 #pragma unroll
                 for (int r = 0; r < CG; ++r) {
                     const uint32_t to = CG == 2 ? map_rank(smem_u32(ring + tile_slot), r) : smem_u32(ring + tile_slot);
                     const uint32_t bar = CG == 2 ? map_rank(smem_u32(tile_full + tile_slot), r) : smem_u32(tile_full + tile_slot);
                     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w.p), "r"(w.m), "r"(w.n), "r"(w.split) : "memory");
-                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16), "r"(w.kb0), "r"(w.kb1), "r"(w.width), "r"(w.pad) : "memory");
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16), "r"(w.kb0), "r"(w.kb1), "r"(w.width), "r"(w.run) : "memory");
                     mbar_arrive_cluster(bar);
                 }
                 if (w.p < 0) break;
@@ -409,10 +422,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
             int stage = 0;
             uint32_t phase = 0;
             int64_t done = 0;   // accumulators
-            const auto multiply = [&](auto a_mn_, const MmTile& w, uint32_t idesc, uint32_t acc) {
+            const auto multiply = [&](auto a_mn_, int32_t kb0, int32_t kb1, uint32_t idesc, uint32_t acc) {
                 constexpr bool A_MN = decltype(a_mn_)::value;
                 const uint64_t da0 = operand_desc(smem_u32(ops), A_MN), db0 = operand_desc(smem_u32(ops) + Shape::kA, B_MN);
-                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                for (int32_t kb = kb0; kb < kb1; ++kb) {
                     ok = mbar_wait_bounded(full + stage, phase);
                     if (!ok) break;
                     tc_fence_after();
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
 #pragma unroll
                     for (int j = 0; j < kTileK / 16; ++j)
                         tc_mma<CG>(acc, da0 + at + j * (A_MN ? kStepMN : kStepK), db0 + at + j * (B_MN ? kStepMN : kStepK), idesc,
-                                   kb > w.kb0 || j > 0);
+                                   kb > kb0 || j > 0);
                     tc_commit<CG>(empty + stage);
                     if (++stage == ST) {
                         stage = 0;
@@ -432,19 +445,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                 if (w.kb0 == w.kb1) continue;
                 // the columns: of the last tile no more than there are (logits: what the box has loaded beyond them does no harm)
                 const uint32_t columns = (uint32_t)(B_MN ? (w.width + 15) / 16 * 16 : a.p[0].bn) >> 3 << 17;
-                const int buf = (int)(done & 1);
-                ok = mbar_wait_bounded(acc_empty + buf, (uint32_t)((done >> 1) & 1) ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                if constexpr (MODE == MM_GRADS) {
-                    if (w.p == 0) multiply(std::false_type{}, w, a.p[0].idesc | columns, tmem + buf * kTileN);
-                    else multiply(std::true_type{}, w, a.p[1].idesc | columns, tmem + buf * kTileN);
-                } else {
-                    multiply(std::false_type{}, w, a.p[0].idesc | columns, tmem + buf * kTileN);
+                for (int32_t k0 = w.kb0; k0 < w.kb1 && ok; k0 += w.run) {
+                    const int32_t k1 = min(k0 + w.run, w.kb1);
+                    const int buf = (int)(done & 1);
+                    ok = mbar_wait_bounded(acc_empty + buf, (uint32_t)((done >> 1) & 1) ^ 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if constexpr (MODE == MM_GRADS) {
+                        if (w.p == 0) multiply(std::false_type{}, k0, k1, a.p[0].idesc | columns, tmem + buf * kTileN);
+                        else multiply(std::true_type{}, k0, k1, a.p[1].idesc | columns, tmem + buf * kTileN);
+                    } else {
+                        multiply(std::false_type{}, k0, k1, a.p[0].idesc | columns, tmem + buf * kTileN);
+                    }
+                    if (!ok) break;
+                    tc_commit<CG>(acc_full + buf);
+                    ++done;
                 }
                 if (!ok) break;
-                tc_commit<CG>(acc_full + buf);
-                ++done;
             }
         }
     } else {
@@ -468,116 +485,161 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
             w.kb0 = __shfl_sync(0xFFFFFFFFu, w.kb0, 0);
             w.kb1 = __shfl_sync(0xFFFFFFFFu, w.kb1, 0);
             w.width = __shfl_sync(0xFFFFFFFFu, w.width, 0);
+            w.run = __shfl_sync(0xFFFFFFFFu, w.run, 0);
             const MmProblem& p = a.p[w.p];
-            const bool any = w.kb0 < w.kb1;   // without a token that counts the sums are zeros
-            const int buf = (int)(done & 1);
             const int64_t row0 = (int64_t)w.m * 128 * CG + rank * 128 + (warp & 3) * 32, row = row0 + lane;
             const bool row_on = row < (w.p == 0 ? rows0 : rows1);
             const int64_t n0 = (int64_t)w.n * p.bn;
-            const int c0 = half * 128, c1 = half == 0 ? min(w.width, 128) : w.width;
-            if (any) {
-                ok = mbar_wait_bounded(acc_full + buf, (uint32_t)(done >> 1) & 1);
+            constexpr int HALF = CG == 1 && MODE != MM_GRADS ? kFewN / 2 : kTileN / 2;
+            const int c0 = half * HALF, c1 = half == 0 ? min(w.width, HALF) : w.width;
+            // the next accumulator is full; it has been read
+            const auto take = [&]() -> uint32_t {
+                ok = mbar_wait_bounded(acc_full + (done & 1), (uint32_t)(done >> 1) & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
                 tc_fence_after();
-            }
-            const uint32_t at = tmem + buf * kTileN + ((uint32_t)((warp & 3) * 32) << 16);
-            [[maybe_unused]] float top = -INFINITY, sum = 0.0f, lse = 0.0f;
-            [[maybe_unused]] int target = -1;
-            if constexpr (MODE != MM_GRADS)
-                if (row_on) target = a.target[row] - (int)n0 - p.n_off;
-            if constexpr (MODE == MM_DZ) lse = row_on ? a.lse[a.row_of[row]] : 0.0f;
-            for (int c = c0; c < c1; c += 32) {
-                float v[32];
-                if (any) {
-                    uint32_t u[32];
-                    tc_ld32(at + c, u);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                }
-                const int left = c1 - c;
-                if constexpr (MODE == MM_STATS) {
-                    if (left < 32) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j >= left) v[j] = -INFINITY;
-                    }
-                    if (target >= c && target < min(c + 32, c1)) {
-                        // predicated stores: of a choice among registers the compiler makes an array in local memory
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %0, %1;\n\t@p st.global.f32 [%2], %3;\n\t}" ::"r"(target - c), "r"(j),
-                                         "l"(a.z_target + row), "f"(v[j])
-                                         : "memory");
-                    }
-                    stats_chunk(v, top, sum);
-                } else if constexpr (MODE == MM_DZ) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = ex2(__fmul_rn(__fsub_rn(v[j], lse), kLog2e));
-                    if (target >= c && target < min(c + 32, c1)) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __fsub_rn(v[j], j == target - c ? 1.0f : 0.0f);
-                    }
-                    if (left < 32) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j >= left) v[j] = 0.0f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = row_on ? __fmul_rn(v[j], a.dz_scale) : 0.0f;
-                    store_row<F>(a.dz + row * a.dz_ld + n0 + c, v, left, false);   // 16 columns at a time: bn % 16 == 0
-                } else if (w.p == 0) {
-                    if (row_on) {
-                        float* q = a.part + (w.split * a.split_rows + row) * a.part_cols + n0 + c;
-                        if (a.part_add) {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                if (h * 8 < left) {   // part_cols % 8 == 0
-                                    uint32_t u[8];
-                                    ld8w(q + h * 8, u);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) v[h * 8 + j] = __fadd_rn(v[h * 8 + j], __uint_as_float(u[j]));
-                                }
-                            }
-                        }
-                        if (a.gh) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
-                            store_row<F>(a.gh + a.row_of[row] * a.d + n0 + c, v, left, false);
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                if (h * 8 < left) {
-                                    uint32_t u[8];
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[h * 8 + j]);
-                                    st8w(q + h * 8, u);
-                                }
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
-                    if (a.gw_vec) {
-                        if (row_on) store_row<F>(a.gw + row * a.d + n0 + c, v, left, a.gw_add);
-                    } else {
-                        store_turned<F>(a.gw + row0 * a.d + n0 + c, a.d, __ballot_sync(0xFFFFFFFFu, row_on), v, left, a.gw_add, sh[warp]);
-                    }
-                }
-            }
-            if (any) {
+                return tmem + (uint32_t)(done & 1) * kTileN + ((uint32_t)((warp & 3) * 32) << 16);
+            };
+            const auto give = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(leader(acc_empty + buf));
+                if (lane == 0) mbar_arrive_remote(leader(acc_empty + (done & 1)));
                 ++done;
+            };
+            if constexpr (MODE != MM_GRADS) {
+                const int target = row_on ? a.target[row] - (int)n0 - p.n_off : -1;
+                [[maybe_unused]] float top = -INFINITY, sum = 0.0f, lse = 0.0f;
+                if constexpr (MODE == MM_DZ) lse = row_on ? a.lse[a.row_of[row]] : 0.0f;
+                // 32 columns of logits from c on, `left` of them (or more) in this half
+                const auto use = [&](float (&v)[32], int c, int left) {
+                    if constexpr (MODE == MM_STATS) {
+                        if (left < 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j >= left) v[j] = -INFINITY;
+                        }
+                        if (target >= c && target < min(c + 32, c1)) {
+                            // predicated stores: of a choice among registers the compiler makes an array in local memory
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %0, %1;\n\t@p st.global.f32 [%2], %3;\n\t}" ::"r"(target - c), "r"(j),
+                                             "l"(a.z_target + row), "f"(v[j])
+                                             : "memory");
+                        }
+                        stats_chunk(v, top, sum);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = ex2(__fmul_rn(__fsub_rn(v[j], lse), kLog2e));
+                        if (target >= c && target < min(c + 32, c1)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = __fsub_rn(v[j], j == target - c ? 1.0f : 0.0f);
+                        }
+                        if (left < 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j >= left) v[j] = 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = row_on ? __fmul_rn(v[j], a.dz_scale) : 0.0f;
+                        store_row<F>(a.dz + row * a.dz_ld + n0 + c, v, left, false);   // 16 columns at a time: bn % 16 == 0
+                    }
+                };
+                if constexpr (CG == 1) {
+                    float z[2][32];
+                    for (int32_t k0 = w.kb0; k0 < w.kb1; k0 += w.run) {
+                        const uint32_t at = take();
+                        if (!ok) break;
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (c0 + g * 32 < c1) {
+                                uint32_t u[32];
+                                tc_ld32(at + c0 + g * 32, u);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    z[g][j] = k0 == w.kb0 ? __uint_as_float(u[j]) : __fadd_rn(z[g][j], __uint_as_float(u[j]));
+                            }
+                        }
+                        give();
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        if (c0 + g * 32 < c1) use(z[g], c0 + g * 32, c1 - c0 - g * 32);
+                } else {
+                    const uint32_t at = take();
+                    if (!ok) break;
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t u[32];
+                        tc_ld32(at + c, u);
+                        tc_wait_ld();
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+                        use(v, c, c1 - c);
+                    }
+                    give();
+                }
+                if constexpr (MODE == MM_STATS)
+                    if (row_on) a.parts[row * a.part_ld + 2 * w.n + half] = make_float2(top, sum);
+            } else {
+                const bool any = w.kb0 < w.kb1;   // without a token that counts the sums are zeros
+                const uint32_t at = any ? take() : 0;
+                if (!ok) break;
+                for (int c = c0; c < c1; c += 32) {
+                    float v[32];
+                    if (any) {
+                        uint32_t u[32];
+                        tc_ld32(at + c, u);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    }
+                    const int left = c1 - c;
+                    if (w.p == 0) {
+                        if (row_on) {
+                            float* q = a.part + (w.split * a.split_rows + row) * a.part_cols + n0 + c;
+                            if (a.part_add) {
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    if (h * 8 < left) {   // part_cols % 8 == 0
+                                        uint32_t u[8];
+                                        ld8w(q + h * 8, u);
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) v[h * 8 + j] = __fadd_rn(v[h * 8 + j], __uint_as_float(u[j]));
+                                    }
+                                }
+                            }
+                            if (a.gh) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
+                                store_row<F>(a.gh + a.row_of[row] * a.d + n0 + c, v, left, false);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    if (h * 8 < left) {
+                                        uint32_t u[8];
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[h * 8 + j]);
+                                        st8w(q + h * 8, u);
+                                    }
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __fmul_rn(v[j], f);
+                        if (a.gw_vec) {
+                            if (row_on) store_row<F>(a.gw + row * a.d + n0 + c, v, left, a.gw_add);
+                        } else {
+                            store_turned<F>(a.gw + row0 * a.d + n0 + c, a.d, __ballot_sync(0xFFFFFFFFu, row_on), v, left, a.gw_add, sh[warp]);
+                        }
+                    }
+                }
+                if (any) give();
             }
-            if constexpr (MODE == MM_STATS)
-                if (row_on) a.parts[row * a.part_ld + 2 * w.n + half] = make_float2(top, sum);
         }
     }
     if (!ok) atomicOr(&a.head->error, ZERO_DEVERR_WAIT_TIMEOUT);
@@ -1002,20 +1064,21 @@ constexpr int64_t kSlots = 152;   // SMs of a GB300: what the splits of work are
 
 int cta_group(int64_t n) { return n <= 128 ? 1 : 2; }
 
-// Columns of a tile: as few tiles as there are at 256, of one width.
-int32_t even_tile(int64_t n) {
-    const int64_t tiles = (n + zk::kTileN - 1) / zk::kTileN;
-    return (int32_t)std::min<int64_t>(zk::kTileN, up((n + tiles - 1) / tiles, 16));
+// Columns of a tile: as few tiles as there are at the widest, of one width.
+int32_t even_tile(int64_t n, int64_t widest) {
+    const int64_t tiles = (n + widest - 1) / widest;
+    return (int32_t)std::min<int64_t>(widest, up((n + tiles - 1) / tiles, 16));
 }
 
 // Columns of a tile of logits.  Few tokens: the weight's read bounds the time,
 // and what the busiest SM has of it: rounds of tiles times their width.
 int32_t logit_tile(int64_t n, int64_t vocab) {
     const int64_t cg = cta_group(n), slots = kSlots / cg, rows = (n + 128 * cg - 1) / (128 * cg);
+    const int64_t widest = cg == 1 ? zk::kFewN : zk::kTileN;
     const auto cost = [&](int64_t bn) { return ((vocab + bn - 1) / bn * rows + slots - 1) / slots * bn; };
-    int64_t best = even_tile(vocab);
+    int64_t best = even_tile(vocab, widest);
     if ((vocab + best - 1) / best * rows < 8 * slots)
-        for (int64_t bn = zk::kTileN; bn >= 96; bn -= 16)
+        for (int64_t bn = widest; bn >= 96; bn -= 16)
             if (cost(bn) < cost(best)) best = bn;
     return (int32_t)best;
 }
@@ -1202,7 +1265,7 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
     zero_status_t rc = ZERO_OK;
     for (int64_t i = 0; i < p.pieces; ++i) {
         const int64_t v0 = i * p.piece, cols = std::min(p.piece, a->vocab - v0);
-        const int32_t bn = std::min<int32_t>(p.logit_bn, even_tile(cols));
+        const int32_t bn = std::min<int32_t>(p.logit_bn, even_tile(cols, CG == 1 ? zk::kFewN : zk::kTileN));
         {   // the logits of the piece, and their gradient
             const Operand h{ws + p.hidden, p.n256, a->d, p.ldh, 128}, w{weight, a->vocab, a->d, p.ldw, bn / CG};
             zk::MmArgs m = base;
