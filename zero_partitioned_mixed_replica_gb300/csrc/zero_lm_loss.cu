@@ -103,9 +103,8 @@ struct MmShape {
 // whose losses no mean over many smooths and whose products wait for the
 // weight, they add a logit's K in runs of up to 512, and the runs are added in
 // registers: losses off by up to 1.8e-6 relatively before, below 1e-6 since, in
-// the same time (a forward call of 37 x 768 x 50257: 40.9 us before, 40.1
-// since).  Tiles are then kFewN wide: for more tokens a thread would hold 128
-// sums of a tile twice as wide, which spills.
+// the same time.  Tiles are then kFewN wide: for more tokens a thread would hold
+// 128 sums of a tile twice as wide, which spills.
 struct alignas(16) MmTile {
     int32_t p;                // problem, or -1: no more tiles
     int32_t m, n, split;      // row tile, column tile
@@ -888,7 +887,9 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ 
     }
 }
 
-// grad_hidden: the splits' sums times the factors, by token; zeros for tokens that do not count.
+// grad_hidden: the splits' sums times the factors, by token; zeros for tokens
+// that do not count.  A warp takes 32 loads' width of a row: with a row each, 45
+// tokens of 2048 in 17 splits took 58 us instead of 11.
 struct FinishArgs {
     const float* part;      // [splits][split_rows][ld]
     const int32_t* slot;
@@ -908,31 +909,33 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
     float f = __fmul_rn(a.scale, *a.share);
     if (a.scale_dev) f = __fmul_rn(f, *a.scale_dev);
     const int64_t step = (int64_t)gridDim.x * kThreads / 32;
-    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; i < a.n; i += step) {
+    const uint32_t pieces = (a.d + 32 * E - 1) / (32 * E);
+    for (int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32; item < a.n * pieces; item += step) {
+        const int64_t i = item / pieces;
+        const uint32_t c = ((uint32_t)(item - i * pieces) * 32 + lane) * E;
+        if (c >= a.d) continue;
         const int32_t at = a.slot[i];
-        uint16_t* dst = a.out + i * (int64_t)a.d;
-        for (uint32_t c = lane * E; c < a.d; c += 32 * E) {
-            float x[E] = {};
-            if (at >= 0) {
-#pragma unroll 4
-                for (int s = 0; s < a.splits; ++s) {
-                    const float* p = a.part + (s * a.split_rows + at) * a.ld + c;
-                    if constexpr (E == 8) {   // ld % 8 == 0
-                        const float4 u = __ldcs(reinterpret_cast<const float4*>(p)), v = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-                        const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        float x[E] = {};
+        if (at >= 0) {
+#pragma unroll 8
+            for (int s = 0; s < a.splits; ++s) {
+                const float* p = a.part + (s * a.split_rows + at) * a.ld + c;
+                if constexpr (E == 8) {   // ld % 8 == 0
+                    const float4 u = __ldcs(reinterpret_cast<const float4*>(p)), v = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+                    const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(x[e], y[e]);
-                    } else {
-                        x[0] = __fadd_rn(x[0], *p);
-                    }
+                    for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(x[e], y[e]);
+                } else {
+                    x[0] = __fadd_rn(x[0], *p);
                 }
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], f);
             }
-            if constexpr (E == 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack_pair(F{}, x[0], x[1]), pack_pair(F{}, x[2], x[3]), pack_pair(F{}, x[4], x[5]),
-                                                                              pack_pair(F{}, x[6], x[7]));
-            else dst[c] = F::enc1(x[0]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = __fmul_rn(x[e], f);
         }
+        uint16_t* dst = a.out + i * (int64_t)a.d + c;
+        if constexpr (E == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(pack_pair(F{}, x[0], x[1]), pack_pair(F{}, x[2], x[3]), pack_pair(F{}, x[4], x[5]),
+                                                                      pack_pair(F{}, x[6], x[7]));
+        else *dst = F::enc1(x[0]);
     }
 }
 
@@ -1070,15 +1073,16 @@ int32_t even_tile(int64_t n, int64_t widest) {
     return (int32_t)std::min<int64_t>(widest, up((n + tiles - 1) / tiles, 16));
 }
 
-// Columns of a tile of logits.  Few tokens: the weight's read bounds the time,
-// and what the busiest SM has of it: rounds of tiles times their width.
+// Columns of a tile of logits.  Few tokens: loads bound the time, and what the
+// busiest SM has of them: rounds of tiles times their rows, for single CTAs
+// (CG = 1) those of the hidden states too.
 int32_t logit_tile(int64_t n, int64_t vocab) {
     const int64_t cg = cta_group(n), slots = kSlots / cg, rows = (n + 128 * cg - 1) / (128 * cg);
-    const int64_t widest = cg == 1 ? zk::kFewN : zk::kTileN;
-    const auto cost = [&](int64_t bn) { return ((vocab + bn - 1) / bn * rows + slots - 1) / slots * bn; };
+    const int64_t widest = cg == 1 ? zk::kFewN : zk::kTileN, least = cg == 1 ? 32 : 96, more = cg == 1 ? 128 : 0;
+    const auto cost = [&](int64_t bn) { return ((vocab + bn - 1) / bn * rows + slots - 1) / slots * (bn + more); };
     int64_t best = even_tile(vocab, widest);
     if ((vocab + best - 1) / best * rows < 8 * slots)
-        for (int64_t bn = widest; bn >= 96; bn -= 16)
+        for (int64_t bn = widest; bn >= least; bn -= 16)
             if (cost(bn) < cost(best)) best = bn;
     return (int32_t)best;
 }
@@ -1190,13 +1194,14 @@ zero_status_t gather_inputs(const zero_lm_loss_args* a, const LossPlan& p, bool 
     k.dst = reinterpret_cast<uint16_t*>(ws + p.hidden);
     k.src_stride = a->hidden_stride;
     k.dst_stride = p.ldh;
-    k.rows = p.n256;
+    k.rows = up(std::max<int64_t>(a->n, 1), 128 * cta_group(a->n));   // whole tiles
     k.vocab = a->vocab;
     k.n = (uint32_t)a->n;
     k.d = (uint32_t)a->d;
     const bool wide = !(reinterpret_cast<uintptr_t>(a->hidden) & 15) && a->d % 8 == 0 && (a->hidden_stride % 8 == 0 || a->n == 1);
     const auto kern = wide ? zk::pick_kernel<8> : zk::pick_kernel<1>;
-    const int grid = persistent_grid(kern, std::min<int64_t>((a->n + 15) / 16, 2 * kSlots), 0, zk::kPickThreads);
+    // 16 tokens a CTA, but CTAs enough for the zeros behind a few tokens: 1 CTA took 30 us for 255 rows, 64 take 6
+    const int grid = persistent_grid(kern, std::min<int64_t>(std::max<int64_t>((a->n + 15) / 16, 64), 2 * kSlots), 0, zk::kPickThreads);
     k.per_cta = (uint32_t)((a->n + grid - 1) / grid);
     kern<<<grid, zk::kPickThreads, 0, s>>>(k);
     const zero_status_t rc = after_launch(what);
@@ -1316,7 +1321,8 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
         f.scale = base.scale;
         const bool wide = !(reinterpret_cast<uintptr_t>(a->grad_hidden) & 15) && a->d % 8 == 0;
         const auto kern = wide ? zk::finish_kernel<F, 8> : zk::finish_kernel<F, 1>;
-        rc = launch_after(kern, dim3((unsigned)persistent_grid(kern, (a->n + 7) / 8)), zk::kThreads, 0, s, what, f);
+        const int64_t width = wide ? 32 * 8 : 32, items = a->n * ((a->d + width - 1) / width);
+        rc = launch_after(kern, dim3((unsigned)persistent_grid(kern, (items + 7) / 8)), zk::kThreads, 0, s, what, f);
         if (rc != ZERO_OK) return rc;
     }
     const zk::VerdictArgs v{base.head, a->n > 0 ? static_cast<uint16_t*>(a->grad_hidden) : nullptr, static_cast<uint16_t*>(a->grad_weight),
