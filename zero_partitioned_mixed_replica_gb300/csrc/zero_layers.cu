@@ -75,6 +75,11 @@ struct Raw {
             else w[0] = __ldg(p);
         }
     }
+    // What is made of the words is made from here on, not where they were loaded.
+    __device__ __forceinline__ void hold() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) asm volatile("" : "+r"(w[k]));
+    }
     __device__ __forceinline__ void get(float (&o)[E]) const {
         if constexpr (sizeof(S) == 4) {
 #pragma unroll
@@ -710,13 +715,17 @@ __device__ __forceinline__ void team_barrier(int team) {
 // elements at a time.  16 columns and 16 warps: 32 columns and 8 warps issue a
 // fifth less and take 71 us; the weight in registers as well leaves 12 warps and
 // 77 us; rows through a ring of bulk copies in shared memory took 65 us where this
-// form took 67.
+// form took 67.  A piece's next load comes after the last use of its registers:
+// before it, binary32 values, which are used as they were loaded, would be copied at
+// the end of the loop, which waits for them (32768 x 1600 fp32: 193 us instead of
+// 111, at an odd place 480 instead of 132).
 template <class F, int E, int NV, int G, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
     using S = typename Store<F>::S;
     constexpr int T = THREADS / 32 / G, C = NV * E;
+    constexpr int P = E == 1 ? 2 : 1;   // single elements: two pieces make a pair
     constexpr bool KEEP = C <= 32;
-    static_assert(T * G * 32 == THREADS && C % 2 == 0, "whole teams, pairs of columns");
+    static_assert(T * G * 32 == THREADS && C % 2 == 0 && NV % P == 0, "whole teams, pairs of columns");
     extern __shared__ __align__(16) float sums[];   // [team][2][d]
     __shared__ float sh[2][T][G][2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, team = warp / G, part = warp % G;
@@ -734,7 +743,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
         for (int j = 0; j < C / 2; ++j) sw[j] = sb[j] = f2(0.0f, 0.0f);
         const S* x_at = static_cast<const S*>(a.x) + (size_t)tid * E;
         const S* g_at = static_cast<const S*>(a.gy) + (size_t)tid * E;
-        Raw<F, E> rx[KEEP ? NV : 1], rg[KEEP ? NV : 1];
+        Raw<F, E> rx[KEEP ? NV : P] = {}, rg[KEEP ? NV : P] = {};
         float next_mean = 0.0f, next_rstd = 0.0f;
         const auto load = [&](int k, int at, int64_t row) {
             rx[at].load(x_at + row * a.x_stride + k * 32 * G * E);
@@ -760,52 +769,40 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
             // c = x - mean, h = gy * w: the sums of h, h c, gy c / std and gy
             [[maybe_unused]] F2 cs[KEEP ? C / 2 : 1], hs[KEEP ? C / 2 : 1];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
+            for (int k = 0; k < NV; k += P) {
                 if (any(k)) {
-                    float x[E] = {}, g[E] = {}, w[E] = {};   // zeros behind the row: they add nothing
-                    if (mine(k)) {
-                        if constexpr (!KEEP) load(k, 0, row);
-                        rx[KEEP ? k : 0].get(x);
-                        rg[KEEP ? k : 0].get(g);
-                        ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)(tid + k * 32 * G) * E, w);
-                        if constexpr (KEEP)
-                            if (more) load(k, k, row + T);
-                    }
-                    if constexpr (E > 1) {
+                    float x[P][E], g[P][E], w[P][E] = {};   // zeros behind the row: they add nothing
 #pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            const int j = (k * E + e) / 2;
-                            const F2 c = add2(f2(x[e], x[e + 1]), minus), gg = f2(g[e], g[e + 1]);
-                            sw[j] = fma2(mul2(gg, by), c, sw[j]);
-                            sb[j] = add2(sb[j], gg);
-                            const F2 h = mul2(gg, f2(w[e], w[e + 1]));
-                            s1 = add2(s1, h);
-                            s2 = fma2(h, c, s2);
-                            if constexpr (KEEP) {
-                                cs[j] = c;
-                                hs[j] = h;
-                            }
+                    for (int q = 0; q < P; ++q) {
+                        const int at = KEEP ? k + q : q;
+                        if constexpr (!KEEP) {
+                            rx[at] = rg[at] = {};
+                            if (mine(k + q)) load(k + q, at, row);
                         }
-                    } else {   // single elements: one of a pair, the other half idle
-                        const bool odd = k & 1;
-                        const int j = k / 2;
-                        const auto put = [odd](F2 old, float v) {
-                            float lo, hi;
-                            split(old, lo, hi);
-                            return odd ? f2(lo, v) : f2(v, hi);
-                        };
-                        const float c = __fsub_rn(x[0], mean), h = __fmul_rn(g[0], w[0]);
-                        float lo, hi;
-                        split(sw[j], lo, hi);
-                        sw[j] = put(sw[j], __fmaf_rn(__fmul_rn(g[0], rstd), c, odd ? hi : lo));
-                        split(sb[j], lo, hi);
-                        sb[j] = put(sb[j], __fadd_rn(odd ? hi : lo, g[0]));
-                        s1 = add2(s1, f2(h, 0.0f));
-                        s2 = fma2(f2(h, 0.0f), f2(c, 0.0f), s2);
+                        rx[at].hold();
+                        rg[at].hold();
+                        rx[at].get(x[q]);
+                        rg[at].get(g[q]);
+                        if (mine(k + q)) ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)(tid + (k + q) * 32 * G) * E, w[q]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < P * E; e += 2) {
+                        const int j = (k * E + e) / 2, q = e / E, i = e % E, q1 = (e + 1) / E, i1 = (e + 1) % E;
+                        const F2 c = add2(f2(x[q][i], x[q1][i1]), minus), gg = f2(g[q][i], g[q1][i1]);
+                        sw[j] = fma2(mul2(gg, by), c, sw[j]);
+                        sb[j] = add2(sb[j], gg);
+                        const F2 h = mul2(gg, f2(w[q][i], w[q1][i1]));
+                        s1 = add2(s1, h);
+                        s2 = fma2(h, c, s2);
                         if constexpr (KEEP) {
-                            cs[j] = put(cs[j], c);
-                            hs[j] = put(hs[j], h);
+                            cs[j] = c;
+                            hs[j] = h;
                         }
+                    }
+                    if constexpr (KEEP) {   // the next row's, into registers that are free now
+#pragma unroll
+                        for (int q = 0; q < P; ++q)
+                            if (more && mine(k + q)) load(k + q, k + q, row + T);
                     }
                 }
             }
@@ -839,29 +836,33 @@ __global__ void __launch_bounds__(THREADS, 1) norm_grad_kernel(const __grid_cons
             const F2 less = f2(l, l), along = f2(k3, k3);
             S* dst = static_cast<S*>(a.gx) + row * (int64_t)a.d + (size_t)tid * E;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
+            for (int k = 0; k < NV; k += P) {
                 if (mine(k)) {
-                    float o[E];
+                    float o[P][E];
                     if constexpr (!KEEP) {
-                        load(k, 0, row);
-                        float x[E], g[E], w[E];
-                        rx[0].get(x);
-                        rg[0].get(g);
-                        ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)(tid + k * 32 * G) * E, w);
 #pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            o[e] = __fmaf_rn(__fsub_rn(x[e], mean), k3, __fmaf_rn(__fmul_rn(g[e], w[e]), rstd, l));
-                    } else if constexpr (E > 1) {
+                        for (int q = 0; q < P; ++q) {
+                            if (mine(k + q)) {
+                                load(k + q, 0, row);
+                                float x[E], g[E], w[E];
+                                rx[0].get(x);
+                                rg[0].get(g);
+                                ld_e<F, E>(static_cast<const S*>(a.weight) + (size_t)(tid + (k + q) * 32 * G) * E, w);
 #pragma unroll
-                        for (int e = 0; e < E; e += 2) {
-                            const int j = (k * E + e) / 2;
-                            split(fma2(cs[j], along, fma2(hs[j], by, less)), o[e], o[e + 1]);
+                                for (int e = 0; e < E; ++e)
+                                    o[q][e] = __fmaf_rn(__fsub_rn(x[e], mean), k3, __fmaf_rn(__fmul_rn(g[e], w[e]), rstd, l));
+                            }
                         }
                     } else {
-                        split(fma2(cs[k / 2], along, fma2(hs[k / 2], by, less)), lo, hi);
-                        o[0] = k & 1 ? hi : lo;
+#pragma unroll
+                        for (int e = 0; e < P * E; e += 2) {
+                            const int j = (k * E + e) / 2;
+                            split(fma2(cs[j], along, fma2(hs[j], by, less)), o[e / E][e % E], o[(e + 1) / E][(e + 1) % E]);
+                        }
                     }
-                    st_e<F, E>(dst + k * 32 * G * E, o);
+#pragma unroll
+                    for (int q = 0; q < P; ++q)
+                        if (mine(k + q)) st_e<F, E>(dst + (k + q) * 32 * G * E, o[q]);
                 }
             }
         }
@@ -1256,17 +1257,22 @@ zero_status_t launch_norm_team(const zk::NormGradArgs& a, cudaStream_t s, const 
     return after_launch(what);
 }
 
-// 16 columns a thread and as many warps a row as that takes; more columns a thread above 4096.
+// 16 columns a thread, 8 of single elements (each takes two registers while it
+// is loaded, and 16 left none for the loads of the next row: 32768 x 1600 bf16 at
+// an odd place 144 us, now 108), and as many warps a row as that takes; more
+// columns a thread above 16 warps.
 template <class F, int E>
 zero_status_t launch_norm_grad(const zk::NormGradArgs& a, cudaStream_t s, const char* what) {
-    constexpr int B = 16 / E;
+    constexpr int C = E == 1 ? 8 : 16, B = C / E;
     if (a.dv <= 16u * B) return launch_norm_team<F, E, B / 2, 1, 512>(a, s, what);
     if (a.dv <= 32u * B) return launch_norm_team<F, E, B, 1, 512>(a, s, what);
     if (a.dv <= 64u * B) return launch_norm_team<F, E, B, 2, 512>(a, s, what);
     if (a.dv <= 128u * B) return launch_norm_team<F, E, B, 4, 512>(a, s, what);
     if (a.dv <= 256u * B) return launch_norm_team<F, E, B, 8, 512>(a, s, what);
-    if (a.dv <= 512u * B) return launch_norm_team<F, E, 2 * B, 8, 256>(a, s, what);
-    return launch_norm_team<F, E, 4 * B, 8, 256>(a, s, what);
+    if constexpr (C == 8)
+        if (a.dv <= 512u * B) return launch_norm_team<F, E, B, 16, 512>(a, s, what);
+    if (a.dv * E <= 8192) return launch_norm_team<F, E, 32 / E, 8, 256>(a, s, what);
+    return launch_norm_team<F, E, 64 / E, 8, 256>(a, s, what);
 }
 
 }  // namespace
