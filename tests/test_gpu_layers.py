@@ -237,6 +237,23 @@ def test_layer_norm_backward(rows, d, dtype, shift, fp32_grad):
         assert torch.equal(gw, first[0]) and torch.equal(gb, first[1])
 
 
+@pytest.mark.parametrize("rows,d,dtype,shift", [(400, 1001, FP, 1), (310, 1600, FP, 0), (470, 1602, BF, 2), (200, 4104, HF, 8), (307, 5001, BF, 0),
+                                                (160, 10000, BF, 0), (333, 2500, FP, 0), (153, 10008, FP, 0), (305, 9002, HF, 2), (154, 16383, BF, 1)])
+def test_layer_norm_of_several_rows_a_block(rows, d, dtype, shift):
+    """More rows than blocks and, capped, many for each CTA: a row is loaded while another is worked on."""
+    x, w, b, gy = norm_inputs(rows, d, dtype, shift)
+    first = L.layer_norm_forward(x, w, b)
+    for a, e, t in zip(first, *norm_exact(x, w, b, 1e-5)):
+        close(a, e, t)
+    B.zero_set_max_ctas(3)
+    assert all(torch.equal(a, e) for a, e in zip(L.layer_norm_forward(x, w, b), first))
+    gw, gb = torch.empty_like(w), torch.empty_like(b)
+    gx = L.layer_norm_backward(gy, x, w, *first[1:], gw, gb)
+    exact, tol = norm_grad_exact(gy, x, w, *first[1:], -(-rows // 152))
+    for a, e, t in zip((gx, gw, gb), exact, tol):
+        close(a, e, t)
+
+
 def test_layer_norm_rows_of_one_value_and_far_from_zero():
     d = 640
     x = torch.zeros(4, d, device="cuda")
