@@ -897,9 +897,10 @@ zero_status_t zero_lm_loss_backward(const zero_lm_loss_args* a, zero_stream_t st
 
 /* Errors that the last call's kernels reported in this workspace, with the
  * bits of zero_step_state.error (*bits = 0: none).  Synchronises the device.
- * A forward call that reports one has NaN in stats[0], a backward call in the
- * first rows of its gradients, so that a step with a norm and a decision is
- * skipped. */
+ * A forward call that reports one has NaN in stats, which makes the loss and
+ * every gradient of a backward call with these stats NaN; a backward call that
+ * reports one has NaN in the first rows of its gradients.  A step with a norm
+ * and a decision is skipped then. */
 zero_status_t zero_lm_loss_device_error(const void* workspace, int32_t* bits);
 
 /* Cap on the CTAs of every later launch by this library (process-wide;

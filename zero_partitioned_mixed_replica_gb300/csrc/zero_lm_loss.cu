@@ -882,8 +882,11 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ 
     }
     if (threadIdx.x == 0) {
         const double share = a.reduction == ZERO_LOSS_MEAN ? __ddiv_rn(1.0, (double)max(count, 1)) : 1.0;
-        a.stats[0] = *(volatile int32_t*)&a.head->error ? NAN : __double2float_rn(__dmul_rn(sums[0], share));
-        a.stats[1] = __double2float_rn(share);
+        // after an error lse is not whole either, and the backward call has no other word of it: share is a factor of each
+        // of its gradients
+        const bool whole = *(volatile int32_t*)&a.head->error == 0;
+        a.stats[0] = whole ? __double2float_rn(__dmul_rn(sums[0], share)) : NAN;
+        a.stats[1] = whole ? __double2float_rn(share) : NAN;
     }
 }
 
