@@ -800,7 +800,8 @@ zero_status_t zero_embedding_forward(const void* weight, const int64_t* ids, int
  * grad_out [n, d] of dtype, grad_weight [vocab, d] of grad_dtype.  Ids outside
  * 0 .. vocab-1 take no part.  Tokens are sorted by id (stable) and each id's
  * rows added in that order, in fixed pieces.  Three launches, the first of two
- * CTAs at least (one sorts, one zeroes). */
+ * CTAs at least where it does not accumulate (one sorts, one zeroes): under a
+ * zero_set_max_ctas of 1 the one launch above the cap. */
 zero_status_t zero_embedding_workspace(int64_t vocab, int64_t d, int64_t n, int64_t* bytes);
 zero_status_t zero_embedding_backward(const void* grad_out, const int64_t* ids, int64_t vocab, int64_t d, int64_t n,
                                       int32_t dtype, int32_t grad_dtype, double scale, int32_t accumulate,

@@ -1,5 +1,5 @@
-"""The grids that the operators' calls launch, read from captured graphs: chosen by the call's own sizes
-whatever calls came before."""
+"""The grids that the operators' calls launch, read from captured graphs: capped as the header says, and chosen by the call's
+own sizes whatever calls came before."""
 import ctypes
 import json
 import os
@@ -54,6 +54,41 @@ def _cuda():
         pytest.skip("needs a CUDA GPU")
     yield
     B.zero_set_max_ctas(0)
+
+
+@pytest.mark.parametrize("cap", [1, 2, 3, 4, 5, 7, 8, 12, 15, 16, 31, 100])
+@pytest.mark.parametrize("n", [100, 2048, 2049, 30000, 200000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_gradient_within_the_cap(n, cap, accumulate):
+    ids = torch.zeros(n, dtype=torch.int64, device="cuda")
+    g = torch.zeros(n, 8, dtype=BF, device="cuda")
+    gw = torch.zeros(40000, 8, dtype=BF, device="cuda")
+    B.zero_set_max_ctas(cap)
+    got = launches(lambda: L.embedding_backward(g, ids, gw, accumulate=accumulate))
+    assert len(got) == 3
+    # the first launch sorts and zeroes: two CTAs at least, where there are zeros to write
+    assert got[0][0] <= max(cap, 1 if accumulate else 2), got
+    assert all(ctas <= cap for ctas, _ in got[1:]), got
+
+
+OPERATORS = ["embedding", "norm", "norm gradient", "loss", "loss gradient", "loss gradient, copies"]
+
+
+@pytest.mark.parametrize("cap", [1, 2, 7, 40])
+@pytest.mark.parametrize("n", [3, 129, 5000])
+@pytest.mark.parametrize("op", OPERATORS)
+def test_the_other_operators_within_the_cap(op, n, cap):
+    d, vocab, at = 128, 3000, 1 if "copies" in op else 0
+    x, w = torch.zeros(n, d, dtype=BF, device="cuda"), torch.zeros(vocab * d + 8, dtype=BF, device="cuda")[at:at + vocab * d].view(vocab, d)
+    ids, row, per_row = torch.zeros(n, dtype=torch.int64, device="cuda"), torch.zeros(d, dtype=BF, device="cuda"), torch.zeros(n, device="cuda")
+    gw, grow, saved = torch.zeros_like(w), torch.zeros_like(row), torch.zeros(2 + n, device="cuda")
+    B.zero_set_max_ctas(cap)
+    got = launches({"embedding": lambda: L.embedding_forward(w, ids),
+                    "norm": lambda: L.layer_norm_forward(x, row),
+                    "norm gradient": lambda: L.layer_norm_backward(x, x, row, per_row, per_row, grow),
+                    "loss": lambda: L.lm_loss_forward(x, w, ids)}.get(op, lambda: L.lm_loss_backward(x, w, ids, saved, gw, piece=1024)))
+    assert got and all(ctas <= cap + cap % 2 for ctas, _ in got if "loss" in op), got   # the next even number
+    assert "loss" in op or all(ctas <= cap for ctas, _ in got), got
 
 
 WIDTHS = [2304, 4096, 8192, 9000, 16384, 1025, 2049, 8191, 16383, 1026, 5002, 16382]    # 16-byte pieces, single elements, pairs

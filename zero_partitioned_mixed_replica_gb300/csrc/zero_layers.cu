@@ -1152,9 +1152,10 @@ extern "C" zero_status_t zero_embedding_backward(const void* grad_out, const int
     sa.passes = 1;
     while (sa.passes < 4 && (vocab >> (8 * sa.passes)) > 0) ++sa.passes;
     const int32_t cap = max_ctas();
-    // the cluster that sorts: 8 CTAs, one for what one can sort as fast
+    // the cluster that sorts: 8 CTAs, one for what one can sort as fast; under a cap with room for one that zeroes beside it
+    const int clusters = sa.zero_bytes > 0 ? 2 : 1;
     int cluster = n <= 2048 ? 1 : 8;
-    while (cap > 0 && cluster > 1 && cluster > cap) cluster /= 2;
+    while (cap > 0 && cluster > 1 && clusters * cluster > cap) cluster /= 2;
     const int64_t warps = (int64_t)cluster * zk::kSortWarps;
     sa.per_warp = (uint32_t)((n + warps * 32 - 1) / (warps * 32) * 32);
     constexpr int64_t kMost = 192 << 10;   // of shared memory for the pairs: 98304 tokens in 8 CTAs
