@@ -31,6 +31,8 @@ constexpr int kBoxBytes = 128 * 128;  // 128 rows of 64
 constexpr int kTileN = 256;           // columns of a tile, at most
 constexpr int kRun = 8;               // blocks of K that the tensor cores add up of a logit for few tokens, at most (MmTile)
 constexpr int kFewN = 128;            // columns of a tile of logits then, at most
+constexpr int kLongRun = 128;         // blocks of K that they add up of other logits, at most
+constexpr int kGradRun = 512;         // and of the gradients
 
 enum { MM_STATS = 0, MM_DZ = 1, MM_GRADS = 2 };
 enum { ROWS_M = 1, ROWS_K = 2 };  // which extent is the number of tokens that count
@@ -87,7 +89,9 @@ struct MmArgs {
     const float* share;
     int32_t part_add, gw_add; // to what is there
     int32_t gw_vec;           // rows begin on 32-byte boundaries, d % 16 == 0
+    float* held;              // [CTA][kHeld]: a tile's sums between its runs; NULL where none has two
 };
+constexpr int kHeld = 128 * kTileN;
 
 constexpr int kMaxStages = 8;
 struct MmShape {
@@ -98,13 +102,17 @@ struct MmShape {
     static constexpr int kBytes = 1024 + kOps + kTurn + kSync;  // and alignment
 };
 
-// The tensor cores cut the sums that they keep instead of rounding them: errors
-// of one sign, 1e-6 of a logit over 2000 of K.  For up to 128 tokens (CG = 1),
-// whose losses no mean over many smooths and whose products wait for the
-// weight, they add a logit's K in runs of up to 512, and the runs are added in
-// registers: losses off by up to 1.8e-6 relatively before, below 1e-6 since, in
-// the same time.  Tiles are then kFewN wide: for more tokens a thread would hold
-// 128 sums of a tile twice as wide, which spills.
+// The tensor cores cut the sums that they keep instead of rounding them, 16 of K at a time, all to one side: where the
+// terms of a sum have one sign it comes out smaller, by about 2^-24 of itself for each 16 of K, or twice that (65536 terms
+// 1.9e-4, 262144 terms 1.4e-3, several steps of fp16).  So they add runs of K, and the runs are added in binary32 with
+// rounding to nearest:
+//  - up to 128 tokens (CG = 1), logits: runs of up to 512 of K, added in registers.  Losses off by up to 1.8e-6
+//    relatively before, below 1e-6 since, in the same time.  Tiles are then kFewN wide: for more tokens a thread would
+//    hold 128 sums of a tile twice as wide, which spills;
+//  - for more tokens logits in runs of up to 8192 of K (within 6e-5 for terms of one sign), the gradients of up to 32768
+//    (within 1e-4, less than half of what fp16 rounds), added in `held`, each thread's own place in memory: 128 KB a CTA of
+//    L2's traffic each way per run.  Gradients in runs of 8192 made the steps of 8192 tokens 3% longer, 3.01 -> 3.14 ms at
+//    d 1600 and fp16.
 struct alignas(16) MmTile {
     int32_t p;                // problem, or -1: no more tiles
     int32_t m, n, split;      // row tile, column tile
@@ -155,6 +163,15 @@ struct MmGrid {
     __device__ MmGrid(const MmArgs& a) : e0(a.p[0], a.head->count), e1(a.p[MODE == MM_GRADS], a.head->count) {
         second = MODE == MM_GRADS && e1.kblocks > e0.kblocks / a.p[0].splits;
     }
+    __device__ static void set_run(MmTile& r, int32_t longest) {   // runs of about one length
+        const int32_t blocks = r.kb1 - r.kb0;
+        if (blocks > longest) {
+            const int32_t runs = (blocks + longest - 1) / longest;
+            r.run = (blocks + runs - 1) / runs;
+        } else {
+            r.run = max(1, blocks);
+        }
+    }
     __device__ int64_t all() const { return MODE == MM_GRADS ? e0.tiles + e1.tiles : e0.tiles; }
     __device__ MmTile tile(const MmArgs& a, int64_t t) const {
         if constexpr (MODE == MM_GRADS) {
@@ -163,13 +180,12 @@ struct MmGrid {
             if (t >= lead) t -= lead;
             MmTile r = p1 ? e1.tile(a.p[1], t) : e0.tile(a.p[0], t);
             r.p = p1;
-            r.run = max(1, r.kb1 - r.kb0);
+            set_run(r, kGradRun);
             return r;
         } else {
             MmTile r = e0.tile(a.p[0], t);
             r.p = 0;
-            const int32_t blocks = r.kb1 - r.kb0, runs = CG == 1 ? (blocks + kRun - 1) / kRun : 1;   // of about one length
-            r.run = (blocks + runs - 1) / runs;
+            set_run(r, CG == 1 ? kRun : kLongRun);
             return r;
         }
     }
@@ -504,6 +520,40 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                 if (lane == 0) mbar_arrive_remote(leader(acc_empty + (done & 1)));
                 ++done;
             };
+            // all runs of K but the last into this thread's place, where the last finds their sums
+            [[maybe_unused]] const bool runs = w.kb0 + w.run < w.kb1;
+            const auto held_at = [&](int c) { return a.held + (int64_t)blockIdx.x * kHeld + warp * (kHeld / kEpiWarps) + (c - c0) * 32 + lane * 8; };
+            const auto add_held = [&](int c, float (&v)[32]) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t u[8];
+                    ld8w(held_at(c) + h * 256, u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[h * 8 + j] = __fadd_rn(__uint_as_float(u[j]), v[h * 8 + j]);
+                }
+            };
+            const auto hold_runs = [&] {
+                for (int32_t k0 = w.kb0; k0 + w.run < w.kb1; k0 += w.run) {
+                    const uint32_t at = take();
+                    if (!ok) return;
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t u[32];
+                        tc_ld32(at + c, u);
+                        tc_wait_ld();
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+                        if (k0 > w.kb0) add_held(c, v);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[h * 8 + j]);
+                            st8w(held_at(c) + h * 256, u);
+                        }
+                    }
+                    give();
+                }
+            };
             if constexpr (MODE != MM_GRADS) {
                 const int target = row_on ? a.target[row] - (int)n0 - p.n_off : -1;
                 [[maybe_unused]] float top = -INFINITY, sum = 0.0f, lse = 0.0f;
@@ -565,6 +615,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                     for (int g = 0; g < 2; ++g)
                         if (c0 + g * 32 < c1) use(z[g], c0 + g * 32, c1 - c0 - g * 32);
                 } else {
+                    hold_runs();
+                    if (!ok) break;
                     const uint32_t at = take();
                     if (!ok) break;
                     for (int c = c0; c < c1; c += 32) {
@@ -574,6 +626,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                         float v[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+                        if (runs) add_held(c, v);
                         use(v, c, c1 - c);
                     }
                     give();
@@ -582,6 +635,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                     if (row_on) a.parts[row * a.part_ld + 2 * w.n + half] = make_float2(top, sum);
             } else {
                 const bool any = w.kb0 < w.kb1;   // without a token that counts the sums are zeros
+                hold_runs();
+                if (!ok) break;
                 const uint32_t at = any ? take() : 0;
                 if (!ok) break;
                 for (int c = c0; c < c1; c += 32) {
@@ -592,6 +647,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
                         tc_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+                        if (runs) add_held(c, v);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
@@ -1007,6 +1063,8 @@ struct Operand {
     int box_rows;
 };
 
+constexpr int64_t kSlots = 152;   // SMs of a GB300: what the splits of work are made for
+
 // Tiles of a launch at most (all tokens counting).
 template <int CG>
 int64_t most_tiles(const zk::MmProblem& p) {
@@ -1044,6 +1102,7 @@ zero_status_t launch_mm(const Operand* oa, const Operand* ob, zk::MmArgs a, cuda
     int64_t groups = std::max(1, sm_count() / CG);
     const int32_t cap = max_ctas();
     if (cap > 0) groups = std::min<int64_t>(groups, (cap + CG - 1) / CG);
+    if (a.held) groups = std::min(groups, kSlots / CG);   // what it has places for
     groups = std::max<int64_t>(1, std::min(groups, most_tiles<CG>(a.p[0]) + most_tiles<CG>(a.p[1])));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(groups * CG));
@@ -1065,8 +1124,6 @@ zero_status_t launch_mm(const Operand* oa, const Operand* ob, zk::MmArgs a, cuda
     }
     return after_launch(what);
 }
-
-constexpr int64_t kSlots = 152;   // SMs of a GB300: what the splits of work are made for
 
 int cta_group(int64_t n) { return n <= 128 ? 1 : 2; }
 
@@ -1098,8 +1155,8 @@ struct LossPlan {
     int64_t piece, pieces, splits, ldo;
     // offsets: of both calls, of the forward, of the backward
     int64_t next, slot, token, target, hidden, weight;
-    int64_t z_target, parts, sums, forward;
-    int64_t dz, part, backward;
+    int64_t z_target, parts, sums, held_f, forward;
+    int64_t dz, part, held_b, backward;   // held: 0 where no sum has two runs
 };
 
 constexpr int64_t kPieceBytes = 512 << 20;
@@ -1128,6 +1185,9 @@ LossPlan make_plan(const zero_lm_loss_args* a) {
     const int64_t tiles1 = (p.piece + 128 * cg - 1) / (128 * cg) * columns, kb1 = (a->n + 63) / 64;
     const int64_t share = std::max<int64_t>(8, (tiles0 * kb0 + tiles1 * kb1) / slots / 2);
     p.splits = std::max<int64_t>(1, std::min<int64_t>({(kb0 + share - 1) / share, 32, (64 << 20) / (p.n256 * p.ldo * 4)}));
+    const bool long_d = cg == 2 && (a->d + 63) / 64 > zk::kLongRun;
+    const bool long_grads = std::max((kb0 + p.splits - 1) / p.splits, kb1) > zk::kGradRun;
+    constexpr int64_t held = kSlots * zk::kHeld * 4;
     int64_t at = 256;
     const auto take = [&](int64_t bytes) { const int64_t o = at; at += up(bytes, 256); return o; };
     p.next = take(4 * (2 * p.pieces + 1));
@@ -1140,10 +1200,12 @@ LossPlan make_plan(const zero_lm_loss_args* a) {
     p.z_target = take(4 * a->n);
     p.parts = take(p.part_ld * a->n * 8);
     p.sums = take((a->n + zk::kLossRows - 1) / zk::kLossRows * 8 + 8);
+    p.held_f = long_d ? take(held) : 0;
     p.forward = at;
     at = common;
     p.dz = take(p.n256 * p.piece * 2);
     p.part = take(p.splits * p.n256 * p.ldo * 4);
+    p.held_b = long_d || long_grads ? take(held) : 0;
     p.backward = at;
     return p;
 }
@@ -1249,6 +1311,7 @@ zero_status_t run_forward(const zero_lm_loss_args* a, const LossPlan& p, const v
     m.parts = reinterpret_cast<float2*>(ws + p.parts);
     m.part_ld = p.part_ld;
     m.z_target = reinterpret_cast<float*>(ws + p.z_target);
+    m.held = p.held_f ? reinterpret_cast<float*>(ws + p.held_f) : nullptr;
     return launch_mm<CG, zk::MM_STATS, F>(&h, &w, m, s, what);
 }
 
@@ -1265,6 +1328,7 @@ zero_status_t run_backward(const zero_lm_loss_args* a, const LossPlan& p, const 
     base.part = reinterpret_cast<float*>(ws + p.part);
     base.split_rows = p.n256;
     base.part_cols = p.ldo;
+    base.held = p.held_b ? reinterpret_cast<float*>(ws + p.held_b) : nullptr;
     base.scale = (float)a->scale / up_by;
     base.scale_dev = a->scale_dev;
     base.share = a->stats + 1;
