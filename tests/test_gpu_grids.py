@@ -71,6 +71,28 @@ def test_embedding_gradient_within_the_cap(n, cap, accumulate):
     assert all(ctas <= cap for ctas, _ in got[1:]), got
 
 
+@pytest.mark.parametrize("n", [2049, 9000, 98304, 98305, 200000])
+def test_embedding_gradient_under_caps_is_the_same(n):
+    # clusters of 1, 2, 4 and 8 that sort, in shared memory and outside it
+    g = torch.Generator("cuda").manual_seed(n)
+    ids = torch.randint(-3, 70000, (n,), generator=g, device="cuda")
+    ids[: n // 2] %= 50
+    go = torch.randn(n, 24, generator=g, device="cuda").to(BF)
+    want = L.embedding_backward(go, ids, torch.empty(66000, 24, dtype=BF, device="cuda"))
+    inside = (ids >= 0) & (ids < 66000)
+    count = torch.bincount(ids[inside], minlength=66000)
+    plain = torch.zeros(66000, 24, dtype=torch.float64, device="cuda").index_add_(0, ids[inside], go[inside].double())
+    size = torch.zeros_like(plain).index_add_(0, ids[inside], go[inside].double().abs())
+    # each addition and the product off by 2^-24 of the magnitudes, then the rounding to bf16
+    tol = (count[:, None] + 3) * 2.0 ** -24 * size
+    assert bool(((want.double() - plain).abs() <= tol + 2.0 ** -8 * (plain.abs() + tol)).all())
+    for accumulate in (False, True):
+        for cap in (1, 2, 4, 5, 7, 8, 15, 16, 100):
+            B.zero_set_max_ctas(cap)
+            got = L.embedding_backward(go, ids, torch.zeros_like(want) if accumulate else torch.full_like(want, 5.0), accumulate=accumulate)
+            assert torch.equal(got, want), (accumulate, cap)
+
+
 OPERATORS = ["embedding", "norm", "norm gradient", "loss", "loss gradient", "loss gradient, copies"]
 
 
