@@ -834,11 +834,12 @@ zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, co
 /* Language-model head and loss                                                */
 /* ------------------------------------------------------------------------ */
 /* Softmax cross entropy of the logits hidden @ weight^T against a target per
- * token, without keeping the logits: [n, vocab] of them (0.8 GB in 16 bits at
- * 8192 tokens of GPT-2) never exist.  The forward call computes tiles of
+ * token, without keeping the logits ([n, vocab], 0.8 GB in 16 bits at 8192
+ * tokens of GPT-2).  The forward call computes tiles of
  * them in tensor memory and keeps each tile's row maximum and sum of
  * exponentials; the backward call computes them again, piece of the
- * vocabulary by piece, turns a piece into its gradient (16-bit, rounded once)
+ * vocabulary by piece, turns a piece into its gradient (16-bit, rounded once;
+ * the piece is in the workspace, and a vocabulary that fits one is one piece)
  * and multiplies that with the weight and with the hidden states.
  *   loss_i = log(sum_k exp(z_ik)) - z_i,target(i),  z_ik = hidden_i . weight_k
  *   dz_ik = (exp(z_ik - lse_i) - [k == target(i)]) * share * scale
@@ -847,8 +848,10 @@ zero_status_t zero_layer_norm_backward(const void* grad_y, int64_t gy_stride, co
  * ZERO_LOSS_SUM.  A target outside 0 .. vocab-1 (padding) makes a token not
  * count: its loss is 0, its row of grad_hidden zeros, its hidden state is
  * read by no product (it may hold NaN).  With no token that counts, the
- * loss and all gradients are zeros.  A logit that is NaN or +inf makes its
- * token's loss NaN.
+ * loss and all gradients are zeros (of a finite scale).  A logit that is NaN
+ * or +inf makes its token's loss NaN.  lse is binary32: where logits are in the
+ * thousands, the backward call's probabilities are off by its rounding, 2^-24
+ * of lse, relatively (1e-4 at 2000).
  *
  * hidden [n, d] with hidden_stride elements between rows (>= d), weight
  * [vocab, d], of dtype ZERO_BF16 or ZERO_FP16; targets [n]; losses, lse [n] and

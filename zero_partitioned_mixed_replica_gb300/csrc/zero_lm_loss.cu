@@ -834,9 +834,11 @@ struct CopyArgs {
     uint32_t d;
 };
 
-// 8 elements a lane, from 5 aligned words shifted by 0 or 16 bits.  Words behind
-// the matrix are not read; what a row's last piece has of the next row lies
-// between d and ld, which no product reads.
+// 8 elements a lane, from 5 aligned words shifted by 0 or 16 bits.  A matrix that
+// begins or ends in the middle of a word has the other two bytes of that word
+// read and thrown away (device allocations are whole words); words wholly behind
+// it are not read.  What a row's last piece has of the next row lies between d
+// and ld, which no product reads.
 __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
     const uint32_t lane = threadIdx.x & 31, pieces = (a.d + 7) / 8;
     const int64_t step = (int64_t)gridDim.x * kThreads / 32;

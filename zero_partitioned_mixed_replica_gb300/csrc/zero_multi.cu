@@ -80,13 +80,11 @@ struct MultiArgs {
     uint32_t seed;
 };
 
-// The kernels are launched so that they may begin while the kernel before them
-// in the stream ends; what that kernel wrote is read after grid_wait() only.
-// The rows and the chunk map are read before it (multi_reset_kernel).
-
 // ----------------------------------------------------------------------------
 // Binding
 // ----------------------------------------------------------------------------
+// The kernels of a step are launched so that they may begin while the kernel before them in the stream ends (launch_early);
+// what that kernel wrote is read after grid_wait() only.  The rows and the chunk map are read before it (multi_reset_kernel).
 struct RowBatch {
     MultiRow rows[kRowsPerLaunch];
 };
